@@ -20,7 +20,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmk.so")
 
 MK_OK, MK_ERR_INVALID, MK_ERR_UNSUPPORTED, MK_ERR_CUDA, MK_ERR_TIMEOUT, MK_ERR_CAPACITY = range(6)
-MK_BF16, MK_F32 = 0, 1
+MK_BF16, MK_F32, MK_F16, MK_E4M3 = 0, 1, 2, 3
 OP_AG_GEMM, OP_GEMM_RS, OP_GEMM_AR, OP_MOE = 0, 1, 2, 3
 MODE_FUSED, MODE_GEMM_ONLY, MODE_UNFUSED = 0, 1, 2
 REDUCE_AUTO, REDUCE_RUNNING_SUM, REDUCE_LAST_ARRIVAL, REDUCE_ATOMIC, REDUCE_SLICED = 0, 1, 2, 3, 4
@@ -99,6 +99,25 @@ def lib() -> ctypes.CDLL:
         return _lib
 
 
+class _Rotation(ctypes.Structure):
+    _fields_ = [("freqs", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("start", ctypes.c_longlong),
+                ("positions_64", ctypes.c_int), ("rot", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("inverse", ctypes.c_int), ("magnitude", ctypes.c_float)]
+
+
+class _Seqs(ctypes.Structure):
+    _fields_ = [("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("pages", ctypes.c_void_p),
+                ("pages_stride", ctypes.c_longlong), ("batch", ctypes.c_int), ("max_pages", ctypes.c_int)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_longlong),
+                ("head_stride", ctypes.c_longlong), ("slot_stride", ctypes.c_longlong),
+                ("n_pages", ctypes.c_longlong), ("dtype", ctypes.c_int), ("heads", ctypes.c_int),
+                ("d", ctypes.c_int), ("page_size", ctypes.c_int)]
+
+
 class use_library:
     """Context manager: every op of this module calls the given library (for
     example the bounds-checking LIB_DEBUG_PATH) instead of libmk.so."""
@@ -170,6 +189,17 @@ def load_library(path: str) -> ctypes.CDLL:
     L.mk_moe_dispatch_gemm.restype = i
     L.mk_moe_dispatch_gemm.argtypes = [P(vp), P(vp), P(vp), i, i, i, ll, ll, ll, ll, vp, vp,
                                        P(vp), vp, P(vp), P(vp), vp, sz, P(_Cfg), vp]
+    f32 = ctypes.c_float
+    L.mk_rope.restype = i
+    L.mk_rope.argtypes = [vp, vp, i, ll, i, i, ll, ll, ll, ll, P(_Rotation), vp]
+    L.mk_kv_append.restype = i
+    L.mk_kv_append.argtypes = [P(_Cache), vp, vp, i, ll, ll, ll, ll, ll, vp, vp, i, ll, ll, ll, ll, P(_Seqs),
+                               P(_Rotation), vp, sz, vp]
+    L.mk_paged_attention_workspace_size.restype = sz
+    L.mk_paged_attention_workspace_size.argtypes = [ll, i, i, i, i]
+    L.mk_paged_attention.restype = i
+    L.mk_paged_attention.argtypes = [vp, vp, vp, i, ll, i, ll, ll, ll, ll, P(_Cache), P(_Seqs), f32, i, i, i, i,
+                                     vp, sz, P(_Cfg), vp]
     return L
 
 
@@ -224,16 +254,17 @@ class Workspace:
 
 
 _default_ws: dict = {}
+_default_paged_ws: dict = {}   # paged attention's partial results must not meet the other ops' ready flags
 
 
-def _ws(workspace, device) -> Workspace:
+def _ws(workspace, device, default=_default_ws) -> Workspace:
     if workspace is not None:
         return workspace
     key = torch.device(device).index if torch.device(device).index is not None else \
         torch.cuda.current_device()
-    if key not in _default_ws:
-        _default_ws[key] = Workspace(torch.device("cuda", key))
-    return _default_ws[key]
+    if key not in default:
+        default[key] = Workspace(torch.device("cuda", key))
+    return default[key]
 
 
 def workspace_size(op: int, R: int, m: int, n: int, k: int, cfg: Config | None = None) -> int:
@@ -242,12 +273,20 @@ def workspace_size(op: int, R: int, m: int, n: int, k: int, cfg: Config | None =
 
 def device_status(workspace: Workspace | None = None, stream=None, device=None):
     """Synchronise the stream and read-and-clear the workspace's device status.
-    Returns (status, detail)."""
+    Returns (status, detail).  Without a workspace: that of the device's default
+    workspaces (paged attention has one of its own)."""
     ws = _ws(workspace, device or "cuda")
-    detail = ctypes.c_longlong(0)
-    st = lib().mk_get_device_status(ctypes.c_void_p(ws.get(256).data_ptr()),
-                                    ctypes.c_void_p(_stream(stream, ws.device)), ctypes.byref(detail))
-    return int(st), int(detail.value)
+    spaces = [ws]
+    if workspace is None and ws.device.index in _default_paged_ws:
+        spaces.append(_default_paged_ws[ws.device.index])
+    first = (MK_OK, 0)
+    for w in spaces:
+        detail = ctypes.c_longlong(0)
+        st = lib().mk_get_device_status(ctypes.c_void_p(w.get(256).data_ptr()),
+                                        ctypes.c_void_p(_stream(stream, w.device)), ctypes.byref(detail))
+        if first[0] == MK_OK:
+            first = (int(st), int(detail.value))
+    return first
 
 
 # ------------------------------------------------------------------ ops
@@ -529,7 +568,232 @@ def ring_attention(q, k, v, *, causal: bool = False, scale: float | None = None,
     return out
 
 
+# ------------------------------------------------------------------ rotary positions and the paged cache
+
+_ROW_DTYPES = {torch.bfloat16: MK_BF16, torch.float16: MK_F16, torch.float32: MK_F32}
+_CACHE_DTYPES = {torch.bfloat16: MK_BF16, torch.float16: MK_F16, FP8: MK_E4M3}
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _new(shape, dtype, device, stream):
+    """An output of a call: taken from the pool of the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _rows(t, name, heads=None, like=None):
+    """(token stride, head stride) of a [tokens x heads x d] tensor."""
+    _need(t.dim() == 3 and t.is_cuda, f"{name} must be a [tokens x heads x d] CUDA tensor")
+    _need(t.stride(2) == 1 or t.shape[2] == 1, f"{name}'s last dimension must be contiguous")
+    if like is not None:
+        _need(t.dtype == like.dtype and t.device == like.device, f"{name}'s type or device is not that of the others")
+        _need(t.shape[0] == like.shape[0] and t.shape[2] == like.shape[2], f"{name}'s tokens or d do not fit")
+    st, sh = t.stride(0), t.stride(1)
+    # the stride of a dimension of one (or no) element says nothing
+    return (st if t.shape[0] > 1 else 0), (sh if t.shape[1] > 1 else 0)
+
+
+def rope_freqs(rot: int, *, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+               original_length: int = 4096, fast: float = 32.0, slow: float = 1.0, device="cuda"):
+    """(frequencies, magnitude) for rope / kv_append: float64 [rot / 2] and a factor.
+
+    Unscaled, frequency i is base^(-2 i / rot).  scaling, for contexts `factor` times as
+    long as the `original_length` a model was trained on:
+      "linear"    every frequency divided by factor (positions interpolated);
+      "ntk"       base grown to base * factor^(rot / (rot - 2)): the fastest frequency stays,
+                  the slowest is divided by factor;
+      "by_parts"  frequencies that turn at least `fast` times over original_length stay, those
+                  that turn at most `slow` times are divided by factor, a linear blend in the
+                  number of turns between; magnitude 1 + 0.1 ln(factor).
+    """
+    _need(rot >= 0 and rot % 2 == 0, "rot must be even")
+    _need(scaling in (None, "linear", "ntk", "by_parts"), f"unknown scaling {scaling!r}")
+    _need(base > 0 and factor >= 1 and fast > slow, "base, factor or the turns' bounds are out of range")
+    i = torch.arange(0, rot, 2, dtype=torch.float64)
+    magnitude = 1.0
+    if scaling == "ntk":
+        _need(rot > 2, "ntk scaling needs rot > 2")
+        base = base * factor ** (rot / (rot - 2))
+    f = base ** (-i / max(rot, 1))
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "by_parts":
+        keep = ((original_length * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0.0, 1.0)
+        f = f * keep + f / factor * (1.0 - keep)
+        magnitude = 1.0 + 0.1 * math.log(factor)
+    return f.to(device), magnitude
+
+
+def _rotation(freqs, positions, tokens, device, *, start=0, interleaved=False, inverse=False, magnitude=1.0):
+    _need(freqs.dtype == torch.float64 and freqs.dim() == 1 and freqs.is_contiguous() and freqs.device == device,
+          "freqs must be a contiguous float64 vector on the tensors' device")
+    pos = None
+    if positions is not None:
+        _need(positions.dtype in (torch.int32, torch.int64) and positions.is_contiguous() and
+              positions.numel() == tokens and positions.device == device,
+              "positions must be int32 or int64, contiguous, one for each token, on the tensors' device")
+        pos = positions.data_ptr()
+    return _Rotation(freqs.data_ptr(), pos, start, int(positions is not None and positions.dtype == torch.int64),
+                     2 * freqs.numel(), int(interleaved), int(inverse), magnitude)
+
+
+def rope(x, freqs, positions=None, *, start: int = 0, interleaved: bool = False, inverse: bool = False,
+         magnitude: float = 1.0, out=None, stream=None):
+    """Rotary positions.  x: [tokens x heads x d] (bf16, fp16 or fp32, any strides with d
+    contiguous; a [heads x s x d] tensor of ring_attention is passed as x.transpose(0, 1)).
+    The first 2 * len(freqs) elements of every head are turned by positions[t] * freqs (or
+    (start + t) * freqs) and scaled by magnitude; interleaved pairs neighbours instead of
+    halves.  inverse=True is the gradient: rope(dy, ..., inverse=True) = dx.
+    Returns out (same shape and strides as x unless given; out=x works in place)."""
+    xs = _rows(x, "x")
+    if out is None:
+        out = torch.empty_like(x) if stream is None else _new(x.shape, x.dtype, x.device, stream)
+    _need(out.shape == x.shape, "out's shape is not x's")
+    ys = _rows(out, "out", like=x)
+    _need(x.dtype in _ROW_DTYPES, f"unsupported dtype {x.dtype}")
+    r = _rotation(freqs, positions, x.shape[0], x.device, start=start, interleaved=interleaved, inverse=inverse,
+                  magnitude=magnitude)
+    st = lib().mk_rope(x.data_ptr(), out.data_ptr(), _ROW_DTYPES[x.dtype], x.shape[0], x.shape[1], x.shape[2],
+                       xs[0], xs[1], ys[0], ys[1], ctypes.byref(r), _stream(stream, x.device))
+    _check(st, "mk_rope")
+    return out
+
+
+class KVCache:
+    """A paged key / value cache: k, v [n_pages x heads x page_size x d] (any strides with d
+    contiguous, the same for both; a cache laid out [n_pages x page_size x heads x d] is passed
+    as k.transpose(1, 2)) in bf16, fp16 or float8_e4m3fn, the latter with k_scale, v_scale
+    [n_pages x heads] fp32.  KVCache.empty allocates one."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        _need(k.dim() == 4 and k.is_cuda and v.device == k.device, "k and v must be 4-D CUDA tensors")
+        _need(k.dtype in _CACHE_DTYPES and v.dtype == k.dtype, f"unsupported cache dtype {k.dtype} / {v.dtype}")
+        _need(v.shape == k.shape and v.stride() == k.stride(), "k and v must have the same shape and strides")
+        _need(k.stride(3) == 1, "the last dimension must be contiguous")
+        if k.dtype == FP8:
+            for t in (k_scale, v_scale):
+                _need(t is not None and t.dtype == torch.float32 and t.is_contiguous() and
+                      tuple(t.shape) == tuple(k.shape[:2]) and t.device == k.device,
+                      "an 8-bit cache needs k_scale and v_scale: contiguous fp32 [n_pages x heads]")
+        else:
+            _need(k_scale is None and v_scale is None, "16-bit caches have no scales")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        n, h, size, d = k.shape
+        sg, sh, ss, _ = k.stride()
+        self._c = _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if k_scale is not None else None,
+                         v_scale.data_ptr() if v_scale is not None else None, sg if n > 1 else 0,
+                         sh if h > 1 else 0, ss, n, _CACHE_DTYPES[k.dtype], h, d, size)
+
+    @staticmethod
+    def empty(n_pages: int, heads: int, page_size: int, d: int, dtype=torch.bfloat16, device="cuda"):
+        """A cache of zeros."""
+        make = lambda s, t: torch.zeros(s, dtype=t, device=device)   # noqa: E731
+        shape = (n_pages, heads, page_size, d)
+        scales = [make((n_pages, heads), torch.float32) for _ in range(2)] if dtype == FP8 else [None, None]
+        return KVCache(make(shape, dtype), make(shape, dtype), *scales)
+
+
+def _seqs(cu_q, kv_len, pages, device) -> _Seqs:
+    for t, name in ((cu_q, "cu_q"), (kv_len, "kv_len"), (pages, "pages")):
+        _need(t.dtype == torch.int32 and t.device == device, f"{name} must be int32 on the tensors' device")
+    B = kv_len.numel()
+    _need(kv_len.is_contiguous() and cu_q.is_contiguous() and cu_q.numel() == B + 1,
+          "cu_q must have one entry more than kv_len, both contiguous")
+    _need(pages.dim() == 2 and pages.shape[0] == B and (pages.stride(1) == 1 or pages.shape[1] <= 1),
+          "pages must be [batch x max_pages] with contiguous rows")
+    return _Seqs(cu_q.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), pages.stride(0), B, pages.shape[1])
+
+
+def kv_append(cache: KVCache, k, v, cu_q, kv_len, pages, *, q=None, freqs=None, positions=None,
+              interleaved: bool = False, magnitude: float = 1.0, q_out=None, workspace: Workspace | None = None,
+              stream=None):
+    """Append a step's keys (rotated) and values to the cache, and rotate its queries.
+
+    k, v: [tokens x heads x d], q: [tokens x heads_q x d]; cu_q [B+1]: sequence b has the tokens
+    cu_q[b] .. cu_q[b+1]-1; kv_len [B]: its length with them; pages [B x max_pages]: its pages
+    (all int32, on the device).  A token's rotary position is its position in the sequence
+    unless `positions` gives another; freqs=None stores k as it is.  8-bit caches are
+    quantised with a power-of-two scale for each page and head (see include/mk.h).
+    Returns q_out (None without q).  Tokens without a slot set the device status."""
+    ks, vs = _rows(k, "k"), _rows(v, "v", like=k)
+    _need(k.shape[1] == v.shape[1] == cache.k.shape[1] and k.shape[2] == cache.k.shape[3],
+          "k and v do not fit the cache's heads and d")
+    _need(k.dtype in (torch.bfloat16, torch.float16) and cache.k.dtype in (k.dtype, FP8) and
+          k.device == cache.k.device, "k and v do not have the cache's type or device")
+    dev = k.device
+    seqs = _seqs(cu_q, kv_len, pages, dev)
+    qs = qo = (0, 0)
+    if q is not None:
+        qs = _rows(q, "q", like=k)
+        if q_out is None:
+            q_out = _new(q.shape, q.dtype, dev, stream)
+        _need(q_out.shape == q.shape, "q_out's shape is not q's")
+        qo = _rows(q_out, "q_out", like=k)
+    r = None
+    if freqs is not None:
+        r = ctypes.byref(_rotation(freqs, positions, k.shape[0], dev, interleaved=interleaved, magnitude=magnitude))
+    elif q is not None:
+        raise ValueError("q is only rotated: give freqs with it")
+    buf = _ws(workspace, dev).get(256)
+    st = lib().mk_kv_append(ctypes.byref(cache._c), k.data_ptr(), v.data_ptr(), _ROW_DTYPES[k.dtype], k.shape[0],
+                            ks[0], ks[1], vs[0], vs[1], q.data_ptr() if q is not None else None,
+                            q_out.data_ptr() if q is not None else None, q.shape[1] if q is not None else 0,
+                            qs[0], qs[1], qo[0], qo[1], ctypes.byref(seqs), r, buf.data_ptr(), buf.numel(),
+                            _stream(stream, dev))
+    _check(st, "mk_kv_append")
+    return q_out if q is not None else None
+
+
+def paged_attention_workspace_size(tokens: int, heads_q: int, heads: int, d: int, batch: int) -> int:
+    return int(lib().mk_paged_attention_workspace_size(tokens, heads_q, heads, d, batch))
+
+
+def paged_attention(q, cache: KVCache, cu_q, kv_len, pages, *, causal: bool = True, window: int = 0, sinks: int = 0,
+                    scale: float | None = None, max_q: int = 0, out=None, return_lse: bool = False,
+                    cfg: Config | None = None, workspace: Workspace | None = None, stream=None):
+    """Attention of the new tokens of a batch of sequences over a paged cache (after kv_append).
+
+    q: [tokens x heads_q x d] (bf16 or fp16, d = 64 or 128, heads_q a multiple of the cache's
+    heads); cu_q, kv_len, pages as for kv_append.  The token at position p sees the keys
+    j <= p (all of them with causal=False) that are among the last `window` (0: no window) or
+    the first `sinks`.  max_q: an upper bound on a sequence's new tokens, if the caller knows
+    one.  Returns out, or (out, lse) with return_lse; rows that see nothing are 0 (-inf)."""
+    qs = _rows(q, "q")
+    dev = q.device
+    T, hq, d = q.shape
+    _need(q.dtype in (torch.bfloat16, torch.float16) and cache.k.dtype in (q.dtype, FP8) and dev == cache.k.device,
+          "q does not have the cache's type or device")
+    _need(cache.k.dtype != FP8 or q.dtype == torch.bfloat16, "an 8-bit cache takes bf16 queries")
+    _need(d == cache.k.shape[3], "q's d is not the cache's")
+    seqs = _seqs(cu_q, kv_len, pages, dev)
+    if out is None:
+        out = _new(q.shape, q.dtype, dev, stream)
+    _need(out.shape == q.shape, "out's shape is not q's")
+    os_ = _rows(out, "out", like=q)
+    lse = _new((T, hq), torch.float32, dev, stream) if return_lse else None
+    nb = paged_attention_workspace_size(T, hq, cache.k.shape[1], d, seqs.batch)
+    if nb == 0:
+        raise MkError(MK_ERR_INVALID, "mk_paged_attention_workspace_size")
+    buf = _ws(workspace, dev, _default_paged_ws).get(nb)
+    st = lib().mk_paged_attention(q.data_ptr(), out.data_ptr(), lse.data_ptr() if return_lse else None,
+                                  _ROW_DTYPES[q.dtype], T, hq, qs[0], qs[1], os_[0], os_[1],
+                                  ctypes.byref(cache._c), ctypes.byref(seqs),
+                                  float(scale) if scale is not None else 1.0 / math.sqrt(d), int(causal), window,
+                                  sinks, max_q, buf.data_ptr(), buf.numel(), _cfgp(cfg), _stream(stream, dev))
+    _check(st, "mk_paged_attention")
+    return (out, lse) if return_lse else out
+
+
 __all__ = ["Config", "MkError", "Workspace", "ag_gemm", "gemm_rs", "gemm_ar", "device_status",
            "workspace_size", "lib", "status_string", "MODE_FUSED", "MODE_GEMM_ONLY",
            "MODE_UNFUSED", "moe_dispatch_gemm", "moe_workspace_size", "moe_combine",
-           "moe_combine_workspace_size", "mlp_ag_rs", "mlp_workspace_size", "ring_attention"]
+           "moe_combine_workspace_size", "mlp_ag_rs", "mlp_workspace_size", "ring_attention", "rope_freqs", "rope",
+           "KVCache", "kv_append", "paged_attention", "paged_attention_workspace_size"]

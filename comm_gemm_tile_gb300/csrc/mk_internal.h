@@ -198,6 +198,9 @@ bool make_map_a(CUtensorMap* m, const void* base, uint64_t k, uint64_t rows, uin
 bool make_map_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                  uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t b0, uint32_t b1,
                  uint32_t b2);
+// Any tiled map (no interleave, out-of-range elements read as zeros).
+bool encode_map(CUtensorMap* m, CUtensorMapDataType type, int rank, void* base, const cuuint64_t* dims,
+                const cuuint64_t* strides, const cuuint32_t* box, const cuuint32_t* steps, CUtensorMapSwizzle swizzle);
 long long default_wait_ns(const mk_config* cfg);
 
 // Launches kernel(a) as a programmatic dependent of the previous launch on s:

@@ -71,7 +71,9 @@ typedef enum {
   MK_ERR_CAPACITY = 5      /* device: MoE rows for a rank exceeded cap_rows                     */
 } mk_status;
 
-typedef enum { MK_BF16 = 0, MK_F32 = 1 } mk_dtype;
+/* The GEMM entry points' outputs are MK_BF16 or MK_F32; the rotary, cache and paged
+ * attention entry points say which they take. */
+typedef enum { MK_BF16 = 0, MK_F32 = 1, MK_F16 = 2, MK_E4M3 = 3 } mk_dtype;
 
 typedef enum { MK_OP_AG_GEMM = 0, MK_OP_GEMM_RS = 1, MK_OP_GEMM_AR = 2, MK_OP_MOE = 3 } mk_op;
 
@@ -393,6 +395,117 @@ size_t mk_moe_trace_entries(int R, int E_loc, int topk, long long T, long long H
  * AllGather copy-in. */
 size_t mk_mlp_trace_entries(int R, long long m, long long h, long long f_r, const mk_config *cfg,
                             size_t *offset);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions, a paged key / value cache, and attention over it: what a
+ * decode step or the next piece of a prompt needs next to mk_ring_attention.
+ * These entry points keep no epoch: a CUDA graph may capture them (with the
+ * workspace, where they take one, reserved for the graph).  Strides count
+ * elements; the last dimension (d) is contiguous.
+ *
+ * Rotation: the pair (a, b) of a head at position p with frequency f becomes
+ *   (a cos(p f) - b sin(p f), b cos(p f) + a sin(p f)) * magnitude.
+ * Pair i is (x[i], x[i + rot/2]), or (x[2i], x[2i+1]) with interleaved != 0;
+ * elements rot .. d-1 are copied.  inverse != 0 turns by -p f: the gradient of
+ * the rotation with respect to x.  Angles are exact to about 1e-7 at any
+ * position; the arithmetic is fp32, rounded once. */
+typedef struct {
+  const double *freqs;     /* [rot / 2], device                                      */
+  const void *positions;   /* [tokens] int32 or int64, device; NULL: the token's own  */
+  long long start;         /* mk_rope with positions == NULL: token t is at start + t */
+  int positions_64;        /* positions are int64                                     */
+  int rot;                 /* rotated elements of a head, even, 0 .. d                */
+  int interleaved;
+  int inverse;             /* mk_rope only                                            */
+  float magnitude;         /* factor on the rotated elements (1 where none is wanted) */
+} mk_rotation;
+
+/* y = x with every head rotated; x, y: [tokens x heads x d] of the same type
+ * (MK_BF16, MK_F16, MK_F32) with any token and head strides, d even and at most
+ * 512; y may be x.  Rows whose base, strides, rot and d are whole 16-byte
+ * pieces move 16 bytes at a time, others element by element. */
+mk_status mk_rope(const void *x, void *y, mk_dtype dtype, long long tokens, int heads, int d,
+                  long long x_token, long long x_head, long long y_token, long long y_head,
+                  const mk_rotation *rotation, mk_stream_t stream);
+
+/* A batch of sequences and where their tokens are.  Sequence b has the new
+ * tokens cu_q[b] .. cu_q[b+1]-1 of the call's token arrays (n of them, possibly
+ * none) and, with them, kv_len[b] tokens.  Its token j is in slot
+ * j % page_size of page pages[b * pages_stride + j / page_size]; new token i has
+ * position kv_len[b] - n + i.  All pointers are device pointers to int32. */
+typedef struct {
+  const int *cu_q;         /* [batch + 1], non-decreasing from 0 */
+  const int *kv_len;       /* [batch]                            */
+  const int *pages;        /* [batch x max_pages]                */
+  long long pages_stride;
+  int batch;
+  int max_pages;
+} mk_seq_batch;
+
+/* A paged cache: element e of slot s, head h, page g of k (and of v) is at
+ * g * page_stride + h * head_stride + s * slot_stride + e.  dtype MK_BF16, MK_F16,
+ * or MK_E4M3: then a value is its code times the scale of its page and head
+ * (k_scale, v_scale: [n_pages x heads] fp32, else NULL).  page_size is a power
+ * of two, 8 .. 256; rows are whole 16-byte pieces. */
+typedef struct {
+  void *k, *v;
+  float *k_scale, *v_scale;
+  long long page_stride, head_stride, slot_stride;
+  long long n_pages;
+  int dtype, heads, d, page_size;
+} mk_kv_cache;
+
+/* Appends the new tokens' k (rotated) and v ([tokens x heads x d], MK_BF16 or
+ * MK_F16; the type of a 16-bit cache) to their slots and, if q is given, writes
+ * q_out = q rotated ([tokens x heads_q x d], same type; q_out may be q).  The
+ * position of a token in its sequence is its rotary position unless
+ * rotation->positions gives another; rotation NULL stores k as it is.
+ * 8-bit caches: a page's scale becomes the least 2^e (e >= -100) with
+ * |value| <= 448 * 2^e for the finite values of the page's new tokens, or stays
+ * what it was if that is larger and the page holds earlier tokens; codes of
+ * earlier tokens are rounded again when it grows.  Rounding is to nearest even,
+ * infinities saturate, NaN stays NaN; rot and d are multiples of 16, rot <= 256.
+ * Two sequences of one call must not append to the same page.  Tokens that have
+ * no slot (position < 0 or past the table, a page outside the cache, rows past
+ * cu_q[batch]) are not stored; the first two kinds set the device status
+ * (MK_ERR_CAPACITY, MK_ERR_INVALID) in the workspace, which holds nothing else
+ * (256 bytes). */
+mk_status mk_kv_append(const mk_kv_cache *cache, const void *k, const void *v, mk_dtype dtype,
+                       long long tokens, long long k_token, long long k_head, long long v_token,
+                       long long v_head, const void *q, void *q_out, int heads_q,
+                       long long q_token, long long q_head, long long qo_token, long long qo_head,
+                       const mk_seq_batch *seqs, const mk_rotation *rotation, void *workspace,
+                       size_t ws_bytes, mk_stream_t stream);
+
+/* Workspace bytes for mk_paged_attention (0 on bad arguments). */
+size_t mk_paged_attention_workspace_size(long long tokens, int heads_q, int heads, int d, int batch);
+
+/* Attention of the new tokens of a batch of sequences over a paged cache that
+ * holds their keys and values already (mk_kv_append):
+ *   out[t][hq] = sum_j softmax_j(scale * q[t][hq] . k_j) v_j,
+ * over the tokens j of t's sequence that t sees, keys and values of head
+ * hq / (heads_q / heads).  The token at position p sees j < kv_len if
+ * (causal == 0 or j <= p) and (window == 0 or j > p - window or j < sinks).
+ * q, out: [tokens x heads_q x d], MK_BF16 or MK_F16, d = 64 or 128; lse (may be
+ * NULL): [tokens x heads_q] fp32, the natural log of the sum of exponentials.
+ * A row that sees nothing gets out = 0, lse = -inf; rows past cu_q[batch] are
+ * not written.  The cache is of q's type, or MK_E4M3 with MK_BF16 q.  What lies
+ * in slots no row of a tile sees (stale pages, NaN) does not reach the result.
+ * Sums are fp32; the weights are rounded to q's type for the products with
+ * the values (to fp16 in decode steps over 8-bit caches).
+ * max_q: no sequence has more new tokens than this (0: not known).  It chooses
+ * kernels; a wrong value costs time, not results.  Sequence lengths stay on the
+ * device.  A page outside the cache or a length past the table reads as zeros
+ * and sets the device status (MK_ERR_INVALID, MK_ERR_CAPACITY).
+ * The workspace needs no clearing except once before its first use, and must
+ * not be shared with the collective entry points above.  cfg (may be NULL):
+ * max_ctas and wait_limit_ns apply. */
+mk_status mk_paged_attention(const void *q, void *out, float *lse, mk_dtype dtype, long long tokens,
+                             int heads_q, long long q_token, long long q_head, long long o_token,
+                             long long o_head, const mk_kv_cache *cache, const mk_seq_batch *seqs,
+                             float scale, int causal, int window, int sinks, int max_q,
+                             void *workspace, size_t ws_bytes, const mk_config *cfg,
+                             mk_stream_t stream);
 
 /* Synchronises `stream`, then reads and clears the device status word of a
  * workspace: MK_OK, MK_ERR_TIMEOUT or MK_ERR_CAPACITY (or MK_ERR_CUDA if the
