@@ -20,7 +20,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmk.so")
 LIB_DEBUG = os.path.join(HERE, "libmk_debug.so")
 SOURCES = ["mk_api.cu", "mk_fused.cu", "mk_moe.cu", "mk_combine.cu", "mk_attn.cu", "mk_noalloc.cu",
-           "mk_rope.cu", "mk_paged.cu"]
+           "mk_rope.cu", "mk_paged.cu", "mk_prompt.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

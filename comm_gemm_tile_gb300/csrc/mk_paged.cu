@@ -115,22 +115,6 @@ __device__ __forceinline__ bool clear_not_finite(uint32_t (&w)[4]) {
       }
   return any;
 }
-// Element offset of the value row of a sequence's token `key`, -1 where its page is not in the cache.
-__device__ __forceinline__ long long value_row(const PagedParams& p, int b, int h, int key) {
-  const int lp = key >> p.c.page_log2;
-  if (lp >= p.s.max_pages) return -1;
-  const int id = p.s.pages[b * p.s.pages_stride + lp];
-  if (id < 0 || id >= p.c.n_pages) return -1;
-  return id * p.c.page_stride + h * p.c.head_stride + (key & (p.c.page_size - 1)) * p.c.slot_stride;
-}
-// The value at an offset if it is NaN or infinite, else 0.
-template <class T, bool E8>
-__device__ __forceinline__ float not_finite(const void* v, long long at) {
-  if (E8) return (static_cast<const uint8_t*>(v)[at] & 0x7f) == 0x7f ? __int_as_float(0x7fffffff) : 0.f;
-  const float x = Piece<T>::one(static_cast<const T*>(v)[at]);
-  return fabsf(x) <= 3.4028235e38f ? 0.f : x;
-}
-
 // Part of a run: tiles k0 .. k1-1 of one unit (sequence b, head h, rows 16 rg ..).
 struct Segment {
   int b, h, rg, n, len, row0;          // new tokens, tokens in all, first token row
@@ -138,12 +122,6 @@ struct Segment {
   KeyTiles t;
   long long u0;                        // number of the unit's first tile
 };
-__device__ __forceinline__ bool sequence_of(const PagedParams& p, int b, int& n, int& len, int& row0) {
-  row0 = p.s.cu_q[b];
-  n = min(p.s.cu_q[b + 1], p.s.tokens) - row0;
-  len = p.s.kv_len[b];
-  return row0 >= 0 && n > 0;
-}
 template <int KT>
 __device__ __forceinline__ Segment segment_at(const PagedParams& p, const long long* pre, int b, long long x,
                                               long long end) {
@@ -168,8 +146,8 @@ template <int KT>
 __device__ __forceinline__ long long sequence_tiles(const PagedParams& p, int b) {
   int n, len, row0;
   if (!sequence_of(p, b, n, len, row0)) return 0;
+  if (!rows_are_ours(p, n)) return 0;
   const long long rows = static_cast<long long>(n) * p.group;
-  if (rows < p.rows_lo || rows > p.rows_hi) return 0;
   return ((rows + DC_ROWS - 1) / DC_ROWS) * key_tiles<KT>(p, len - n, len - 1, len).count();
 }
 
@@ -284,6 +262,11 @@ __global__ void __launch_bounds__(DC_THREADS, 1) mk_paged_decode_kernel(const __
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b <= batch; b += DC_THREADS) p.prefix[b] = pre[b];
   const Deal deal(pre[batch] * p.c.heads, p.grid);
+  for (int b = blockIdx.x; b < batch; b += gridDim.x) {   // sequences without a key: nothing is seen
+    int n, len, row0;
+    if (pre[b + 1] == pre[b] && sequence_of(p, b, n, len, row0) && rows_are_ours(p, n))
+      no_keys<T, D>(p, row0, n, DC_THREADS);
+  }
   if (static_cast<int>(blockIdx.x) >= deal.c) return;
   long long x = deal.start(blockIdx.x);
   const long long end = deal.start(blockIdx.x + 1);
@@ -504,7 +487,8 @@ __global__ void __launch_bounds__(DC_THREADS, 1) mk_paged_decode_kernel(const __
             odd[1] = __reduce_or_sync(0xffffffffu, odd[1]);
             for (int key = 0; (odd[0] | odd[1]) != 0u && key < KT; ++key) {
               if (!((odd[key >> 5] >> (key & 31)) & 1u)) continue;
-              const long long row = value_row(p, g.b, g.h, key0 + key);
+              int page;
+              const long long row = value_row(p, g.b, g.h, key0 + key, page);
               if (row < 0) continue;
 #pragma unroll
               for (int j = 0; j < OT; ++j)
@@ -663,63 +647,21 @@ __global__ void __launch_bounds__(DC_THREADS, 1) mk_paged_decode_kernel(const __
 
 // ------------------------------------------------------------------ join
 
-// One warp a row (token, query head) of this launch's sequences: the partial
-// rows of its unit in CTA order, weighted by 2^(lse_i - max).  Rows whose unit
-// one CTA finished are left alone; rows of a unit without tiles see nothing and
-// become 0 with lse = -inf.
+// Block i - 1: if CTA i's run begins inside a unit that CTA i - 1 began, that unit's rows.
 template <class T, int D, int KT>
 __global__ void __launch_bounds__(256) mk_paged_join_kernel(const __grid_constant__ PagedParams p) {
-  const int lane = threadIdx.x & 31;
-  const long long w = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int t = static_cast<int>(w / p.heads_q), head = static_cast<int>(w - static_cast<long long>(t) * p.heads_q);
-  const int b = warp_last_le(p.s.batch + 1, t, [&](int i) { return p.s.cu_q[i]; });
-  int n = 0, len = 0, row0 = 0;
-  const bool mine = t < p.s.tokens && b >= 0 && b < p.s.batch && sequence_of(p, b, n, len, row0) && t - row0 < n;
-  griddep_wait();   // by every warp: what follows on the stream waits for this launch alone
-  if (!mine) return;
-  const long long rows = static_cast<long long>(n) * p.group;
-  if (rows < p.rows_lo || rows > p.rows_hi) return;
-  const int h = head / p.group, prow = (t - row0) * p.group + head - h * p.group;
+  griddep_wait();
   const Deal deal(p.prefix[p.s.batch] * p.c.heads, p.grid);
-  const int count = key_tiles<KT>(p, len - n, len - 1, len).count();
-  const int groups = static_cast<int>((rows + DC_ROWS - 1) / DC_ROWS);
-  const int rg = prow / DC_ROWS, r = prow - rg * DC_ROWS;
-  T* dst = static_cast<T*>(p.out) + static_cast<long long>(t) * p.os_t + head * p.os_h + lane * (D / 32);
-  float acc[D / 32], lse2 = -INFINITY;
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
-  if (count > 0) {
-    const long long u0 = p.prefix[b] * p.c.heads + (static_cast<long long>(h) * groups + rg) * count;
-    const int c0 = deal.owner(u0), c1 = deal.owner(u0 + count - 1);
-    if (c0 == c1) return;
-    float top = -INFINITY;
-    for (int i = c0 + lane; i <= c1; i += 32)
-      top = fmaxf(top, p.part_lse[static_cast<long long>(part_slot(deal, i, u0)) * DC_ROWS + r]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float ref = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
-#pragma unroll 4
-    for (int i = c0; i <= c1; ++i) {
-      const long long at = static_cast<long long>(part_slot(deal, i, u0)) * DC_ROWS + r;
-      const float f = pg_ex2(p.part_lse[at] - ref);
-      const float* src = p.part + at * D + lane * (D / 32);
-      sum += f;
-#pragma unroll
-      for (int e = 0; e < D / 32; e += 2) {
-        const float2 v = *reinterpret_cast<const float2*>(src + e);
-        acc[e] += f * v.x;
-        acc[e + 1] += f * v.y;
-      }
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) acc[e] *= inv;
-    lse2 = sum == 0.f ? -INFINITY : ref + log2f(sum);
-  }
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) dst[e] = Piece<T>::of(acc[e]);
-  if (p.lse != nullptr && lane == 0) p.lse[static_cast<long long>(t) * p.heads_q + head] = lse2 * LN2;
+  const int i = blockIdx.x + 1;
+  if (i >= deal.c) return;
+  const long long x = deal.start(i), before = deal.start(i - 1);
+  const int b = warp_last_le(p.s.batch, 0, [&](int j) { return p.prefix[j] * p.c.heads <= x ? 0 : 1; });
+  const Segment g = segment_at<KT>(p, p.prefix, b, x, x + 1);
+  if (g.u0 == x || before > g.u0) return;
+  const int row = threadIdx.x >> 4, prow = g.rg * DC_ROWS + row;
+  if (prow >= g.n * p.group) return;
+  const int tok = prow / p.group;
+  join_row<T, D, DC_ROWS>(p, deal, i - 1, g.u0, g.count, row, g.row0 + tok, g.h * p.group + prow - tok * p.group);
 }
 
 // ------------------------------------------------------------------ host
@@ -740,9 +682,8 @@ cudaError_t launch_decode(const PagedParams& p, cudaStream_t s) {
   mk_paged_decode_kernel<T, E8, D><<<p.grid, DC_THREADS, S::SMEM, s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const long long blocks = ceil_div_ll(static_cast<long long>(p.s.tokens) * p.heads_q, 8);
-  if (blocks >= (1LL << 31)) return cudaErrorInvalidValue;
-  return launch_dependent(mk_paged_join_kernel<T, D, S::KT>, dim3(static_cast<unsigned>(blocks)), dim3(256), s, p);
+  if (p.grid < 2) return e;
+  return launch_dependent(mk_paged_join_kernel<T, D, S::KT>, dim3(p.grid - 1), dim3(256), s, p);
 }
 
 // K / V as [d, slots, heads, pages]; a box is the part of a page that falls into a tile of `tile` keys.
@@ -766,16 +707,23 @@ bool cache_map(CUtensorMap* m, const mk_kv_cache* c, const void* base, const voi
   return encode_map(m, type, 4, const_cast<void*>(c->n_pages > 0 ? base : spare), dims, strides, box, one, sw);
 }
 
-constexpr int PG_DECODE_ROWS = 64;     // packed rows up to which a sequence is the decode kernel's
+// Packed rows (new tokens times query heads of a key head) up to which a sequence is the decode
+// kernel's: that kernel reads the keys once per 16 rows, the prompt kernel computes 256 at a time.
+constexpr int PG_DECODE_ROWS = 64;
 
 struct PagedLayout {
   size_t prefix_off, part_off, lse_off, total;
 };
-bool paged_layout(int d, int batch, int sms, PagedLayout& L) {
+// Whether a call with this many tokens in all may hold a sequence for the prompt kernel.
+bool may_be_prompt(long long max_tokens, int group) { return group <= 128 && max_tokens * group > PG_DECODE_ROWS; }
+bool paged_layout(long long tokens, int group, int d, int batch, int sms, PagedLayout& L) {
   if (d != 64 && d != 128) return false;
-  const size_t rows = static_cast<size_t>(2) * sms * DC_ROWS;
+  const bool prompt = may_be_prompt(tokens, group);
+  const size_t rows = static_cast<size_t>(2) * sms * (prompt ? prompt_part_rows() : DC_ROWS);
+  const size_t units = std::max<size_t>(std::min(batch, DC_BATCH),
+                                        prompt ? prompt_entries(static_cast<int>(tokens), group, batch) : 0);
   L.prefix_off = WS_HDR_BYTES;
-  L.part_off = L.prefix_off + ((static_cast<size_t>(std::min(batch, DC_BATCH) + 1) * 8 + 255) & ~size_t(255));
+  L.part_off = L.prefix_off + (((units + 1) * 8 + 255) & ~size_t(255));
   L.lse_off = L.part_off + rows * d * 4;
   L.total = (L.lse_off + rows * 4 + 255) & ~size_t(255);
   return true;
@@ -789,10 +737,10 @@ using namespace mk;
 extern "C" {
 
 size_t mk_paged_attention_workspace_size(long long tokens, int heads_q, int heads, int d, int batch) {
-  if (tokens < 0 || heads < 1 || heads_q < 1 || heads_q % heads || batch < 0) return 0;
+  if (tokens < 0 || tokens >= (1LL << 31) || heads < 1 || heads_q < 1 || heads_q % heads || batch < 0) return 0;
   PagedLayout L;
   const int sms = std::max(1, device_sm_count());
-  return paged_layout(d, batch, sms, L) ? L.total : 0;
+  return paged_layout(tokens, heads_q / heads, d, batch, sms, L) ? L.total : 0;
 }
 
 mk_status mk_paged_attention(const void* q, void* out, float* lse, mk_dtype dtype, long long tokens, int heads_q,
@@ -812,7 +760,7 @@ mk_status mk_paged_attention(const void* q, void* out, float* lse, mk_dtype dtyp
   if (cfg && (cfg->operand != 0 || cfg->mode != 0 || cfg->max_ctas < 0)) return MK_ERR_INVALID;
   PagedLayout L;
   const int dev_sms = device_sm_count();
-  if (!paged_layout(d, seqs->batch, std::max(1, dev_sms), L)) return MK_ERR_INVALID;
+  if (!paged_layout(tokens, heads_q / cache->heads, d, seqs->batch, std::max(1, dev_sms), L)) return MK_ERR_INVALID;
   if (!workspace || ws_bytes < L.total || (reinterpret_cast<uintptr_t>(workspace) & 15u)) return MK_ERR_INVALID;
   if (tokens == 0 || seqs->batch == 0) return MK_OK;
   if (!q || !out) return MK_ERR_INVALID;
@@ -844,24 +792,50 @@ mk_status mk_paged_attention(const void* q, void* out, float* lse, mk_dtype dtyp
   p.map_pages = static_cast<int>(std::max(1LL, cache->n_pages));
   p.grid = grid_cap(cfg);
   if (p.grid <= 0) return MK_ERR_UNSUPPORTED;
-  p.rows_lo = 1;
-  p.rows_hi = 0x7fffffff;
-  const int tile = !e8 && d == 128 ? Shape<__nv_bfloat16, false, 128>::KT : Shape<__nv_bfloat16, true, 128>::KT;
-  if (!cache_map(&p.tmK, cache, cache->k, ws, tile, true) || !cache_map(&p.tmV, cache, cache->v, ws, tile, true))
-    return MK_ERR_CUDA;
-  for (int b0 = 0; b0 < seqs->batch; b0 += DC_BATCH) {
-    PagedParams part = p;
-    part.s.batch = std::min(DC_BATCH, seqs->batch - b0);
-    part.s.cu_q = seqs->cu_q + b0;
-    part.s.kv_len = seqs->kv_len + b0;
-    part.s.pages = seqs->pages + static_cast<long long>(b0) * seqs->pages_stride;
-    cudaError_t e;
-    if (e8) e = d == 128 ? launch_decode<__nv_bfloat16, true, 128>(part, s) : launch_decode<__nv_bfloat16, true, 64>(part, s);
-    else if (dtype == MK_BF16)
-      e = d == 128 ? launch_decode<__nv_bfloat16, false, 128>(part, s) : launch_decode<__nv_bfloat16, false, 64>(part, s);
-    else
-      e = d == 128 ? launch_decode<__half, false, 128>(part, s) : launch_decode<__half, false, 64>(part, s);
-    if (e != cudaSuccess) return MK_ERR_CUDA;
+  // Which kernels: by the most new tokens a sequence can have.  A kernel that is launched alone
+  // takes every sequence, whatever the hint was; of two, each takes its side of PG_DECODE_ROWS.
+  const long long most = max_q > 0 ? std::min<long long>(max_q, tokens) : tokens;
+  const bool prompt = may_be_prompt(most, p.group);
+  const bool decode = !prompt || (seqs->batch > 1 && most * seqs->batch != tokens);
+  if (decode) {
+    const int tile = !e8 && d == 128 ? Shape<__nv_bfloat16, false, 128>::KT : Shape<__nv_bfloat16, true, 128>::KT;
+    if (!cache_map(&p.tmK, cache, cache->k, ws, tile, true) || !cache_map(&p.tmV, cache, cache->v, ws, tile, true))
+      return MK_ERR_CUDA;
+    p.rows_lo = 1;
+    p.rows_hi = prompt ? PG_DECODE_ROWS : 0x7fffffff;
+    for (int b0 = 0; b0 < seqs->batch; b0 += DC_BATCH) {
+      PagedParams part = p;
+      part.s.batch = std::min(DC_BATCH, seqs->batch - b0);
+      part.s.cu_q = seqs->cu_q + b0;
+      part.s.kv_len = seqs->kv_len + b0;
+      part.s.pages = seqs->pages + static_cast<long long>(b0) * seqs->pages_stride;
+      cudaError_t e;
+      if (e8)
+        e = d == 128 ? launch_decode<__nv_bfloat16, true, 128>(part, s) : launch_decode<__nv_bfloat16, true, 64>(part, s);
+      else if (dtype == MK_BF16)
+        e = d == 128 ? launch_decode<__nv_bfloat16, false, 128>(part, s) : launch_decode<__nv_bfloat16, false, 64>(part, s);
+      else
+        e = d == 128 ? launch_decode<__half, false, 128>(part, s) : launch_decode<__half, false, 64>(part, s);
+      if (e != cudaSuccess) return MK_ERR_CUDA;
+    }
+  }
+  if (prompt) {
+    if (!cache_map(&p.tmK, cache, cache->k, ws, 128, !e8) || !cache_map(&p.tmV, cache, cache->v, ws, 128, !e8))
+      return MK_ERR_CUDA;
+    // Q as [d, query heads, tokens]: a box holds the heads of one key head for the tokens of a tile
+    const cuuint64_t row = static_cast<cuuint64_t>(d) * 2;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads_q),
+                                static_cast<cuuint64_t>(tokens)};
+    const cuuint64_t strides[2] = {q_head > 0 ? static_cast<cuuint64_t>(q_head) * 2 : row,
+                                   q_token > 0 ? static_cast<cuuint64_t>(q_token) * 2 : row};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.group), static_cast<cuuint32_t>(128 / p.group)};
+    const cuuint32_t one[3] = {1, 1, 1};
+    if (!encode_map(&p.tmQ, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(q), dims, strides, box, one,
+                    CU_TENSOR_MAP_SWIZZLE_128B))
+      return MK_ERR_CUDA;
+    p.rows_lo = decode ? PG_DECODE_ROWS + 1 : 1;
+    p.rows_hi = 0x7fffffff;
+    if (launch_prompt(p, d, dtype, e8, s) != cudaSuccess) return MK_ERR_CUDA;
   }
   return MK_OK;
 }

@@ -3,6 +3,8 @@
 // partial results and their join.
 #pragma once
 
+#include <type_traits>
+
 #include "mk_seq.cuh"
 
 namespace mk {
@@ -110,8 +112,86 @@ __device__ __forceinline__ float pg_ex2(float x) {
 
 constexpr float LN2 = 0.69314718055994530942f;
 
-// Joins the partial rows of the units that several CTAs shared (mk_paged.cu).
-cudaError_t launch_prefill(PagedParams& p, const mk_kv_cache* c, mk_dtype dtype, int sms, cudaStream_t s);
-size_t prefill_part_rows(int sms);
+// ------------------------------------------------------------------ rows and values
+
+__device__ __forceinline__ bool sequence_of(const PagedParams& p, int b, int& n, int& len, int& row0) {
+  row0 = p.s.cu_q[b];
+  n = min(p.s.cu_q[b + 1], p.s.tokens) - row0;
+  len = p.s.kv_len[b];
+  return row0 >= 0 && n > 0;
+}
+__device__ __forceinline__ bool rows_are_ours(const PagedParams& p, int n) {
+  const long long rows = static_cast<long long>(n) * p.group;
+  return rows >= p.rows_lo && rows <= p.rows_hi;
+}
+// The rows of n tokens from row0 see nothing: out = 0, lse = -inf (by a whole block).
+template <class T, int D>
+__device__ __forceinline__ void no_keys(const PagedParams& p, int row0, int n, int threads) {
+  const long long pieces = static_cast<long long>(n) * p.heads_q * (D / 8);
+  for (long long i = threadIdx.x; i < pieces; i += threads) {
+    const long long r = i / (D / 8);
+    const long long t = row0 + r / p.heads_q;
+    const int head = static_cast<int>(r % p.heads_q), piece = static_cast<int>(i % (D / 8));
+    *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + t * p.os_t + head * p.os_h + piece * 8) =
+        make_uint4(0u, 0u, 0u, 0u);
+    if (p.lse != nullptr && piece == 0) p.lse[t * p.heads_q + head] = -INFINITY;
+  }
+}
+// Element offset of the value row of a sequence's token `key`, -1 where its page is not in the cache.
+__device__ __forceinline__ long long value_row(const PagedParams& p, int b, int h, int key, int& page) {
+  const int lp = key >> p.c.page_log2;
+  if (lp >= p.s.max_pages) return -1;
+  const int id = page = p.s.pages[b * p.s.pages_stride + lp];
+  if (id < 0 || id >= p.c.n_pages) return -1;
+  return id * p.c.page_stride + h * p.c.head_stride + (key & (p.c.page_size - 1)) * p.c.slot_stride;
+}
+// The value at an offset if it is NaN or infinite, else 0.
+template <class T, bool E8>
+__device__ __forceinline__ float not_finite(const void* v, long long at) {
+  if (E8) return (static_cast<const uint8_t*>(v)[at] & 0x7f) == 0x7f ? __int_as_float(0x7fffffff) : 0.f;
+  const float x = Piece<T>::one(static_cast<const T*>(v)[at]);
+  return fabsf(x) <= 3.4028235e38f ? 0.f : x;
+}
+
+// Row r of a unit of ROWS rows and `count` tiles from tile u0: the partial rows of CTAs c0 .. in
+// order, weighted by 2^(lse - max), into out[t][head].  16 threads a row, D / 16 elements each.
+template <class T, int D, int ROWS>
+__device__ __forceinline__ void join_row(const PagedParams& p, const Deal& deal, int c0, long long u0, int count, int r,
+                                         long long t, int head) {
+  constexpr int EL = D / 16;
+  const int c1 = deal.owner(u0 + count - 1), d0 = (threadIdx.x & 15) * EL;
+  float top = -INFINITY;
+  for (int i = c0; i <= c1; ++i)
+    top = fmaxf(top, p.part_lse[static_cast<long long>(part_slot(deal, i, u0)) * ROWS + r]);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float sum = 0.f, acc[EL];
+#pragma unroll
+  for (int e = 0; e < EL; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int i = c0; i <= c1; ++i) {
+    const long long at = static_cast<long long>(part_slot(deal, i, u0)) * ROWS + r;
+    const float f = pg_ex2(p.part_lse[at] - ref);
+    sum += f;
+#pragma unroll
+    for (int e = 0; e < EL; e += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p.part + at * D + d0 + e);
+      acc[e] += f * v.x;
+      acc[e + 1] += f * v.y;
+      acc[e + 2] += f * v.z;
+      acc[e + 3] += f * v.w;
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  T* dst = static_cast<T*>(p.out) + t * p.os_t + head * p.os_h + d0;
+#pragma unroll
+  for (int e = 0; e < EL; ++e) dst[e] = Piece<T>::of(acc[e] * inv);
+  if (p.lse != nullptr && d0 == 0)
+    p.lse[t * p.heads_q + head] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * LN2;
+}
+
+// The prompt kernel (mk_prompt.cu): entries of its work list, partial rows of a CTA's place.
+int prompt_entries(int tokens, int group, int batch);
+int prompt_part_rows();
+cudaError_t launch_prompt(const PagedParams& p, int d, mk_dtype dtype, bool e8, cudaStream_t s);
 
 }  // namespace mk
