@@ -151,12 +151,6 @@ __device__ __forceinline__ long long sequence_tiles(const PagedParams& p, int b)
   return ((rows + DC_ROWS - 1) / DC_ROWS) * key_tiles<KT>(p, len - n, len - 1, len).count();
 }
 
-// Whether any of the rows at positions p0 .. p1 sees any of the keys key .. key+7.
-__device__ __forceinline__ bool group_seen(const PagedParams& p, int p0, int p1, int len, int key) {
-  const int end = p.causal ? min(len, p1 + 1) : len;
-  return key < end && (p.window == 0 || p0 - (key + 7) < p.window || key < p.sinks);
-}
-
 template <int KT, bool E8, int D>
 __device__ void dc_producer(const PagedParams& p, const long long* pre, volatile int* dead, uint32_t full, uint32_t empty,
                             uint32_t ring, int stages, long long x, long long end) {
@@ -177,7 +171,8 @@ __device__ void dc_producer(const PagedParams& p, const long long* pre, volatile
       if (lane >= boxes || lp >= n_pages) return p.map_pages;
       const int id = table[lp];
       if (id >= 0 && id < p.c.n_pages) return id;
-      seq_error(p.hdr, MK_ERR_INVALID, WHERE_PRODUCER, g.b);
+      if (keys_seen(p, g.len - g.n, g.len - 1, g.len, g.t.tile(k) * KT + lane * box, box))
+        seq_error(p.hdr, MK_ERR_INVALID, WHERE_PRODUCER, g.b);
       return p.map_pages;
     };
     if (lane == 0 && ((g.len - 1) >> p.c.page_log2) >= p.s.max_pages)
@@ -345,7 +340,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1) mk_paged_decode_kernel(const __
         const int n_pages = min(p.s.max_pages, (p1 >> p.c.page_log2) + 1);
         auto id_of = [&](int k) {      // -1 for keys no row sees: their scales may be anything
           const int key = g.t.tile(k) * KT + 8 * (lane & 7), lp = key >> p.c.page_log2;
-          if (lp >= n_pages || !group_seen(p, p0, p1, g.len, key)) return -1;
+          if (lp >= n_pages || !keys_seen(p, p0, p1, g.len, key, 8)) return -1;
           const int id = table[lp];
           return id < p.c.n_pages ? id : -1;
         };

@@ -64,6 +64,12 @@ __device__ __forceinline__ bool key_seen_by_any(const PagedParams& p, int p0, in
   return key < len && (!p.causal || key <= p1) && (p.window == 0 || p0 - key < p.window || key < p.sinks);
 }
 
+// Whether any of the rows at positions p0 .. p1 sees any of keys key .. key+n-1.
+__device__ __forceinline__ bool keys_seen(const PagedParams& p, int p0, int p1, int len, int key, int n) {
+  const int end = p.causal ? min(len, p1 + 1) : len;
+  return key < end && (p.window == 0 || p0 - (key + n - 1) < p.window || key < p.sinks);
+}
+
 // N tiles dealt to C = min(grid, N) CTAs in runs that differ by at most one
 // tile; a unit (the tiles of one set of rows) may be cut by several runs.
 struct Deal {

@@ -12,14 +12,14 @@
 //
 // Roles of a CTA's warps:
 //   0-3, 4-7  softmax of query tile 0 / 1, one row a thread: the 128 scores of a
-//             key tile are held in registers, the weights 2^(c s - m) go back into
-//             tensor memory in 16 bits, over the scores; m is the running maximum,
-//             which moves only when it grows by more than 2^8 (then O is scaled)
-//   8         loads Q and K, 10 loads V: one TMA box a page and 64 columns
-//   9         issues the MMAs: S_i = Q_i K^T, O_i += P_i V, in the order PV_0(u-1),
-//             S_0(u), PV_1(u-1), S_1(u): one tile's products run while the other's
-//             softmax does
-//   11        clears the values that no row sees (see prompt_clear)
+//             key tile in two halves, the weights 2^(c s - m) go back into
+//             tensor memory in 16 bits, over the scores; m is the largest score of the
+//             first tile and moves only when weights grow too large (then O is scaled)
+//   8         loads Q and K, 10 loads V (and clears what must not count, see pr_load_v): one
+//             TMA box a page and 64 columns
+//   9, 11     issue the MMAs of query tile 0 / 1: O_i += P_i V of the tile before, in two halves
+//             as their weights appear, then S_i = Q_i K^T.  A warp each, because the issuing
+//             warp's own instructions take as long as the products they start
 //   12-15     8-bit caches only: turn codes into bf16 tiles, scale and all
 #include <algorithm>
 #include <cmath>
@@ -36,8 +36,10 @@ constexpr int PR_T = 128;                    // query rows / keys of a tile
 constexpr int PR_ST = 2;                     // K stages, V stages
 constexpr uint32_t PR_COLS = 512;            // tensor memory: S_0, S_1, O_0, O_1, 128 columns each
 constexpr uint32_t PR_O = 256;
-constexpr float RESCALE = 8.f;
-enum { W_LOAD = 8, W_MMA = 9, W_LOADV = 10, W_CLEAR = 11, W_TURN = 12 };
+// Changing items (queries, the first maximum, the output) takes about as long as this many tiles:
+// an item's first OVER places in a run stand for that, its tiles come after them.
+constexpr int OVER = 2;
+enum { W_MMA = 0, W_LOAD = 1, W_LOADV = 2, W_MMA1 = 3, W_SOFT = 4, W_TURN = 12 };
 
 template <bool E8, int D>
 struct Plan {
@@ -48,23 +50,18 @@ struct Plan {
   static constexpr uint32_t BARS = RV + RAW;
   static constexpr int SMEM = 1024 + BARS + 512;
   static_assert(SMEM <= 232448, "dynamic shared memory per block");
-  // registers: the launch gives every thread 168 (384 threads) or 128 (512); the softmax warps
-  // hold a row of scores each, the others need few
-  static constexpr int MANY = E8 ? 184 : 200, FEW = E8 ? 72 : 104;
-  static_assert(256 * MANY + (THREADS - 256) * FEW <= THREADS * (E8 ? 128 : 168), "no more than the launch has");
 };
 // barriers (byte offsets)
 constexpr uint32_t B_QFULL = 0, B_QEMPTY = 8, B_KFULL = 16, B_KEMPTY = 32, B_VFULL = 48, B_VEMPTY = 64, B_VREADY = 80,
-                   B_S = 96, B_GO = 112, B_O = 128, B_DRAIN = 144, B_RKFULL = 152, B_RKEMPTY = 160, B_RVFULL = 168,
-                   B_RVEMPTY = 176, B_TMEM = 192, B_DEAD = 196, B_ODD = 200;
+                   B_S = 96, B_GO = 112, B_O = 144, B_DRAIN = 160, B_RKFULL = 176, B_RKEMPTY = 184, B_RVFULL = 192,
+                   B_RVEMPTY = 200, B_TURN = 208, B_TMEM = 240, B_DEAD = 244, B_ODD = 248, B_HALF = 280;
 
 __device__ __forceinline__ uint32_t idesc(int n, bool b_mn, bool half) {
   return idesc_bf16_f32(PR_T, n, false, b_mn) & (half ? ~((1u << 7) | (1u << 10)) : ~0u);
 }
 
-// Waits of a whole warp, which agrees by vote.  Inline: a kernel that divides its registers
-// between warps cannot make calls.
-__device__ __forceinline__ bool pr_wait_loop(volatile int* dead, const PagedParams& p, uint32_t bar, uint32_t parity,
+// Waits of a whole warp, which agrees by vote.
+__device__ __noinline__ bool pr_wait_loop(volatile int* dead, const PagedParams& p, uint32_t bar, uint32_t parity,
                                           int where) {
   const uint64_t t0 = globaltimer_ns();
   uint32_t it = 0;
@@ -85,9 +82,10 @@ __device__ __forceinline__ bool pr_wait_loop(volatile int* dead, const PagedPara
   }
   return true;
 }
+// The first look is the non-blocking test: a satisfied try_wait costs several hundred cycles.
 __device__ __forceinline__ bool pr_wait(volatile int* dead, const PagedParams& p, uint32_t bar, uint32_t parity,
                                         int where) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
   return pr_wait_loop(dead, p, bar, parity, where);
 }
 
@@ -115,7 +113,7 @@ __device__ __forceinline__ bool item_of(const PagedParams& p, int e, int b, Item
   return true;
 }
 
-// prefix[e] = tiles of one head in the entries before e; rows of items without tiles see nothing.
+// prefix[e] = places of one head in the entries before e; rows of items without tiles see nothing.
 template <class T>
 __global__ void __launch_bounds__(1024) mk_prompt_plan_kernel(const __grid_constant__ PagedParams p, int entries) {
   __shared__ long long part[33];
@@ -135,6 +133,7 @@ __global__ void __launch_bounds__(1024) mk_prompt_plan_kernel(const __grid_const
       }
       Item it;
       if (item_of(p, e, lo, it)) n = it.t.count();
+      if (n > 0) n += OVER;
     }
     long long incl = n;
 #pragma unroll
@@ -167,6 +166,7 @@ __global__ void __launch_bounds__(1024) mk_prompt_plan_kernel(const __grid_const
 struct Walk {
   long long x, end;
   int e, entries;                            // current entry
+  long long e_start, e_end;                  // its first place, the place after its last
   Item it;
   int h, k0, k1, count;
   long long u0;
@@ -174,26 +174,41 @@ struct Walk {
     x = d.start(blockIdx.x);
     end = d.start(blockIdx.x + 1);
     e = -1;
+    e_start = e_end = 0;
   }
   // The segment at x (by a whole warp); false at the run's end.
   __device__ __forceinline__ bool next(const PagedParams& p) {
-    if (x >= end) return false;
     const long long heads = p.c.heads;
-    if (e < 0) e = warp_last_le(entries, 0, [&](int i) { return p.prefix[i] * heads <= x ? 0 : 1; });
-    while (p.prefix[e + 1] * heads <= x) ++e;
-    const int per = 2 * (PR_T / p.group);
-    const int b = warp_last_le(p.s.batch, e, [&](int i) { return p.s.cu_q[i] / per + i; });
-    item_of(p, e, b, it);
-    count = it.t.count();
-    const long long rem = x - p.prefix[e] * heads;
-    h = static_cast<int>(rem / count);
-    k0 = static_cast<int>(rem - static_cast<long long>(h) * count);
-    u0 = x - k0;
-    k1 = static_cast<int>(min(static_cast<long long>(count), k0 + (end - x)));
-    x += k1 - k0;
-    return true;
+    while (x < end) {
+      if (x >= e_end) {                        // another item; else only another head of this one
+        if (e < 0) e = warp_last_le(entries, 0, [&](int i) { return p.prefix[i] * heads <= x ? 0 : 1; });
+        while ((e_end = p.prefix[e + 1] * heads) <= x) ++e;
+        e_start = p.prefix[e] * heads;
+        const int per = 2 * (PR_T / p.group);
+        const int b = warp_last_le(p.s.batch, e, [&](int i) { return p.s.cu_q[i] / per + i; });
+        item_of(p, e, b, it);
+        count = it.t.count();
+      }
+      const long long rem = x - e_start;       // heads * (count + OVER) places: 32 bits but for monstrous items
+      const uint32_t places = static_cast<uint32_t>(count) + OVER;
+      h = (rem >> 32) == 0 ? static_cast<int>(static_cast<uint32_t>(rem) / places) : static_cast<int>(rem / places);
+      const int at = static_cast<int>(rem - static_cast<long long>(h) * places);
+      const int to = static_cast<int>(min(static_cast<long long>(count + OVER), at + (end - x)));
+      u0 = x - at + OVER;                      // the place of the item's first tile
+      k0 = max(at - OVER, 0);
+      k1 = to - OVER;
+      x += to - at;
+      if (k1 > k0) return true;                // a run may end among an item's first places
+    }
+    return false;
   }
 };
+
+// The positions of an item's rows.
+__device__ __forceinline__ void item_span(const PagedParams& p, const Item& it, int& p0, int& p1) {
+  p0 = it.len - it.n + it.tok0;
+  p1 = min(p0 + 2 * (PR_T / p.group), it.len) - 1;
+}
 
 // The pages of a tile: box i of the tile has `box` keys from slot `slot`.
 struct Pages {
@@ -211,7 +226,9 @@ struct Pages {
     if (lane >= boxes || lp >= n) return p.map_pages;
     const int id = table[lp];
     if (id >= 0 && id < p.c.n_pages) return id;
-    seq_error(p.hdr, MK_ERR_INVALID, WHERE_PRODUCER, it.b);
+    int p0, p1;
+    item_span(p, it, p0, p1);
+    if (keys_seen(p, p0, p1, it.len, tile * PR_T + lane * box, box)) seq_error(p.hdr, MK_ERR_INVALID, WHERE_PRODUCER, it.b);
     return p.map_pages;
   }
 };
@@ -281,88 +298,100 @@ __device__ void pr_load(const PagedParams& p, Walk w, volatile int* dead, uint32
   }
 }
 
-// Warp 10 (16-bit caches): V.
-template <int D>
-__device__ void pr_load_v(const PagedParams& p, Walk w, volatile int* dead, uint32_t bars, uint32_t base) {
-  using P = Plan<false, D>;
-  const int lane = threadIdx.x & 31;
-  uint32_t u = 0;
-  while (w.next(p)) {
-    const Pages g(p, w.it);
-    int next = g.of(p, w.it, w.it.t.tile(w.k0), lane);
-    for (int k = w.k0; k < w.k1; ++k, ++u) {
-      const int tile = w.it.t.tile(k), page = next;
-      if (k + 1 < w.k1) next = g.of(p, w.it, w.it.t.tile(k + 1), lane);
-      const uint32_t st = u % PR_ST, ph = (u / PR_ST) & 1u;
-      if (!pr_wait(dead, p, bars + B_VEMPTY + 8u * st, ph ^ 1u, WHERE_PRODUCER)) return;
-      load_tile<false, D>(p, &p.tmV, base + P::V + st * P::TILE, bars + B_VFULL + 8u * st, g, tile, page, w.h, lane);
-    }
-  }
-}
-
 // ------------------------------------------------------------------ values that must not count
 
-// The positions of an item's rows.
-__device__ __forceinline__ void item_span(const PagedParams& p, const Item& it, int& p0, int& p1) {
-  p0 = it.len - it.n + it.tok0;
-  p1 = min(p0 + 2 * (PR_T / p.group), it.len) - 1;
-}
 __device__ __forceinline__ uint32_t v_piece(int key, int ch) {   // 16-byte piece of a value row in its tile
   return (ch >> 3) * 16384u + key * 128u + (((ch & 7) ^ (key & 7)) << 4);
 }
 template <class T>
-__device__ __forceinline__ bool clear_not_finite16(uint4& w) {
+__device__ __forceinline__ void clear_not_finite16(uint4& w) {
   constexpr uint32_t MASK = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
-  bool any = false;
   uint32_t* v = reinterpret_cast<uint32_t*>(&w);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if ((v[i] & MASK) == MASK) { v[i] &= 0xffff0000u; any = true; }
-    if (((v[i] >> 16) & MASK) == MASK) { v[i] &= 0xffffu; any = true; }
+    if ((v[i] & MASK) == MASK) v[i] &= 0xffff0000u;
+    if (((v[i] >> 16) & MASK) == MASK) v[i] &= 0xffffu;
   }
-  return any;
 }
 
-// Warp 11 (16-bit caches): a weight of 0 times a NaN is NaN, so in a tile that not every row
-// sees whole, values no row sees (past the end, before the window: whatever the slot holds) are
-// cleared, and of the others what is not finite; if there was any, the item's rows that do see
-// it add it when they are stored (B_ODD, one word for each of four segments in turn).
+// The same question for all 8 at once: a full exponent field carries into the bit above it.
+template <class T>
+__device__ __forceinline__ bool has_not_finite16(const uint4& w) {
+  constexpr uint32_t MASK = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
+  constexpr uint32_t ONE = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;
+  return ((((w.x & MASK) + ONE) | ((w.y & MASK) + ONE) | ((w.z & MASK) + ONE) | ((w.w & MASK) + ONE)) & 0x80008000u) != 0u;
+}
+
+// Whether a value tile holds anything that is not finite: 0 * x summed, which is 0 otherwise; two
+// instructions for 16 bytes, since nearly always there is nothing and the products wait for it.
 template <class T, int D>
-__device__ void pr_clear(const PagedParams& p, Walk w, volatile int* dead, uint32_t bars, uint32_t base, uint8_t* sm,
-                         volatile int* odd) {
+__device__ __forceinline__ bool any_not_finite(const uint8_t* tile, int lane) {
+  using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+  T2 acc[4], zero;
+  const uint32_t none = 0u;
+  memcpy(&zero, &none, 4);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) acc[j] = zero;
+#pragma unroll 8
+  for (int i = lane; i < PR_T * (D / 8); i += 32) {
+    const uint4 v = *reinterpret_cast<const uint4*>(tile + 16 * i);   // in any order
+    T2 x[4];
+    memcpy(x, &v, 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = __hfma2(x[j], zero, acc[j]);
+  }
+  uint32_t bits[4];
+  memcpy(bits, acc, 16);
+  return __any_sync(0xffffffffu, ((bits[0] | bits[1] | bits[2] | bits[3]) & 0x7fff7fffu) != 0u);
+}
+
+// Warp 10 (16-bit caches): V.  A weight of 0 times a NaN is NaN, so in a tile that not every row
+// sees whole, slots past the sequence's end (whatever they hold) and values that are not finite
+// are cleared before the products may read it; if some row does see one of those, the item's rows
+// that see it add it when they are stored.  B_ODD: a word for each of eight segments in turn,
+// cleared one segment ahead; this warp is at most four segments ahead of the rows' last read.
+template <class T, int D>
+__device__ void pr_load_v(const PagedParams& p, Walk w, volatile int* dead, uint32_t bars, uint32_t base, uint8_t* sm,
+                          volatile int* odd) {
   using P = Plan<false, D>;
   const int lane = threadIdx.x & 31;
   uint32_t u = 0;
   for (int seg = 0; w.next(p); ++seg) {
+    const Pages g(p, w.it);
     int p0, p1;
     item_span(p, w.it, p0, p1);
     if (lane == 0) odd[(seg + 1) & 7] = 0;
     __syncwarp();
+    int next = g.of(p, w.it, w.it.t.tile(w.k0), lane);
     for (int k = w.k0; k < w.k1; ++k, ++u) {
+      const int number = w.it.t.tile(k), page = next, key0 = number * PR_T;
+      if (k + 1 < w.k1) next = g.of(p, w.it, w.it.t.tile(k + 1), lane);
       const uint32_t st = u % PR_ST, ph = (u / PR_ST) & 1u;
-      if (!pr_wait(dead, p, bars + B_VFULL + 8u * st, ph, WHERE_COPY)) return;
-      const int key0 = w.it.t.tile(k) * PR_T;
+      if (!pr_wait(dead, p, bars + B_VEMPTY + 8u * st, ph ^ 1u, WHERE_PRODUCER)) return;
+      load_tile<false, D>(p, &p.tmV, base + P::V + st * P::TILE, bars + B_VFULL + 8u * st, g, number, page, w.h, lane);
       if (!all_seen(p, p0, p1, w.it.len, key0, PR_T)) {
+        if (!pr_wait(dead, p, bars + B_VFULL + 8u * st, ph, WHERE_COPY)) return;
         uint8_t* tile = sm + P::V + st * P::TILE;
-        bool any = false;
-        for (int i = lane; i < PR_T * (D / 8); i += 32) {
-          const int key = i / (D / 8);
-          uint4* at = reinterpret_cast<uint4*>(tile + v_piece(key, i - key * (D / 8)));
-          if (!key_seen_by_any(p, p0, p1, w.it.len, key0 + key)) {
-            *at = make_uint4(0u, 0u, 0u, 0u);
-          } else {
+        for (int i = max(w.it.len - key0, 0) * (D / 8) + lane; i < PR_T * (D / 8); i += 32)   // slots without a token
+          *reinterpret_cast<uint4*>(tile + v_piece(i / (D / 8), i % (D / 8))) = make_uint4(0u, 0u, 0u, 0u);
+        __syncwarp();
+        if (any_not_finite<T, D>(tile, lane)) {
+          bool any = false;
+          for (int i = lane; i < PR_T * (D / 8); i += 32) {
+            const int key = i / (D / 8);
+            uint4* at = reinterpret_cast<uint4*>(tile + v_piece(key, i % (D / 8)));
             uint4 v = *at;
-            if (clear_not_finite16<T>(v)) {
-              *at = v;
-              any = true;
-            }
+            if (!has_not_finite16<T>(v)) continue;
+            any |= key_seen_by_any(p, p0, p1, w.it.len, key0 + key);
+            clear_not_finite16<T>(v);
+            *at = v;
           }
+          if (any) odd[seg & 7] = 1;
         }
-        if (any) odd[seg & 7] = 1;
         fence_proxy_async_smem();
+        __syncwarp();
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + B_VREADY + 8u * st);
+      if (lane == 0) mbar_arrive(bars + B_VREADY + 8u * st);   // waited for where not every row sees the tile
     }
   }
 }
@@ -425,9 +454,10 @@ __device__ void pr_turn(const PagedParams& p, Walk w, volatile int* dead, uint32
           if (v && masked) {
             if (!key_seen_by_any(p, p0, p1, w.it.len, key0 + key)) {
               lo = hi = make_uint4(0u, 0u, 0u, 0u);
-            } else {
-              any |= clear_not_finite16<__nv_bfloat16>(lo);
-              any |= clear_not_finite16<__nv_bfloat16>(hi);
+            } else if (has_not_finite16<__nv_bfloat16>(lo) || has_not_finite16<__nv_bfloat16>(hi)) {
+              clear_not_finite16<__nv_bfloat16>(lo);
+              clear_not_finite16<__nv_bfloat16>(hi);
+              any = true;
             }
           }
           *reinterpret_cast<uint4*>(out + v_piece(key, 2 * c)) = lo;
@@ -448,138 +478,223 @@ __device__ void pr_turn(const PagedParams& p, Walk w, volatile int* dead, uint32
 
 // ------------------------------------------------------------------ MMAs (warp 9)
 
-template <class T, bool E8, int D>
-__device__ __forceinline__ void issue_s(uint32_t base, uint32_t tmem, int i, uint32_t st) {
-  using P = Plan<E8, D>;
-  constexpr bool HALF = std::is_same<T, __half>::value;
-  const uint64_t dq = sdesc_sw128(base + P::Q + static_cast<uint32_t>(i) * P::TILE, 16u, 1024u);
-  const uint64_t dk = sdesc_sw128(base + P::K + st * P::TILE, 16u, 1024u);
-  if (elect_one_sync()) {
-#pragma unroll
-    for (int a = 0; a < D / 64; ++a)
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        tc_mma_bf16(tmem + static_cast<uint32_t>(i) * PR_T, dq + ((16384u * a + 32u * k) >> 4),
-                    dk + ((16384u * a + 32u * k) >> 4), idesc(PR_T, false, HALF), (a | k) ? 1u : 0u);
-  }
-  __syncwarp();
-}
-template <class T, bool E8, int D>
-__device__ __forceinline__ void issue_pv(uint32_t base, uint32_t tmem, int i, uint32_t st, bool first) {
-  using P = Plan<E8, D>;
-  constexpr bool HALF = std::is_same<T, __half>::value;
-  const uint64_t dv = sdesc_sw128(base + P::V + st * P::TILE, 16384u, 1024u);
-  if (elect_one_sync()) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      tc_mma_bf16_ts(tmem + PR_O + static_cast<uint32_t>(i) * PR_T, tmem + static_cast<uint32_t>(i) * PR_T + 8u * k,
-                     dv + ((2048u * k) >> 4), idesc(D, true, HALF), (!first || k) ? 1u : 0u);
-  }
-  __syncwarp();
-}
 __device__ __forceinline__ void commit(uint32_t bar) {
   if (elect_one_sync()) tc_commit(bar);
   __syncwarp();
 }
 
+// Query tile i: for every key tile u, [V(u-1) there; first, second half of P_i(u-1) written] O_i += P_i V,
+// then [K(u) there] S_i = Q_i K^T over the weights just read (the tensor pipe runs a thread's MMAs in
+// order).  Stages are free once both warps' products have read them.
 template <class T, bool E8, int D>
-__device__ void pr_mma(const PagedParams& p, Walk w, volatile int* dead, uint32_t bars, uint32_t base, uint32_t tmem) {
+__device__ void pr_mma(const PagedParams& p, Walk w, volatile int* dead, uint32_t bars, uint32_t base, uint32_t tmem,
+                       int i) {
+  using P = Plan<E8, D>;
+  constexpr bool HALF = std::is_same<T, __half>::value;
+  const uint32_t scol = tmem + static_cast<uint32_t>(i) * PR_T, ocol = scol + PR_O;
+  const uint64_t dq = sdesc_sw128(base + P::Q + static_cast<uint32_t>(i) * P::TILE, 16u, 1024u);
+  const uint64_t dk0 = sdesc_sw128(base + P::K, 16u, 1024u), dv0 = sdesc_sw128(base + P::V, 16384u, 1024u);
+  const uint32_t go = bars + B_GO + 16u * i;
   uint32_t u = 0, q_ph = 0;
-  bool prev_first = false, prev_last = false;
-  auto value_step = [&](int i, uint32_t v) {       // O_i += P_i V of tile v, once both are there
+  bool first = false, last = false, masked = false;          // of the tile before
+  // The tiles take turns: PV_0(u-1), S_0(u), PV_1(u-1), S_1(u), PV_0(u), ...  So they stay half a
+  // period out of step, and one's products run while the other's softmax does (left to
+  // themselves they fall into step: 3800 cycles a key tile).  Each S_i(n) is handed over to the
+  // other warp on barrier n % 2 of its pair; neither gets two ahead of a wait, as S_i(n+2) needs
+  // the K stage that the other's S(n) has read.  An item's last products do not wait: the next
+  // item's S waits for its queries.
+  auto handed = [&](uint32_t n) {
+    return pr_wait(dead, p, bars + B_TURN + 16u * i + 8u * (n % 2), (n / 2) & 1u, WHERE_MMA);
+  };
+  auto values = [&](uint32_t v) {
     const uint32_t st = v % PR_ST;
-    if (i == 0 && !pr_wait(dead, p, bars + B_VREADY + 8u * st, (v / PR_ST) & 1u, WHERE_MMA)) return false;
-    if (!pr_wait(dead, p, bars + B_GO + 8u * i, v & 1u, WHERE_MMA)) return false;
-    tc_fence_after();
-    issue_pv<T, E8, D>(base, tmem, i, st, prev_first);
-    if (i == 1) commit(bars + B_VEMPTY + 8u * st);
-    if (prev_last) commit(bars + B_O + 8u * i);
+    if (!pr_wait(dead, p, bars + (E8 || masked ? B_VREADY : B_VFULL) + 8u * st, (v / PR_ST) & 1u, WHERE_MMA)) return false;
+    const uint64_t dv = dv0 + ((P::TILE * st) >> 4);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if (!pr_wait(dead, p, go + 8u * half, v & 1u, WHERE_MMA)) return false;
+      if (half == 0 && !last && !handed(v + i)) return false;
+      tc_fence_after();
+      if (elect_one_sync()) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tc_mma_bf16_ts(ocol, scol + 32u * half + 8u * k, dv + ((8192u * half + 2048u * k) >> 4), idesc(D, true, HALF),
+                         (!first || half || k) ? 1u : 0u);
+      }
+      __syncwarp();
+      if (half == 0) commit(bars + B_HALF + 8u * i);
+    }
     return true;
   };
+  auto values_done = [&](uint32_t v) {
+    commit(bars + B_VEMPTY + 8u * (v % PR_ST));
+    if (last) commit(bars + B_O + 8u * i);
+  };
   while (w.next(p)) {
+    int p0, p1;
+    item_span(p, w.it, p0, p1);
     for (int k = w.k0; k < w.k1; ++k, ++u) {
       const uint32_t st = u % PR_ST;
-      if (k == w.k0) {
-        // the last products of the item before need not wait for this one's queries
-        if (u > 0 && !value_step(0, u - 1)) goto done;
+      const bool opens = k == w.k0;
+      if (opens && u > 0) {               // the products before need not wait for this item's queries
+        if (!values(u - 1)) goto done;
+        values_done(u - 1);
+      }
+      if (opens) {
         if (!pr_wait(dead, p, bars + B_QFULL, q_ph, WHERE_MMA)) goto done;
         q_ph ^= 1u;
-        if (!pr_wait(dead, p, bars + B_KFULL + 8u * st, (u / PR_ST) & 1u, WHERE_MMA)) goto done;
-      } else {
-        if (!pr_wait(dead, p, bars + B_KFULL + 8u * st, (u / PR_ST) & 1u, WHERE_MMA)) goto done;
-        if (!value_step(0, u - 1)) goto done;
       }
+      if (!pr_wait(dead, p, bars + B_KFULL + 8u * st, (u / PR_ST) & 1u, WHERE_MMA)) goto done;
+      if (!opens && !values(u - 1)) goto done;
       tc_fence_after();
-      issue_s<T, E8, D>(base, tmem, 0, st);
-      commit(bars + B_S);
-      if (u > 0 && !value_step(1, u - 1)) goto done;
-      issue_s<T, E8, D>(base, tmem, 1, st);
-      commit(bars + B_S + 8u);
+      {
+        const uint64_t dk = dk0 + ((P::TILE * st) >> 4);
+        if (elect_one_sync()) {
+#pragma unroll
+          for (int a = 0; a < D / 64; ++a)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_bf16(scol, dq + ((16384u * a + 32u * kk) >> 4), dk + ((16384u * a + 32u * kk) >> 4),
+                          idesc(PR_T, false, HALF), (a | kk) ? 1u : 0u);
+        }
+        __syncwarp();
+      }
+      commit(bars + B_S + 8u * i);
+      if ((threadIdx.x & 31) == 0) mbar_arrive(bars + B_TURN + 16u * (1 - i) + 8u * (u % 2));
       commit(bars + B_KEMPTY + 8u * st);
-      if (k == w.k1 - 1) commit(bars + B_QEMPTY);
-      prev_first = (k == w.k0);
-      prev_last = (k == w.k1 - 1);
+      if (!opens) values_done(u - 1);
+      first = opens;
+      last = k == w.k1 - 1;
+      if (last) commit(bars + B_QEMPTY);
+      masked = !all_seen(p, p0, p1, w.it.len, w.it.t.tile(k) * PR_T, PR_T);
     }
   }
-  if (u > 0 && value_step(0, u - 1)) value_step(1, u - 1);
+  if (u > 0 && values(u - 1)) values_done(u - 1);
 done:
-  commit(bars + B_DRAIN);
+  commit(bars + B_DRAIN + 8u * i);
   // even after giving up: nothing may run on when the tensor memory is freed
   {
     const uint64_t t0 = globaltimer_ns();
-    while (!__all_sync(0xffffffffu, mbar_try_wait(bars + B_DRAIN, 0)))
+    while (!__all_sync(0xffffffffu, mbar_try_wait(bars + B_DRAIN + 8u * i, 0)))
       if (globaltimer_ns() - t0 > static_cast<uint64_t>(p.wait_ns)) break;
   }
 }
 
 // ------------------------------------------------------------------ softmax (warps 0-3, 4-7)
 
-// Weights of a row from its 128 scores: 2^(c s - ref), keys outside [lo, hi) that are not below
-// snk get 0 (MASK); stored as 16-bit pairs over the scores' columns.  Returns their sum; the largest
-// score goes to mx.
-template <class T, bool MASK>
-__device__ __forceinline__ float emit(const uint32_t (&sv)[4][32], uint32_t col, float c, float ref, int lo, int hi,
-                                      int snk) {
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int a = 0; a < 4; ++a) {
-    uint32_t w[16];
-#pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      const int k = 32 * a + 2 * q;
-      float x = pg_ex2(fmaf(__uint_as_float(sv[a][2 * q]), c, -ref));
-      float y = pg_ex2(fmaf(__uint_as_float(sv[a][2 * q + 1]), c, -ref));
-      if (MASK) {
-        x = (k < hi && (k >= lo || k < snk)) ? x : 0.f;
-        y = (k + 1 < hi && (k + 1 >= lo || k + 1 < snk)) ? y : 0.f;
-      }
-      sum[q & 1] += x;
-      sum[2 + (q & 1)] += y;
-      w[q] = std::is_same<T, __half>::value ? Piece<__half>::pack(x, y) : pack_bf16x2(x, y);
-    }
-    tc_st_32x32b_x16(col + 16u * a, w);
-  }
-  return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+// Two fp32 values in one 64-bit register: a * b + c and a + b on both at once.
+__device__ __forceinline__ uint64_t two(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
 }
-template <bool MASK>
-__device__ __forceinline__ float largest(const uint32_t (&sv)[4][32], int lo, int hi, int snk) {
-  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+__device__ __forceinline__ void split(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// The weights 2^(c s - ref) of 64 scores as 16-bit pairs; returns their sum.
+template <class T>
+__device__ __forceinline__ float weights(const uint32_t (&sv)[2][32], uint32_t (&w)[32], float c, float nref) {
+  const uint64_t c2 = two(c, c), nref2 = two(nref, nref);
+  uint64_t sum[2] = {two(0.f, 0.f), two(0.f, 0.f)};
 #pragma unroll
-  for (int a = 0; a < 4; ++a)
+  for (int q = 0; q < 32; ++q) {
+    const uint32_t (&s)[32] = sv[q >> 4];
+    float x, y;
+    split(fma2(two(__uint_as_float(s[2 * (q & 15)]), __uint_as_float(s[2 * (q & 15) + 1])), c2, nref2), x, y);
+    x = pg_ex2(x);
+    y = pg_ex2(y);
+    sum[q & 1] = add2(sum[q & 1], two(x, y));
+    w[q] = std::is_same<T, __half>::value ? Piece<__half>::pack(x, y) : pack_bf16x2(x, y);
+  }
+  float s0, s1;
+  split(add2(sum[0], sum[1]), s0, s1);
+  return s0 + s1;
+}
+__device__ __forceinline__ float largest(const uint32_t (&sv)[2][32]) {
+  float m[8];
 #pragma unroll
-    for (int q = 0; q < 32; ++q) {
-      const int k = 32 * a + q;
-      if (!MASK || (k < hi && (k >= lo || k < snk))) m[q & 3] = fmaxf(m[q & 3], __uint_as_float(sv[a][q]));
-    }
+  for (int j = 0; j < 8; ++j) m[j] = __uint_as_float(sv[j & 1][j >> 1]);
+#pragma unroll
+  for (int q = 4; q < 32; ++q)
+#pragma unroll
+    for (int a = 0; a < 2; ++a) m[a + 2 * (q & 3)] = fmaxf(m[a + 2 * (q & 3)], __uint_as_float(sv[a][q]));
+#pragma unroll
+  for (int j = 0; j < 4; ++j) m[j] = fmaxf(m[j], m[j + 4]);
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+// Bits 0 .. 31: keys 32 a .. 32 a + 31 that are below n.
+__device__ __forceinline__ uint32_t below(int n, int a) {
+  const int k = n - 32 * a;
+  return k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u;
+}
+
+// Pieces of four rows by row -> by place: lane i of four gets piece i of each of their rows.
+__device__ __forceinline__ void trade4(uint4 (&c)[4], int lane) {
+  auto swap = [&](uint4& lo, uint4& hi, int bit) {
+    const bool up = lane & bit;
+    const uint4 give = up ? lo : hi;
+    uint4 got;
+    got.x = __shfl_xor_sync(0xffffffffu, give.x, bit);
+    got.y = __shfl_xor_sync(0xffffffffu, give.y, bit);
+    got.z = __shfl_xor_sync(0xffffffffu, give.z, bit);
+    got.w = __shfl_xor_sync(0xffffffffu, give.w, bit);
+    if (up) lo = got;
+    else hi = got;
+  };
+  swap(c[0], c[1], 1);
+  swap(c[2], c[3], 1);
+  swap(c[0], c[2], 2);
+  swap(c[1], c[3], 2);
+}
+
+// This row's share of values that were cleared because they are not finite (elements d0 ..).
+template <class T, bool E8>
+__device__ __forceinline__ void add_not_finite(const PagedParams& p, const Walk& w, int pos, int d0, float (&f)[32]) {
+  int p0, p1;
+  item_span(p, w.it, p0, p1);
+  for (int k = w.k0; k < w.k1; ++k) {
+    const int key0 = w.it.t.tile(k) * PR_T;
+    if (all_seen(p, p0, p1, w.it.len, key0, PR_T)) continue;
+    for (int key = key0; key < key0 + PR_T; ++key) {
+      if (!key_seen(p, pos, w.it.len, key)) continue;
+      int page;
+      const long long vr = value_row(p, w.it.b, w.h, key, page);
+      if (vr < 0) continue;
+      if (E8 && !(fabsf(p.c.v_scale[static_cast<long long>(page) * p.c.heads + w.h]) <= 3.4028235e38f)) {
+#pragma unroll
+        for (int q = 0; q < 32; ++q) f[q] = __int_as_float(0x7fffffff);
+        continue;
+      }
+#pragma unroll
+      for (int q = 0; q < 32; ++q) f[q] += not_finite<T, E8>(p.c.v, vr + d0 + q);
+    }
+  }
 }
 
 template <class T, bool E8, int D>
 __device__ void pr_softmax(const PagedParams& p, Walk w, const Deal& deal, volatile int* dead, uint32_t bars,
                            uint32_t tmem, volatile int* odd) {
-  constexpr float SHIFT = std::is_same<T, __half>::value ? 7.f : 0.f;   // fp16 weights: 2^7 high, 2^15 at most
+  // fp16 weights are taken 2^7 high, so that small ones keep their bits, and stay below 2^15
+  constexpr bool HALF = std::is_same<T, __half>::value;
+  constexpr float SHIFT = HALF ? 7.f : 0.f, LIMIT = HALF ? 32768.f : 1.152921504606847e18f;   // 2^15, 2^60
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = warp >> 2, row = 32 * (warp & 3) + lane;
+  const int g = (warp - W_SOFT) >> 2, row = 32 * (warp & 3) + lane;
   const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
   const uint32_t scol = tmem + lanes + static_cast<uint32_t>(g) * PR_T, ocol = scol + PR_O;
   const int toks = PR_T / p.group;
@@ -594,62 +709,81 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, const Deal& deal, volat
     const int g0 = it.len - it.n + it.tok0 + g * toks;       // positions of the tile's real rows
     const int g1 = min(g0 + toks, it.len) - 1;
     float m = -INFINITY, l = 0.f;
+    bool ready = false;                                    // every row of the warp has a reference
     for (int k = w.k0; k < w.k1; ++k, ++u) {
       const int key0 = it.t.tile(k) * PR_T;
       const bool masked = g1 >= g0 && !all_seen(p, g0, g1, it.len, key0, PR_T);
       if (!pr_wait(dead, p, bars + B_S + 8u * g, u & 1u, WHERE_EPILOGUE)) return;
       tc_fence_after();
-      uint32_t sv[4][32];
+      // Half the row at a time, its weights handed over once written: the products start on the
+      // first while the second is being computed.  (One copy of this code for both halves, 64
+      // scores in registers: with the whole row unrolled the instructions did not come fast enough.)
+      float s_a = 0.f;
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        uint32_t sv[2][32], wt[32];
+        tc_ld_32x32b_x32(scol + 64u * half, sv[0]);
+        tc_ld_32x32b_x32(scol + 64u * half + 32u, sv[1]);
+        tc_wait_ld_regs(sv[0]);
+        reg_fence(sv[1]);
+        if (masked && real) {
+          const int hi = (p.causal ? min(it.len, pos + 1) : it.len) - key0;
+          const int lo = p.window > 0 ? pos - p.window + 1 - key0 : 0, snk = p.sinks - key0;
 #pragma unroll
-      for (int a = 0; a < 4; ++a) tc_ld_32x32b_x32(scol + 32u * a, sv[a]);
-      tc_wait_ld();
+          for (int a = 0; a < 2; ++a) {
+            uint32_t see = below(hi, 2 * half + a);
+            if (p.window > 0) see &= ~below(lo, 2 * half + a) | below(snk, 2 * half + a);
 #pragma unroll
-      for (int a = 0; a < 4; ++a) reg_fence(sv[a]);
-      float factor = 1.f, sum;
-      auto grow = [&](float top) {                         // moves the maximum
-        const float mn = fmaxf(m, top * c);
-        if (m == -INFINITY) {
-          m = mn;
-        } else if (mn > m + RESCALE) {
-          factor = pg_ex2(m - mn);
-          m = mn;
-          l *= factor;
-        }
-      };
-      if (masked) {
-        int hi = PR_T, lo = 0, snk = 0;
-        if (real) {
-          hi = (p.causal ? min(it.len, pos + 1) : it.len) - key0;
-          if (p.window > 0) {
-            lo = pos - p.window + 1 - key0;
-            snk = p.sinks - key0;
+            for (int q = 0; q < 32; ++q)
+              if (!(see & (1u << q))) sv[a][q] = 0xff800000u;      // -inf
           }
         }
-        grow(largest<true>(sv, lo, hi, snk));
-        const float ref = (m == -INFINITY ? 0.f : m) - SHIFT;
-        sum = emit<T, true>(sv, scol, c, ref, lo, hi, snk);
-      } else {
-        const float top = largest<false>(sv, 0, 0, 0);
-        grow(top);
-        sum = emit<T, false>(sv, scol, c, (m == -INFINITY ? 0.f : m) - SHIFT, 0, 0, 0);
-      }
-      l += sum;
-      // S_g(u) complete implies the product of tile u-1 complete: O_g is settled until P_g(u) is published
-      if (k > w.k0 && __any_sync(0xffffffffu, factor != 1.f)) {
+        // No maximum is taken of a tile: the reference m, the largest of the first scores, stands as
+        // long as no sum of weights passes LIMIT, which bounds each weight too.
+        bool move = !ready;
+        float sum;
+        while (true) {
+          if (move) {
+            // m to the largest score so far, and what has been summed along with it.  O_g is settled
+            // before P_g(u) is handed over, since S_g(u) complete implies the product of tile u-1
+            // is; after the first half has been, once that half's product is complete.
+            const float mn = fmaxf(m, largest(sv) * c);
+            float factor = 1.f;
+            if (mn > m) {
+              if (m != -INFINITY) factor = pg_ex2(m - mn);
+              m = mn;
+            }
+            l *= factor;
+            s_a *= factor;
+            ready = __all_sync(0xffffffffu, m != -INFINITY);
+            if ((half != 0 || k > w.k0) && __any_sync(0xffffffffu, factor != 1.f)) {
+              if (half != 0) {
+                if (!pr_wait(dead, p, bars + B_HALF + 8u * g, u & 1u, WHERE_EPILOGUE)) return;
+                tc_fence_after();
+              }
 #pragma unroll 1
-        for (int a = 0; a < D / 32; ++a) {
-          uint32_t v[32];
-          tc_ld_32x32b_x32(ocol + 32u * a, v);
-          tc_wait_ld();
+              for (int a = 0; a < D / 16; ++a) {
+                uint32_t v[16];
+                tc_ld_32x32b_x16(ocol + 16u * a, v);
+                tc_wait_ld();
 #pragma unroll
-          for (int q = 0; q < 32; ++q) v[q] = __float_as_uint(__uint_as_float(v[q]) * factor);
-          tc_st_32x32b_x32(ocol + 32u * a, v);
+                for (int q = 0; q < 16; ++q) v[q] = __float_as_uint(__uint_as_float(v[q]) * factor);
+                tc_st_32x32b_x16(ocol + 16u * a, v);
+              }
+            }
+          }
+          sum = weights<T>(sv, wt, c, SHIFT - (m == -INFINITY ? 0.f : m));
+          move = __any_sync(0xffffffffu, sum > LIMIT);
+          if (!move) break;
         }
+        tc_st_32x32b_x32(scol + 32u * half, wt);
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + B_GO + 16u * g + 8u * half);
+        if (half == 0) s_a = sum;
+        else l += s_a + sum;
       }
-      tc_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + B_GO + 8u * g);
     }
     if (!pr_wait(dead, p, bars + B_O + 8u * g, o_ph, WHERE_EPILOGUE)) return;
     o_ph ^= 1u;
@@ -661,50 +795,46 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, const Deal& deal, volat
     const bool whole = w.k1 - w.k0 == w.count;
     const long long at = static_cast<long long>(part_slot(deal, blockIdx.x, w.u0)) * (2 * PR_T) + g * PR_T + row;
     const bool add = odd[seg & 7] != 0;
-    T* dst = static_cast<T*>(p.out) + t * p.os_t + head * p.os_h;
-    float* part = p.part + at * D;
+    // 32 columns at a time; four lanes trade 16-byte pieces so that a store instruction covers 64
+    // neighbouring bytes of 8 rows, not 16 of 32
+    uint8_t* mine = whole ? reinterpret_cast<uint8_t*>(static_cast<T*>(p.out) + t * p.os_t + head * p.os_h)
+                          : reinterpret_cast<uint8_t*>(p.part + at * D);
+    uint8_t* to[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const unsigned long long a = real ? reinterpret_cast<unsigned long long>(mine) : 0ull;
+      to[j] = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, a, (lane & ~3) + j));
+    }
+    const uint32_t piece = 16u * (lane & 3);
 #pragma unroll 1
     for (int a = 0; a < D / 32; ++a) {
       uint32_t v[32];
       __syncwarp();
       tc_ld_32x32b_x32(ocol + 32u * a, v);
       tc_wait_ld();
-      if (!real) continue;
       float f[32];
 #pragma unroll
       for (int q = 0; q < 32; ++q) f[q] = __uint_as_float(v[q]) * inv;
-      if (add) {
-        // values that were cleared because they are not finite: this row's share of them
-        for (int k = w.k0; k < w.k1; ++k) {
-          const int key0 = it.t.tile(k) * PR_T;
-          int p0, p1;
-          item_span(p, it, p0, p1);
-          if (all_seen(p, p0, p1, it.len, key0, PR_T)) continue;
-          for (int key = key0; key < key0 + PR_T; ++key) {
-            if (!key_seen(p, pos, it.len, key)) continue;
-            int page;
-            const long long vr = value_row(p, it.b, w.h, key, page);
-            if (vr < 0) continue;
-            if (E8 && !(fabsf(p.c.v_scale[static_cast<long long>(page) * p.c.heads + w.h]) <= 3.4028235e38f)) {
-#pragma unroll
-              for (int q = 0; q < 32; ++q) f[q] = __int_as_float(0x7fffffff);
-              continue;
-            }
-#pragma unroll
-            for (int q = 0; q < 32; ++q) f[q] += not_finite<T, E8>(p.c.v, vr + 32 * a + q);
-          }
-        }
-      }
+      if (add && real) add_not_finite<T, E8>(p, w, pos, 32 * a, f);
+      __syncwarp();
+      uint4 out[4];
       if (whole) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float (&f8)[8] = *reinterpret_cast<const float (*)[8]>(f + 8 * q);
-          *reinterpret_cast<uint4*>(dst + 32 * a + 8 * q) = Piece<T>::put(f8);
-        }
+        for (int j = 0; j < 4; ++j) out[j] = Piece<T>::put(*reinterpret_cast<const float (*)[8]>(f + 8 * j));
+        trade4(out, lane);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (to[j] != nullptr) *reinterpret_cast<uint4*>(to[j] + 64 * a + piece) = out[j];
       } else {
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          *reinterpret_cast<float4*>(part + 32 * a + 4 * q) = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+        for (int h2 = 0; h2 < 2; ++h2) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) out[j] = Piece<float>::put(*reinterpret_cast<const float (*)[4]>(f + 16 * h2 + 4 * j));
+          trade4(out, lane);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (to[j] != nullptr) *reinterpret_cast<uint4*>(to[j] + 128 * a + 64 * h2 + piece) = out[j];
+        }
       }
     }
     __syncwarp();
@@ -732,20 +862,23 @@ __global__ void __launch_bounds__(Plan<E8, D>::THREADS, 1)
     *dead = 0;
     for (int i = 0; i < 8; ++i) odd[i] = 0;
     mbar_init(bars + B_QFULL, 1);
-    mbar_init(bars + B_QEMPTY, 1);
+    mbar_init(bars + B_QEMPTY, 2);                          // both query tiles' MMA warps
     for (int s = 0; s < PR_ST; ++s) {
       mbar_init(bars + B_KFULL + 8u * s, E8 ? 4 : 1);
-      mbar_init(bars + B_KEMPTY + 8u * s, 1);
+      mbar_init(bars + B_KEMPTY + 8u * s, 2);
       mbar_init(bars + B_VFULL + 8u * s, 1);
-      mbar_init(bars + B_VEMPTY + 8u * s, 1);
+      mbar_init(bars + B_VEMPTY + 8u * s, 2);
       mbar_init(bars + B_VREADY + 8u * s, E8 ? 4 : 1);
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(bars + B_S + 8u * g, 1);
-      mbar_init(bars + B_GO + 8u * g, 4);
+      mbar_init(bars + B_GO + 16u * g, 4);
+      mbar_init(bars + B_GO + 16u * g + 8u, 4);
       mbar_init(bars + B_O + 8u * g, 1);
+      mbar_init(bars + B_HALF + 8u * g, 1);
+      mbar_init(bars + B_DRAIN + 8u * g, 1);
     }
-    mbar_init(bars + B_DRAIN, 1);
+    for (int s = 0; s < 4; ++s) mbar_init(bars + B_TURN + 8u * s, 1);
     mbar_init(bars + B_RKFULL, 1);
     mbar_init(bars + B_RKEMPTY, 4);
     mbar_init(bars + B_RVFULL, 1);
@@ -786,15 +919,13 @@ __global__ void __launch_bounds__(Plan<E8, D>::THREADS, 1)
   }
   if (static_cast<int>(blockIdx.x) < deal.c) {
     const Walk w(p, entries, deal);
-    if (warp < 8) {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(P::MANY));
+    if (warp >= W_SOFT && warp < W_SOFT + 8) {
       pr_softmax<T, E8, D>(p, w, deal, dead, bars, tmem, odd);
     } else {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(P::FEW));
       if (warp == W_LOAD) pr_load<E8, D>(p, w, dead, bars, base);
-      else if (warp == W_MMA) pr_mma<T, E8, D>(p, w, dead, bars, base, tmem);
-      else if (!E8 && warp == W_LOADV) pr_load_v<D>(p, w, dead, bars, base);
-      else if (!E8 && warp == W_CLEAR) pr_clear<T, D>(p, w, dead, bars, base, sm, odd);
+      else if (warp == W_MMA || warp == W_MMA1)
+        pr_mma<T, E8, D>(p, w, dead, bars, base, tmem, warp == W_MMA1);
+      else if (!E8 && warp == W_LOADV) pr_load_v<T, D>(p, w, dead, bars, base, sm, odd);
       else if (E8 && warp >= W_TURN) pr_turn<D>(p, w, dead, bars, base, sm, odd);
     }
     __syncwarp();
@@ -829,9 +960,9 @@ __global__ void __launch_bounds__(256) mk_prompt_join_kernel(const __grid_consta
   if (e < 0 || b < 0 || !item_of(p, e, b, it)) return;
   const int count = it.t.count();
   const long long rem = x - p.prefix[e] * heads;
-  const int h = static_cast<int>(rem / count);
-  const long long u0 = x - (rem - static_cast<long long>(h) * count);
-  if (u0 == x || deal.start(i - 1) > u0) return;
+  const int h = static_cast<int>(rem / (count + OVER));
+  const long long u0 = x - (rem - static_cast<long long>(h) * (count + OVER)) + OVER;
+  if (u0 >= x || deal.start(i - 1) > u0) return;
   const int r = blockIdx.y * 16 + (threadIdx.x >> 4);
   const int q = r / PR_T, rr = r - q * PR_T, toks = PR_T / p.group;
   const int tok = it.tok0 + q * toks + rr / p.group;
@@ -849,11 +980,6 @@ cudaError_t launch(const PagedParams& p, cudaStream_t s) {
   if (configured_dev != dev) {
     e = cudaFuncSetAttribute(mk_prompt_kernel<T, E8, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM);
     if (e != cudaSuccess) return e;
-    // the warps' shares come out of what the block is launched with: never ask for more
-    cudaFuncAttributes attr;
-    e = cudaFuncGetAttributes(&attr, mk_prompt_kernel<T, E8, D>);
-    if (e != cudaSuccess) return e;
-    if (attr.numRegs * P::THREADS < 256 * P::MANY + (P::THREADS - 256) * P::FEW) return cudaErrorLaunchOutOfResources;
     configured_dev = dev;
   }
   const int entries = prompt_entries(p.s.tokens, p.group, p.s.batch);
