@@ -275,6 +275,8 @@ __global__ void __launch_bounds__(DC_THREADS, 1) mk_paged_decode_kernel(const __
     while (x < end) {
       while (pre[b + 1] * p.c.heads <= x) ++b;
       const Segment g = segment_at<KT>(p, pre, b, x, end);
+      if (done == 0 && threadIdx.x == 0)
+        p.cut[blockIdx.x] = CutUnit{g.u0 < x ? g.u0 : -1, g.count, g.row0, g.n, g.h, g.rg};
       const int p0 = g.len - g.n, p1 = g.len - 1;
       const int tiles = g.k1 - g.k0;
       const int first = (warp - static_cast<int>(done % DC_WARPS) + DC_WARPS) % DC_WARPS;
@@ -643,17 +645,14 @@ __global__ void __launch_bounds__(DC_THREADS, 1) mk_paged_decode_kernel(const __
 // ------------------------------------------------------------------ join
 
 // Block i - 1: if CTA i's run begins inside a unit that CTA i - 1 began, that unit's rows.
-template <class T, int D, int KT>
+template <class T, int D>
 __global__ void __launch_bounds__(256) mk_paged_join_kernel(const __grid_constant__ PagedParams p) {
   griddep_wait();
-  const Deal deal(p.prefix[p.s.batch] * p.c.heads, p.grid);
   const int i = blockIdx.x + 1;
-  if (i >= deal.c) return;
-  const long long x = deal.start(i), before = deal.start(i - 1);
-  const int b = warp_last_le(p.s.batch, 0, [&](int j) { return p.prefix[j] * p.c.heads <= x ? 0 : 1; });
-  const Segment g = segment_at<KT>(p, p.prefix, b, x, x + 1);
-  if (g.u0 == x || before > g.u0) return;
-  const int row = threadIdx.x >> 4, prow = g.rg * DC_ROWS + row;
+  const CutUnit g = p.cut[i];
+  const Deal deal(p.prefix[p.s.batch] * p.c.heads, p.grid);
+  if (i >= deal.c || g.u0 < 0 || deal.start(i - 1) > g.u0) return;
+  const int row = threadIdx.x >> 4, prow = g.at * DC_ROWS + row;
   if (prow >= g.n * p.group) return;
   const int tok = prow / p.group;
   join_row<T, D, DC_ROWS>(p, deal, i - 1, g.u0, g.count, row, g.row0 + tok, g.h * p.group + prow - tok * p.group);
@@ -678,7 +677,7 @@ cudaError_t launch_decode(const PagedParams& p, cudaStream_t s) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (p.grid < 2) return e;
-  return launch_dependent(mk_paged_join_kernel<T, D, S::KT>, dim3(p.grid - 1), dim3(256), s, p);
+  return launch_dependent(mk_paged_join_kernel<T, D>, dim3(p.grid - 1), dim3(256), s, p);
 }
 
 // K / V as [d, slots, heads, pages]; a box is the part of a page that falls into a tile of `tile` keys.
@@ -707,7 +706,7 @@ bool cache_map(CUtensorMap* m, const mk_kv_cache* c, const void* base, const voi
 constexpr int PG_DECODE_ROWS = 64;
 
 struct PagedLayout {
-  size_t prefix_off, part_off, lse_off, total;
+  size_t cut_off, prefix_off, part_off, lse_off, total;
 };
 // Whether a call with this many tokens in all may hold a sequence for the prompt kernel.
 bool may_be_prompt(long long max_tokens, int group) { return group <= 128 && max_tokens * group > PG_DECODE_ROWS; }
@@ -717,7 +716,8 @@ bool paged_layout(long long tokens, int group, int d, int batch, int sms, PagedL
   const size_t rows = static_cast<size_t>(2) * sms * (prompt ? prompt_part_rows() : DC_ROWS);
   const size_t units = std::max<size_t>(std::min(batch, DC_BATCH),
                                         prompt ? prompt_entries(static_cast<int>(tokens), group, batch) : 0);
-  L.prefix_off = WS_HDR_BYTES;
+  L.cut_off = WS_HDR_BYTES;
+  L.prefix_off = L.cut_off + ((static_cast<size_t>(sms) * sizeof(CutUnit) + 255) & ~size_t(255));
   L.part_off = L.prefix_off + (((units + 1) * 8 + 255) & ~size_t(255));
   L.lse_off = L.part_off + rows * d * 4;
   L.total = (L.lse_off + rows * 4 + 255) & ~size_t(255);
@@ -774,6 +774,7 @@ mk_status mk_paged_attention(const void* q, void* out, float* lse, mk_dtype dtyp
   p.os_h = o_head;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.hdr = reinterpret_cast<uint32_t*>(ws);
+  p.cut = reinterpret_cast<CutUnit*>(ws + L.cut_off);
   p.prefix = reinterpret_cast<long long*>(ws + L.prefix_off);
   p.part = reinterpret_cast<float*>(ws + L.part_off);
   p.part_lse = reinterpret_cast<float*>(ws + L.lse_off);

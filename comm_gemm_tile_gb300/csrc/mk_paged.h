@@ -9,6 +9,14 @@
 
 namespace mk {
 
+// What a CTA leaves for the join: the unit that its run begins inside of, u0 = -1 if there is none.
+struct CutUnit {
+  long long u0;                        // number (place) of the unit's first tile
+  int count;                           // its tiles
+  int row0, n, h;                      // its sequence's first token row and new tokens; key head
+  int at;                              // decode: row group; prompts: the item's first token
+};
+
 struct PagedParams {
   CUtensorMap tmK, tmV, tmQ;
   const void* q;
@@ -20,6 +28,7 @@ struct PagedParams {
   uint32_t* hdr;
   float* part;                         // partial rows: o [slot][row][d], then their log2 sums
   float* part_lse;
+  CutUnit* cut;                        // one for each CTA
   long long* prefix;                   // tiles of the units before each sequence / item (see the kernels)
   long long wait_ns;
   float scale_log2;                    // softmax scale * log2(e)

@@ -701,7 +701,11 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, const Deal& deal, volat
   const int my_tok = row / p.group, my_head = row - my_tok * p.group;
   const float c = p.scale_log2;
   uint32_t u = 0, o_ph = 0;
+  const long long begin = w.x;
+  if (threadIdx.x == 32 * W_SOFT) p.cut[blockIdx.x].u0 = -1;
   for (int seg = 0; w.next(p); ++seg) {
+    if (seg == 0 && threadIdx.x == 32 * W_SOFT && w.u0 < begin)
+      p.cut[blockIdx.x] = CutUnit{w.u0, w.count, w.it.row0, w.it.n, w.h, w.it.tok0};
     const Item& it = w.it;
     const int tok = it.tok0 + g * toks + my_tok;           // new token of this row
     const bool real = my_tok < toks && tok < it.n;
@@ -944,30 +948,22 @@ __global__ void __launch_bounds__(Plan<E8, D>::THREADS, 1)
 
 // ------------------------------------------------------------------ join
 
-// Block (i, y): if CTA i's run begins inside an item that CTA i-1 began, the item's rows 16 y ..
-// from the partial rows of all CTAs that worked on it.
+// Block (i - 1, y): if CTA i's run begins inside an item that CTA i-1 began, a quarter of the item's
+// rows from the partial rows of all CTAs that worked on it.
+constexpr int JOIN_Y = 4;
 template <class T, int D>
 __global__ void __launch_bounds__(256) mk_prompt_join_kernel(const __grid_constant__ PagedParams p, int entries) {
   griddep_wait();
-  const Deal deal(p.prefix[entries] * p.c.heads, p.grid);
   const int i = blockIdx.x + 1;
-  if (i >= deal.c) return;
-  const long long x = deal.start(i), heads = p.c.heads;
-  const int e = warp_last_le(entries, 0, [&](int j) { return p.prefix[j] * heads <= x ? 0 : 1; });
-  const int per = 2 * (PR_T / p.group);
-  const int b = warp_last_le(p.s.batch, e, [&](int j) { return p.s.cu_q[j] / per + j; });
-  Item it;
-  if (e < 0 || b < 0 || !item_of(p, e, b, it)) return;
-  const int count = it.t.count();
-  const long long rem = x - p.prefix[e] * heads;
-  const int h = static_cast<int>(rem / (count + OVER));
-  const long long u0 = x - (rem - static_cast<long long>(h) * (count + OVER)) + OVER;
-  if (u0 >= x || deal.start(i - 1) > u0) return;
-  const int r = blockIdx.y * 16 + (threadIdx.x >> 4);
-  const int q = r / PR_T, rr = r - q * PR_T, toks = PR_T / p.group;
-  const int tok = it.tok0 + q * toks + rr / p.group;
-  if (rr / p.group >= toks || tok >= it.n) return;
-  join_row<T, D, 2 * PR_T>(p, deal, i - 1, u0, count, r, it.row0 + tok, h * p.group + rr % p.group);
+  const CutUnit g = p.cut[i];
+  const Deal deal(p.prefix[entries] * p.c.heads, p.grid);
+  if (i >= deal.c || g.u0 < 0 || deal.start(i - 1) > g.u0) return;
+  const int toks = PR_T / p.group;
+  for (int r = blockIdx.y * 16 + (threadIdx.x >> 4); r < 2 * PR_T; r += 16 * JOIN_Y) {
+    const int q = r / PR_T, rr = r - q * PR_T, tok = g.at + q * toks + rr / p.group;
+    if (rr / p.group >= toks || tok >= g.n) continue;
+    join_row<T, D, 2 * PR_T>(p, deal, i - 1, g.u0, g.count, r, g.row0 + tok, g.h * p.group + rr % p.group);
+  }
 }
 
 template <class T, bool E8, int D>
@@ -998,7 +994,7 @@ cudaError_t launch(const PagedParams& p, cudaStream_t s) {
   cfg.dynamicSmemBytes = P::SMEM;
   e = cudaLaunchKernelEx(&cfg, mk_prompt_kernel<T, E8, D>, p, entries);
   if (e != cudaSuccess || p.grid < 2) return e;
-  cfg.gridDim = dim3(p.grid - 1, 2 * PR_T / 16);
+  cfg.gridDim = dim3(p.grid - 1, JOIN_Y);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, mk_prompt_join_kernel<T, D>, p, entries);
