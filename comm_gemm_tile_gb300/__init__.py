@@ -570,8 +570,31 @@ def ring_attention(q, k, v, *, causal: bool = False, scale: float | None = None,
 
 # ------------------------------------------------------------------ rotary positions and the paged cache
 
-_ROW_DTYPES = {torch.bfloat16: MK_BF16, torch.float16: MK_F16, torch.float32: MK_F32}
-_CACHE_DTYPES = {torch.bfloat16: MK_BF16, torch.float16: MK_F16, FP8: MK_E4M3}
+_bound = None
+
+
+def _bind():
+    """The native marshalling module (csrc/mk_bind.c), built in-tree like the library."""
+    global _bound
+    if _bound is None:
+        try:
+            from . import _mkbind
+        except ImportError as e:
+            raise RuntimeError("_mkbind.so is not built; run comm_gemm_tile_gb300/build.py "
+                               "(or __graft_entry__.build())") from e
+        _mkbind.setup((torch.bfloat16, torch.float32, torch.float16, FP8, torch.int32, torch.int64, torch.float64),
+                      torch._C._cuda_getCurrentRawStream)
+        _bound = _mkbind
+    return _bound
+
+
+def _address(name: str) -> int:
+    """Address of an entry point of the library in use."""
+    L = _lib or lib()
+    found = L.__dict__.setdefault("_addresses", {})
+    if name not in found:
+        found[name] = ctypes.cast(getattr(L, name), ctypes.c_void_p).value
+    return found[name]
 
 
 def _need(ok: bool, what: str):
@@ -580,25 +603,15 @@ def _need(ok: bool, what: str):
 
 
 def _new(shape, dtype, device, stream):
-    """An output of a call: taken from the pool of the stream the call runs on."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+    """An output of a call on a given stream, taken from that stream's pool."""
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _rows(t, name, heads=None, like=None):
-    """(token stride, head stride) of a [tokens x heads x d] tensor."""
-    _need(t.dim() == 3 and t.is_cuda, f"{name} must be a [tokens x heads x d] CUDA tensor")
-    _need(t.stride(2) == 1 or t.shape[2] == 1, f"{name}'s last dimension must be contiguous")
-    if like is not None:
-        _need(t.dtype == like.dtype and t.device == like.device, f"{name}'s type or device is not that of the others")
-        _need(t.shape[0] == like.shape[0] and t.shape[2] == like.shape[2], f"{name}'s tokens or d do not fit")
-    st, sh = t.stride(0), t.stride(1)
-    # the stride of a dimension of one (or no) element says nothing
-    return (st if t.shape[0] > 1 else 0), (sh if t.shape[1] > 1 else 0)
+def _raw(stream):
+    return None if stream is None else stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def rope_freqs(rot: int, *, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
@@ -632,19 +645,6 @@ def rope_freqs(rot: int, *, base: float = 10000.0, scaling: str | None = None, f
     return f.to(device), magnitude
 
 
-def _rotation(freqs, positions, tokens, device, *, start=0, interleaved=False, inverse=False, magnitude=1.0):
-    _need(freqs.dtype == torch.float64 and freqs.dim() == 1 and freqs.is_contiguous() and freqs.device == device,
-          "freqs must be a contiguous float64 vector on the tensors' device")
-    pos = None
-    if positions is not None:
-        _need(positions.dtype in (torch.int32, torch.int64) and positions.is_contiguous() and
-              positions.numel() == tokens and positions.device == device,
-              "positions must be int32 or int64, contiguous, one for each token, on the tensors' device")
-        pos = positions.data_ptr()
-    return _Rotation(freqs.data_ptr(), pos, start, int(positions is not None and positions.dtype == torch.int64),
-                     2 * freqs.numel(), int(interleaved), int(inverse), magnitude)
-
-
 def rope(x, freqs, positions=None, *, start: int = 0, interleaved: bool = False, inverse: bool = False,
          magnitude: float = 1.0, out=None, stream=None):
     """Rotary positions.  x: [tokens x heads x d] (bf16, fp16 or fp32, any strides with d
@@ -653,17 +653,12 @@ def rope(x, freqs, positions=None, *, start: int = 0, interleaved: bool = False,
     (start + t) * freqs) and scaled by magnitude; interleaved pairs neighbours instead of
     halves.  inverse=True is the gradient: rope(dy, ..., inverse=True) = dx.
     Returns out (same shape and strides as x unless given; out=x works in place)."""
-    xs = _rows(x, "x")
     if out is None:
+        _need(isinstance(x, torch.Tensor), "x is not a tensor")
         out = torch.empty_like(x) if stream is None else _new(x.shape, x.dtype, x.device, stream)
-    _need(out.shape == x.shape, "out's shape is not x's")
-    ys = _rows(out, "out", like=x)
-    _need(x.dtype in _ROW_DTYPES, f"unsupported dtype {x.dtype}")
-    r = _rotation(freqs, positions, x.shape[0], x.device, start=start, interleaved=interleaved, inverse=inverse,
-                  magnitude=magnitude)
-    st = lib().mk_rope(x.data_ptr(), out.data_ptr(), _ROW_DTYPES[x.dtype], x.shape[0], x.shape[1], x.shape[2],
-                       xs[0], xs[1], ys[0], ys[1], ctypes.byref(r), _stream(stream, x.device))
-    _check(st, "mk_rope")
+    st = _bind().rope(_address("mk_rope"), x, out, freqs, positions, start, interleaved, inverse, magnitude, _raw(stream))
+    if st:
+        _check(st, "mk_rope")
     return out
 
 
@@ -674,23 +669,8 @@ class KVCache:
     [n_pages x heads] fp32.  KVCache.empty allocates one."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
-        _need(k.dim() == 4 and k.is_cuda and v.device == k.device, "k and v must be 4-D CUDA tensors")
-        _need(k.dtype in _CACHE_DTYPES and v.dtype == k.dtype, f"unsupported cache dtype {k.dtype} / {v.dtype}")
-        _need(v.shape == k.shape and v.stride() == k.stride(), "k and v must have the same shape and strides")
-        _need(k.stride(3) == 1, "the last dimension must be contiguous")
-        if k.dtype == FP8:
-            for t in (k_scale, v_scale):
-                _need(t is not None and t.dtype == torch.float32 and t.is_contiguous() and
-                      tuple(t.shape) == tuple(k.shape[:2]) and t.device == k.device,
-                      "an 8-bit cache needs k_scale and v_scale: contiguous fp32 [n_pages x heads]")
-        else:
-            _need(k_scale is None and v_scale is None, "16-bit caches have no scales")
+        self._c, self._device = _bind().cache(k, v, k_scale, v_scale)   # the bytes of an mk_kv_cache
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        n, h, size, d = k.shape
-        sg, sh, ss, _ = k.stride()
-        self._c = _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if k_scale is not None else None,
-                         v_scale.data_ptr() if v_scale is not None else None, sg if n > 1 else 0,
-                         sh if h > 1 else 0, ss, n, _CACHE_DTYPES[k.dtype], h, d, size)
 
     @staticmethod
     def empty(n_pages: int, heads: int, page_size: int, d: int, dtype=torch.bfloat16, device="cuda"):
@@ -699,17 +679,6 @@ class KVCache:
         shape = (n_pages, heads, page_size, d)
         scales = [make((n_pages, heads), torch.float32) for _ in range(2)] if dtype == FP8 else [None, None]
         return KVCache(make(shape, dtype), make(shape, dtype), *scales)
-
-
-def _seqs(cu_q, kv_len, pages, device) -> _Seqs:
-    for t, name in ((cu_q, "cu_q"), (kv_len, "kv_len"), (pages, "pages")):
-        _need(t.dtype == torch.int32 and t.device == device, f"{name} must be int32 on the tensors' device")
-    B = kv_len.numel()
-    _need(kv_len.is_contiguous() and cu_q.is_contiguous() and cu_q.numel() == B + 1,
-          "cu_q must have one entry more than kv_len, both contiguous")
-    _need(pages.dim() == 2 and pages.shape[0] == B and (pages.stride(1) == 1 or pages.shape[1] <= 1),
-          "pages must be [batch x max_pages] with contiguous rows")
-    return _Seqs(cu_q.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), pages.stride(0), B, pages.shape[1])
 
 
 def kv_append(cache: KVCache, k, v, cu_q, kv_len, pages, *, q=None, freqs=None, positions=None,
@@ -723,33 +692,15 @@ def kv_append(cache: KVCache, k, v, cu_q, kv_len, pages, *, q=None, freqs=None, 
     unless `positions` gives another; freqs=None stores k as it is.  8-bit caches are
     quantised with a power-of-two scale for each page and head (see include/mk.h).
     Returns q_out (None without q).  Tokens without a slot set the device status."""
-    ks, vs = _rows(k, "k"), _rows(v, "v", like=k)
-    _need(k.shape[1] == v.shape[1] == cache.k.shape[1] and k.shape[2] == cache.k.shape[3],
-          "k and v do not fit the cache's heads and d")
-    _need(k.dtype in (torch.bfloat16, torch.float16) and cache.k.dtype in (k.dtype, FP8) and
-          k.device == cache.k.device, "k and v do not have the cache's type or device")
-    dev = k.device
-    seqs = _seqs(cu_q, kv_len, pages, dev)
-    qs = qo = (0, 0)
-    if q is not None:
-        qs = _rows(q, "q", like=k)
-        if q_out is None:
-            q_out = _new(q.shape, q.dtype, dev, stream)
-        _need(q_out.shape == q.shape, "q_out's shape is not q's")
-        qo = _rows(q_out, "q_out", like=k)
-    r = None
-    if freqs is not None:
-        r = ctypes.byref(_rotation(freqs, positions, k.shape[0], dev, interleaved=interleaved, magnitude=magnitude))
-    elif q is not None:
-        raise ValueError("q is only rotated: give freqs with it")
-    buf = _ws(workspace, dev).get(256)
-    st = lib().mk_kv_append(ctypes.byref(cache._c), k.data_ptr(), v.data_ptr(), _ROW_DTYPES[k.dtype], k.shape[0],
-                            ks[0], ks[1], vs[0], vs[1], q.data_ptr() if q is not None else None,
-                            q_out.data_ptr() if q is not None else None, q.shape[1] if q is not None else 0,
-                            qs[0], qs[1], qo[0], qo[1], ctypes.byref(seqs), r, buf.data_ptr(), buf.numel(),
-                            _stream(stream, dev))
-    _check(st, "mk_kv_append")
-    return q_out if q is not None else None
+    _need(isinstance(cache, KVCache), "cache is not a KVCache")
+    if q is not None and q_out is None and stream is not None:
+        q_out = _new(q.shape, q.dtype, q.device, stream)
+    st, q_out = _bind().append(_address("mk_kv_append"), cache._c, cache._device, k, v, cu_q, kv_len, pages, q, q_out,
+                               freqs, positions, interleaved, magnitude, (workspace or _default_ws.get(cache._device) or _ws(None, cache.k.device)).get(256),
+                               _raw(stream))
+    if st:
+        _check(st, "mk_kv_append")
+    return q_out
 
 
 def paged_attention_workspace_size(tokens: int, heads_q: int, heads: int, d: int, batch: int) -> int:
@@ -766,29 +717,22 @@ def paged_attention(q, cache: KVCache, cu_q, kv_len, pages, *, causal: bool = Tr
     j <= p (all of them with causal=False) that are among the last `window` (0: no window) or
     the first `sinks`.  max_q: an upper bound on a sequence's new tokens, if the caller knows
     one.  Returns out, or (out, lse) with return_lse; rows that see nothing are 0 (-inf)."""
-    qs = _rows(q, "q")
-    dev = q.device
-    T, hq, d = q.shape
-    _need(q.dtype in (torch.bfloat16, torch.float16) and cache.k.dtype in (q.dtype, FP8) and dev == cache.k.device,
-          "q does not have the cache's type or device")
-    _need(cache.k.dtype != FP8 or q.dtype == torch.bfloat16, "an 8-bit cache takes bf16 queries")
-    _need(d == cache.k.shape[3], "q's d is not the cache's")
-    seqs = _seqs(cu_q, kv_len, pages, dev)
-    if out is None:
-        out = _new(q.shape, q.dtype, dev, stream)
-    _need(out.shape == q.shape, "out's shape is not q's")
-    os_ = _rows(out, "out", like=q)
-    lse = _new((T, hq), torch.float32, dev, stream) if return_lse else None
-    nb = paged_attention_workspace_size(T, hq, cache.k.shape[1], d, seqs.batch)
-    if nb == 0:
-        raise MkError(MK_ERR_INVALID, "mk_paged_attention_workspace_size")
-    buf = _ws(workspace, dev, _default_paged_ws).get(nb)
-    st = lib().mk_paged_attention(q.data_ptr(), out.data_ptr(), lse.data_ptr() if return_lse else None,
-                                  _ROW_DTYPES[q.dtype], T, hq, qs[0], qs[1], os_[0], os_[1],
-                                  ctypes.byref(cache._c), ctypes.byref(seqs),
-                                  float(scale) if scale is not None else 1.0 / math.sqrt(d), int(causal), window,
-                                  sinks, max_q, buf.data_ptr(), buf.numel(), _cfgp(cfg), _stream(stream, dev))
-    _check(st, "mk_paged_attention")
+    _need(isinstance(cache, KVCache), "cache is not a KVCache")
+    lse = True if return_lse else None
+    if stream is not None:
+        _need(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be a [tokens x heads x d] CUDA tensor")
+        if out is None:
+            out = _new(q.shape, q.dtype, q.device, stream)
+        if return_lse:
+            lse = _new(q.shape[:2], torch.float32, q.device, stream)
+    c = cfg.c() if cfg is not None else None
+    st, out, lse = _bind().attention(_address("mk_paged_attention"), _address("mk_paged_attention_workspace_size"),
+                                     (workspace or _default_paged_ws.get(cache._device) or
+                                      _ws(None, cache.k.device, _default_paged_ws)).get, q, cache._c, cache._device,
+                                     cu_q, kv_len, pages, causal, window, sinks, scale, max_q, out, lse,
+                                     ctypes.addressof(c) if c is not None else None, _raw(stream))
+    if st:
+        _check(st, "mk_paged_attention")
     return (out, lse) if return_lse else out
 
 

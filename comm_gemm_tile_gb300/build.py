@@ -1,6 +1,7 @@
 """Builds libmk.so in-tree with nvcc for sm_103a (GB300).
 
-The library is plain CUDA C++ behind the C ABI in include/mk.h; each
+The library is plain CUDA C++ behind the C ABI in include/mk.h (with a small
+CPython module, _mkbind.so, that reads the arguments of its sequence operators); each
 translation unit compiles in parallel and the objects link with nvcc.
 The same sources also build libmk_debug.so with MK_DEBUG_BOUNDS=1: device-side
 index checks that report MK_ERR_INVALID instead of touching memory out of range.
@@ -12,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -21,6 +23,8 @@ LIB = os.path.join(HERE, "libmk.so")
 LIB_DEBUG = os.path.join(HERE, "libmk_debug.so")
 SOURCES = ["mk_api.cu", "mk_fused.cu", "mk_moe.cu", "mk_combine.cu", "mk_attn.cu", "mk_noalloc.cu",
            "mk_rope.cu", "mk_paged.cu", "mk_prompt.cu"]
+BIND = os.path.join(HERE, "_mkbind.so")
+BIND_SOURCE = os.path.join(CSRC, "mk_bind.c")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -46,10 +50,25 @@ def _fresh(lib: str) -> bool:
     return os.path.exists(lib) and os.path.getmtime(lib) >= _deps_mtime()
 
 
+def build_bind(force: bool = False) -> str:
+    """Build _mkbind.so, the Python marshalling of the sequence operators, with the C compiler."""
+    if not force and _fresh(BIND):
+        return BIND
+    cmd = [os.environ.get("CC") or shutil.which("cc") or "gcc", "-O2", "-std=c11", "-shared", "-fPIC",
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(ROOT, "include"), BIND_SOURCE, "-o",
+           BIND + ".tmp", "-lm"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for mk_bind.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(BIND + ".tmp", BIND)
+    return BIND
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     """Build libmk.so (and with debug=True also libmk_debug.so, the
     bounds-checking build); returns the path of libmk.so.  Every translation
     unit of both libraries compiles in parallel."""
+    build_bind(force)
     targets = [(LIB, BUILD, [])]
     if debug:
         targets.append((LIB_DEBUG, os.path.join(BUILD, "debug"), ["-DMK_DEBUG_BOUNDS=1"]))

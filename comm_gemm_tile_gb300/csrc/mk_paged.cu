@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1) mk_paged_decode_kernel(const __
             }
             if (p.lse != nullptr && d0 == 0) p.lse[t * p.heads_q + head] = lse2 * LN2;
           } else {
-            const long long at = static_cast<long long>(part_slot(deal, blockIdx.x, g.u0)) * DC_ROWS + row;
+            const long long at = static_cast<long long>(part_slot(blockIdx.x, g.k0 == 0)) * DC_ROWS + row;
 #pragma unroll
             for (int e = 0; e < EL; e += 4)
               *reinterpret_cast<float4*>(p.part + at * D + d0 + e) =
@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(256) mk_paged_join_kernel(const __grid_constan
   const int row = threadIdx.x >> 4, prow = g.at * DC_ROWS + row;
   if (prow >= g.n * p.group) return;
   const int tok = prow / p.group;
-  join_row<T, D, DC_ROWS>(p, deal, i - 1, g.u0, g.count, row, g.row0 + tok, g.h * p.group + prow - tok * p.group);
+  join_row<T, D, DC_ROWS>(p, i - 1, deal.owner(g.u0 + g.count - 1), row, g.row0 + tok, g.h * p.group + prow - tok * p.group);
 }
 
 // ------------------------------------------------------------------ host

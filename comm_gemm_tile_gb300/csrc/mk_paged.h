@@ -88,9 +88,9 @@ struct Deal {
   __device__ __forceinline__ long long start(int i) const { return n * i / c; }
   __device__ __forceinline__ int owner(long long x) const { return static_cast<int>(((x + 1) * c + n - 1) / n) - 1; }
 };
-// Where CTA i leaves its partial result of the unit that begins at tile u0: one
-// place for a unit begun by an earlier CTA, one for a unit it does not finish.
-__device__ __forceinline__ int part_slot(const Deal& d, int i, long long u0) { return 2 * i + (d.start(i) > u0 ? 0 : 1); }
+// Where CTA i leaves its partial result of a unit: one place for a unit begun by an earlier
+// CTA, one for a unit that it begins and does not finish.
+__device__ __forceinline__ int part_slot(int i, bool begins) { return 2 * i + (begins ? 1 : 0); }
 
 // ------------------------------------------------------------------ bounded waits
 // No CTA of these kernels waits for another, so giving up is a CTA's own
@@ -168,23 +168,25 @@ __device__ __forceinline__ float not_finite(const void* v, long long at) {
   return fabsf(x) <= 3.4028235e38f ? 0.f : x;
 }
 
-// Row r of a unit of ROWS rows and `count` tiles from tile u0: the partial rows of CTAs c0 .. in
-// order, weighted by 2^(lse - max), into out[t][head].  16 threads a row, D / 16 elements each.
+// Row r of a unit of ROWS rows: the partial rows of CTAs c0 .. c1 in order, weighted by 2^(lse - max),
+// into out[t][head].  16 threads a row, D / 16 elements each.
 template <class T, int D, int ROWS>
-__device__ __forceinline__ void join_row(const PagedParams& p, const Deal& deal, int c0, long long u0, int count, int r,
-                                         long long t, int head) {
+__device__ __forceinline__ void join_row(const PagedParams& p, int c0, int c1, int r, long long t, int head) {
   constexpr int EL = D / 16;
-  const int c1 = deal.owner(u0 + count - 1), d0 = (threadIdx.x & 15) * EL;
+  const int lane = threadIdx.x & 15, d0 = lane * EL;
+  const unsigned mask = 0xffffu << (threadIdx.x & 16);
   float top = -INFINITY;
-  for (int i = c0; i <= c1; ++i)
-    top = fmaxf(top, p.part_lse[static_cast<long long>(part_slot(deal, i, u0)) * ROWS + r]);
+  for (int i = c0 + lane; i <= c1; i += 16)
+    top = fmaxf(top, p.part_lse[static_cast<long long>(part_slot(i, i == c0)) * ROWS + r]);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(mask, top, o));
   const float ref = top == -INFINITY ? 0.f : top;
   float sum = 0.f, acc[EL];
 #pragma unroll
   for (int e = 0; e < EL; ++e) acc[e] = 0.f;
 #pragma unroll 4
   for (int i = c0; i <= c1; ++i) {
-    const long long at = static_cast<long long>(part_slot(deal, i, u0)) * ROWS + r;
+    const long long at = static_cast<long long>(part_slot(i, i == c0)) * ROWS + r;
     const float f = pg_ex2(p.part_lse[at] - ref);
     sum += f;
 #pragma unroll

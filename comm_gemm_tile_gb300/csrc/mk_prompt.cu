@@ -688,7 +688,7 @@ __device__ __forceinline__ void add_not_finite(const PagedParams& p, const Walk&
 }
 
 template <class T, bool E8, int D>
-__device__ void pr_softmax(const PagedParams& p, Walk w, const Deal& deal, volatile int* dead, uint32_t bars,
+__device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uint32_t bars,
                            uint32_t tmem, volatile int* odd) {
   // fp16 weights are taken 2^7 high, so that small ones keep their bits, and stay below 2^15
   constexpr bool HALF = std::is_same<T, __half>::value;
@@ -797,7 +797,7 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, const Deal& deal, volat
     const int head = w.h * p.group + my_head;
     const long long t = it.row0 + tok;
     const bool whole = w.k1 - w.k0 == w.count;
-    const long long at = static_cast<long long>(part_slot(deal, blockIdx.x, w.u0)) * (2 * PR_T) + g * PR_T + row;
+    const long long at = static_cast<long long>(part_slot(blockIdx.x, w.k0 == 0)) * (2 * PR_T) + g * PR_T + row;
     const bool add = odd[seg & 7] != 0;
     // 32 columns at a time; four lanes trade 16-byte pieces so that a store instruction covers 64
     // neighbouring bytes of 8 rows, not 16 of 32
@@ -924,7 +924,7 @@ __global__ void __launch_bounds__(Plan<E8, D>::THREADS, 1)
   if (static_cast<int>(blockIdx.x) < deal.c) {
     const Walk w(p, entries, deal);
     if (warp >= W_SOFT && warp < W_SOFT + 8) {
-      pr_softmax<T, E8, D>(p, w, deal, dead, bars, tmem, odd);
+      pr_softmax<T, E8, D>(p, w, dead, bars, tmem, odd);
     } else {
       if (warp == W_LOAD) pr_load<E8, D>(p, w, dead, bars, base);
       else if (warp == W_MMA || warp == W_MMA1)
@@ -958,11 +958,11 @@ __global__ void __launch_bounds__(256) mk_prompt_join_kernel(const __grid_consta
   const CutUnit g = p.cut[i];
   const Deal deal(p.prefix[entries] * p.c.heads, p.grid);
   if (i >= deal.c || g.u0 < 0 || deal.start(i - 1) > g.u0) return;
-  const int toks = PR_T / p.group;
+  const int toks = PR_T / p.group, c1 = deal.owner(g.u0 + g.count - 1);
   for (int r = blockIdx.y * 16 + (threadIdx.x >> 4); r < 2 * PR_T; r += 16 * JOIN_Y) {
     const int q = r / PR_T, rr = r - q * PR_T, tok = g.at + q * toks + rr / p.group;
     if (rr / p.group >= toks || tok >= g.n) continue;
-    join_row<T, D, 2 * PR_T>(p, deal, i - 1, g.u0, g.count, r, g.row0 + tok, g.h * p.group + rr % p.group);
+    join_row<T, D, 2 * PR_T>(p, i - 1, c1, r, g.row0 + tok, g.h * p.group + rr % p.group);
   }
 }
 
