@@ -77,6 +77,7 @@ constexpr int RP_THREADS = 256;
 constexpr int RP_UNITS = 4;            // units (2 x 16 bytes) a thread loads before it uses any
 constexpr int RP_TABLE = 4096;         // (token, frequency) entries of a block's table: 32 KB
 constexpr int RP_TOKENS = 64;          // tokens of a block at most
+constexpr int RP_FREQS = 256;          // frequencies at most
 constexpr int AP_CHUNK = 32;           // tokens of a page whose angles are in the table at once
 constexpr int AP_HEADS = 4;            // heads of a block of the 8-bit append: 8 warps, k and v each
 constexpr float E4M3_MAX = 448.f;
@@ -112,24 +113,28 @@ __device__ __forceinline__ long long rope_position(const Rotation& r, int t, lon
                         : static_cast<long long>(static_cast<const int*>(r.positions)[t]);
 }
 
-// cos and sin of position * frequency, times the magnitude (see the head of the file).
-__device__ __forceinline__ void rope_angle(const Rotation& r, long long position, double freq, float& c, float& s) {
-  double turn = freq * 0.15915494309189533577;       // 1 / (2 pi)
-  turn -= floor(turn);
-  const unsigned long long frac = __double2ull_rn(turn * 18446744073709551616.0);
-  const unsigned long long a = static_cast<unsigned long long>(position) * frac;
-  const float half = static_cast<float>(static_cast<int>(a >> 32)) * 4.656612873077393e-10f;   // 2^-31
-  sincospif(half, &s, &c);
-  c *= r.magnitude;
-  s *= r.inverse ? -r.magnitude : r.magnitude;
+// The frequencies as 64-bit fractions of a turn, once a block: 64-bit floating point is slow here
+// (2 operations a clock and SM; done for every angle it took half of a large call's time).
+__device__ __forceinline__ void rope_turns(const Rotation& r, unsigned long long* turns) {
+  for (int i = threadIdx.x; i < (r.rot >> 1); i += RP_THREADS) {
+    double turn = r.freqs[i] * 0.15915494309189533577;       // 1 / (2 pi)
+    turn -= floor(turn);
+    turns[i] = __double2ull_rn(turn * 18446744073709551616.0);
+  }
 }
 
-// The cosine / sine table of nt tokens: entry tok * rot/2 + i.
-__device__ __forceinline__ void rope_table(const Rotation& r, int nt, const long long* pos, float* tc, float* ts) {
+// The cosine / sine table of nt tokens, times the magnitude: entry tok * rot/2 + i (see the head of the file).
+__device__ __forceinline__ void rope_table(const Rotation& r, int nt, const long long* pos,
+                                           const unsigned long long* turns, float* tc, float* ts) {
   const int half = r.rot >> 1;
+  const float ms = r.inverse ? -r.magnitude : r.magnitude;
   for (int e = threadIdx.x; e < nt * half; e += RP_THREADS) {
     const int tok = e / half;
-    rope_angle(r, pos[tok], r.freqs[e - tok * half], tc[e], ts[e]);
+    const unsigned long long a = static_cast<unsigned long long>(pos[tok]) * turns[e - tok * half];
+    float c, s;
+    sincospif(static_cast<float>(static_cast<int>(a >> 32)) * 4.656612873077393e-10f, &s, &c);   // 2^-31
+    tc[e] = c * r.magnitude;
+    ts[e] = s * ms;
   }
 }
 
@@ -246,6 +251,7 @@ __device__ __forceinline__ void rows_block(const RowsParams& p, int block, float
   constexpr int N = U::N;
   __shared__ long long pos[RP_TOKENS];
   __shared__ long long slot[RP_TOKENS];      // element offset of the token's slot in the cache, -1: none
+  __shared__ unsigned long long turns[RP_FREQS];
   const int tb = block / p.row_blocks, rb = block - tb * p.row_blocks;
   const int t0 = tb * p.block_tokens, nt = min(p.block_tokens, p.tokens - t0);
   const int rows_all = p.heads + (CACHE ? 2 * p.c.heads : 0);
@@ -276,6 +282,7 @@ __device__ __forceinline__ void rows_block(const RowsParams& p, int block, float
     const int i = threadIdx.x + j * RP_THREADS;
     if (i < total) load(i, un[j]);
   }
+  rope_turns(p.r, turns);
   if (SEQ) {
     for (int tok = threadIdx.x >> 5; tok < nt; tok += RP_THREADS / 32) {
       const int t = t0 + tok;
@@ -298,7 +305,7 @@ __device__ __forceinline__ void rows_block(const RowsParams& p, int block, float
   }
   __syncthreads();
   if (p.r.rot > 0) {
-    rope_table(p.r, nt, pos, tc, ts);
+    rope_table(p.r, nt, pos, turns, tc, ts);
     __syncthreads();
   }
 #pragma unroll
@@ -368,10 +375,12 @@ __device__ __forceinline__ void quant_block(const RowsParams& p, float* tc, floa
   using U = Unit<T, INTER, true>;
   constexpr int N = U::N;
   __shared__ long long pos[AP_CHUNK];
-  __shared__ int sh[6];
+  __shared__ unsigned long long turns[RP_FREQS];
+  __shared__ int sh[5];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int piece = blockIdx.x / p.head_blocks, hb = blockIdx.x - piece * p.head_blocks;
   const int size = p.c.page_size;
+  rope_turns(p.r, turns);
   if (warp == 0) {
     // sequence b's pieces start at number cu_q[b] / page + 2 b: room for all of them
     const int b = warp_last_le(p.s.batch, piece, [&](int i) { return (p.s.cu_q[i] >> p.c.page_log2) + 2 * i; });
@@ -417,7 +426,7 @@ __device__ __forceinline__ void quant_block(const RowsParams& p, float* tc, floa
         __syncthreads();
         if (threadIdx.x < nc) pos[threadIdx.x] = rope_position(p.r, tok0 + c0 + threadIdx.x, own0 + c0 + threadIdx.x);
         __syncthreads();
-        rope_table(p.r, nc, pos, tc, ts);
+        rope_table(p.r, nc, pos, turns, tc, ts);
         __syncthreads();
       }
       if (!act) continue;
