@@ -105,6 +105,7 @@ struct RowsParams {
   int tokens, block_tokens, block_rows;
   int row_blocks;                      // blocks of rows per block of tokens
   int piece_blocks, head_blocks;       // 8-bit append: blocks that quantise come first
+  int table;                           // entries of a block's cosine table (in shared memory, the sines after it)
 };
 
 __device__ __forceinline__ long long rope_position(const Rotation& r, int t, long long own) {
@@ -241,6 +242,30 @@ struct Unit {
   }
 };
 
+// A unit's place, token / row / unit of the row, counted up without dividing.
+struct Place {
+  int tok, row, u;
+  __device__ __forceinline__ Place(int i, int rows, int units) {
+    const int r = i / units;
+    u = i - r * units;
+    tok = r / rows;
+    row = r - tok * rows;
+  }
+  __device__ __forceinline__ void add(const Place& step, int rows, int units) {
+    u += step.u;
+    row += step.row;
+    tok += step.tok;
+    if (u >= units) {
+      u -= units;
+      ++row;
+    }
+    if (row >= rows) {
+      row -= rows;
+      ++tok;
+    }
+  }
+};
+
 // Rows of a block of tokens: the p.heads rows of x go rotated to y; with a
 // 16-bit cache also the token's new keys (rotated) and values (copied) to
 // their slots.  One unit of 2 x 16 bytes a thread and step: 256 bytes of a row
@@ -259,28 +284,28 @@ __device__ __forceinline__ void rows_block(const RowsParams& p, int block, float
   const int total = nt * nr * p.units;
   const int half = p.r.rot >> 1;
   U un[RP_UNITS];
-  auto split = [&](int i, int& tok, int& row, int& u) {
-    tok = i / (nr * p.units);
-    const int rest = i - tok * nr * p.units;
-    row = rest / p.units;
-    u = rest - row * p.units;
-    row += r0;
-  };
-  auto load = [&](int i, U& w) {
-    int tok, row, u, o0, o1;
-    split(i, tok, row, u);
-    const long long t = t0 + tok;
+  const Place step(RP_THREADS, nr, p.units);
+  Place at[RP_UNITS] = {Place(threadIdx.x, nr, p.units), Place(0, 1, 1), Place(0, 1, 1), Place(0, 1, 1)};
+#pragma unroll
+  for (int j = 1; j < RP_UNITS; ++j) {
+    at[j] = at[j - 1];
+    at[j].add(step, nr, p.units);
+  }
+  auto load = [&](const Place& at, U& w) {
+    int o0, o1;
+    const int row = r0 + at.row;
+    const long long t = t0 + at.tok;
     const T* src;
     if (!CACHE || row < p.heads) src = static_cast<const T*>(p.x) + t * p.xs_t + row * p.xs_h;
     else if (row < p.heads + p.c.heads) src = static_cast<const T*>(p.nk) + t * p.ks_t + (row - p.heads) * p.ks_h;
     else src = static_cast<const T*>(p.nv) + t * p.vs_t + (row - p.heads - p.c.heads) * p.vs_h;
-    U::where(u, p.r.rot, !CACHE || row < p.heads + p.c.heads, o0, o1);
+    U::where(at.u, p.r.rot, !CACHE || row < p.heads + p.c.heads, o0, o1);
     w.load(src, o0, o1);
   };
 #pragma unroll
   for (int j = 0; j < RP_UNITS; ++j) {
     const int i = threadIdx.x + j * RP_THREADS;
-    if (i < total) load(i, un[j]);
+    if (i < total) load(at[j], un[j]);
   }
   rope_turns(p.r, turns);
   if (SEQ) {
@@ -312,8 +337,8 @@ __device__ __forceinline__ void rows_block(const RowsParams& p, int block, float
   for (int j = 0; j < RP_UNITS; ++j) {
     const int i = threadIdx.x + j * RP_THREADS;
     if (i >= total) break;
-    int tok, row, u, o0, o1;
-    split(i, tok, row, u);
+    int o0, o1;
+    const int tok = at[j].tok, row = r0 + at[j].row, u = at[j].u;
     const bool is_v = CACHE && row >= p.heads + p.c.heads;
     T* dst;
     if (!CACHE || row < p.heads) {
@@ -336,10 +361,9 @@ __device__ __forceinline__ void rows_block(const RowsParams& p, int block, float
 }
 
 template <class T, bool INTER, bool VEC, bool SEQ, bool CACHE>
-__global__ void __launch_bounds__(RP_THREADS) mk_rows_kernel(const __grid_constant__ RowsParams p) {
-  __shared__ __align__(16) float tc[RP_TABLE];
-  __shared__ __align__(16) float ts[RP_TABLE];
-  rows_block<T, INTER, VEC, SEQ, CACHE>(p, blockIdx.x, tc, ts);
+__global__ void __launch_bounds__(RP_THREADS, VEC ? 4 : 1) mk_rows_kernel(const __grid_constant__ RowsParams p) {
+  extern __shared__ __align__(16) float table[];
+  rows_block<T, INTER, VEC, SEQ, CACHE>(p, blockIdx.x, table, table + p.table);
 }
 
 // ------------------------------------------------------------------ 8-bit cache
@@ -414,6 +438,7 @@ __device__ __forceinline__ void quant_block(const RowsParams& p, float* tc, floa
   const bool is_v = warp & 1, act = h < p.c.heads;
   const int half = p.r.rot >> 1;
   const int upr = p.units;                    // units (16 elements) of a row
+  const Place step(32, 1 << 30, upr);
   const T* src = is_v ? static_cast<const T*>(p.nv) + h * p.vs_h : static_cast<const T*>(p.nk) + h * p.ks_h;
   const long long st = is_v ? p.vs_t : p.ks_t;
   uint8_t* dst = static_cast<uint8_t*>(is_v ? p.c.v : p.c.k) + page * p.c.page_stride + h * p.c.head_stride;
@@ -431,6 +456,7 @@ __device__ __forceinline__ void quant_block(const RowsParams& p, float* tc, floa
       }
       if (!act) continue;
       // two units a lane in flight
+      Place at(lane, 1 << 30, upr);
       for (int i0 = lane; i0 < nc * upr; i0 += 64) {
         U w[2];
         int tk[2], uu[2];
@@ -439,13 +465,14 @@ __device__ __forceinline__ void quant_block(const RowsParams& p, float* tc, floa
           const int i = i0 + 32 * k;
           if (i < nc * upr) {
             int o0, o1;
-            tk[k] = i / upr;
-            uu[k] = i - tk[k] * upr;
+            tk[k] = at.row;
+            uu[k] = at.u;
             U::where(uu[k], p.r.rot, !is_v, o0, o1);
             const T* row = src + (tok0 + c0 + tk[k]) * st;
             w[k].w0 = *reinterpret_cast<const uint4*>(row + o0);
             w[k].w1 = *reinterpret_cast<const uint4*>(row + o1);
           }
+          at.add(step, 1 << 30, upr);
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -503,11 +530,11 @@ __device__ __forceinline__ void quant_block(const RowsParams& p, float* tc, floa
 
 // The blocks that quantise come first (they are the long ones); the rest rotate the queries.
 template <class T, bool INTER>
-__global__ void __launch_bounds__(RP_THREADS) mk_append8_kernel(const __grid_constant__ RowsParams p) {
-  __shared__ __align__(16) float tc[RP_TABLE];
-  __shared__ __align__(16) float ts[RP_TABLE];
-  if (static_cast<int>(blockIdx.x) < p.piece_blocks) quant_block<T, INTER>(p, tc, ts);
-  else rows_block<T, INTER, true, true, false>(p, blockIdx.x - p.piece_blocks, tc, ts);
+__global__ void __launch_bounds__(RP_THREADS, 3) mk_append8_kernel(const __grid_constant__ RowsParams p) {
+  extern __shared__ __align__(16) float table[];
+  float* ts = table + p.table;
+  if (static_cast<int>(blockIdx.x) < p.piece_blocks) quant_block<T, INTER>(p, table, ts);
+  else rows_block<T, INTER, true, true, false>(p, blockIdx.x - p.piece_blocks, table, ts);
 }
 
 // ------------------------------------------------------------------ launches
@@ -518,11 +545,12 @@ __global__ void __launch_bounds__(RP_THREADS) mk_append8_kernel(const __grid_con
 // spread over more SMs.  Rows of at most RP_TABLE angles a block.
 void split_rows(RowsParams& p, int rows) {
   const long long per_token = static_cast<long long>(rows) * p.units;
-  const long long target = per_token * p.tokens < 1024LL * 304 ? 256 : 1024;
+  const long long target = per_token * p.tokens < 1024LL * 304 ? 256 : 256 * RP_UNITS;
   const int half = std::max(1, p.r.rot / 2);
   int tb = static_cast<int>(std::max(1LL, target / std::max(1LL, per_token)));
   tb = std::min({tb, RP_TOKENS, std::max(1, RP_TABLE / half)});
   p.block_tokens = tb;
+  p.table = (tb * (p.r.rot / 2) + 3) & ~3;
   int br = rows;
   if (tb == 1) br = static_cast<int>(std::min<long long>(rows, std::max(1LL, target / p.units)));
   p.block_rows = std::max(1, br);
@@ -536,7 +564,7 @@ cudaError_t launch_rows(RowsParams& p, cudaStream_t s) {
   split_rows(p, rows);
   const long long blocks = ceil_div_ll(p.tokens, p.block_tokens) * p.row_blocks;
   if (blocks >= (1LL << 31)) return cudaErrorInvalidValue;
-  mk_rows_kernel<T, INTER, VEC, SEQ, CACHE><<<static_cast<unsigned>(blocks), RP_THREADS, 0, s>>>(p);
+  mk_rows_kernel<T, INTER, VEC, SEQ, CACHE><<<static_cast<unsigned>(blocks), RP_THREADS, 8 * p.table, s>>>(p);
   return cudaGetLastError();
 }
 template <class T, bool SEQ, bool CACHE>
@@ -560,7 +588,8 @@ cudaError_t launch_append8(RowsParams& p, cudaStream_t s) {
   }
   if (pieces * p.head_blocks + blocks >= (1LL << 31)) return cudaErrorInvalidValue;
   p.piece_blocks = static_cast<int>(pieces * p.head_blocks);
-  mk_append8_kernel<T, INTER><<<static_cast<unsigned>(p.piece_blocks + blocks), RP_THREADS, 0, s>>>(p);
+  p.table = std::max(p.table, p.r.rot / 2 * std::min(p.c.page_size, AP_CHUNK));
+  mk_append8_kernel<T, INTER><<<static_cast<unsigned>(p.piece_blocks + blocks), RP_THREADS, 8 * p.table, s>>>(p);
   return cudaGetLastError();
 }
 
