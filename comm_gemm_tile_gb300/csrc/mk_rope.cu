@@ -82,6 +82,40 @@ constexpr int AP_CHUNK = 32;           // tokens of a page whose angles are in t
 constexpr int AP_HEADS = 4;            // heads of a block of the 8-bit append: 8 warps, k and v each
 constexpr float E4M3_MAX = 448.f;
 
+// A thread's place in a block's work (token, row, unit of the row; or token, frequency): found by
+// multiplication and counted up from there.
+struct Divide {
+  uint32_t by, m;                            // m = ceil(2^32 / by): exact for numbers below 2^32 / by
+  __host__ void set(int d) {
+    by = static_cast<uint32_t>(std::max(1, d));
+    m = static_cast<uint32_t>((0x100000000ull + by - 1) / by);
+  }
+  __device__ __forceinline__ int of(int n) const { return by == 1 ? n : static_cast<int>(__umulhi(n, m)); }
+};
+struct Place {
+  int tok, row, u;
+  __device__ __forceinline__ Place() {}
+  __device__ __forceinline__ Place(int i, const Divide& rows, const Divide& units) {
+    const int r = units.of(i);
+    u = i - r * units.by;
+    tok = rows.of(r);
+    row = r - tok * rows.by;
+  }
+  __device__ __forceinline__ void add(const Place& step, const Divide& rows, const Divide& units) {
+    u += step.u;
+    row += step.row;
+    tok += step.tok;
+    if (u >= static_cast<int>(units.by)) {
+      u -= units.by;
+      ++row;
+    }
+    if (row >= static_cast<int>(rows.by)) {
+      row -= rows.by;
+      ++tok;
+    }
+  }
+};
+
 struct Rotation {
   const double* freqs;
   const void* positions;
@@ -102,6 +136,7 @@ struct RowsParams {
   CacheView c;
   uint32_t* hdr;
   int heads, d, units;                 // query rows of a token; units of a row
+  Divide by_rows, by_units, by_half;   // a block's rows of a token, units, frequencies
   int tokens, block_tokens, block_rows;
   int row_blocks;                      // blocks of rows per block of tokens
   int piece_blocks, head_blocks;       // 8-bit append: blocks that quantise come first
@@ -125,12 +160,12 @@ __device__ __forceinline__ void rope_turns(const Rotation& r, unsigned long long
 }
 
 // The cosine / sine table of nt tokens, times the magnitude: entry tok * rot/2 + i (see the head of the file).
-__device__ __forceinline__ void rope_table(const Rotation& r, int nt, const long long* pos,
+__device__ __forceinline__ void rope_table(const Rotation& r, const Divide& by_half, int nt, const long long* pos,
                                            const unsigned long long* turns, float* tc, float* ts) {
   const int half = r.rot >> 1;
   const float ms = r.inverse ? -r.magnitude : r.magnitude;
   for (int e = threadIdx.x; e < nt * half; e += RP_THREADS) {
-    const int tok = e / half;
+    const int tok = by_half.of(e);
     const unsigned long long a = static_cast<unsigned long long>(pos[tok]) * turns[e - tok * half];
     float c, s;
     sincospif(static_cast<float>(static_cast<int>(a >> 32)) * 4.656612873077393e-10f, &s, &c);   // 2^-31
@@ -153,6 +188,11 @@ __device__ __forceinline__ int cache_page(const RowsParams& p, int b, long long 
     return -1;
   }
   return page;
+}
+
+// n strides, n >= 0: a 32- by 64-bit product (strides may be negative: modulo 2^64).
+__device__ __forceinline__ long long offset(int n, long long stride) {
+  return static_cast<long long>(static_cast<unsigned>(n) * static_cast<unsigned long long>(stride));
 }
 
 // One unit of a row, 2 N elements: N pairs, or 2 N elements that are copied.
@@ -242,30 +282,6 @@ struct Unit {
   }
 };
 
-// A unit's place, token / row / unit of the row, counted up without dividing.
-struct Place {
-  int tok, row, u;
-  __device__ __forceinline__ Place(int i, int rows, int units) {
-    const int r = i / units;
-    u = i - r * units;
-    tok = r / rows;
-    row = r - tok * rows;
-  }
-  __device__ __forceinline__ void add(const Place& step, int rows, int units) {
-    u += step.u;
-    row += step.row;
-    tok += step.tok;
-    if (u >= units) {
-      u -= units;
-      ++row;
-    }
-    if (row >= rows) {
-      row -= rows;
-      ++tok;
-    }
-  }
-};
-
 // Rows of a block of tokens: the p.heads rows of x go rotated to y; with a
 // 16-bit cache also the token's new keys (rotated) and values (copied) to
 // their slots.  One unit of 2 x 16 bytes a thread and step: 256 bytes of a row
@@ -284,21 +300,25 @@ __device__ __forceinline__ void rows_block(const RowsParams& p, int block, float
   const int total = nt * nr * p.units;
   const int half = p.r.rot >> 1;
   U un[RP_UNITS];
-  const Place step(RP_THREADS, nr, p.units);
-  Place at[RP_UNITS] = {Place(threadIdx.x, nr, p.units), Place(0, 1, 1), Place(0, 1, 1), Place(0, 1, 1)};
+  const Place step(RP_THREADS, p.by_rows, p.by_units);
+  Place at[RP_UNITS];
+  at[0] = Place(threadIdx.x, p.by_rows, p.by_units);
 #pragma unroll
   for (int j = 1; j < RP_UNITS; ++j) {
     at[j] = at[j - 1];
-    at[j].add(step, nr, p.units);
+    at[j].add(step, p.by_rows, p.by_units);
   }
+  const T* x0 = static_cast<const T*>(p.x) + t0 * p.xs_t;
+  const T* k0 = CACHE ? static_cast<const T*>(p.nk) + t0 * p.ks_t : nullptr;
+  const T* v0 = CACHE ? static_cast<const T*>(p.nv) + t0 * p.vs_t : nullptr;
+  T* y0 = static_cast<T*>(p.y) + t0 * p.ys_t;
   auto load = [&](const Place& at, U& w) {
     int o0, o1;
     const int row = r0 + at.row;
-    const long long t = t0 + at.tok;
     const T* src;
-    if (!CACHE || row < p.heads) src = static_cast<const T*>(p.x) + t * p.xs_t + row * p.xs_h;
-    else if (row < p.heads + p.c.heads) src = static_cast<const T*>(p.nk) + t * p.ks_t + (row - p.heads) * p.ks_h;
-    else src = static_cast<const T*>(p.nv) + t * p.vs_t + (row - p.heads - p.c.heads) * p.vs_h;
+    if (!CACHE || row < p.heads) src = x0 + offset(at.tok, p.xs_t) + offset(row, p.xs_h);
+    else if (row < p.heads + p.c.heads) src = k0 + offset(at.tok, p.ks_t) + offset(row - p.heads, p.ks_h);
+    else src = v0 + offset(at.tok, p.vs_t) + offset(row - p.heads - p.c.heads, p.vs_h);
     U::where(at.u, p.r.rot, !CACHE || row < p.heads + p.c.heads, o0, o1);
     w.load(src, o0, o1);
   };
@@ -330,7 +350,7 @@ __device__ __forceinline__ void rows_block(const RowsParams& p, int block, float
   }
   __syncthreads();
   if (p.r.rot > 0) {
-    rope_table(p.r, nt, pos, turns, tc, ts);
+    rope_table(p.r, p.by_half, nt, pos, turns, tc, ts);
     __syncthreads();
   }
 #pragma unroll
@@ -342,11 +362,11 @@ __device__ __forceinline__ void rows_block(const RowsParams& p, int block, float
     const bool is_v = CACHE && row >= p.heads + p.c.heads;
     T* dst;
     if (!CACHE || row < p.heads) {
-      dst = static_cast<T*>(p.y) + (t0 + tok) * p.ys_t + row * p.ys_h;
+      dst = y0 + offset(tok, p.ys_t) + offset(row, p.ys_h);
     } else {
       if (slot[tok] < 0) continue;
       const int h = row - p.heads - (is_v ? p.c.heads : 0);
-      dst = static_cast<T*>(is_v ? p.c.v : p.c.k) + slot[tok] + h * p.c.head_stride;
+      dst = static_cast<T*>(is_v ? p.c.v : p.c.k) + slot[tok] + offset(h, p.c.head_stride);
     }
     U::where(u, p.r.rot, !is_v, o0, o1);
     if (is_v || 2 * N * u >= p.r.rot) {
@@ -438,7 +458,6 @@ __device__ __forceinline__ void quant_block(const RowsParams& p, float* tc, floa
   const bool is_v = warp & 1, act = h < p.c.heads;
   const int half = p.r.rot >> 1;
   const int upr = p.units;                    // units (16 elements) of a row
-  const Place step(32, 1 << 30, upr);
   const T* src = is_v ? static_cast<const T*>(p.nv) + h * p.vs_h : static_cast<const T*>(p.nk) + h * p.ks_h;
   const long long st = is_v ? p.vs_t : p.ks_t;
   uint8_t* dst = static_cast<uint8_t*>(is_v ? p.c.v : p.c.k) + page * p.c.page_stride + h * p.c.head_stride;
@@ -451,12 +470,11 @@ __device__ __forceinline__ void quant_block(const RowsParams& p, float* tc, floa
         __syncthreads();
         if (threadIdx.x < nc) pos[threadIdx.x] = rope_position(p.r, tok0 + c0 + threadIdx.x, own0 + c0 + threadIdx.x);
         __syncthreads();
-        rope_table(p.r, nc, pos, turns, tc, ts);
+        rope_table(p.r, p.by_half, nc, pos, turns, tc, ts);
         __syncthreads();
       }
       if (!act) continue;
       // two units a lane in flight
-      Place at(lane, 1 << 30, upr);
       for (int i0 = lane; i0 < nc * upr; i0 += 64) {
         U w[2];
         int tk[2], uu[2];
@@ -465,14 +483,13 @@ __device__ __forceinline__ void quant_block(const RowsParams& p, float* tc, floa
           const int i = i0 + 32 * k;
           if (i < nc * upr) {
             int o0, o1;
-            tk[k] = at.row;
-            uu[k] = at.u;
+            tk[k] = p.by_units.of(i);
+            uu[k] = i - tk[k] * upr;
             U::where(uu[k], p.r.rot, !is_v, o0, o1);
             const T* row = src + (tok0 + c0 + tk[k]) * st;
             w[k].w0 = *reinterpret_cast<const uint4*>(row + o0);
             w[k].w1 = *reinterpret_cast<const uint4*>(row + o1);
           }
-          at.add(step, 1 << 30, upr);
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -555,11 +572,14 @@ void split_rows(RowsParams& p, int rows) {
   if (tb == 1) br = static_cast<int>(std::min<long long>(rows, std::max(1LL, target / p.units)));
   p.block_rows = std::max(1, br);
   p.row_blocks = (rows + p.block_rows - 1) / p.block_rows;
+  p.by_rows.set(p.block_rows);               // (where the last block has fewer, its block is of one token)
 }
 
 template <class T, bool INTER, bool VEC, bool SEQ, bool CACHE>
 cudaError_t launch_rows(RowsParams& p, cudaStream_t s) {
   p.units = p.d / (2 * Unit<T, INTER, VEC>::N);
+  p.by_units.set(p.units);
+  p.by_half.set(p.r.rot / 2);
   const int rows = p.heads + (CACHE ? 2 * p.c.heads : 0);
   split_rows(p, rows);
   const long long blocks = ceil_div_ll(p.tokens, p.block_tokens) * p.row_blocks;
@@ -576,6 +596,8 @@ cudaError_t launch_rows(RowsParams& p, bool inter, bool vec, cudaStream_t s) {
 template <class T, bool INTER>
 cudaError_t launch_append8(RowsParams& p, cudaStream_t s) {
   p.units = p.d / 16;
+  p.by_units.set(p.units);
+  p.by_half.set(p.r.rot / 2);
   p.head_blocks = (p.c.heads + AP_HEADS - 1) / AP_HEADS;
   const long long pieces = (p.tokens >> p.c.page_log2) + 2LL * p.s.batch;
   long long blocks = 0;
