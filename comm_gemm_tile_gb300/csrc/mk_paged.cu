@@ -11,15 +11,20 @@
 //     of them and a call can be captured into a graph;
 //   * one warp issues a TMA load per page and 128 bytes of row into a ring of
 //     32- or 64-key stages (128 KB), so a page's end inside a tile costs nothing;
-//   * eight warps take the tiles in turn, each with its own running maximum,
-//     sum and 16 x d accumulator (mma.sync m16n8k16: the 16 rows fill the
-//     instruction; a 128-row tcgen05 tile would be 7/8 empty), joined in shared
-//     memory at the end of a run's part of a unit;
+//   * twelve warps take the tiles in turn, each with its own running maximum, sum and accumulator.
+//     They compute the transposes, S^T = K Q^T and O^T += V^T P^T (mma.sync m16n8k16): keys and
+//     elements fill the 16 rows of the instruction and the 8 query rows its 8 columns, so with
+//     groups of up to 8 heads nothing is wasted (query rows as the 16 rows take twice the MMAs and
+//     registers; a 128-row tcgen05 tile would be 15/16 empty).  More than 8 packed rows: two
+//     column groups share the operands of K and V, on eight warps;
+//   * the warps' results are joined in shared memory at the end of a run's part of a unit;
 //   * units cut by a run's end leave normalised fp32 partial rows with their
 //     log2 sums, joined by a second, programmatically dependent launch.
-// 8-bit caches: codes become fp16, exactly; the query row is scaled by a power
-// of two to fit fp16 (bf16 has fewer bits), the key scale multiplies the
-// scores, the value scale (relative to the largest so far) the weights.
+// 8-bit caches: codes become fp16, exactly (the fp8 form of mma.sync does the same conversions
+// inside, with more instructions); the query row is scaled by a power of two to fit fp16 (bf16 has
+// fewer bits), the key scale multiplies the scores, the value scale the weights, and those
+// products have a running maximum of their own: a small weight of a page with a large scale keeps
+// its bits.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -36,24 +41,28 @@ __device__ __noinline__ bool pg_wait_loop(volatile int* dead, const PagedParams&
 
 namespace {
 
-constexpr int DC_WARPS = 8;            // consumer warps; one more loads
-constexpr int DC_THREADS = 32 * (DC_WARPS + 1);
-constexpr int DC_ROWS = 16;            // packed query rows of a unit
+constexpr int DC_MAX_ROWS = 16;        // packed query rows of a unit, at most
 constexpr int DC_BATCH = 1024;         // sequences of one launch (the entry point slices larger batches)
+constexpr int DC_JOIN = 256;           // threads that join a segment
+constexpr int DC_ROUND = 4;            // warps whose rows are in the join buffer at a time
 
-template <class T, bool E8, int D>
+// NQ: groups of 8 query rows of a unit.
+template <class T, bool E8, int D, int NQ>
 struct Shape {
-  static constexpr int KT = (!E8 && D == 128) ? 32 : 64;              // keys of a tile: stages of 8 or 16 KB
+  static constexpr int KT = !E8 && D == 128 ? 32 : 64;                // keys of a tile: 16 KB (8-bit, d = 64: 8 KB)
+  static constexpr int ROWS = 8 * NQ;
+  static constexpr int WARPS = NQ == 1 ? 12 : 8;                      // consumer warps; one more loads
+  static constexpr int THREADS = 32 * (WARPS + 1);
   static constexpr int TILE = KT * D * (E8 ? 1 : 2);
   static constexpr int STAGE = 2 * TILE;
   static constexpr int PITCH = D + 4;                                 // floats of a row in the join buffer
-  static constexpr int MERGE = DC_WARPS * DC_ROWS * PITCH * 4;
-  static constexpr int ML = DC_WARPS * DC_ROWS * 3 * 4;               // maximum, sum, value scale
+  static constexpr int MERGE = DC_ROUND * ROWS * PITCH * 4;
+  static constexpr int ML = WARPS * ROWS * 3 * 4;                     // maximum, sum, value factor
   static constexpr int PREFIX = (DC_BATCH + 1) * 8;
   static constexpr int FIXED = 1024 + MERGE + ML + ((PREFIX + 15) & ~15) + 512;
-  // A warp's tiles come DC_WARPS apart.  With a multiple of that many stages the fill before
-  // the one it waits for was its own, so the barrier's phase parity cannot be mistaken.
-  static constexpr int STAGES = std::min((232448 - FIXED) / STAGE, 16) / DC_WARPS * DC_WARPS;
+  // A warp's tiles come WARPS apart.  With a multiple of that many stages the fill before the one
+  // it waits for was its own, so the barrier's phase parity cannot be mistaken.
+  static constexpr int STAGES = std::min((232448 - FIXED) / STAGE, 24) / WARPS * WARPS;
   static constexpr int SMEM = FIXED + STAGES * STAGE;
 };
 
@@ -89,6 +98,12 @@ __device__ __forceinline__ uint32_t e4m3_f16x2(uint32_t two) {   // two codes ->
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
   return h;
 }
+// An 8 x 8 matrix of 16-bit values turned: rows in lanes / 4, two neighbours of a row in a lane.
+__device__ __forceinline__ uint32_t turn8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 __device__ __forceinline__ uint32_t f16x2(float a, float b) { return Piece<__half>::pack(a, b); }
 // Byte offset of 16-byte piece ch of key row `key` in a tile: rows of 128 bytes
 // (16-bit types: d / 64 such atoms, one after the other) or of 64 bytes, with
@@ -122,7 +137,7 @@ struct Segment {
   KeyTiles t;
   long long u0;                        // number of the unit's first tile
 };
-template <int KT>
+template <int KT, int ROWS>
 __device__ __forceinline__ Segment segment_at(const PagedParams& p, const long long* pre, int b, long long x,
                                               long long end) {
   Segment g;
@@ -130,7 +145,7 @@ __device__ __forceinline__ Segment segment_at(const PagedParams& p, const long l
   sequence_of(p, b, g.n, g.len, g.row0);
   g.t = key_tiles<KT>(p, g.len - g.n, g.len - 1, g.len);
   g.count = g.t.count();
-  const int groups = (g.n * p.group + DC_ROWS - 1) / DC_ROWS;
+  const int groups = (g.n * p.group + ROWS - 1) / ROWS;
   const long long rem = x - pre[b] * p.c.heads;
   const int unit = static_cast<int>(rem / g.count);
   g.k0 = static_cast<int>(rem - static_cast<long long>(unit) * g.count);
@@ -142,19 +157,19 @@ __device__ __forceinline__ Segment segment_at(const PagedParams& p, const long l
 }
 
 // Tiles of sequence b for one head, all its row groups; 0 for sequences of the other launch.
-template <int KT>
+template <int KT, int ROWS>
 __device__ __forceinline__ long long sequence_tiles(const PagedParams& p, int b) {
   int n, len, row0;
   if (!sequence_of(p, b, n, len, row0)) return 0;
   if (!rows_are_ours(p, n)) return 0;
   const long long rows = static_cast<long long>(n) * p.group;
-  return ((rows + DC_ROWS - 1) / DC_ROWS) * key_tiles<KT>(p, len - n, len - 1, len).count();
+  return ((rows + ROWS - 1) / ROWS) * key_tiles<KT>(p, len - n, len - 1, len).count();
 }
 
-template <int KT, bool E8, int D>
+template <int KT, bool E8, int D, int NQ>
 __device__ void dc_producer(const PagedParams& p, const long long* pre, volatile int* dead, uint32_t full, uint32_t empty,
                             uint32_t ring, int stages, long long x, long long end) {
-  constexpr int TILE = KT * D * (E8 ? 1 : 2);
+  constexpr int TILE = KT * D * (E8 ? 1 : 2), ROWS = 8 * NQ;
   const int lane = threadIdx.x & 31;
   const int box = min(p.c.page_size, KT), boxes = KT / box;
   int b = warp_last_le(p.s.batch, 0, [&](int i) { return pre[i] * p.c.heads <= x ? 0 : 1; });
@@ -162,40 +177,46 @@ __device__ void dc_producer(const PagedParams& p, const long long* pre, volatile
   uint32_t ph = 0;
   while (x < end) {
     while (pre[b + 1] * p.c.heads <= x) ++b;
-    const Segment g = segment_at<KT>(p, pre, b, x, end);
+    const Segment g = segment_at<KT, ROWS>(p, pre, b, x, end);
     const int n_pages = min(p.s.max_pages, ((g.len - 1) >> p.c.page_log2) + 1);
     const int* table = p.s.pages + g.b * p.s.pages_stride;
-    // the page of this lane's box of tile k; the maps' first absent page where there is none
-    auto page_of = [&](int k) {
-      const int lp = (g.t.tile(k) * KT + lane * box) >> p.c.page_log2;
-      if (lane >= boxes || lp >= n_pages) return p.map_pages;
+    // The pages of 32 boxes at a time, a lane each, the next 32 on their way meanwhile (a look-up for
+    // every tile held the loads up for 700 cycles a tile): lane i has box i % boxes of tile
+    // k + i / boxes; the maps' first absent page where there is none.
+    auto pages_of = [&](int k) {
+      k += lane / boxes;
+      if (k >= g.k1) return p.map_pages;
+      const int key = g.t.tile(k) * KT + (lane % boxes) * box, lp = key >> p.c.page_log2;
+      if (lp >= n_pages) return p.map_pages;
       const int id = table[lp];
       if (id >= 0 && id < p.c.n_pages) return id;
-      if (keys_seen(p, g.len - g.n, g.len - 1, g.len, g.t.tile(k) * KT + lane * box, box))
-        seq_error(p.hdr, MK_ERR_INVALID, WHERE_PRODUCER, g.b);
+      if (keys_seen(p, g.len - g.n, g.len - 1, g.len, key, box)) seq_error(p.hdr, MK_ERR_INVALID, WHERE_PRODUCER, g.b);
       return p.map_pages;
     };
     if (lane == 0 && ((g.len - 1) >> p.c.page_log2) >= p.s.max_pages)
       seq_error(p.hdr, MK_ERR_CAPACITY, WHERE_PRODUCER, g.b);
-    int next = page_of(g.k0);
-    for (int k = g.k0; k < g.k1; ++k) {
-      const int page = next;
-      if (k + 1 < g.k1) next = page_of(k + 1);
+    const int batch = 32 / boxes;
+    int pages = 0, next = pages_of(g.k0);
+    for (int k = g.k0, at = batch; k < g.k1; ++k, ++at) {
+      if (at == batch) {
+        at = 0;
+        pages = next;
+        if (k + batch < g.k1) next = pages_of(k + batch);
+      }
+      const int page = __shfl_sync(0xffffffffu, pages, at * boxes + (lane % boxes));
       if (!__all_sync(0xffffffffu, pg_wait(dead, p, empty + 8u * st, ph ^ 1u, WHERE_PRODUCER))) return;
       const uint32_t bar = full + 8u * st;
       if (lane == 0) mbar_arrive_expect_tx(bar, 2u * TILE);
       __syncwarp();
-      if (lane < boxes) {
-        const uint32_t kdst = ring + static_cast<uint32_t>(st) * 2u * TILE;
-        const int slot = (g.t.tile(k) * KT + lane * box) & (p.c.page_size - 1);
+      // lanes below 16 load K, the others V
+      if ((lane & 15) < boxes) {
+        const int slot = (g.t.tile(k) * KT + (lane & 15) * box) & (p.c.page_size - 1);
         constexpr int ATOMS = E8 ? 1 : D / 64;
         constexpr uint32_t ROW = E8 ? D : 128;
+        const uint32_t dst = ring + static_cast<uint32_t>(st) * 2u * TILE + (lane >> 4) * TILE + (lane & 15) * box * ROW;
 #pragma unroll
-        for (int a = 0; a < ATOMS; ++a) {
-          const uint32_t off = a * (KT * 128u) + lane * box * ROW;
-          tma_load_4d(kdst + off, &p.tmK, bar, 64 * a, slot, g.h, page);
-          tma_load_4d(kdst + TILE + off, &p.tmV, bar, 64 * a, slot, g.h, page);
-        }
+        for (int a = 0; a < ATOMS; ++a)
+          tma_load_4d(dst + a * (KT * 128u), lane < 16 ? &p.tmK : &p.tmV, bar, 64 * a, slot, g.h, page);
       }
       if (++st == stages) {
         st = 0;
@@ -206,20 +227,442 @@ __device__ void dc_producer(const PagedParams& p, const long long* pre, volatile
   }
 }
 
-template <class T, bool E8, int D>
-__global__ void __launch_bounds__(DC_THREADS, 1) mk_paged_decode_kernel(const __grid_constant__ PagedParams p) {
-  using S = Shape<T, E8, D>;
+// The first tile of a segment that is a warp's: the run's tiles are dealt to the warps in turn.
+template <int WARPS>
+__device__ __forceinline__ int first_tile(int warp, uint32_t done) {
+  const int skip = static_cast<int>(done % WARPS);
+  return warp >= skip ? warp - skip : warp - skip + WARPS;
+}
+
+// A consumer warp's part of a segment: what it needs, and where its result goes.
+struct Work {
+  volatile int* dead;
+  uint32_t ring, full, empty;
+  uint32_t done;                       // tiles of the run before this segment
+  int first;                           // this warp's first tile of it
+  float* merge;                        // the join buffer, and maximum, sum and value factor of
+  float* ml;                           // every warp's rows
+};
+
+// In a tile that not every row sees whole: 0 * NaN is NaN, so values no row sees (past the end,
+// before the window) may hold anything and are cleared, and of those only some rows see (several
+// new tokens) what is not finite is cleared; returns whether there was any of the latter, with the
+// keys as bits.
+template <class T, bool E8, int D, int KT>
+__device__ __forceinline__ bool clear_values(const PagedParams& p, const Segment& g, uint32_t vt, int key0,
+                                             uint32_t (&odd)[2]) {
+  constexpr int CH = D * (E8 ? 1 : 2) / 16;
+  const int lane = threadIdx.x & 31, p0 = g.len - g.n, p1 = g.len - 1;
+  odd[0] = odd[1] = 0u;
+  for (int e = lane; e < KT * CH; e += 32) {
+    const int key = e / CH;
+    const uint32_t at = vt + piece_at<KT, E8, D>(key, e - key * CH);
+    if (!key_seen_by_any(p, p0, p1, g.len, key0 + key)) {
+      sts128(at, make_uint4(0u, 0u, 0u, 0u));
+    } else if (!all_seen(p, p0, p1, g.len, key0 + key, 1)) {
+      uint32_t w[4];
+      lds128(at, w);
+      if (clear_not_finite<T, E8>(w)) {
+        sts128(at, make_uint4(w[0], w[1], w[2], w[3]));
+        odd[key >> 5] |= 1u << (key & 31);
+      }
+    }
+  }
+  odd[0] = __reduce_or_sync(0xffffffffu, odd[0]);
+  odd[1] = __reduce_or_sync(0xffffffffu, odd[1]);
+  __syncwarp();
+  return (odd[0] | odd[1]) != 0u;
+}
+
+// A consumer warp's share of a segment, and of its end.
+template <class T, bool E8, int D, int NQ>
+__device__ __forceinline__ void consume(const PagedParams& p, const Segment& g, const Work& wk) {
+  using S = Shape<T, E8, D, NQ>;
   constexpr bool HALF = E8 || !std::is_same<T, __nv_bfloat16>::value;   // fp16 operands of the products
   constexpr float SHIFT = HALF ? 10.f : 0.f;   // fp16 weights are taken 2^10 high: small ones keep their bits
-  constexpr int KT = S::KT, KS = D / 16, NT = KT / 8, OT = D / 8;
+  constexpr int KT = S::KT, KS = D / 16, MT = KT / 16, OT = D / 16;
+  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  const int p0 = g.len - g.n, p1 = g.len - 1, tiles = g.k1 - g.k0;
+  // per column of S^T and O^T that this lane holds: query rows 8 q + 2 c and + 1
+  float m[NQ][2], l[NQ][2];            // maximum and sum of the weights
+  float mv[NQ][2];                     // 8-bit: maximum of weight times value scale, O's reference
+#pragma unroll
+  for (int q = 0; q < NQ; ++q)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      m[q][e] = mv[q][e] = -INFINITY;
+      l[q][e] = 0.f;
+    }
+  float o[NQ][OT][4];
+#pragma unroll
+  for (int q = 0; q < NQ; ++q)
+#pragma unroll
+    for (int j = 0; j < OT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[q][j][e] = 0.f;
+  if (wk.first < tiles) {
+    // query rows 8 q + r as operand registers
+    uint32_t qf[NQ][KS][2];
+    int pos[NQ][2];
+    float row_scale[NQ][2];
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      const int row = g.rg * S::ROWS + 8 * q + r;
+      const int tok = row / p.group, head = g.h * p.group + row - tok * p.group;
+      const bool ok = tok < g.n;
+      const T* src = static_cast<const T*>(p.q) + static_cast<long long>(g.row0 + (ok ? tok : 0)) * p.qs_t +
+                     (ok ? head : 0) * p.qs_h;
+      const int my_pos = p0 + (ok ? tok : 0);
+      float my_scale = p.scale_log2;
+      if (!E8) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            qf[q][ks][e] = ok ? *reinterpret_cast<const uint32_t*>(src + 16 * ks + 2 * c + 8 * e) : 0u;
+      } else {
+        // 16 neighbouring elements of every 64: the order in which the codes are read
+        float f[D / 4], top = 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            float v[8];
+            const uint4 raw = ok ? *reinterpret_cast<const uint4*>(src + 64 * j + 16 * c + 8 * w)
+                                 : make_uint4(0u, 0u, 0u, 0u);
+            Piece<T>::get(raw, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              f[16 * j + 8 * w + e] = v[e];
+              top = fmaxf(top, fabsf(v[e]));
+            }
+          }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // a power of two that brings the row's largest magnitude to 2^10 .. 2^11
+        const int ex = min(max(static_cast<int>((__float_as_uint(top) >> 23) & 255) - 127, -100), 126);
+        const float up = __uint_as_float(static_cast<uint32_t>(10 - ex + 127) << 23);
+        my_scale *= __uint_as_float(static_cast<uint32_t>(ex - 10 + 127) << 23);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            qf[q][ks][e] = f16x2(f[4 * ks + 2 * e] * up, f[4 * ks + 2 * e + 1] * up);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        pos[q][e] = __shfl_sync(0xffffffffu, my_pos, 4 * (2 * c + e));
+        row_scale[q][e] = __shfl_sync(0xffffffffu, my_scale, 4 * (2 * c + e));
+      }
+    }
+    // 8-bit: lane j < KT / 8 holds the scales of keys 8 j .. 8 j + 7 of a tile
+    const int* table = p.s.pages + g.b * p.s.pages_stride;
+    const int n_pages = min(p.s.max_pages, (p1 >> p.c.page_log2) + 1);
+    auto id_of = [&](int k) {          // -1 for keys no row sees: their scales may be anything
+      const int key = g.t.tile(k) * KT + 8 * (lane & (KT / 8 - 1)), lp = key >> p.c.page_log2;
+      if (lp >= n_pages || !keys_seen(p, p0, p1, g.len, key, 8)) return -1;
+      const int id = table[lp];
+      return id < p.c.n_pages ? id : -1;
+    };
+    float ks_next = 0.f, vs_next = 0.f;
+    auto scales_of = [&](int id) {
+      const long long at = static_cast<long long>(id) * p.c.heads + g.h;
+      ks_next = id >= 0 ? p.c.k_scale[at] : 0.f;
+      vs_next = id >= 0 ? p.c.v_scale[at] : 0.f;
+    };
+    if (E8) scales_of(id_of(g.k0 + wk.first));
+    for (int k = wk.first; k < tiles; k += S::WARPS) {
+      const uint32_t i = wk.done + k;
+      const int st = i % S::STAGES;
+      const uint32_t kt = wk.ring + st * S::STAGE, vt = kt + S::TILE;
+      int next_id = -1;
+      if (E8 && k + S::WARPS < tiles) next_id = id_of(g.k0 + k + S::WARPS);
+      const float ks_tile = ks_next, vs_tile = vs_next;
+      const int there = pg_wait(wk.dead, p, wk.full + 8u * st, (i / S::STAGES) & 1u, WHERE_MMA) ? 1 : 0;
+      if (!__all_sync(0xffffffffu, there)) break;
+      const int key0 = g.t.tile(g.k0 + k) * KT;
+      const bool masked = !all_seen(p, p0, p1, g.len, key0, KT);
+      // ---- S^T = K Q^T: rows of 16-key group t are its keys, in order (16-bit) or permuted so that
+      // neighbouring lanes read different banks (8-bit: row x is key (x >> 1 & 3) | (x & 1) << 2 | x & 8)
+      float s[NQ][MT][4];
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[q][t][e] = 0.f;
+      const int perm = E8 ? (r >> 1) | ((r & 1) << 2) : r;
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        if (!E8) {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            uint32_t f[4];
+            ldsm4(kt + piece_at<KT, E8, D>(16 * t + (lane & 15), 2 * ks + (lane >> 4)), f);
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) mma16816(s[q][t], f, qf[q][ks][0], qf[q][ks][1], HALF);
+          }
+        } else {
+#pragma unroll
+          for (int a = 0; a < D / 64; ++a) {
+            uint32_t f[2][4];
+            lds128(kt + piece_at<KT, E8, D>(16 * t + perm, 4 * a + c), f[0]);
+            lds128(kt + piece_at<KT, E8, D>(16 * t + 8 + perm, 4 * a + c), f[1]);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t x[4] = {e4m3_f16x2(f[0][w] & 0xffffu), e4m3_f16x2(f[1][w] & 0xffffu),
+                                     e4m3_f16x2(f[0][w] >> 16), e4m3_f16x2(f[1][w] >> 16)};
+#pragma unroll
+              for (int q = 0; q < NQ; ++q) mma16816(s[q][t], x, qf[q][4 * a + w][0], qf[q][4 * a + w][1], HALF);
+            }
+          }
+        }
+      }
+      if (E8) scales_of(next_id);
+      // ---- softmax of columns 2 c + e over keys 16 t + perm + 8 h
+      float ks[2 * MT], lv[2 * MT], vs[2 * MT];
+      if (E8) {
+        const float lv_tile = log2f(vs_tile);
+#pragma unroll
+        for (int x = 0; x < 2 * MT; ++x) {
+          ks[x] = __shfl_sync(0xffffffffu, ks_tile, x);
+          vs[x] = __shfl_sync(0xffffffffu, vs_tile, x);
+          lv[x] = __shfl_sync(0xffffffffu, lv_tile, x);
+        }
+      }
+      uint32_t pf[NQ][MT][2];
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        float top[2] = {-INFINITY, -INFINITY}, top_v[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int e = x & 1, h = x >> 1;
+            if (E8) s[q][t][x] *= row_scale[q][e] * ks[2 * t + h];
+            if (masked && !key_seen(p, pos[q][e], g.len, key0 + 16 * t + perm + 8 * h)) s[q][t][x] = -INFINITY;
+            top[e] = fmaxf(top[e], s[q][t][x]);
+            if (E8) top_v[e] = fmaxf(top_v[e], s[q][t][x] + lv[2 * t + h]);
+          }
+        float nref[2], alpha[2], rel[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int y = 4; y < 32; y <<= 1) {
+            top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], y));
+            if (E8) top_v[e] = fmaxf(top_v[e], __shfl_xor_sync(0xffffffffu, top_v[e], y));
+          }
+          const float mn = fmaxf(m[q][e], E8 ? top[e] : top[e] * p.scale_log2);
+          const float mref = mn == -INFINITY ? 0.f : mn;
+          alpha[e] = pg_ex2(m[q][e] - mref);
+          m[q][e] = mn;
+          l[q][e] *= alpha[e];
+          nref[e] = SHIFT - mref;
+          if (E8) {
+            const float mvn = fmaxf(mv[q][e], top_v[e]), vref = mvn == -INFINITY ? 0.f : mvn;
+            alpha[e] = pg_ex2(mv[q][e] - vref);
+            mv[q][e] = mvn;
+            rel[e] = mvn == -INFINITY ? 0.f : pg_ex2(mref - vref);
+          }
+        }
+        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+          for (int j = 0; j < OT; ++j)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[q][j][x] *= alpha[x & 1];
+        }
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          float w[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int e = x & 1;
+            w[x] = pg_ex2(E8 ? s[q][t][x] + nref[e] : fmaf(s[q][t][x], p.scale_log2, nref[e]));
+            l[q][e] += w[x];
+            if (E8) w[x] = w[x] == 0.f ? 0.f : w[x] * (vs[2 * t + (x >> 1)] * rel[e]);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            pf[q][t][h] = turn8x8(HALF ? f16x2(w[2 * h], w[2 * h + 1]) : pack_bf16x2(w[2 * h], w[2 * h + 1]));
+        }
+      }
+      if (masked) {
+        uint32_t odd[2];
+        if (clear_values<T, E8, D, KT>(p, g, vt, key0, odd))
+          for (int key = 0; key < KT; ++key) {     // the rows that see what was cleared get it here
+            if (!((odd[key >> 5] >> (key & 31)) & 1u)) continue;
+            int page;
+            const long long row = value_row(p, g.b, g.h, key0 + key, page);
+            if (row < 0) continue;
+#pragma unroll
+            for (int j = 0; j < OT; ++j)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const int el = E8 ? (D / 8) * r + 2 * j + (x >> 1) : 16 * j + r + 8 * (x >> 1);
+                const float v = not_finite<T, E8>(p.c.v, row + el);
+#pragma unroll
+                for (int q = 0; q < NQ; ++q)
+                  if (v != 0.f && key_seen(p, pos[q][x & 1], g.len, key0 + key)) o[q][j][x] += v;
+              }
+          }
+      }
+      // ---- O^T += V^T P^T: row x of 16-element group j is element 16 j + x (16-bit) or, 8-bit, element
+      // (D / 8) (x % 8) + 2 j + x / 8: lane (r, c) reads keys c, c+4, c+8, c+12 of 16, D / 8 codes each
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        if (!E8) {
+#pragma unroll
+          for (int j = 0; j < OT; ++j) {
+            uint32_t f[4];
+            ldsm4_t(vt + piece_at<KT, E8, D>(16 * t + (lane & 7) + ((lane >> 4) << 3), 2 * j + ((lane >> 3) & 1)), f);
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) mma16816(o[q][j], f, pf[q][t][0], pf[q][t][1], HALF);
+          }
+        } else {
+          uint32_t f[4][4];
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int key = 16 * t + c + 4 * w;
+            if (D == 128) {
+              lds128(vt + piece_at<KT, E8, D>(key, r), f[w]);
+            } else {
+              asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                           : "=r"(f[w][0]), "=r"(f[w][1])
+                           : "r"(vt + piece_at<KT, E8, D>(key, r >> 1) + 8u * (r & 1))
+                           : "memory");
+            }
+          }
+#pragma unroll
+          for (int w = 0; w < D / 32; ++w) {    // 4 x 4 bytes turned into pairs of keys
+            const uint32_t x0 = __byte_perm(f[0][w], f[1][w], 0x5140), x1 = __byte_perm(f[0][w], f[1][w], 0x7362);
+            const uint32_t y0 = __byte_perm(f[2][w], f[3][w], 0x5140), y1 = __byte_perm(f[2][w], f[3][w], 0x7362);
+            const uint32_t a0[4] = {e4m3_f16x2(x0 & 0xffffu), e4m3_f16x2(x0 >> 16), e4m3_f16x2(y0 & 0xffffu),
+                                    e4m3_f16x2(y0 >> 16)};
+            const uint32_t a1[4] = {e4m3_f16x2(x1 & 0xffffu), e4m3_f16x2(x1 >> 16), e4m3_f16x2(y1 & 0xffffu),
+                                    e4m3_f16x2(y1 >> 16)};
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+              mma16816(o[q][2 * w], a0, pf[q][t][0], pf[q][t][1], HALF);
+              mma16816(o[q][2 * w + 1], a1, pf[q][t][0], pf[q][t][1], HALF);
+            }
+          }
+        }
+      }
+      if (masked) fence_proxy_async_smem();   // the cleared rows before the next load of this stage
+      __syncwarp();
+      if (lane == 0) mbar_arrive(wk.empty + 8u * st);
+    }
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int y = 4; y < 32; y <<= 1) l[q][e] += __shfl_xor_sync(0xffffffffu, l[q][e], y);
+  }
+  const int warp = threadIdx.x >> 5;
+  if (r == 0) {
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float* at = wk.ml + (warp * S::ROWS + 8 * q + 2 * c + e) * 3;
+        at[0] = m[q][e];
+        at[1] = l[q][e];
+        at[2] = !E8 ? 1.f : mv[q][e] == -INFINITY ? 0.f : pg_ex2(mv[q][e] - m[q][e]);
+      }
+  }
+  auto barrier = [] { asm volatile("bar.sync 1, %0;" ::"n"(32 * S::WARPS) : "memory"); };
+  barrier();
+  // The join: DC_JOIN threads share out the rows, EL neighbouring elements each; a few warps' rows
+  // are in the buffer at a time.
+  constexpr int PER = DC_JOIN / S::ROWS, EL = D / PER, V = EL < 4 ? EL : 4;
+  const bool joins = threadIdx.x < DC_JOIN;
+  const int row = joins ? threadIdx.x / PER : 0, d0 = (threadIdx.x % PER) * EL;
+  float top = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < S::WARPS; ++w) top = fmaxf(top, wk.ml[(w * S::ROWS + row) * 3]);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float sum = 0.f, acc[EL];
+#pragma unroll
+  for (int e = 0; e < EL; ++e) acc[e] = 0.f;
+  for (int w0 = 0; w0 < S::WARPS; w0 += DC_ROUND) {
+    bool any = false;                          // none of these warps had a tile: nothing to add
+#pragma unroll
+    for (int w = 0; w < DC_ROUND; ++w) any |= first_tile<S::WARPS>(w0 + w, wk.done) < tiles;
+    if (!any) continue;
+    if (warp >= w0 && warp < w0 + DC_ROUND) {
+      float* mine = wk.merge + (warp - w0) * S::ROWS * S::PITCH;
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+#pragma unroll
+        for (int j = 0; j < OT; ++j)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            mine[(8 * q + 2 * c + (x & 1)) * S::PITCH +
+                 (E8 ? (D / 8) * r + 2 * j + (x >> 1) : 16 * j + r + 8 * (x >> 1))] = o[q][j][x];
+    }
+    barrier();
+    if (joins) {
+#pragma unroll
+      for (int w = 0; w < DC_ROUND; ++w) {
+        const float* at = wk.ml + ((w0 + w) * S::ROWS + row) * 3;
+        if (at[1] == 0.f) continue;            // no tile, or nothing seen (NaN stays in)
+        const float f = pg_ex2(at[0] - ref);
+        sum += f * at[1];
+        const float fv = f * at[2];
+        const float* from = wk.merge + (w * S::ROWS + row) * S::PITCH + d0;
+#pragma unroll
+        for (int e = 0; e < EL; e += V) {
+          float v[V];
+          if constexpr (V == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(from + e);
+          else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(from + e);
+#pragma unroll
+          for (int x = 0; x < V; ++x) acc[e + x] += fv * v[x];
+        }
+      }
+    }
+    barrier();
+  }
+  const int prow = g.rg * S::ROWS + row;
+  if (!joins || prow >= g.n * p.group) return;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const float lse2 = sum == 0.f ? -INFINITY : ref + log2f(sum) - SHIFT;
+#pragma unroll
+  for (int e = 0; e < EL; ++e) acc[e] *= inv;
+  if (tiles == g.count) {                      // the whole unit: final
+    const int tok = prow / p.group, head = g.h * p.group + prow - tok * p.group;
+    const long long t = g.row0 + tok;
+    T* dst = static_cast<T*>(p.out) + t * p.os_t + head * p.os_h + d0;
+    if constexpr (EL == 8) {
+      *reinterpret_cast<uint4*>(dst) = Piece<T>::put(*reinterpret_cast<const float (*)[8]>(acc));
+    } else {
+#pragma unroll
+      for (int e = 0; e < EL; e += 2)
+        *reinterpret_cast<uint32_t*>(dst + e) =
+            std::is_same<T, __half>::value ? f16x2(acc[e], acc[e + 1]) : pack_bf16x2(acc[e], acc[e + 1]);
+    }
+    if (p.lse != nullptr && d0 == 0) p.lse[t * p.heads_q + head] = lse2 * LN2;
+  } else {
+    const long long at = static_cast<long long>(part_slot(blockIdx.x, g.k0 == 0)) * S::ROWS + row;
+#pragma unroll
+    for (int e = 0; e < EL; e += 2) *reinterpret_cast<float2*>(p.part + at * D + d0 + e) = make_float2(acc[e], acc[e + 1]);
+    if (d0 == 0) p.part_lse[at] = lse2;
+  }
+}
+
+template <class T, bool E8, int D, int NQ>
+__global__ void __launch_bounds__(Shape<T, E8, D, NQ>::THREADS, 1)
+    mk_paged_decode_kernel(const __grid_constant__ PagedParams p) {
+  using S = Shape<T, E8, D, NQ>;
+  constexpr int KT = S::KT, ROWS = S::ROWS;
   extern __shared__ uint8_t dyn[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~static_cast<uintptr_t>(1023));
   float* merge = reinterpret_cast<float*>(sm + S::STAGES * S::STAGE);
   float* ml = reinterpret_cast<float*>(sm + S::STAGES * S::STAGE + S::MERGE);
   long long* pre = reinterpret_cast<long long*>(sm + S::STAGES * S::STAGE + S::MERGE + S::ML);
   uint8_t* tail = reinterpret_cast<uint8_t*>(pre) + ((S::PREFIX + 15) & ~15);
-  volatile int* dead = reinterpret_cast<int*>(tail + 256);
-  const uint32_t ring = smem_u32(sm), full = smem_u32(tail), empty = full + 128u;
+  volatile int* dead = reinterpret_cast<int*>(tail + 448);
+  const uint32_t ring = smem_u32(sm), full = smem_u32(tail), empty = full + 8u * 24u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int batch = p.s.batch;
 
@@ -235,7 +678,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1) mk_paged_decode_kernel(const __
     tma_prefetch_map(&p.tmK);
     tma_prefetch_map(&p.tmV);
   }
-  for (int b = threadIdx.x; b < batch; b += DC_THREADS) pre[b + 1] = sequence_tiles<KT>(p, b);
+  for (int b = threadIdx.x; b < batch; b += S::THREADS) pre[b + 1] = sequence_tiles<KT, ROWS>(p, b);
   __syncthreads();
   if (warp == 0) {                       // prefix sums, a run of sequences a lane
     const int per = (batch + 31) / 32, lo = min(batch, lane * per), hi = min(batch, lo + per);
@@ -254,386 +697,31 @@ __global__ void __launch_bounds__(DC_THREADS, 1) mk_paged_decode_kernel(const __
     }
   }
   __syncthreads();
-  if (blockIdx.x == 0)
-    for (int b = threadIdx.x; b <= batch; b += DC_THREADS) p.prefix[b] = pre[b];
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.prefix[batch] = pre[batch];   // for the join
   const Deal deal(pre[batch] * p.c.heads, p.grid);
   for (int b = blockIdx.x; b < batch; b += gridDim.x) {   // sequences without a key: nothing is seen
     int n, len, row0;
     if (pre[b + 1] == pre[b] && sequence_of(p, b, n, len, row0) && rows_are_ours(p, n))
-      no_keys<T, D>(p, row0, n, DC_THREADS);
+      no_keys<T, D>(p, row0, n, S::THREADS);
   }
   if (static_cast<int>(blockIdx.x) >= deal.c) return;
   long long x = deal.start(blockIdx.x);
   const long long end = deal.start(blockIdx.x + 1);
-  if (warp == DC_WARPS) {
-    dc_producer<KT, E8, D>(p, pre, dead, full, empty, ring, S::STAGES, x, end);
+  if (warp == S::WARPS) {
+    dc_producer<KT, E8, D, NQ>(p, pre, dead, full, empty, ring, S::STAGES, x, end);
     __syncwarp();
   } else {
-    const int r = lane >> 2, c = lane & 3;
     int b = warp_last_le(batch, 0, [&](int i) { return pre[i] * p.c.heads <= x ? 0 : 1; });
     uint32_t done = 0;                   // tiles of the run before this segment
     while (x < end) {
       while (pre[b + 1] * p.c.heads <= x) ++b;
-      const Segment g = segment_at<KT>(p, pre, b, x, end);
+      const Segment g = segment_at<KT, ROWS>(p, pre, b, x, end);
       if (done == 0 && threadIdx.x == 0)
         p.cut[blockIdx.x] = CutUnit{g.u0 < x ? g.u0 : -1, g.count, g.row0, g.n, g.h, g.rg};
-      const int p0 = g.len - g.n, p1 = g.len - 1;
-      const int tiles = g.k1 - g.k0;
-      const int first = (warp - static_cast<int>(done % DC_WARPS) + DC_WARPS) % DC_WARPS;
-      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, vrun = 0.f;
-      float o[OT][4];
-#pragma unroll
-      for (int j = 0; j < OT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-      if (first < tiles) {
-        // the query rows r and r + 8 of the group, as operand registers
-        uint32_t qf[KS][4];
-        int pos[2];
-        float row_scale[2] = {p.scale_log2, p.scale_log2};
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int row = g.rg * DC_ROWS + r + 8 * i;
-          const int tok = row / p.group, head = g.h * p.group + row - tok * p.group;
-          const bool ok = tok < g.n;
-          pos[i] = p0 + (ok ? tok : 0);
-          const T* src = static_cast<const T*>(p.q) + static_cast<long long>(g.row0 + (ok ? tok : 0)) * p.qs_t +
-                         (ok ? head : 0) * p.qs_h;
-          if (!E8) {
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-              qf[ks][i] = ok ? *reinterpret_cast<const uint32_t*>(src + 16 * ks + 2 * c) : 0u;
-              qf[ks][i + 2] = ok ? *reinterpret_cast<const uint32_t*>(src + 16 * ks + 2 * c + 8) : 0u;
-            }
-          } else {
-            // 16 neighbouring elements for every 64: the order in which the codes are read
-            float f[D / 4], top = 0.f;
-#pragma unroll
-            for (int j = 0; j < D / 64; ++j) {
-#pragma unroll
-              for (int w = 0; w < 2; ++w) {
-                float v[8];
-                const uint4 raw = ok ? *reinterpret_cast<const uint4*>(src + 64 * j + 16 * c + 8 * w)
-                                     : make_uint4(0u, 0u, 0u, 0u);
-                Piece<T>::get(raw, v);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  f[16 * j + 8 * w + e] = v[e];
-                  top = fmaxf(top, fabsf(v[e]));
-                }
-              }
-            }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // a power of two that brings the row's largest magnitude to 2^10 .. 2^11
-            const int ex = min(max(static_cast<int>((__float_as_uint(top) >> 23) & 255) - 127, -100), 126);
-            const float up = __uint_as_float(static_cast<uint32_t>(10 - ex + 127) << 23);
-            row_scale[i] *= __uint_as_float(static_cast<uint32_t>(max(ex - 10, -126) + 127) << 23);
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-              const int e = 16 * (ks >> 2) + 4 * (ks & 3);
-              qf[ks][i] = f16x2(f[e] * up, f[e + 1] * up);
-              qf[ks][i + 2] = f16x2(f[e + 2] * up, f[e + 3] * up);
-            }
-          }
-        }
-        // 8-bit: lane j < 8 holds the scales of keys 8 j .. 8 j + 7 of a tile
-        const int* table = p.s.pages + g.b * p.s.pages_stride;
-        const int n_pages = min(p.s.max_pages, (p1 >> p.c.page_log2) + 1);
-        auto id_of = [&](int k) {      // -1 for keys no row sees: their scales may be anything
-          const int key = g.t.tile(k) * KT + 8 * (lane & 7), lp = key >> p.c.page_log2;
-          if (lp >= n_pages || !keys_seen(p, p0, p1, g.len, key, 8)) return -1;
-          const int id = table[lp];
-          return id < p.c.n_pages ? id : -1;
-        };
-        float ks_now = 0.f, vs_now = 0.f;
-        auto scales_of = [&](int id) {
-          const long long at = static_cast<long long>(id) * p.c.heads + g.h;
-          ks_now = id >= 0 ? p.c.k_scale[at] : 0.f;
-          vs_now = id >= 0 ? p.c.v_scale[at] : 0.f;
-        };
-        if (E8) scales_of(id_of(g.k0 + first));
-        for (int k = first; k < tiles; k += DC_WARPS) {
-          const uint32_t i = done + k;
-          const int st = i % S::STAGES;
-          const uint32_t kt = ring + st * S::STAGE, vt = kt + S::TILE;
-          int next_id = -1;
-          if (E8 && k + DC_WARPS < tiles) next_id = id_of(g.k0 + k + DC_WARPS);
-          const float ks_tile = ks_now, vs_tile = vs_now;
-          const int ok = pg_wait(dead, p, full + 8u * st, (i / S::STAGES) & 1u, WHERE_MMA) ? 1 : 0;
-          if (!__all_sync(0xffffffffu, ok)) break;
-          const int key0 = g.t.tile(g.k0 + k) * KT;
-          const bool masked = !all_seen(p, p0, p1, g.len, key0, KT);
-          // ---- scores
-          float s[NT][4];
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
-          if (!E8) {
-            const int krow = ((lane >> 4) << 3) + (lane & 7), kch = (lane >> 3) & 1;
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-              for (int j = 0; j < NT; j += 2) {
-                uint32_t f[4];
-                ldsm4(kt + piece_at<KT, E8, D>(8 * j + krow, 2 * ks + kch), f);
-                mma16816(s[j], qf[ks], f[0], f[1], HALF);
-                mma16816(s[j + 1], qf[ks], f[2], f[3], HALF);
-              }
-          } else {
-            // column n of a group of 8 is key (n >> 1) | (n & 1) << 2: the four lanes of
-            // neighbouring columns then read different banks
-            const int kperm = (r >> 1) | ((r & 1) << 2);
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-              for (int a = 0; a < D / 64; ++a) {
-                uint32_t f[4];
-                lds128(kt + piece_at<KT, E8, D>(8 * j + kperm, 4 * a + c), f);
-#pragma unroll
-                for (int w = 0; w < 4; ++w)
-                  mma16816(s[j], qf[4 * a + w], e4m3_f16x2(f[w] & 0xffffu), e4m3_f16x2(f[w] >> 16), HALF);
-              }
-          }
-          // ---- softmax of rows r (e = 0, 1) and r + 8 (e = 2, 3)
-          float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            const float f = E8 ? __shfl_sync(0xffffffffu, ks_tile, j) : 1.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float z = s[j][e] * (E8 ? row_scale[e >> 1] * f : p.scale_log2);
-              if (masked) {
-                const int key = key0 + 8 * j + (E8 ? c + 4 * (e & 1) : 2 * c + (e & 1));
-                if (!key_seen(p, pos[e >> 1], g.len, key)) z = -INFINITY;
-              }
-              s[j][e] = z;
-              top[e >> 1] = fmaxf(top[e >> 1], z);
-            }
-          }
-          float mref[2], alpha[2];
-#pragma unroll
-          for (int i2 = 0; i2 < 2; ++i2) {
-            top[i2] = fmaxf(top[i2], __shfl_xor_sync(0xffffffffu, top[i2], 1));
-            top[i2] = fmaxf(top[i2], __shfl_xor_sync(0xffffffffu, top[i2], 2));
-            const float mn = fmaxf(m[i2], top[i2]);
-            mref[i2] = mn == -INFINITY ? 0.f : mn;
-            alpha[i2] = pg_ex2(m[i2] - mref[i2]);
-            m[i2] = mn;
-            l[i2] *= alpha[i2];
-          }
-          if (E8) {                      // O is kept in units of the largest value scale so far
-            float top_v = vs_tile;
-            top_v = fmaxf(top_v, __shfl_xor_sync(0xffffffffu, top_v, 1));
-            top_v = fmaxf(top_v, __shfl_xor_sync(0xffffffffu, top_v, 2));
-            top_v = fmaxf(top_v, __shfl_xor_sync(0xffffffffu, top_v, 4));
-            if (top_v > vrun) {
-              const float f = vrun / top_v;
-              alpha[0] *= f;
-              alpha[1] *= f;
-              vrun = top_v;
-            }
-          }
-          if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-            for (int j = 0; j < OT; ++j) {
-              o[j][0] *= alpha[0];
-              o[j][1] *= alpha[0];
-              o[j][2] *= alpha[1];
-              o[j][3] *= alpha[1];
-            }
-          }
-          uint32_t pf[NT][2];
-          const float vinv = E8 && vrun > 0.f ? 1.f / vrun : 0.f;
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            float w[4];
-            const float f = E8 ? __shfl_sync(0xffffffffu, vs_tile, j) * vinv : 1.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              w[e] = pg_ex2(s[j][e] - mref[e >> 1] + SHIFT);
-              l[e >> 1] += w[e];
-              if (E8) w[e] = w[e] == 0.f ? 0.f : w[e] * f;
-            }
-            pf[j][0] = HALF ? f16x2(w[0], w[1]) : pack_bf16x2(w[0], w[1]);
-            pf[j][1] = HALF ? f16x2(w[2], w[3]) : pack_bf16x2(w[2], w[3]);
-          }
-          if (E8) scales_of(next_id);
-          if (masked) {
-            // 0 * NaN is NaN: values no row sees (past the end, before the window) may hold
-            // anything and are cleared, and of those only some rows see (several new tokens)
-            // what is not finite is cleared and added below to the rows that do see it
-            constexpr int CH = D * (E8 ? 1 : 2) / 16;
-            uint32_t odd[2] = {0u, 0u};
-            for (int e = lane; e < KT * CH; e += 32) {
-              const int key = e / CH;
-              const uint32_t at = vt + piece_at<KT, E8, D>(key, e - key * CH);
-              if (!key_seen_by_any(p, p0, p1, g.len, key0 + key)) {
-                sts128(at, make_uint4(0u, 0u, 0u, 0u));
-              } else if (!all_seen(p, p0, p1, g.len, key0 + key, 1)) {
-                uint32_t w[4];
-                lds128(at, w);
-                if (clear_not_finite<T, E8>(w)) {
-                  sts128(at, make_uint4(w[0], w[1], w[2], w[3]));
-                  odd[key >> 5] |= 1u << (key & 31);
-                }
-              }
-            }
-            odd[0] = __reduce_or_sync(0xffffffffu, odd[0]);
-            odd[1] = __reduce_or_sync(0xffffffffu, odd[1]);
-            for (int key = 0; (odd[0] | odd[1]) != 0u && key < KT; ++key) {
-              if (!((odd[key >> 5] >> (key & 31)) & 1u)) continue;
-              int page;
-              const long long row = value_row(p, g.b, g.h, key0 + key, page);
-              if (row < 0) continue;
-#pragma unroll
-              for (int j = 0; j < OT; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const int col = 2 * c + (e & 1);
-                  const float v = not_finite<T, E8>(p.c.v, row + (E8 ? (D / 8) * col + j : 8 * j + col));
-                  if (v != 0.f && key_seen(p, pos[e >> 1], g.len, key0 + key)) o[j][e] += v;
-                }
-            }
-            __syncwarp();
-          }
-          // ---- O += P V
-          if (!E8) {
-            const int vrow = (((lane >> 3) & 1) << 3) + (lane & 7), vch = lane >> 4;
-#pragma unroll
-            for (int t = 0; t < KT / 16; ++t) {
-              const uint32_t a[4] = {pf[2 * t][0], pf[2 * t][1], pf[2 * t + 1][0], pf[2 * t + 1][1]};
-#pragma unroll
-              for (int j = 0; j < OT; j += 2) {
-                uint32_t f[4];
-                ldsm4_t(vt + piece_at<KT, E8, D>(16 * t + vrow, j + vch), f);
-                mma16816(o[j], a, f[0], f[1], HALF);
-                mma16816(o[j + 1], a, f[2], f[3], HALF);
-              }
-            }
-          } else {
-            // lane (r, c) reads keys c, c+4, c+8, c+12 of 16, elements (D/8) r ..: output
-            // tile j has element (D/8) n + j in column n
-#pragma unroll
-            for (int t = 0; t < KT / 16; ++t) {
-              const uint32_t a[4] = {pf[2 * t][0], pf[2 * t][1], pf[2 * t + 1][0], pf[2 * t + 1][1]};
-              uint32_t f[4][4];
-#pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                const int key = 16 * t + c + 4 * w;
-                if (D == 128) {
-                  lds128(vt + piece_at<KT, E8, D>(key, r), f[w]);
-                } else {
-                  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
-                               : "=r"(f[w][0]), "=r"(f[w][1])
-                               : "r"(vt + piece_at<KT, E8, D>(key, r >> 1) + 8u * (r & 1))
-                               : "memory");
-                }
-              }
-#pragma unroll
-              for (int w = 0; w < D / 32; ++w) {    // 4 x 4 bytes turned: element j of the four keys
-                const uint32_t x0 = __byte_perm(f[0][w], f[1][w], 0x5140), x1 = __byte_perm(f[0][w], f[1][w], 0x7362);
-                const uint32_t y0 = __byte_perm(f[2][w], f[3][w], 0x5140), y1 = __byte_perm(f[2][w], f[3][w], 0x7362);
-                mma16816(o[4 * w], a, e4m3_f16x2(x0 & 0xffffu), e4m3_f16x2(y0 & 0xffffu), HALF);
-                mma16816(o[4 * w + 1], a, e4m3_f16x2(x0 >> 16), e4m3_f16x2(y0 >> 16), HALF);
-                mma16816(o[4 * w + 2], a, e4m3_f16x2(x1 & 0xffffu), e4m3_f16x2(y1 & 0xffffu), HALF);
-                mma16816(o[4 * w + 3], a, e4m3_f16x2(x1 >> 16), e4m3_f16x2(y1 >> 16), HALF);
-              }
-            }
-          }
-          if (masked) fence_proxy_async_smem();   // the cleared rows before the next load of this stage
-          __syncwarp();
-          if (lane == 0) mbar_arrive(empty + 8u * st);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-          l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-        }
-        float* mine = merge + warp * DC_ROWS * S::PITCH;
-#pragma unroll
-        for (int j = 0; j < OT; ++j)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float* at = mine + (r + 8 * i) * S::PITCH;
-            if (!E8) {
-              *reinterpret_cast<float2*>(at + 8 * j + 2 * c) = make_float2(o[j][2 * i], o[j][2 * i + 1]);
-            } else {
-              at[(D / 8) * (2 * c) + j] = o[j][2 * i];
-              at[(D / 8) * (2 * c + 1) + j] = o[j][2 * i + 1];
-            }
-          }
-      }
-      if (c == 0) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float* at = ml + (warp * DC_ROWS + r + 8 * i) * 3;
-          at[0] = m[i];
-          at[1] = l[i];
-          at[2] = E8 ? vrun : 1.f;
-        }
-      }
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      {
-        // join: 16 threads a row, D / 16 neighbouring elements each
-        constexpr int EL = D / 16;
-        const int row = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * EL;
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < DC_WARPS; ++w) top = fmaxf(top, ml[(w * DC_ROWS + row) * 3]);
-        const float ref = top == -INFINITY ? 0.f : top;
-        float sum = 0.f, acc[EL];
-#pragma unroll
-        for (int e = 0; e < EL; ++e) acc[e] = 0.f;
-        for (int w = 0; w < DC_WARPS; ++w) {
-          const float* at = ml + (w * DC_ROWS + row) * 3;
-          if (at[1] == 0.f) continue;             // no tile, or nothing seen (NaN stays in)
-          const float f = pg_ex2(at[0] - ref);
-          sum += f * at[1];
-          const float fv = f * at[2];
-#pragma unroll
-          for (int e = 0; e < EL; e += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(merge + (w * DC_ROWS + row) * S::PITCH + d0 + e);
-            acc[e] += fv * v.x;
-            acc[e + 1] += fv * v.y;
-            acc[e + 2] += fv * v.z;
-            acc[e + 3] += fv * v.w;
-          }
-        }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const float lse2 = sum == 0.f ? -INFINITY : ref + log2f(sum) - SHIFT;
-        const int prow = g.rg * DC_ROWS + row;
-        if (prow < g.n * p.group) {
-          if (tiles == g.count) {                 // the whole unit: final
-            const int tok = prow / p.group, head = g.h * p.group + prow - tok * p.group;
-            const long long t = g.row0 + tok;
-            T* dst = static_cast<T*>(p.out) + t * p.os_t + head * p.os_h + d0;
-            if constexpr (EL == 8) {
-              float v[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] = acc[e] * inv;
-              *reinterpret_cast<uint4*>(dst) = Piece<T>::put(v);
-            } else {
-              uint2 w;
-              w.x = HALF && !E8 ? f16x2(acc[0] * inv, acc[1] * inv) : pack_bf16x2(acc[0] * inv, acc[1] * inv);
-              w.y = HALF && !E8 ? f16x2(acc[2] * inv, acc[3] * inv) : pack_bf16x2(acc[2] * inv, acc[3] * inv);
-              *reinterpret_cast<uint2*>(dst) = w;
-            }
-            if (p.lse != nullptr && d0 == 0) p.lse[t * p.heads_q + head] = lse2 * LN2;
-          } else {
-            const long long at = static_cast<long long>(part_slot(blockIdx.x, g.k0 == 0)) * DC_ROWS + row;
-#pragma unroll
-            for (int e = 0; e < EL; e += 4)
-              *reinterpret_cast<float4*>(p.part + at * D + d0 + e) =
-                  make_float4(acc[e] * inv, acc[e + 1] * inv, acc[e + 2] * inv, acc[e + 3] * inv);
-            if (d0 == 0) p.part_lse[at] = lse2;
-          }
-        }
-      }
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      done += tiles;
-      x += tiles;
+      const Work wk = {dead, ring, full, empty, done, first_tile<S::WARPS>(warp, done), merge, ml};
+      consume<T, E8, D, NQ>(p, g, wk);
+      done += g.k1 - g.k0;
+      x += g.k1 - g.k0;
     }
   }
   if (*dead) {   // loads whose barrier nobody waited for may still be landing
@@ -645,39 +733,44 @@ __global__ void __launch_bounds__(DC_THREADS, 1) mk_paged_decode_kernel(const __
 // ------------------------------------------------------------------ join
 
 // Block i - 1: if CTA i's run begins inside a unit that CTA i - 1 began, that unit's rows.
-template <class T, int D>
+template <class T, int D, int ROWS>
 __global__ void __launch_bounds__(256) mk_paged_join_kernel(const __grid_constant__ PagedParams p) {
   griddep_wait();
   const int i = blockIdx.x + 1;
   const CutUnit g = p.cut[i];
   const Deal deal(p.prefix[p.s.batch] * p.c.heads, p.grid);
   if (i >= deal.c || g.u0 < 0 || deal.start(i - 1) > g.u0) return;
-  const int row = threadIdx.x >> 4, prow = g.at * DC_ROWS + row;
-  if (prow >= g.n * p.group) return;
+  const int row = threadIdx.x >> 4, prow = g.at * ROWS + row;
+  if (row >= ROWS || prow >= g.n * p.group) return;
   const int tok = prow / p.group;
-  join_row<T, D, DC_ROWS>(p, i - 1, deal.owner(g.u0 + g.count - 1), row, g.row0 + tok, g.h * p.group + prow - tok * p.group);
+  join_row<T, D, ROWS>(p, i - 1, deal.owner(g.u0 + g.count - 1), row, g.row0 + tok, g.h * p.group + prow - tok * p.group);
 }
 
 // ------------------------------------------------------------------ host
 
-template <class T, bool E8, int D>
+template <class T, bool E8, int D, int NQ>
 cudaError_t launch_decode(const PagedParams& p, cudaStream_t s) {
-  using S = Shape<T, E8, D>;
-  static_assert(S::STAGES >= DC_WARPS, "a stage for each warp");
+  using S = Shape<T, E8, D, NQ>;
+  static_assert(S::STAGES >= S::WARPS && S::SMEM <= 232448, "a stage for each warp");
   static int configured_dev = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (configured_dev != dev) {
-    e = cudaFuncSetAttribute(mk_paged_decode_kernel<T, E8, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    e = cudaFuncSetAttribute(mk_paged_decode_kernel<T, E8, D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (e != cudaSuccess) return e;
     configured_dev = dev;
   }
-  mk_paged_decode_kernel<T, E8, D><<<p.grid, DC_THREADS, S::SMEM, s>>>(p);
+  mk_paged_decode_kernel<T, E8, D, NQ><<<p.grid, S::THREADS, S::SMEM, s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (p.grid < 2) return e;
-  return launch_dependent(mk_paged_join_kernel<T, D>, dim3(p.grid - 1), dim3(256), s, p);
+  return launch_dependent(mk_paged_join_kernel<T, D, S::ROWS>, dim3(p.grid - 1), dim3(256), s, p);
+}
+template <class T, bool E8>
+cudaError_t launch_decode(const PagedParams& p, int nq, cudaStream_t s) {
+  if (p.c.d == 128) return nq == 1 ? launch_decode<T, E8, 128, 1>(p, s) : launch_decode<T, E8, 128, 2>(p, s);
+  return nq == 1 ? launch_decode<T, E8, 64, 1>(p, s) : launch_decode<T, E8, 64, 2>(p, s);
 }
 
 // K / V as [d, slots, heads, pages]; a box is the part of a page that falls into a tile of `tile` keys.
@@ -713,7 +806,7 @@ bool may_be_prompt(long long max_tokens, int group) { return group <= 128 && max
 bool paged_layout(long long tokens, int group, int d, int batch, int sms, PagedLayout& L) {
   if (d != 64 && d != 128) return false;
   const bool prompt = may_be_prompt(tokens, group);
-  const size_t rows = static_cast<size_t>(2) * sms * (prompt ? prompt_part_rows() : DC_ROWS);
+  const size_t rows = static_cast<size_t>(2) * sms * (prompt ? prompt_part_rows() : DC_MAX_ROWS);
   const size_t units = std::max<size_t>(std::min(batch, DC_BATCH),
                                         prompt ? prompt_entries(static_cast<int>(tokens), group, batch) : 0);
   L.cut_off = WS_HDR_BYTES;
@@ -794,7 +887,9 @@ mk_status mk_paged_attention(const void* q, void* out, float* lse, mk_dtype dtyp
   const bool prompt = may_be_prompt(most, p.group);
   const bool decode = !prompt || (seqs->batch > 1 && most * seqs->batch != tokens);
   if (decode) {
-    const int tile = !e8 && d == 128 ? Shape<__nv_bfloat16, false, 128>::KT : Shape<__nv_bfloat16, true, 128>::KT;
+    const int tile = d == 128 && !e8 ? Shape<__half, false, 128, 1>::KT : 64;
+    // 8 packed rows to a unit where no sequence has more, else 16: the keys are read once for either
+    const int nq = most * p.group <= 8 ? 1 : 2;
     if (!cache_map(&p.tmK, cache, cache->k, ws, tile, true) || !cache_map(&p.tmV, cache, cache->v, ws, tile, true))
       return MK_ERR_CUDA;
     p.rows_lo = 1;
@@ -806,12 +901,9 @@ mk_status mk_paged_attention(const void* q, void* out, float* lse, mk_dtype dtyp
       part.s.kv_len = seqs->kv_len + b0;
       part.s.pages = seqs->pages + static_cast<long long>(b0) * seqs->pages_stride;
       cudaError_t e;
-      if (e8)
-        e = d == 128 ? launch_decode<__nv_bfloat16, true, 128>(part, s) : launch_decode<__nv_bfloat16, true, 64>(part, s);
-      else if (dtype == MK_BF16)
-        e = d == 128 ? launch_decode<__nv_bfloat16, false, 128>(part, s) : launch_decode<__nv_bfloat16, false, 64>(part, s);
-      else
-        e = d == 128 ? launch_decode<__half, false, 128>(part, s) : launch_decode<__half, false, 64>(part, s);
+      if (e8) e = launch_decode<__nv_bfloat16, true>(part, nq, s);
+      else if (dtype == MK_BF16) e = launch_decode<__nv_bfloat16, false>(part, nq, s);
+      else e = launch_decode<__half, false>(part, nq, s);
       if (e != cudaSuccess) return MK_ERR_CUDA;
     }
   }
