@@ -11,16 +11,18 @@
 // Items cut by a run's end leave fp32 partial rows for the join (mk_paged.cu).
 //
 // Roles of a CTA's warps:
-//   0-3, 4-7  softmax of query tile 0 / 1, one row a thread: the 128 scores of a
+//   4-7, 8-11 softmax of query tile 0 / 1, one row a thread: the 128 scores of a
 //             key tile in two halves, the weights 2^(c s - m) go back into
 //             tensor memory in 16 bits, over the scores; m is the largest score of the
 //             first tile and moves only when weights grow too large (then O is scaled)
-//   8         loads Q and K, 10 loads V (and clears what must not count, see pr_load_v): one
+//   1         loads Q and K, 2 loads V (and clears what must not count, see pr_load_v): one
 //             TMA box a page and 64 columns
-//   9, 11     issue the MMAs of query tile 0 / 1: O_i += P_i V of the tile before, in two halves
+//   0, 3      issue the MMAs of query tile 0 / 1: O_i += P_i V of the tile before, in two halves
 //             as their weights appear, then S_i = Q_i K^T.  A warp each, because the issuing
 //             warp's own instructions take as long as the products they start
-//   12-15     8-bit caches only: turn codes into bf16 tiles, scale and all
+//   12-15     8-bit caches only: turn the codes of K into fp16 (one conversion for two, exact; the
+//             scale multiplies the scores) and those of V into bf16, scale and all; and an
+//             item's queries into fp16, each row times a power of two
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -48,13 +50,16 @@ struct Plan {
   static constexpr uint32_t RAW = E8 ? PR_T * D : 0;      // codes as they arrive
   static constexpr uint32_t Q = 0, K = 2 * TILE, V = K + PR_ST * TILE, RK = V + PR_ST * TILE, RV = RK + RAW;
   static constexpr uint32_t BARS = RV + RAW;
-  static constexpr int SMEM = 1024 + BARS + 512;
+  static constexpr uint32_t QEXP = BARS + 384;             // 8-bit: exponents of the query rows' factors,
+  static constexpr uint32_t KSC = QEXP + (E8 ? 512 : 0);   // by segment parity; key scales of four tiles
+  static constexpr int SMEM = 1024 + KSC + (E8 ? 256 : 0);
   static_assert(SMEM <= 232448, "dynamic shared memory per block");
 };
 // barriers (byte offsets)
 constexpr uint32_t B_QFULL = 0, B_QEMPTY = 8, B_KFULL = 16, B_KEMPTY = 32, B_VFULL = 48, B_VEMPTY = 64, B_VREADY = 80,
                    B_S = 96, B_GO = 112, B_O = 144, B_DRAIN = 160, B_RKFULL = 176, B_RKEMPTY = 184, B_RVFULL = 192,
-                   B_RVEMPTY = 200, B_TURN = 208, B_TMEM = 240, B_DEAD = 244, B_ODD = 248, B_HALF = 280;
+                   B_RVEMPTY = 200, B_TURN = 208, B_TMEM = 240, B_DEAD = 244, B_ODD = 248, B_HALF = 280, B_QREADY = 296;
+static_assert(B_QREADY + 8 <= 384, "barrier block");
 
 __device__ __forceinline__ uint32_t idesc(int n, bool b_mn, bool half) {
   return idesc_bf16_f32(PR_T, n, false, b_mn) & (half ? ~((1u << 7) | (1u << 10)) : ~0u);
@@ -396,62 +401,119 @@ __device__ void pr_load_v(const PagedParams& p, Walk w, volatile int* dead, uint
   }
 }
 
-// Warps 12-15 (8-bit caches): codes -> bf16 with the page's scale (a power of two: exact), K
-// then V of every tile, and the clearing of warp 11.  A lane takes 16 codes of a row at a time.
+__device__ __forceinline__ uint32_t codes_f16(uint32_t two_codes) {   // two e4m3 codes -> two fp16, exactly
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two_codes)));
+  return h;
+}
+
+// Warps 12-15 (8-bit caches): an item's queries, then K and V of every tile, with the clearing of
+// pr_load_v.  A lane takes 16 codes of a row at a time.
 template <int D>
 __device__ void pr_turn(const PagedParams& p, Walk w, volatile int* dead, uint32_t bars, uint32_t base, uint8_t* sm,
                         volatile int* odd) {
   using P = Plan<true, D>;
   const int lane = threadIdx.x & 31, tw = (threadIdx.x >> 5) - W_TURN;
+  const int used = PR_T / p.group * p.group;               // query rows of a tile that are loaded
   uint32_t u = 0;
   for (int seg = 0; w.next(p); ++seg) {
     int p0, p1;
     item_span(p, w.it, p0, p1);
     if (lane == 0 && tw == 0) odd[(seg + 1) & 7] = 0;
+    // lane i: the scale of keys 8 (i % 16) .. + 7 of a tile, K's for i < 16, V's above; keys no row
+    // sees may have any, and none of the tile's scores is multiplied by 0 (they may be -inf)
     const int n_pages = min(p.s.max_pages, ((w.it.len - 1) >> p.c.page_log2) + 1);
     const int* table = p.s.pages + w.it.b * p.s.pages_stride;
-    // lane i: the scale of keys 8 (i % 16) .. + 7 of a tile, K's for i < 16, V's above
     auto id_of = [&](int k) {
-      const int lp = (w.it.t.tile(k) * PR_T + 8 * (lane & 15)) >> p.c.page_log2;
-      const int id = lp < n_pages ? table[lp] : -1;
+      const int key = w.it.t.tile(k) * PR_T + 8 * (lane & 15), lp = key >> p.c.page_log2;
+      if (lp >= n_pages || !keys_seen(p, p0, p1, w.it.len, key, 8)) return -1;
+      const int id = table[lp];
       return id < p.c.n_pages ? id : -1;
     };
     auto scale_of = [&](int id) {
-      if (id < 0) return 0.f;
+      if (id < 0) return 1.f;
       return (lane < 16 ? p.c.k_scale : p.c.v_scale)[static_cast<long long>(id) * p.c.heads + w.h];
     };
     float scale = scale_of(id_of(w.k0));
+    // queries: bf16 -> fp16 in place, the row's largest magnitude brought to 2^10 .. 2^11 (below
+    // 2^-100 it stays smaller)
+    if (!pr_wait(dead, p, bars + B_QFULL, seg & 1u, WHERE_COPY)) return;
+    {
+      constexpr int PER = D / 8, ROWS = 32 / PER;          // lanes of a row, rows of a step
+      const int ch = lane % PER;
+#pragma unroll 2
+      for (int r0 = tw * ROWS; r0 < 2 * PR_T; r0 += 4 * ROWS) {
+        const int r = r0 + lane / PER, row = r & (PR_T - 1);
+        uint4* at = reinterpret_cast<uint4*>(sm + P::Q + (r / PR_T) * P::TILE + v_piece(row, ch));
+        float f[8], top = 0.f;
+        Piece<__nv_bfloat16>::get(*at, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+#pragma unroll
+        for (int o = PER / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int ex = min(max(static_cast<int>((__float_as_uint(top) >> 23) & 255) - 127, -100), 126);
+        const float up = __uint_as_float(static_cast<uint32_t>(10 - ex + 127) << 23);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= up;
+        if (row < used) *at = Piece<__half>::put(f);
+        if (ch == 0) reinterpret_cast<signed char*>(sm + P::QEXP)[(seg & 1) * 2 * PR_T + r] = static_cast<signed char>(ex - 10);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + B_QREADY);
+    }
     for (int k = w.k0; k < w.k1; ++k, ++u) {
       const uint32_t st = u % PR_ST, ph = (u / PR_ST) & 1u;
       const int next_id = k + 1 < w.k1 ? id_of(k + 1) : -1;
       const int key0 = w.it.t.tile(k) * PR_T;
       const bool masked = !all_seen(p, p0, p1, w.it.len, key0, PR_T);
-#pragma unroll 1
-      for (int v = 0; v < 2; ++v) {
-        if (!pr_wait(dead, p, bars + (v ? B_RVFULL : B_RKFULL), u & 1u, WHERE_COPY)) return;
-        if (!pr_wait(dead, p, bars + (v ? B_VEMPTY : B_KEMPTY) + 8u * st, ph ^ 1u, WHERE_COPY)) return;
-        const uint8_t* raw = sm + (v ? P::RV : P::RK);
-        uint8_t* out = sm + (v ? P::V : P::K) + st * P::TILE;
-        bool any = false;
-        constexpr int PER = D / 16;                    // pieces of 16 codes in a row
+      constexpr int PER = D / 16;                          // pieces of 16 codes in a row
+      // ---- K
+      if (!pr_wait(dead, p, bars + B_RKFULL, u & 1u, WHERE_COPY)) return;
+      if (!pr_wait(dead, p, bars + B_KEMPTY + 8u * st, ph ^ 1u, WHERE_COPY)) return;
+      if (tw == 0 && lane < 16)
+        reinterpret_cast<float*>(sm + P::KSC)[(u & 3u) * 16 + lane] = scale == 0.f ? 1e-30f : scale;
+      {
+        uint8_t* out = sm + P::K + st * P::TILE;
 #pragma unroll 4
         for (int i = tw * 32 + lane; i < PR_T * PER; i += 128) {
           const int key = i / PER, c = i - key * PER;
-          const float f = __shfl_sync(0xffffffffu, scale, (key >> 3) + 16 * v);
-          const uint4 in = *reinterpret_cast<const uint4*>(raw + key * D + 16 * c);
+          const uint4 in = *reinterpret_cast<const uint4*>(sm + P::RK + 16 * i);
+          *reinterpret_cast<uint4*>(out + v_piece(key, 2 * c)) =
+              make_uint4(codes_f16(in.x & 0xffffu), codes_f16(in.x >> 16), codes_f16(in.y & 0xffffu), codes_f16(in.y >> 16));
+          *reinterpret_cast<uint4*>(out + v_piece(key, 2 * c + 1)) =
+              make_uint4(codes_f16(in.z & 0xffffu), codes_f16(in.z >> 16), codes_f16(in.w & 0xffffu), codes_f16(in.w >> 16));
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bars + B_KFULL + 8u * st);
+        mbar_arrive(bars + B_RKEMPTY);
+      }
+      // ---- V
+      if (!pr_wait(dead, p, bars + B_RVFULL, u & 1u, WHERE_COPY)) return;
+      if (!pr_wait(dead, p, bars + B_VEMPTY + 8u * st, ph ^ 1u, WHERE_COPY)) return;
+      bool any = false;
+      {
+        uint8_t* out = sm + P::V + st * P::TILE;
+#pragma unroll 4
+        for (int i = tw * 32 + lane; i < PR_T * PER; i += 128) {
+          const int key = i / PER, c = i - key * PER;
+          const float f = __shfl_sync(0xffffffffu, scale, 16 + (key >> 3));
+          const uint4 in = *reinterpret_cast<const uint4*>(sm + P::RV + 16 * i);
           const uint32_t x[4] = {in.x, in.y, in.z, in.w};
           uint32_t y[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            uint32_t h2;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(x[j >> 1] >> (16 * (j & 1)))));
+            const uint32_t h2 = codes_f16((x[j >> 1] >> (16 * (j & 1))) & 0xffffu);
             __half2 hv;
             memcpy(&hv, &h2, 4);
             const float2 fv = __half22float2(hv);
             y[j] = pack_bf16x2(fv.x * f, fv.y * f);
           }
           uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
-          if (v && masked) {
+          if (masked) {
             if (!key_seen_by_any(p, p0, p1, w.it.len, key0 + key)) {
               lo = hi = make_uint4(0u, 0u, 0u, 0u);
             } else if (has_not_finite16<__nv_bfloat16>(lo) || has_not_finite16<__nv_bfloat16>(hi)) {
@@ -463,13 +525,13 @@ __device__ void pr_turn(const PagedParams& p, Walk w, volatile int* dead, uint32
           *reinterpret_cast<uint4*>(out + v_piece(key, 2 * c)) = lo;
           *reinterpret_cast<uint4*>(out + v_piece(key, 2 * c + 1)) = hi;
         }
-        if (any) odd[seg & 7] = 1;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bars + (v ? B_VREADY : B_KFULL) + 8u * st);
-          mbar_arrive(bars + (v ? B_RVEMPTY : B_RKEMPTY));
-        }
+      }
+      if (any) odd[seg & 7] = 1;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bars + B_VREADY + 8u * st);
+        mbar_arrive(bars + B_RVEMPTY);
       }
       scale = scale_of(next_id);
     }
@@ -541,7 +603,7 @@ __device__ void pr_mma(const PagedParams& p, Walk w, volatile int* dead, uint32_
         values_done(u - 1);
       }
       if (opens) {
-        if (!pr_wait(dead, p, bars + B_QFULL, q_ph, WHERE_MMA)) goto done;
+        if (!pr_wait(dead, p, bars + (E8 ? B_QREADY : B_QFULL), q_ph, WHERE_MMA)) goto done;
         q_ph ^= 1u;
       }
       if (!pr_wait(dead, p, bars + B_KFULL + 8u * st, (u / PR_ST) & 1u, WHERE_MMA)) goto done;
@@ -555,7 +617,7 @@ __device__ void pr_mma(const PagedParams& p, Walk w, volatile int* dead, uint32_
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               tc_mma_bf16(scol, dq + ((16384u * a + 32u * kk) >> 4), dk + ((16384u * a + 32u * kk) >> 4),
-                          idesc(PR_T, false, HALF), (a | kk) ? 1u : 0u);
+                          idesc(PR_T, false, E8 || HALF), (a | kk) ? 1u : 0u);   // (8-bit: fp16 scores)
         }
         __syncwarp();
       }
@@ -601,22 +663,22 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
-// The weights 2^(c s - ref) of 64 scores as 16-bit pairs; returns their sum.
-template <class T>
-__device__ __forceinline__ float weights(const uint32_t (&sv)[2][32], uint32_t (&w)[32], float c, float nref) {
-  const uint64_t c2 = two(c, c), nref2 = two(nref, nref);
+// The weights 2^(c s - ref) of 32 scores as 16-bit pairs; returns their sum.
+// E8: ks has the key scales of the 4 groups of 8 keys, which c is multiplied by.
+template <class T, bool E8>
+__device__ __forceinline__ float weights(const uint32_t (&s)[32], uint32_t* w, float c, float nref, const float* ks) {
+  const uint64_t nref2 = two(nref, nref);
+  uint64_t c2 = two(c, c);
   uint64_t sum[2] = {two(0.f, 0.f), two(0.f, 0.f)};
 #pragma unroll
-  for (int q = 0; q < 32; ++q) {
-    const uint32_t (&s)[32] = sv[q >> 4];
+  for (int q = 0; q < 16; ++q) {
+    if (E8 && (q & 3) == 0) {
+      float cg = c * ks[q >> 2];
+      if (cg == 0.f) cg = 1e-37f;              // a score of -infinity (masked) stays one
+      c2 = two(cg, cg);
+    }
     float x, y;
-    split(fma2(two(__uint_as_float(s[2 * (q & 15)]), __uint_as_float(s[2 * (q & 15) + 1])), c2, nref2), x, y);
+    split(fma2(two(__uint_as_float(s[2 * q]), __uint_as_float(s[2 * q + 1])), c2, nref2), x, y);
     x = pg_ex2(x);
     y = pg_ex2(y);
     sum[q & 1] = add2(sum[q & 1], two(x, y));
@@ -626,14 +688,16 @@ __device__ __forceinline__ float weights(const uint32_t (&sv)[2][32], uint32_t (
   split(add2(sum[0], sum[1]), s0, s1);
   return s0 + s1;
 }
-__device__ __forceinline__ float largest(const uint32_t (&sv)[2][32]) {
+template <bool E8>
+__device__ __forceinline__ float largest(const uint32_t (&s)[32], const float* ks) {
   float m[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m[j] = __uint_as_float(sv[j & 1][j >> 1]);
+  for (int j = 0; j < 8; ++j) m[j] = -INFINITY;
 #pragma unroll
-  for (int q = 4; q < 32; ++q)
-#pragma unroll
-    for (int a = 0; a < 2; ++a) m[a + 2 * (q & 3)] = fmaxf(m[a + 2 * (q & 3)], __uint_as_float(sv[a][q]));
+  for (int q = 0; q < 32; ++q) {
+    const float x = __uint_as_float(s[q]);
+    m[q & 7] = fmaxf(m[q & 7], E8 ? x * ks[q >> 3] : x);
+  }
 #pragma unroll
   for (int j = 0; j < 4; ++j) m[j] = fmaxf(m[j], m[j + 4]);
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
@@ -688,7 +752,7 @@ __device__ __forceinline__ void add_not_finite(const PagedParams& p, const Walk&
 }
 
 template <class T, bool E8, int D>
-__device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uint32_t bars,
+__device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uint32_t bars, const uint8_t* sm,
                            uint32_t tmem, volatile int* odd) {
   // fp16 weights are taken 2^7 high, so that small ones keep their bits, and stay below 2^15
   constexpr bool HALF = std::is_same<T, __half>::value;
@@ -699,7 +763,7 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uin
   const uint32_t scol = tmem + lanes + static_cast<uint32_t>(g) * PR_T, ocol = scol + PR_O;
   const int toks = PR_T / p.group;
   const int my_tok = row / p.group, my_head = row - my_tok * p.group;
-  const float c = p.scale_log2;
+  float c = p.scale_log2;
   uint32_t u = 0, o_ph = 0;
   const long long begin = w.x;
   if (threadIdx.x == 32 * W_SOFT) p.cut[blockIdx.x].u0 = -1;
@@ -719,29 +783,53 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uin
       const bool masked = g1 >= g0 && !all_seen(p, g0, g1, it.len, key0, PR_T);
       if (!pr_wait(dead, p, bars + B_S + 8u * g, u & 1u, WHERE_EPILOGUE)) return;
       tc_fence_after();
+      if (E8 && k == w.k0) {
+        const int ex = reinterpret_cast<const signed char*>(sm + Plan<E8, D>::QEXP)[(seg & 1) * 2 * PR_T + g * PR_T + row];
+        c = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
+      }
       // Half the row at a time, its weights handed over once written: the products start on the
       // first while the second is being computed.  (One copy of this code for both halves, 64
       // scores in registers: with the whole row unrolled the instructions did not come fast enough.)
       float s_a = 0.f;
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
-        uint32_t sv[2][32], wt[32];
-        tc_ld_32x32b_x32(scol + 64u * half, sv[0]);
-        tc_ld_32x32b_x32(scol + 64u * half + 32u, sv[1]);
-        tc_wait_ld_regs(sv[0]);
-        reg_fence(sv[1]);
-        if (masked && real) {
-          const int hi = (p.causal ? min(it.len, pos + 1) : it.len) - key0;
-          const int lo = p.window > 0 ? pos - p.window + 1 - key0 : 0, snk = p.sinks - key0;
-#pragma unroll
-          for (int a = 0; a < 2; ++a) {
+        const float* ks = E8 ? reinterpret_cast<const float*>(sm + Plan<E8, D>::KSC) + (u & 3u) * 16 + 8 * half : nullptr;
+        // 16-bit caches hold the half's 64 scores; with 8-bit ones there are four more warps and
+        // fewer registers: 32 scores at a time, read again when the reference moves
+        constexpr int HELD = E8 ? 1 : 2;
+        uint32_t sv[HELD][32], wt[32];
+        auto fetch = [&](int a) {
+          uint32_t (&s)[32] = sv[a & (HELD - 1)];
+          tc_ld_32x32b_x32(scol + 64u * half + 32u * a, s);
+        };
+        auto cover = [&](int a) {
+          uint32_t (&s)[32] = sv[a & (HELD - 1)];
+          if (masked && real) {
+            const int hi = (p.causal ? min(it.len, pos + 1) : it.len) - key0;
             uint32_t see = below(hi, 2 * half + a);
-            if (p.window > 0) see &= ~below(lo, 2 * half + a) | below(snk, 2 * half + a);
+            if (p.window > 0)
+              see &= ~below(pos - p.window + 1 - key0, 2 * half + a) | below(p.sinks - key0, 2 * half + a);
 #pragma unroll
             for (int q = 0; q < 32; ++q)
-              if (!(see & (1u << q))) sv[a][q] = 0xff800000u;      // -inf
+              if (!(see & (1u << q))) s[q] = 0xff800000u;          // -inf
           }
+        };
+        if (!E8) {
+          fetch(0);
+          fetch(1);
+          tc_wait_ld_regs(sv[0]);
+          reg_fence(sv[HELD - 1]);
+          cover(0);
+          cover(1);
         }
+        auto scores = [&](int a) -> const uint32_t (&)[32] {
+          if (E8) {
+            fetch(a);
+            tc_wait_ld_regs(sv[0]);
+            cover(a);
+          }
+          return sv[a & (HELD - 1)];
+        };
         // No maximum is taken of a tile: the reference m, the largest of the first scores, stands as
         // long as no sum of weights passes LIMIT, which bounds each weight too.
         bool move = !ready;
@@ -751,7 +839,8 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uin
             // m to the largest score so far, and what has been summed along with it.  O_g is settled
             // before P_g(u) is handed over, since S_g(u) complete implies the product of tile u-1
             // is; after the first half has been, once that half's product is complete.
-            const float mn = fmaxf(m, largest(sv) * c);
+            float mn = largest<E8>(scores(0), ks);
+            mn = fmaxf(m, fmaxf(mn, largest<E8>(scores(1), E8 ? ks + 4 : ks)) * c);
             float factor = 1.f;
             if (mn > m) {
               if (m != -INFINITY) factor = pg_ex2(m - mn);
@@ -776,7 +865,9 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uin
               }
             }
           }
-          sum = weights<T>(sv, wt, c, SHIFT - (m == -INFINITY ? 0.f : m));
+          const float nref = SHIFT - (m == -INFINITY ? 0.f : m);
+          sum = weights<T, E8>(scores(0), wt, c, nref, ks);
+          sum += weights<T, E8>(scores(1), wt + 16, c, nref, E8 ? ks + 4 : ks);
           move = __any_sync(0xffffffffu, sum > LIMIT);
           if (!move) break;
         }
@@ -866,6 +957,7 @@ __global__ void __launch_bounds__(Plan<E8, D>::THREADS, 1)
     *dead = 0;
     for (int i = 0; i < 8; ++i) odd[i] = 0;
     mbar_init(bars + B_QFULL, 1);
+    mbar_init(bars + B_QREADY, 4);
     mbar_init(bars + B_QEMPTY, 2);                          // both query tiles' MMA warps
     for (int s = 0; s < PR_ST; ++s) {
       mbar_init(bars + B_KFULL + 8u * s, E8 ? 4 : 1);
@@ -924,7 +1016,7 @@ __global__ void __launch_bounds__(Plan<E8, D>::THREADS, 1)
   if (static_cast<int>(blockIdx.x) < deal.c) {
     const Walk w(p, entries, deal);
     if (warp >= W_SOFT && warp < W_SOFT + 8) {
-      pr_softmax<T, E8, D>(p, w, dead, bars, tmem, odd);
+      pr_softmax<T, E8, D>(p, w, dead, bars, sm, tmem, odd);
     } else {
       if (warp == W_LOAD) pr_load<E8, D>(p, w, dead, bars, base);
       else if (warp == W_MMA || warp == W_MMA1)
