@@ -20,9 +20,9 @@
 //   0, 3      issue the MMAs of query tile 0 / 1: O_i += P_i V of the tile before, in two halves
 //             as their weights appear, then S_i = Q_i K^T.  A warp each, because the issuing
 //             warp's own instructions take as long as the products they start
-//   12-15     8-bit caches only: turn the codes of K into fp16 (one conversion for two, exact; the
-//             scale multiplies the scores) and those of V into bf16, scale and all; and an
-//             item's queries into fp16, each row times a power of two
+//   12-15     8-bit caches only: turn codes into fp16 (one conversion for two, exact; the scales
+//             multiply the scores and the weights), and an item's queries, each row times a
+//             power of two
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -51,8 +51,8 @@ struct Plan {
   static constexpr uint32_t Q = 0, K = 2 * TILE, V = K + PR_ST * TILE, RK = V + PR_ST * TILE, RV = RK + RAW;
   static constexpr uint32_t BARS = RV + RAW;
   static constexpr uint32_t QEXP = BARS + 384;             // 8-bit: exponents of the query rows' factors,
-  static constexpr uint32_t KSC = QEXP + (E8 ? 512 : 0);   // by segment parity; key scales of four tiles
-  static constexpr int SMEM = 1024 + KSC + (E8 ? 256 : 0);
+  static constexpr uint32_t SCALES = QEXP + (E8 ? 512 : 0);  // by segment parity; scales of four tiles: 16 of
+  static constexpr int SMEM = 1024 + SCALES + (E8 ? 512 : 0);  // keys and 16 of values, one for 8 tokens
   static_assert(SMEM <= 232448, "dynamic shared memory per block");
 };
 // barriers (byte offsets)
@@ -407,11 +407,50 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t two_codes) {   // two e4m
   return h;
 }
 
-// Warps 12-15 (8-bit caches): an item's queries, then K and V of every tile, with the clearing of
-// pr_load_v.  A lane takes 16 codes of a row at a time.
+// A tile of codes to fp16, in the order the products read.  A lane takes 8 codes of a row at a time:
+// eight lanes then store to eight different 16-byte columns (with 16 codes a lane, two to each).
 template <int D>
-__device__ void pr_turn(const PagedParams& p, Walk w, volatile int* dead, uint32_t bars, uint32_t base, uint8_t* sm,
-                        volatile int* odd) {
+struct Turn {
+  static constexpr int PER = D / 8, ROWS = 128 / PER, N = PR_T / ROWS;   // lanes of a row, rows of a step, steps
+  uint2 x[N];
+  __device__ __forceinline__ void get(const uint8_t* in, int tw, int lane) {
+    const uint8_t* from = in + (tw * (32 / PER) + lane / PER) * D + 8 * (lane % PER);
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = *reinterpret_cast<const uint2*>(from + j * ROWS * D);
+  }
+  __device__ __forceinline__ void put(uint8_t* out, int tw, int lane) const {
+    uint8_t* to = out + v_piece(tw * (32 / PER) + lane / PER, lane % PER);
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      *reinterpret_cast<uint4*>(to + j * ROWS * 128) = make_uint4(
+          codes_f16(x[j].x & 0xffffu), codes_f16(x[j].x >> 16), codes_f16(x[j].y & 0xffffu), codes_f16(x[j].y >> 16));
+  }
+  // Over what put stored: 0 for keys that no row sees and for what is not finite (true if there was any).
+  __device__ __forceinline__ static bool clear(const PagedParams& p, int p0, int p1, int len, int key0, uint8_t* out,
+                                               int tw, int lane) {
+    const int row = tw * (32 / PER) + lane / PER;
+    uint8_t* to = out + v_piece(row, lane % PER);
+    bool any = false;
+#pragma unroll 1
+    for (int j = 0; j < N; ++j) {
+      uint4* at = reinterpret_cast<uint4*>(to + j * ROWS * 128);
+      uint4 v = *at;
+      if (!key_seen_by_any(p, p0, p1, len, key0 + row + j * ROWS)) {
+        *at = make_uint4(0u, 0u, 0u, 0u);
+      } else if (has_not_finite16<__half>(v)) {
+        clear_not_finite16<__half>(v);
+        *at = v;
+        any = true;
+      }
+    }
+    return any;
+  }
+};
+
+// Warps 12-15 (8-bit caches): an item's queries, then K and V of every tile, with the clearing of
+// pr_load_v.  Codes go to registers first, so that the next ones can come while these wait for room.
+template <int D>
+__device__ void pr_turn(const PagedParams& p, Walk w, volatile int* dead, uint32_t bars, uint8_t* sm, volatile int* odd) {
   using P = Plan<true, D>;
   const int lane = threadIdx.x & 31, tw = (threadIdx.x >> 5) - W_TURN;
   const int used = PR_T / p.group * p.group;               // query rows of a tile that are loaded
@@ -419,29 +458,14 @@ __device__ void pr_turn(const PagedParams& p, Walk w, volatile int* dead, uint32
   for (int seg = 0; w.next(p); ++seg) {
     int p0, p1;
     item_span(p, w.it, p0, p1);
-    if (lane == 0 && tw == 0) odd[(seg + 1) & 7] = 0;
-    // lane i: the scale of keys 8 (i % 16) .. + 7 of a tile, K's for i < 16, V's above; keys no row
-    // sees may have any, and none of the tile's scores is multiplied by 0 (they may be -inf)
-    const int n_pages = min(p.s.max_pages, ((w.it.len - 1) >> p.c.page_log2) + 1);
-    const int* table = p.s.pages + w.it.b * p.s.pages_stride;
-    auto id_of = [&](int k) {
-      const int key = w.it.t.tile(k) * PR_T + 8 * (lane & 15), lp = key >> p.c.page_log2;
-      if (lp >= n_pages || !keys_seen(p, p0, p1, w.it.len, key, 8)) return -1;
-      const int id = table[lp];
-      return id < p.c.n_pages ? id : -1;
-    };
-    auto scale_of = [&](int id) {
-      if (id < 0) return 1.f;
-      return (lane < 16 ? p.c.k_scale : p.c.v_scale)[static_cast<long long>(id) * p.c.heads + w.h];
-    };
-    float scale = scale_of(id_of(w.k0));
+    if (lane == 0 && tw == 0) odd[(seg + 2) & 7] = 0;      // (pr_scales may be two tiles ahead)
     // queries: bf16 -> fp16 in place, the row's largest magnitude brought to 2^10 .. 2^11 (below
     // 2^-100 it stays smaller)
     if (!pr_wait(dead, p, bars + B_QFULL, seg & 1u, WHERE_COPY)) return;
     {
       constexpr int PER = D / 8, ROWS = 32 / PER;          // lanes of a row, rows of a step
       const int ch = lane % PER;
-#pragma unroll 2
+#pragma unroll 4
       for (int r0 = tw * ROWS; r0 < 2 * PR_T; r0 += 4 * ROWS) {
         const int r = r0 + lane / PER, row = r & (PR_T - 1);
         uint4* at = reinterpret_cast<uint4*>(sm + P::Q + (r / PR_T) * P::TILE + v_piece(row, ch));
@@ -464,76 +488,69 @@ __device__ void pr_turn(const PagedParams& p, Walk w, volatile int* dead, uint32
     }
     for (int k = w.k0; k < w.k1; ++k, ++u) {
       const uint32_t st = u % PR_ST, ph = (u / PR_ST) & 1u;
-      const int next_id = k + 1 < w.k1 ? id_of(k + 1) : -1;
-      const int key0 = w.it.t.tile(k) * PR_T;
-      const bool masked = !all_seen(p, p0, p1, w.it.len, key0, PR_T);
-      constexpr int PER = D / 16;                          // pieces of 16 codes in a row
+      Turn<D> turn;
       // ---- K
       if (!pr_wait(dead, p, bars + B_RKFULL, u & 1u, WHERE_COPY)) return;
+      turn.get(sm + P::RK, tw, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + B_RKEMPTY);
       if (!pr_wait(dead, p, bars + B_KEMPTY + 8u * st, ph ^ 1u, WHERE_COPY)) return;
-      if (tw == 0 && lane < 16)
-        reinterpret_cast<float*>(sm + P::KSC)[(u & 3u) * 16 + lane] = scale == 0.f ? 1e-30f : scale;
-      {
-        uint8_t* out = sm + P::K + st * P::TILE;
-#pragma unroll 4
-        for (int i = tw * 32 + lane; i < PR_T * PER; i += 128) {
-          const int key = i / PER, c = i - key * PER;
-          const uint4 in = *reinterpret_cast<const uint4*>(sm + P::RK + 16 * i);
-          *reinterpret_cast<uint4*>(out + v_piece(key, 2 * c)) =
-              make_uint4(codes_f16(in.x & 0xffffu), codes_f16(in.x >> 16), codes_f16(in.y & 0xffffu), codes_f16(in.y >> 16));
-          *reinterpret_cast<uint4*>(out + v_piece(key, 2 * c + 1)) =
-              make_uint4(codes_f16(in.z & 0xffffu), codes_f16(in.z >> 16), codes_f16(in.w & 0xffffu), codes_f16(in.w >> 16));
-        }
-      }
+      turn.put(sm + P::K + st * P::TILE, tw, lane);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bars + B_KFULL + 8u * st);
-        mbar_arrive(bars + B_RKEMPTY);
-      }
+      if (lane == 0) mbar_arrive(bars + B_KFULL + 8u * st);
       // ---- V
       if (!pr_wait(dead, p, bars + B_RVFULL, u & 1u, WHERE_COPY)) return;
+      turn.get(sm + P::RV, tw, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + B_RVEMPTY);
       if (!pr_wait(dead, p, bars + B_VEMPTY + 8u * st, ph ^ 1u, WHERE_COPY)) return;
-      bool any = false;
-      {
-        uint8_t* out = sm + P::V + st * P::TILE;
-#pragma unroll 4
-        for (int i = tw * 32 + lane; i < PR_T * PER; i += 128) {
-          const int key = i / PER, c = i - key * PER;
-          const float f = __shfl_sync(0xffffffffu, scale, 16 + (key >> 3));
-          const uint4 in = *reinterpret_cast<const uint4*>(sm + P::RV + 16 * i);
-          const uint32_t x[4] = {in.x, in.y, in.z, in.w};
-          uint32_t y[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint32_t h2 = codes_f16((x[j >> 1] >> (16 * (j & 1))) & 0xffffu);
-            __half2 hv;
-            memcpy(&hv, &h2, 4);
-            const float2 fv = __half22float2(hv);
-            y[j] = pack_bf16x2(fv.x * f, fv.y * f);
-          }
-          uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
-          if (masked) {
-            if (!key_seen_by_any(p, p0, p1, w.it.len, key0 + key)) {
-              lo = hi = make_uint4(0u, 0u, 0u, 0u);
-            } else if (has_not_finite16<__nv_bfloat16>(lo) || has_not_finite16<__nv_bfloat16>(hi)) {
-              clear_not_finite16<__nv_bfloat16>(lo);
-              clear_not_finite16<__nv_bfloat16>(hi);
-              any = true;
-            }
-          }
-          *reinterpret_cast<uint4*>(out + v_piece(key, 2 * c)) = lo;
-          *reinterpret_cast<uint4*>(out + v_piece(key, 2 * c + 1)) = hi;
-        }
-      }
-      if (any) odd[seg & 7] = 1;
+      uint8_t* out = sm + P::V + st * P::TILE;
+      turn.put(out, tw, lane);
+      const int key0 = w.it.t.tile(k) * PR_T;
+      if (!all_seen(p, p0, p1, w.it.len, key0, PR_T) && Turn<D>::clear(p, p0, p1, w.it.len, key0, out, tw, lane))
+        odd[seg & 7] = 1;
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bars + B_VREADY + 8u * st);
-        mbar_arrive(bars + B_RVEMPTY);
-      }
-      scale = scale_of(next_id);
+      if (lane == 0) mbar_arrive(bars + B_VREADY + 8u * st);
+    }
+  }
+}
+
+// Warp 2 (8-bit caches): the scales of every tile, with its K: 16 of keys, 16 of values, one for 8
+// tokens.  Those of tokens that no row sees may be anything; 1 stands in for them.
+template <int D>
+__device__ void pr_scales(const PagedParams& p, Walk w, volatile int* dead, uint32_t bars, uint8_t* sm, volatile int* odd) {
+  using P = Plan<true, D>;
+  const int lane = threadIdx.x & 31;
+  uint32_t u = 0;
+  for (int seg = 0; w.next(p); ++seg) {
+    int p0, p1;
+    item_span(p, w.it, p0, p1);
+    const int n_pages = min(p.s.max_pages, ((w.it.len - 1) >> p.c.page_log2) + 1);
+    const int* table = p.s.pages + w.it.b * p.s.pages_stride;
+    auto id_of = [&](int k) {
+      const int key = w.it.t.tile(k) * PR_T + 8 * (lane & 15), lp = key >> p.c.page_log2;
+      if (k >= w.k1 || lp >= n_pages || !keys_seen(p, p0, p1, w.it.len, key, 8)) return -1;
+      const int id = table[lp];
+      return id < p.c.n_pages ? id : -1;
+    };
+    auto scale_of = [&](int id) {
+      return id < 0 ? 1.f : (lane < 16 ? p.c.k_scale : p.c.v_scale)[static_cast<long long>(id) * p.c.heads + w.h];
+    };
+    float scale = scale_of(id_of(w.k0));
+    int id = id_of(w.k0 + 1);
+    for (int k = w.k0; k < w.k1; ++k, ++u) {
+      const uint32_t st = u % PR_ST, ph = (u / PR_ST) & 1u;
+      const float next = scale_of(id);
+      id = id_of(k + 2);
+      if (!pr_wait(dead, p, bars + B_KEMPTY + 8u * st, ph ^ 1u, WHERE_COPY)) return;
+      const bool bad = lane >= 16 && !(fabsf(scale) <= 3.4028235e38f);
+      if (bad) odd[seg & 7] = 1;                           // rows that see these values: NaN, when stored
+      reinterpret_cast<float*>(sm + P::SCALES)[(u & 3u) * 32 + lane] = bad ? 0.f : scale;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + B_KFULL + 8u * st);
+      scale = next;
     }
   }
 }
@@ -580,7 +597,7 @@ __device__ void pr_mma(const PagedParams& p, Walk w, volatile int* dead, uint32_
       if (elect_one_sync()) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          tc_mma_bf16_ts(ocol, scol + 32u * half + 8u * k, dv + ((8192u * half + 2048u * k) >> 4), idesc(D, true, HALF),
+          tc_mma_bf16_ts(ocol, scol + 32u * half + 8u * k, dv + ((8192u * half + 2048u * k) >> 4), idesc(D, true, E8 || HALF),
                          (!first || half || k) ? 1u : 0u);
       }
       __syncwarp();
@@ -617,7 +634,7 @@ __device__ void pr_mma(const PagedParams& p, Walk w, volatile int* dead, uint32_
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               tc_mma_bf16(scol, dq + ((16384u * a + 32u * kk) >> 4), dk + ((16384u * a + 32u * kk) >> 4),
-                          idesc(PR_T, false, E8 || HALF), (a | kk) ? 1u : 0u);   // (8-bit: fp16 scores)
+                          idesc(PR_T, false, E8 || HALF), (a | kk) ? 1u : 0u);
         }
         __syncwarp();
       }
@@ -658,49 +675,81 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// The weights 2^(c s - ref) of 32 scores as 16-bit pairs; returns their sum.
-// E8: ks has the key scales of the 4 groups of 8 keys, which c is multiplied by.
+// The weights 2^(c s + nref) of 32 scores as 16-bit pairs; returns their sum.  8-bit caches: scales
+// has those of the four groups of 8 keys, which c is multiplied by, and from 16 on those of their
+// values; the weight of a value is the weight times its scale and F, summed in sum_v.
 template <class T, bool E8>
-__device__ __forceinline__ float weights(const uint32_t (&s)[32], uint32_t* w, float c, float nref, const float* ks) {
+__device__ __forceinline__ float weights(const uint32_t (&s)[32], uint32_t* w, float c, float nref, const float* scales,
+                                         float F, float& sum_v) {
   const uint64_t nref2 = two(nref, nref);
-  uint64_t c2 = two(c, c);
+  float total = 0.f;
   uint64_t sum[2] = {two(0.f, 0.f), two(0.f, 0.f)};
 #pragma unroll
-  for (int q = 0; q < 16; ++q) {
-    if (E8 && (q & 3) == 0) {
-      float cg = c * ks[q >> 2];
+  for (int g = 0; g < 4; ++g) {
+    float cg = c, vg = 1.f;
+    if (E8) {
+      cg *= scales[g];
       if (cg == 0.f) cg = 1e-37f;              // a score of -infinity (masked) stays one
-      c2 = two(cg, cg);
+      vg = fminf(fmaxf(F * scales[16 + g], -3e38f), 3e38f);
     }
-    float x, y;
-    split(fma2(two(__uint_as_float(s[2 * q]), __uint_as_float(s[2 * q + 1])), c2, nref2), x, y);
-    x = pg_ex2(x);
-    y = pg_ex2(y);
-    sum[q & 1] = add2(sum[q & 1], two(x, y));
-    w[q] = std::is_same<T, __half>::value ? Piece<__half>::pack(x, y) : pack_bf16x2(x, y);
+    const uint64_t c2 = two(cg, cg), v2 = two(vg, vg);
+#pragma unroll
+    for (int q = 4 * g; q < 4 * g + 4; ++q) {
+      float x, y;
+      split(fma2(two(__uint_as_float(s[2 * q]), __uint_as_float(s[2 * q + 1])), c2, nref2), x, y);
+      x = pg_ex2(x);
+      y = pg_ex2(y);
+      const uint64_t xy = two(x, y);
+      sum[q & 1] = E8 && q < 4 * g + 2 ? xy : add2(sum[q & 1], xy);
+      if (E8) split(mul2(xy, v2), x, y);
+      w[q] = E8 || std::is_same<T, __half>::value ? Piece<__half>::pack(x, y) : pack_bf16x2(x, y);
+    }
+    if (E8) {
+      float x, y;
+      split(add2(sum[0], sum[1]), x, y);
+      total += x + y;
+      sum_v = fmaf(x + y, fabsf(vg), sum_v);
+    }
   }
+  if (E8) return total;
   float s0, s1;
   split(add2(sum[0], sum[1]), s0, s1);
   return s0 + s1;
 }
+// Raises m to the largest of 32 scores times c and, for 8-bit caches, mv to the largest of those plus
+// the logarithm of the value's scale.
 template <bool E8>
-__device__ __forceinline__ float largest(const uint32_t (&s)[32], const float* ks) {
-  float m[8];
+__device__ __forceinline__ void largest(const uint32_t (&s)[32], float c, const float* scales, float& m, float& mv) {
+  float top[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m[j] = -INFINITY;
+  for (int g = 0; g < 8; ++g) top[g] = -INFINITY;
+  if (E8) {
 #pragma unroll
-  for (int q = 0; q < 32; ++q) {
-    const float x = __uint_as_float(s[q]);
-    m[q & 7] = fmaxf(m[q & 7], E8 ? x * ks[q >> 3] : x);
+    for (int g = 0; g < 4; ++g) {
+      float cg = c * scales[g];
+      if (cg == 0.f) cg = 1e-37f;
+#pragma unroll
+      for (int q = 8 * g; q < 8 * g + 8; ++q) top[g] = fmaxf(top[g], __uint_as_float(s[q]) * cg);
+      mv = fmaxf(mv, top[g] + __log2f(fabsf(scales[16 + g])));
+    }
+    m = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+  } else {
+#pragma unroll
+    for (int q = 0; q < 32; ++q) top[q & 7] = fmaxf(top[q & 7], __uint_as_float(s[q]));
+#pragma unroll
+    for (int g = 0; g < 4; ++g) top[g] = fmaxf(top[g], top[g + 4]);
+    m = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c);
   }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) m[j] = fmaxf(m[j], m[j + 4]);
-  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 // Bits 0 .. 31: keys 32 a .. 32 a + 31 that are below n.
 __device__ __forceinline__ uint32_t below(int n, int a) {
@@ -734,7 +783,7 @@ __device__ __forceinline__ void add_not_finite(const PagedParams& p, const Walk&
   item_span(p, w.it, p0, p1);
   for (int k = w.k0; k < w.k1; ++k) {
     const int key0 = w.it.t.tile(k) * PR_T;
-    if (all_seen(p, p0, p1, w.it.len, key0, PR_T)) continue;
+    if (!E8 && all_seen(p, p0, p1, w.it.len, key0, PR_T)) continue;   // (8-bit: scales, of any tile)
     for (int key = key0; key < key0 + PR_T; ++key) {
       if (!key_seen(p, pos, w.it.len, key)) continue;
       int page;
@@ -777,6 +826,10 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uin
     const int g0 = it.len - it.n + it.tok0 + g * toks;       // positions of the tile's real rows
     const int g1 = min(g0 + toks, it.len) - 1;
     float m = -INFINITY, l = 0.f;
+    // 8-bit caches: a weight meets its value's code as fp16(weight x scale x F), F = 2^f; f brings
+    // the largest so far (mv, its logarithm) to 2^2, and moves like m, on its own.  (At most 100, so
+    // that its product with a scale below 2^27 is finite, and scales from 2^-100 on keep their bits.)
+    float mv = -INFINITY, f = 0.f, F = 1.f;
     bool ready = false;                                    // every row of the warp has a reference
     for (int k = w.k0; k < w.k1; ++k, ++u) {
       const int key0 = it.t.tile(k) * PR_T;
@@ -793,7 +846,7 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uin
       float s_a = 0.f;
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
-        const float* ks = E8 ? reinterpret_cast<const float*>(sm + Plan<E8, D>::KSC) + (u & 3u) * 16 + 8 * half : nullptr;
+        const float* scales = E8 ? reinterpret_cast<const float*>(sm + Plan<E8, D>::SCALES) + (u & 3u) * 32 + 8 * half : nullptr;
         // 16-bit caches hold the half's 64 scores; with 8-bit ones there are four more warps and
         // fewer registers: 32 scores at a time, read again when the reference moves
         constexpr int HELD = E8 ? 1 : 2;
@@ -839,17 +892,24 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uin
             // m to the largest score so far, and what has been summed along with it.  O_g is settled
             // before P_g(u) is handed over, since S_g(u) complete implies the product of tile u-1
             // is; after the first half has been, once that half's product is complete.
-            float mn = largest<E8>(scores(0), ks);
-            mn = fmaxf(m, fmaxf(mn, largest<E8>(scores(1), E8 ? ks + 4 : ks)) * c);
-            float factor = 1.f;
-            if (mn > m) {
-              if (m != -INFINITY) factor = pg_ex2(m - mn);
+            float mn = m;
+            largest<E8>(scores(0), c, scales, mn, mv);
+            largest<E8>(scores(1), c, E8 ? scales + 4 : scales, mn, mv);
+            float factor = 1.f, factor_o = 1.f;
+            const float f_was = f;
+            if (E8) f = fminf(fmaxf(mn - mv + 2.f, -126.f), 100.f);
+            if (mn > m || (E8 && f != f_was)) {
+              if (m != -INFINITY) {
+                factor = pg_ex2(m - mn);
+                factor_o = E8 ? pg_ex2(m - mn + f - f_was) : factor;
+              }
               m = mn;
             }
+            if (E8) F = pg_ex2(f);
             l *= factor;
             s_a *= factor;
             ready = __all_sync(0xffffffffu, m != -INFINITY);
-            if ((half != 0 || k > w.k0) && __any_sync(0xffffffffu, factor != 1.f)) {
+            if ((half != 0 || k > w.k0) && __any_sync(0xffffffffu, factor_o != 1.f)) {
               if (half != 0) {
                 if (!pr_wait(dead, p, bars + B_HALF + 8u * g, u & 1u, WHERE_EPILOGUE)) return;
                 tc_fence_after();
@@ -860,15 +920,16 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uin
                 tc_ld_32x32b_x16(ocol + 16u * a, v);
                 tc_wait_ld();
 #pragma unroll
-                for (int q = 0; q < 16; ++q) v[q] = __float_as_uint(__uint_as_float(v[q]) * factor);
+                for (int q = 0; q < 16; ++q) v[q] = __float_as_uint(__uint_as_float(v[q]) * factor_o);
                 tc_st_32x32b_x16(ocol + 16u * a, v);
               }
             }
           }
           const float nref = SHIFT - (m == -INFINITY ? 0.f : m);
-          sum = weights<T, E8>(scores(0), wt, c, nref, ks);
-          sum += weights<T, E8>(scores(1), wt + 16, c, nref, E8 ? ks + 4 : ks);
-          move = __any_sync(0xffffffffu, sum > LIMIT);
+          float sum_v = 0.f;
+          sum = weights<T, E8>(scores(0), wt, c, nref, scales, F, sum_v);
+          sum += weights<T, E8>(scores(1), wt + 16, c, nref, E8 ? scales + 4 : scales, F, sum_v);
+          move = __any_sync(0xffffffffu, sum > LIMIT || (E8 && sum_v > 32768.f));
           if (!move) break;
         }
         tc_st_32x32b_x32(scol + 32u * half, wt);
@@ -883,7 +944,7 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uin
     if (!pr_wait(dead, p, bars + B_O + 8u * g, o_ph, WHERE_EPILOGUE)) return;
     o_ph ^= 1u;
     tc_fence_after();
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float inv = l == 0.f ? 0.f : 1.f / l, inv_f = E8 ? pg_ex2(-f) : 1.f;
     const float lse2 = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) + log2f(l) - SHIFT;
     const int head = w.h * p.group + my_head;
     const long long t = it.row0 + tok;
@@ -909,7 +970,7 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uin
       tc_wait_ld();
       float f[32];
 #pragma unroll
-      for (int q = 0; q < 32; ++q) f[q] = __uint_as_float(v[q]) * inv;
+      for (int q = 0; q < 32; ++q) f[q] = (E8 ? __uint_as_float(v[q]) * inv_f : __uint_as_float(v[q])) * inv;
       if (add && real) add_not_finite<T, E8>(p, w, pos, 32 * a, f);
       __syncwarp();
       uint4 out[4];
@@ -960,7 +1021,7 @@ __global__ void __launch_bounds__(Plan<E8, D>::THREADS, 1)
     mbar_init(bars + B_QREADY, 4);
     mbar_init(bars + B_QEMPTY, 2);                          // both query tiles' MMA warps
     for (int s = 0; s < PR_ST; ++s) {
-      mbar_init(bars + B_KFULL + 8u * s, E8 ? 4 : 1);
+      mbar_init(bars + B_KFULL + 8u * s, E8 ? 5 : 1);          // 8-bit: the turning warps, the scales
       mbar_init(bars + B_KEMPTY + 8u * s, 2);
       mbar_init(bars + B_VFULL + 8u * s, 1);
       mbar_init(bars + B_VEMPTY + 8u * s, 2);
@@ -1022,7 +1083,8 @@ __global__ void __launch_bounds__(Plan<E8, D>::THREADS, 1)
       else if (warp == W_MMA || warp == W_MMA1)
         pr_mma<T, E8, D>(p, w, dead, bars, base, tmem, warp == W_MMA1);
       else if (!E8 && warp == W_LOADV) pr_load_v<T, D>(p, w, dead, bars, base, sm, odd);
-      else if (E8 && warp >= W_TURN) pr_turn<D>(p, w, dead, bars, base, sm, odd);
+      else if (E8 && warp == W_LOADV) pr_scales<D>(p, w, dead, bars, sm, odd);
+      else if (E8 && warp >= W_TURN) pr_turn<D>(p, w, dead, bars, sm, odd);
     }
     __syncwarp();
   }

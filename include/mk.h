@@ -492,7 +492,7 @@ size_t mk_paged_attention_workspace_size(long long tokens, int heads_q, int head
  * not written.  The cache is of q's type, or MK_E4M3 with MK_BF16 q.  What lies
  * in slots no row of a tile sees (stale pages, NaN) does not reach the result.
  * Sums are fp32; the weights are rounded to q's type for the products with
- * the values (to fp16 in decode steps over 8-bit caches).
+ * the values (to fp16 over 8-bit caches).
  * max_q: no sequence has more new tokens than this (0: not known).  It chooses
  * kernels; a wrong value costs time, not results.  Sequence lengths stay on the
  * device.  A page outside the cache or a length past the table reads as zeros
