@@ -19,7 +19,9 @@
 //     column groups share the operands of K and V, on eight warps;
 //   * the warps' results are joined in shared memory at the end of a run's part of a unit;
 //   * units cut by a run's end leave normalised fp32 partial rows with their
-//     log2 sums, joined by a second, programmatically dependent launch.
+//     log2 sums; the last of their CTAs to be done joins them, in the order of
+//     the runs, so the result does not depend on which one it is.  (A second,
+//     programmatically dependent launch for that took 3 to 5 us more a call.)
 // 8-bit caches: codes become fp16, exactly (the fp8 form of mma.sync does the same conversions
 // inside, with more instructions); the query row is scaled by a power of two to fit fp16 (bf16 has
 // fewer bits), the key scale multiplies the scores, the value scale the weights, and those
@@ -242,6 +244,8 @@ struct Work {
   int first;                           // this warp's first tile of it
   float* merge;                        // the join buffer, and maximum, sum and value factor of
   float* ml;                           // every warp's rows
+  const Deal& deal;
+  volatile int* share;                 // the CTAs whose partial rows are this one's to join
 };
 
 // In a tile that not every row sees whole: 0 * NaN is NaN, so values no row sees (past the end,
@@ -624,12 +628,11 @@ __device__ __forceinline__ void consume(const PagedParams& p, const Segment& g, 
     barrier();
   }
   const int prow = g.rg * S::ROWS + row;
-  if (!joins || prow >= g.n * p.group) return;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const float lse2 = sum == 0.f ? -INFINITY : ref + log2f(sum) - SHIFT;
+  const bool real = joins && prow < g.n * p.group;
+  auto store = [&](float total, float from) {    // acc / total, and the sum of exponentials total * 2^from
+    const float inv = total == 0.f ? 0.f : 1.f / total;
 #pragma unroll
-  for (int e = 0; e < EL; ++e) acc[e] *= inv;
-  if (tiles == g.count) {                      // the whole unit: final
+    for (int e = 0; e < EL; ++e) acc[e] *= inv;
     const int tok = prow / p.group, head = g.h * p.group + prow - tok * p.group;
     const long long t = g.row0 + tok;
     T* dst = static_cast<T*>(p.out) + t * p.os_t + head * p.os_h + d0;
@@ -641,13 +644,61 @@ __device__ __forceinline__ void consume(const PagedParams& p, const Segment& g, 
         *reinterpret_cast<uint32_t*>(dst + e) =
             std::is_same<T, __half>::value ? f16x2(acc[e], acc[e + 1]) : pack_bf16x2(acc[e], acc[e + 1]);
     }
-    if (p.lse != nullptr && d0 == 0) p.lse[t * p.heads_q + head] = lse2 * LN2;
-  } else {
+    if (p.lse != nullptr && d0 == 0) p.lse[t * p.heads_q + head] = total == 0.f ? -INFINITY : (from + log2f(total)) * LN2;
+  };
+  if (tiles == g.count) {                      // the whole unit: final
+    if (real) store(sum, ref - SHIFT);
+    return;
+  }
+  if (real) {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const long long at = static_cast<long long>(part_slot(blockIdx.x, g.k0 == 0)) * S::ROWS + row;
 #pragma unroll
-    for (int e = 0; e < EL; e += 2) *reinterpret_cast<float2*>(p.part + at * D + d0 + e) = make_float2(acc[e], acc[e + 1]);
-    if (d0 == 0) p.part_lse[at] = lse2;
+    for (int e = 0; e < EL; e += 2)
+      *reinterpret_cast<float2*>(p.part + at * D + d0 + e) = make_float2(acc[e] * inv, acc[e + 1] * inv);
+    if (d0 == 0) p.part_lse[at] = sum == 0.f ? -INFINITY : ref + log2f(sum) - SHIFT;
   }
+  barrier();
+  if (threadIdx.x == 0) {                      // every CTA of the unit comes here once, waits run out or not
+    const int c0 = wk.deal.owner(g.u0), c1 = wk.deal.owner(g.u0 + g.count - 1);
+    __threadfence();
+    const bool last = atomicAdd(p.turn + c0, 1u) == static_cast<uint32_t>(c1 - c0);
+    if (last) {
+      p.turn[c0] = 0u;
+      __threadfence();
+    }
+    wk.share[0] = last ? c0 : -1;
+    wk.share[1] = c1;
+  }
+  barrier();
+  const int c0 = wk.share[0], c1 = wk.share[1];
+  if (c0 < 0 || !joins) return;
+  // The partial rows of CTAs c0 .. c1 in order, weighted by 2^(log2 sum - largest); PER threads a row.
+  top = -INFINITY;
+  for (int i = c0 + threadIdx.x % PER; i <= c1; i += PER)
+    top = fmaxf(top, __ldcg(p.part_lse + static_cast<long long>(part_slot(i, i == c0)) * S::ROWS + row));
+#pragma unroll
+  for (int y = PER / 2; y > 0; y >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, y));
+  const float first = top == -INFINITY ? 0.f : top;
+  sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < EL; ++e) acc[e] = 0.f;
+#pragma unroll 8
+  for (int i = c0; i <= c1; ++i) {
+    const long long at = static_cast<long long>(part_slot(i, i == c0)) * S::ROWS + row;
+    const float f = pg_ex2(__ldcg(p.part_lse + at) - first);
+    sum += f;
+#pragma unroll
+    for (int e = 0; e < EL; e += V) {
+      float v[V];
+      const float* from = p.part + at * D + d0 + e;
+      if constexpr (V == 4) *reinterpret_cast<float4*>(v) = __ldcg(reinterpret_cast<const float4*>(from));
+      else *reinterpret_cast<float2*>(v) = __ldcg(reinterpret_cast<const float2*>(from));
+#pragma unroll
+      for (int x = 0; x < V; ++x) acc[e + x] += f * v[x];
+    }
+  }
+  if (real) store(sum, first);
 }
 
 template <class T, bool E8, int D, int NQ>
@@ -666,7 +717,6 @@ __global__ void __launch_bounds__(Shape<T, E8, D, NQ>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int batch = p.s.batch;
 
-  griddep_launch_dependents();
   if (threadIdx.x == 0) {
     *dead = 0;
     for (int i = 0; i < S::STAGES; ++i) {
@@ -697,7 +747,6 @@ __global__ void __launch_bounds__(Shape<T, E8, D, NQ>::THREADS, 1)
     }
   }
   __syncthreads();
-  if (blockIdx.x == 0 && threadIdx.x == 0) p.prefix[batch] = pre[batch];   // for the join
   const Deal deal(pre[batch] * p.c.heads, p.grid);
   for (int b = blockIdx.x; b < batch; b += gridDim.x) {   // sequences without a key: nothing is seen
     int n, len, row0;
@@ -716,9 +765,7 @@ __global__ void __launch_bounds__(Shape<T, E8, D, NQ>::THREADS, 1)
     while (x < end) {
       while (pre[b + 1] * p.c.heads <= x) ++b;
       const Segment g = segment_at<KT, ROWS>(p, pre, b, x, end);
-      if (done == 0 && threadIdx.x == 0)
-        p.cut[blockIdx.x] = CutUnit{g.u0 < x ? g.u0 : -1, g.count, g.row0, g.n, g.h, g.rg};
-      const Work wk = {dead, ring, full, empty, done, first_tile<S::WARPS>(warp, done), merge, ml};
+      const Work wk = {dead, ring, full, empty, done, first_tile<S::WARPS>(warp, done), merge, ml, deal, dead + 2};
       consume<T, E8, D, NQ>(p, g, wk);
       done += g.k1 - g.k0;
       x += g.k1 - g.k0;
@@ -728,22 +775,6 @@ __global__ void __launch_bounds__(Shape<T, E8, D, NQ>::THREADS, 1)
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < 50000ull) __nanosleep(1000);
   }
-}
-
-// ------------------------------------------------------------------ join
-
-// Block i - 1: if CTA i's run begins inside a unit that CTA i - 1 began, that unit's rows.
-template <class T, int D, int ROWS>
-__global__ void __launch_bounds__(256) mk_paged_join_kernel(const __grid_constant__ PagedParams p) {
-  griddep_wait();
-  const int i = blockIdx.x + 1;
-  const CutUnit g = p.cut[i];
-  const Deal deal(p.prefix[p.s.batch] * p.c.heads, p.grid);
-  if (i >= deal.c || g.u0 < 0 || deal.start(i - 1) > g.u0) return;
-  const int row = threadIdx.x >> 4, prow = g.at * ROWS + row;
-  if (row >= ROWS || prow >= g.n * p.group) return;
-  const int tok = prow / p.group;
-  join_row<T, D, ROWS>(p, i - 1, deal.owner(g.u0 + g.count - 1), row, g.row0 + tok, g.h * p.group + prow - tok * p.group);
 }
 
 // ------------------------------------------------------------------ host
@@ -762,10 +793,7 @@ cudaError_t launch_decode(const PagedParams& p, cudaStream_t s) {
     configured_dev = dev;
   }
   mk_paged_decode_kernel<T, E8, D, NQ><<<p.grid, S::THREADS, S::SMEM, s>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  if (p.grid < 2) return e;
-  return launch_dependent(mk_paged_join_kernel<T, D, S::ROWS>, dim3(p.grid - 1), dim3(256), s, p);
+  return cudaGetLastError();
 }
 template <class T, bool E8>
 cudaError_t launch_decode(const PagedParams& p, int nq, cudaStream_t s) {
@@ -795,11 +823,12 @@ bool cache_map(CUtensorMap* m, const mk_kv_cache* c, const void* base, const voi
 }
 
 // Packed rows (new tokens times query heads of a key head) up to which a sequence is the decode
-// kernel's: that kernel reads the keys once per 16 rows, the prompt kernel computes 256 at a time.
+// kernel's: that kernel reads the keys once per 16 rows (or 8, see nq), the prompt kernel computes
+// 256 at a time.
 constexpr int PG_DECODE_ROWS = 64;
 
 struct PagedLayout {
-  size_t cut_off, prefix_off, part_off, lse_off, total;
+  size_t turn_off, cut_off, prefix_off, part_off, lse_off, total;
 };
 // Whether a call with this many tokens in all may hold a sequence for the prompt kernel.
 bool may_be_prompt(long long max_tokens, int group) { return group <= 128 && max_tokens * group > PG_DECODE_ROWS; }
@@ -809,7 +838,8 @@ bool paged_layout(long long tokens, int group, int d, int batch, int sms, PagedL
   const size_t rows = static_cast<size_t>(2) * sms * (prompt ? prompt_part_rows() : DC_MAX_ROWS);
   const size_t units = std::max<size_t>(std::min(batch, DC_BATCH),
                                         prompt ? prompt_entries(static_cast<int>(tokens), group, batch) : 0);
-  L.cut_off = WS_HDR_BYTES;
+  L.turn_off = WS_HDR_BYTES;
+  L.cut_off = L.turn_off + ((static_cast<size_t>(sms) * 4 + 255) & ~size_t(255));
   L.prefix_off = L.cut_off + ((static_cast<size_t>(sms) * sizeof(CutUnit) + 255) & ~size_t(255));
   L.part_off = L.prefix_off + (((units + 1) * 8 + 255) & ~size_t(255));
   L.lse_off = L.part_off + rows * d * 4;
@@ -867,6 +897,7 @@ mk_status mk_paged_attention(const void* q, void* out, float* lse, mk_dtype dtyp
   p.os_h = o_head;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.hdr = reinterpret_cast<uint32_t*>(ws);
+  p.turn = reinterpret_cast<uint32_t*>(ws + L.turn_off);
   p.cut = reinterpret_cast<CutUnit*>(ws + L.cut_off);
   p.prefix = reinterpret_cast<long long*>(ws + L.prefix_off);
   p.part = reinterpret_cast<float*>(ws + L.part_off);

@@ -9,12 +9,13 @@
 
 namespace mk {
 
-// What a CTA leaves for the join: the unit that its run begins inside of, u0 = -1 if there is none.
+// What a CTA of the prompt kernel leaves for the join: the item that its run begins inside of, u0 = -1
+// if there is none.
 struct CutUnit {
-  long long u0;                        // number (place) of the unit's first tile
+  long long u0;                        // place of the item's first tile
   int count;                           // its tiles
   int row0, n, h;                      // its sequence's first token row and new tokens; key head
-  int at;                              // decode: row group; prompts: the item's first token
+  int at;                              // its first token
 };
 
 struct PagedParams {
@@ -28,7 +29,8 @@ struct PagedParams {
   uint32_t* hdr;
   float* part;                         // partial rows: o [slot][row][d], then their log2 sums
   float* part_lse;
-  CutUnit* cut;                        // one for each CTA
+  uint32_t* turn;                      // decode: CTAs that are done with the unit begun by each CTA; 0 between calls
+  CutUnit* cut;                        // prompts: one for each CTA
   long long* prefix;                   // tiles of the units before each sequence / item (see the kernels)
   long long wait_ns;
   float scale_log2;                    // softmax scale * log2(e)
