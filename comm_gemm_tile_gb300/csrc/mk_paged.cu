@@ -717,6 +717,7 @@ __global__ void __launch_bounds__(Shape<T, E8, D, NQ>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int batch = p.s.batch;
 
+  griddep_launch_dependents();           // the prompt kernel's plan
   if (threadIdx.x == 0) {
     *dead = 0;
     for (int i = 0; i < S::STAGES; ++i) {
@@ -954,7 +955,7 @@ mk_status mk_paged_attention(const void* q, void* out, float* lse, mk_dtype dtyp
       return MK_ERR_CUDA;
     p.rows_lo = decode ? PG_DECODE_ROWS + 1 : 1;
     p.rows_hi = 0x7fffffff;
-    if (launch_prompt(p, d, dtype, e8, s) != cudaSuccess) return MK_ERR_CUDA;
+    if (launch_prompt(p, d, dtype, e8, decode, s) != cudaSuccess) return MK_ERR_CUDA;
   }
   return MK_OK;
 }

@@ -211,6 +211,6 @@ __device__ __forceinline__ void join_row(const PagedParams& p, int c0, int c1, i
 // The prompt kernel (mk_prompt.cu): entries of its work list, partial rows of a CTA's place.
 int prompt_entries(int tokens, int group, int batch);
 int prompt_part_rows();
-cudaError_t launch_prompt(const PagedParams& p, int d, mk_dtype dtype, bool e8, cudaStream_t s);
+cudaError_t launch_prompt(const PagedParams& p, int d, mk_dtype dtype, bool e8, bool after_decode, cudaStream_t s);
 
 }  // namespace mk

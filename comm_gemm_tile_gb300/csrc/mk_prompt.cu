@@ -119,6 +119,7 @@ __device__ __forceinline__ bool item_of(const PagedParams& p, int e, int b, Item
 }
 
 // prefix[e] = places of one head in the entries before e; rows of items without tiles see nothing.
+// Runs beside a decode launch before it (which has no part in this), and ends after it.
 template <class T>
 __global__ void __launch_bounds__(1024) mk_prompt_plan_kernel(const __grid_constant__ PagedParams p, int entries) {
   __shared__ long long part[33];
@@ -165,6 +166,7 @@ __global__ void __launch_bounds__(1024) mk_prompt_plan_kernel(const __grid_const
     __syncthreads();
   }
   if (threadIdx.x == 0) p.prefix[entries] = base;
+  griddep_wait();
 }
 
 // A run's walk over its segments: the part of one item and head that lies in the run.
@@ -1121,7 +1123,7 @@ __global__ void __launch_bounds__(256) mk_prompt_join_kernel(const __grid_consta
 }
 
 template <class T, bool E8, int D>
-cudaError_t launch(const PagedParams& p, cudaStream_t s) {
+cudaError_t launch(const PagedParams& p, bool after_decode, cudaStream_t s) {
   using P = Plan<E8, D>;
   static int configured_dev = -1;
   int dev = 0;
@@ -1133,16 +1135,18 @@ cudaError_t launch(const PagedParams& p, cudaStream_t s) {
     configured_dev = dev;
   }
   const int entries = prompt_entries(p.s.tokens, p.group, p.s.batch);
-  mk_prompt_plan_kernel<T><<<1, 1024, 0, s>>>(p, entries);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = after_decode ? 1 : 0;
   cfg.stream = s;
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(1024);
+  e = cudaLaunchKernelEx(&cfg, mk_prompt_plan_kernel<T>, p, entries);
+  if (e != cudaSuccess) return e;
+  cfg.numAttrs = 1;
   cfg.gridDim = dim3(p.grid);
   cfg.blockDim = dim3(P::THREADS);
   cfg.dynamicSmemBytes = P::SMEM;
@@ -1159,11 +1163,11 @@ cudaError_t launch(const PagedParams& p, cudaStream_t s) {
 int prompt_entries(int tokens, int group, int batch) { return tokens / (2 * (PR_T / group)) + batch; }
 int prompt_part_rows() { return 2 * PR_T; }
 
-cudaError_t launch_prompt(const PagedParams& p, int d, mk_dtype dtype, bool e8, cudaStream_t s) {
-  if (e8) return d == 128 ? launch<__nv_bfloat16, true, 128>(p, s) : launch<__nv_bfloat16, true, 64>(p, s);
-  if (dtype == MK_BF16)
-    return d == 128 ? launch<__nv_bfloat16, false, 128>(p, s) : launch<__nv_bfloat16, false, 64>(p, s);
-  return d == 128 ? launch<__half, false, 128>(p, s) : launch<__half, false, 64>(p, s);
+cudaError_t launch_prompt(const PagedParams& p, int d, mk_dtype dtype, bool e8, bool after_decode, cudaStream_t s) {
+  const auto f = e8 ? (d == 128 ? launch<__nv_bfloat16, true, 128> : launch<__nv_bfloat16, true, 64>)
+                 : dtype == MK_BF16 ? (d == 128 ? launch<__nv_bfloat16, false, 128> : launch<__nv_bfloat16, false, 64>)
+                                    : (d == 128 ? launch<__half, false, 128> : launch<__half, false, 64>);
+  return f(p, after_decode, s);
 }
 
 }  // namespace mk
