@@ -19,10 +19,11 @@ typedef struct {
 } tensor;
 enum { T_I32 = 16, T_I64 = 17, T_F64 = 18, T_OTHER = 19 };
 
-static PyObject *s_data_ptr, *s_dtype, *s_shape, *s_stride, *s_get_device, *s_new_empty, *s_kw_dtype;
+static PyObject *s_data_ptr, *s_dtype, *s_shape, *s_stride, *s_get_device, *s_device, *s_kw;
 static PyObject *dtypes[7];        /* bf16, f32, f16, e4m3, i32, i64, f64 */
 static const int dtype_codes[7] = {MK_BF16, MK_F32, MK_F16, MK_E4M3, T_I32, T_I64, T_F64};
 static PyObject *raw_stream;       /* torch._C._cuda_getCurrentRawStream */
+static PyObject *empty;            /* torch.empty: 1.6 us; the method new_empty takes 5 */
 
 static int refuse(const char *what) {
   PyErr_SetString(PyExc_ValueError, what);
@@ -159,10 +160,12 @@ static int read_stream(PyObject *stream, int device, mk_stream_t *s) {
 
 static PyObject *empty_like_rows(PyObject *t, long long tokens, long long heads, long long d, PyObject *dtype) {
   PyObject *shape = d ? Py_BuildValue("(LLL)", tokens, heads, d) : Py_BuildValue("(LL)", tokens, heads);
-  if (!shape) return NULL;
-  PyObject *args[3] = {t, shape, dtype};
-  PyObject *r = PyObject_VectorcallMethod(s_new_empty, args, 2, dtype ? s_kw_dtype : NULL);
-  Py_DECREF(shape);
+  PyObject *type = dtype ? Py_NewRef(dtype) : PyObject_GetAttr(t, s_dtype), *device = PyObject_GetAttr(t, s_device);
+  PyObject *args[3] = {shape, type, device};
+  PyObject *r = shape && type && device ? PyObject_Vectorcall(empty, args, 1, s_kw) : NULL;
+  Py_XDECREF(shape);
+  Py_XDECREF(type);
+  Py_XDECREF(device);
   return r;
 }
 
@@ -350,12 +353,13 @@ end:
   return result;
 }
 
-/* setup(dtypes in the order of `dtypes`, raw_stream) */
+/* setup(dtypes in the order of `dtypes`, raw_stream, empty) */
 static PyObject *bind_setup(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   (void)self;
-  NEED(n == 2 && PyTuple_Check(a[0]) && PyTuple_GET_SIZE(a[0]) == 7, "setup: (7 dtypes, function)");
+  NEED(n == 3 && PyTuple_Check(a[0]) && PyTuple_GET_SIZE(a[0]) == 7, "setup: (7 dtypes, two functions)");
   for (int i = 0; i < 7; ++i) Py_XSETREF(dtypes[i], Py_NewRef(PyTuple_GET_ITEM(a[0], i)));
   Py_XSETREF(raw_stream, Py_NewRef(a[1]));
+  Py_XSETREF(empty, Py_NewRef(a[2]));
   Py_RETURN_NONE;
 }
 
@@ -373,7 +377,7 @@ PyMODINIT_FUNC PyInit__mkbind(void) {
   s_shape = PyUnicode_InternFromString("shape");
   s_stride = PyUnicode_InternFromString("stride");
   s_get_device = PyUnicode_InternFromString("get_device");
-  s_new_empty = PyUnicode_InternFromString("new_empty");
-  s_kw_dtype = Py_BuildValue("(s)", "dtype");
+  s_device = PyUnicode_InternFromString("device");
+  s_kw = Py_BuildValue("(ss)", "dtype", "device");
   return PyModule_Create(&module);
 }
