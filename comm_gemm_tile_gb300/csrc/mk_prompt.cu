@@ -1106,7 +1106,7 @@ __global__ void __launch_bounds__(Plan<E8, D>::THREADS, 1)
 
 // Block (i - 1, y): if CTA i's run begins inside an item that CTA i-1 began, a quarter of the item's
 // rows from the partial rows of all CTAs that worked on it.
-constexpr int JOIN_Y = 4;
+constexpr int JOIN_Y = 8;
 template <class T, int D>
 __global__ void __launch_bounds__(256) mk_prompt_join_kernel(const __grid_constant__ PagedParams p, int entries) {
   griddep_wait();
