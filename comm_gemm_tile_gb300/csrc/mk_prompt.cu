@@ -220,6 +220,12 @@ struct Walk {
   }
 };
 
+// Whether query tile g of the item has no rows (short sequences, ends of prompts): its warps keep step,
+// and do nothing.
+__device__ __forceinline__ bool no_rows(const PagedParams& p, const Item& it, int g) {
+  return it.tok0 + g * (PR_T / p.group) >= it.n;
+}
+
 // The positions of an item's rows.
 __device__ __forceinline__ void item_span(const PagedParams& p, const Item& it, int& p0, int& p1) {
   p0 = it.len - it.n + it.tok0;
@@ -586,7 +592,7 @@ __device__ void pr_mma(const PagedParams& p, Walk w, volatile int* dead, uint32_
   const uint64_t dk0 = sdesc_sw128(base + P::K, 16u, 1024u), dv0 = sdesc_sw128(base + P::V, 16384u, 1024u);
   const uint32_t go = bars + B_GO + 16u * i;
   uint32_t u = 0, q_ph = 0;
-  bool first = false, last = false, masked = false;          // of the tile before
+  bool first = false, last = false, masked = false, idle = false;   // of the tile before
   // The tiles take turns: PV_0(u-1), S_0(u), PV_1(u-1), S_1(u), PV_0(u), ...  So they stay half a
   // period out of step, and one's products run while the other's softmax does (left to
   // themselves they fall into step: 3800 cycles a key tile).  Each S_i(n) is handed over to the
@@ -605,7 +611,7 @@ __device__ void pr_mma(const PagedParams& p, Walk w, volatile int* dead, uint32_
       if (!pr_wait(dead, p, go + 8u * half, v & 1u, WHERE_MMA)) return false;
       if (half == 0 && !last && !handed(v + i)) return false;
       tc_fence_after();
-      if (elect_one_sync()) {
+      if (!idle && elect_one_sync()) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           tc_mma_bf16_ts(ocol, scol + 32u * half + 8u * k, dv + ((8192u * half + 2048u * k) >> 4), idesc(D, true, E8 || HALF),
@@ -636,10 +642,11 @@ __device__ void pr_mma(const PagedParams& p, Walk w, volatile int* dead, uint32_
       }
       if (!pr_wait(dead, p, bars + B_KFULL + 8u * st, (u / PR_ST) & 1u, WHERE_MMA)) goto done;
       if (!opens && !values(u - 1)) goto done;
+      idle = no_rows(p, w.it, i);
       tc_fence_after();
       {
         const uint64_t dk = dk0 + ((P::TILE * st) >> 4);
-        if (elect_one_sync()) {
+        if (!idle && elect_one_sync()) {
 #pragma unroll
           for (int a = 0; a < D / 64; ++a)
 #pragma unroll
@@ -842,10 +849,18 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uin
     // that its product with a scale below 2^27 is finite, and scales from 2^-100 on keep their bits.)
     float mv = -INFINITY, f = 0.f, F = 1.f;
     bool ready = false;                                    // every row of the warp has a reference
+    const bool idle = no_rows(p, it, g);
     for (int k = w.k0; k < w.k1; ++k, ++u) {
       const int key0 = it.t.tile(k) * PR_T;
       const bool masked = g1 >= g0 && !all_seen(p, g0, g1, it.len, key0, PR_T);
       if (!pr_wait(dead, p, bars + B_S + 8u * g, u & 1u, WHERE_EPILOGUE)) return;
+      if (idle) {
+        if (lane == 0) {
+          mbar_arrive(bars + B_GO + 16u * g);
+          mbar_arrive(bars + B_GO + 16u * g + 8u);
+        }
+        continue;
+      }
       tc_fence_after();
       if (E8 && k == w.k0) {
         const int ex = reinterpret_cast<const signed char*>(sm + Plan<E8, D>::QEXP)[(seg & 1) * 2 * PR_T + g * PR_T + row];
@@ -859,7 +874,8 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uin
       for (int half = 0; half < 2; ++half) {
         const float* scales = E8 ? reinterpret_cast<const float*>(sm + Plan<E8, D>::SCALES) + (u & 3u) * 32 + 8 * half : nullptr;
         // 16-bit caches hold the half's 64 scores; with 8-bit ones there are four more warps and
-        // fewer registers: 32 scores at a time, read again when the reference moves
+        // fewer registers: 32 scores at a time, read again when the reference moves (64: spills; 16,
+        // the next on their way: 767 us where 32 take 645)
         constexpr int HELD = E8 ? 1 : 2;
         uint32_t sv[HELD][32], wt[32];
         auto fetch = [&](int a) {
@@ -954,6 +970,7 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uin
     }
     if (!pr_wait(dead, p, bars + B_O + 8u * g, o_ph, WHERE_EPILOGUE)) return;
     o_ph ^= 1u;
+    if (idle) continue;
     tc_fence_after();
     const float inv = l == 0.f ? 0.f : 1.f / l, inv_f = E8 ? pg_ex2(-f) : 1.f;
     const float lse2 = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) + log2f(l) - SHIFT;
