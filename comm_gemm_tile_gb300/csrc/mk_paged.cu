@@ -830,9 +830,9 @@ bool cache_map(CUtensorMap* m, const mk_kv_cache* c, const void* base, const voi
 
 // Packed rows (new tokens times query heads of a key head) up to which a sequence is the decode
 // kernel's: that kernel reads the keys once per 16 rows, the prompt kernel computes 256 at a time.
-// 16 sequences of 16000 tokens, 8 key heads, d = 128, bf16, decode / prompt kernel: 16 rows 197 /
-// 216 us, 32 rows 353 / 218, 64 rows 669 / 220 (e4m3: 32 rows 313 / 277); of 1000 tokens: 16 rows
-// 45 / 52, 32 rows 60 / 52.
+// 16 sequences of 16000 tokens, 8 key heads, d = 128, decode / prompt kernel: 16 rows bf16 198 / 189
+// us, e4m3 174 / 201; 20 rows 357 / 191 and 307 / 203; 64 rows bf16 669 / 194.  Of 1000 tokens, bf16:
+// 16 rows 45 / 48, 20 rows 61 / 50.
 constexpr int PG_DECODE_ROWS = 16;
 
 struct PagedLayout {

@@ -24,13 +24,13 @@
 //             multiply the scores and the weights), and an item's queries, each row times a
 //             power of two; warp 2 brings the scales
 //
-// A prompt of 8192 tokens, 32 query heads on 8, d = 128, bf16, causal: 430 us, 1.28 PFLOP/s of what
+// A prompt of 8192 tokens, 32 query heads on 8, d = 128, bf16, causal: 427 us, 1.29 PFLOP/s of what
 // the mask leaves (67 % of the burst rate of a plain product, 75 % of its rate under the power cap).
 // The tensor pipe is busy 61 % of the time; a key tile takes the softmax warps about as long as the
 // products (the exponentials alone half of that), and changing items 5 %.  Over 8-bit caches the same
 // loop is bound by issue slots and shared memory together: the codes' conversion adds 128 conversions a
-// scheduler and 96 KB of shared memory traffic to a key tile (two pieces of 1000 tokens after 25000,
-// 626 us, 1.02 PFLOP/s; the same over a bf16 cache 520 us).
+// scheduler and 96 KB of shared memory traffic to a key tile (two pieces of 1000 tokens after 15000 to
+// 30000: 614 us, 1.04 PFLOP/s; the same over a bf16 cache 520 us).
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -48,7 +48,7 @@ constexpr uint32_t PR_COLS = 512;            // tensor memory: S_0, S_1, O_0, O_
 constexpr uint32_t PR_O = 256;
 // Changing items (queries, the first maximum, the output) takes about as long as this many tiles:
 // an item's first OVER places in a run stand for that, its tiles come after them.  (The prompt
-// above with 0, 1, 2, 3 places: 579, 463, 430, 432 us; ragged windowed prompts 70, 65, 63, 64.)
+// above with 0, 1, 2, 3 places: 579, 463, 430, 432 us; six ragged windowed prompts 70, 65, 63, 64.)
 constexpr int OVER = 2;
 enum { W_MMA = 0, W_LOAD = 1, W_LOADV = 2, W_MMA1 = 3, W_SOFT = 4, W_TURN = 12 };
 
@@ -67,8 +67,9 @@ struct Plan {
 // barriers (byte offsets)
 constexpr uint32_t B_QFULL = 0, B_QEMPTY = 8, B_KFULL = 16, B_KEMPTY = 32, B_VFULL = 48, B_VEMPTY = 64, B_VREADY = 80,
                    B_S = 96, B_GO = 112, B_O = 144, B_DRAIN = 160, B_RKFULL = 176, B_RKEMPTY = 184, B_RVFULL = 192,
-                   B_RVEMPTY = 200, B_TURN = 208, B_TMEM = 240, B_DEAD = 244, B_ODD = 248, B_HALF = 280, B_QREADY = 296;
-static_assert(B_QREADY + 8 <= 384, "barrier block");
+                   B_RVEMPTY = 200, B_TURN = 208, B_TMEM = 240, B_DEAD = 244, B_ODD = 248, B_HALF = 280, B_QREADY = 296,
+                   B_OTHER = 304, B_TAKEN = 312;
+static_assert(B_TAKEN + 8 <= 384, "barrier block");
 
 __device__ __forceinline__ uint32_t idesc(int n, bool b_mn, bool half) {
   return idesc_bf16_f32(PR_T, n, false, b_mn) & (half ? ~((1u << 7) | (1u << 10)) : ~0u);
@@ -220,10 +221,12 @@ struct Walk {
   }
 };
 
-// Whether query tile g of the item has no rows (short sequences, ends of prompts): its warps keep step,
-// and do nothing.
-__device__ __forceinline__ bool no_rows(const PagedParams& p, const Item& it, int g) {
-  return it.tok0 + g * (PR_T / p.group) >= it.n;
+// A narrow item has rows for one query tile only (short sequences, ends of prompts): both query tiles are
+// that one, each takes every other key tile of a segment, and the softmax warps of the first merge the two
+// results.  16 sequences of 16000 tokens, 8 key heads, d = 128, 32 rows: bf16 192 us (5.5 TB/s), e4m3 199;
+// with the second query tile left idle 203 and 258.
+__device__ __forceinline__ bool narrow_item(const PagedParams& p, const Item& it) {
+  return it.tok0 + PR_T / p.group >= it.n;
 }
 
 // The positions of an item's rows.
@@ -302,13 +305,14 @@ __device__ void pr_load(const PagedParams& p, Walk w, volatile int* dead, uint32
         if (!pr_wait(dead, p, bars + B_QEMPTY, q_ph ^ 1u, WHERE_PRODUCER)) return;
         q_ph ^= 1u;
         if (lane == 0) {
+          const int second = narrow_item(p, w.it) ? 0 : toks;
           mbar_arrive_expect_tx(bars + B_QFULL, 2u * toks * p.group * D * 2u);
 #pragma unroll
           for (int q = 0; q < 2; ++q)
 #pragma unroll
             for (int a = 0; a < D / 64; ++a)
               tma_load_3d(base + P::Q + q * P::TILE + a * 16384u, &p.tmQ, bars + B_QFULL, 64 * a, w.h * p.group,
-                          w.it.row0 + w.it.tok0 + q * toks);
+                          w.it.row0 + w.it.tok0 + q * second);
         }
         __syncwarp();
       }
@@ -592,26 +596,33 @@ __device__ void pr_mma(const PagedParams& p, Walk w, volatile int* dead, uint32_
   const uint64_t dk0 = sdesc_sw128(base + P::K, 16u, 1024u), dv0 = sdesc_sw128(base + P::V, 16384u, 1024u);
   const uint32_t go = bars + B_GO + 16u * i;
   uint32_t u = 0, q_ph = 0;
-  bool first = false, last = false, masked = false, idle = false;   // of the tile before
+  bool first = false, masked = false, idle = false, narrow = false;   // of the tile before
+  uint32_t n = 0, turn = 0, taken = 0;                       // own tiles; tiles that took turns; narrow segments
   // The tiles take turns: PV_0(u-1), S_0(u), PV_1(u-1), S_1(u), PV_0(u), ...  So they stay half a
   // period out of step, and one's products run while the other's softmax does (left to
   // themselves they fall into step: 3800 cycles a key tile).  Each S_i(n) is handed over to the
   // other warp on barrier n % 2 of its pair; neither gets two ahead of a wait, as S_i(n+2) needs
   // the K stage that the other's S(n) has read.  An item's last products do not wait: the next
-  // item's S waits for its queries.
+  // item's S waits for its queries.  In narrow items each warp goes its own way.
   auto handed = [&](uint32_t n) {
     return pr_wait(dead, p, bars + B_TURN + 16u * i + 8u * (n % 2), (n / 2) & 1u, WHERE_MMA);
   };
-  auto values = [&](uint32_t v) {
+  auto arrive = [](uint32_t bar) {
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+    __syncwarp();
+  };
+  // O_i += P_i V of the tile before, number v (idle: the other query tile's; turns: it has to wait for its turn)
+  auto values = [&](uint32_t v, bool idle, bool turns) {
     const uint32_t st = v % PR_ST;
     if (!pr_wait(dead, p, bars + (E8 || masked ? B_VREADY : B_VFULL) + 8u * st, (v / PR_ST) & 1u, WHERE_MMA)) return false;
+    if (idle) return true;
     const uint64_t dv = dv0 + ((P::TILE * st) >> 4);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      if (!pr_wait(dead, p, go + 8u * half, v & 1u, WHERE_MMA)) return false;
-      if (half == 0 && !last && !handed(v + i)) return false;
+      if (!pr_wait(dead, p, go + 8u * half, (n - 1) & 1u, WHERE_MMA)) return false;
+      if (half == 0 && turns && !handed(turn - 1 + i)) return false;
       tc_fence_after();
-      if (!idle && elect_one_sync()) {
+      if (elect_one_sync()) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           tc_mma_bf16_ts(ocol, scol + 32u * half + 8u * k, dv + ((8192u * half + 2048u * k) >> 4), idesc(D, true, E8 || HALF),
@@ -622,31 +633,32 @@ __device__ void pr_mma(const PagedParams& p, Walk w, volatile int* dead, uint32_
     }
     return true;
   };
-  auto values_done = [&](uint32_t v) {
-    commit(bars + B_VEMPTY + 8u * (v % PR_ST));
-    if (last) commit(bars + B_O + 8u * i);
+  auto values_done = [&](uint32_t v, bool idle) {
+    if (!idle) commit(bars + B_VEMPTY + 8u * (v % PR_ST));
+    else arrive(bars + B_VEMPTY + 8u * (v % PR_ST));
   };
-  while (w.next(p)) {
+  // the last ones of a segment
+  auto close = [&] {
+    if (u == 0) return true;
+    if (!values(u - 1, idle, false)) return false;
+    values_done(u - 1, idle);
+    commit(bars + B_O + 8u * i);
+    return true;
+  };
+  auto segment = [&](auto kind) {
+    constexpr bool NARROW = decltype(kind)::value;
     int p0, p1;
     item_span(p, w.it, p0, p1);
     for (int k = w.k0; k < w.k1; ++k, ++u) {
       const uint32_t st = u % PR_ST;
-      const bool opens = k == w.k0;
-      if (opens && u > 0) {               // the products before need not wait for this item's queries
-        if (!values(u - 1)) goto done;
-        values_done(u - 1);
-      }
-      if (opens) {
-        if (!pr_wait(dead, p, bars + (E8 ? B_QREADY : B_QFULL), q_ph, WHERE_MMA)) goto done;
-        q_ph ^= 1u;
-      }
-      if (!pr_wait(dead, p, bars + B_KFULL + 8u * st, (u / PR_ST) & 1u, WHERE_MMA)) goto done;
-      if (!opens && !values(u - 1)) goto done;
-      idle = no_rows(p, w.it, i);
-      tc_fence_after();
-      {
+      const bool opens = k == w.k0, mine = !NARROW || ((k - w.k0) & 1) == i;
+      if (!pr_wait(dead, p, bars + B_KFULL + 8u * st, (u / PR_ST) & 1u, WHERE_MMA)) return false;
+      if (!mine) arrive(bars + B_KEMPTY + 8u * st);
+      if (!opens && !values(u - 1, NARROW && mine, !NARROW)) return false;
+      if (mine) {
+        tc_fence_after();
         const uint64_t dk = dk0 + ((P::TILE * st) >> 4);
-        if (!idle && elect_one_sync()) {
+        if (elect_one_sync()) {
 #pragma unroll
           for (int a = 0; a < D / 64; ++a)
 #pragma unroll
@@ -655,18 +667,34 @@ __device__ void pr_mma(const PagedParams& p, Walk w, volatile int* dead, uint32_
                           idesc(PR_T, false, E8 || HALF), (a | kk) ? 1u : 0u);
         }
         __syncwarp();
+        commit(bars + B_S + 8u * i);
+        if (!NARROW) {
+          if ((threadIdx.x & 31) == 0) mbar_arrive(bars + B_TURN + 16u * (1 - i) + 8u * (turn % 2));
+          ++turn;
+        }
+        commit(bars + B_KEMPTY + 8u * st);
+        ++n;
       }
-      commit(bars + B_S + 8u * i);
-      if ((threadIdx.x & 31) == 0) mbar_arrive(bars + B_TURN + 16u * (1 - i) + 8u * (u % 2));
-      commit(bars + B_KEMPTY + 8u * st);
-      if (!opens) values_done(u - 1);
-      first = opens;
-      last = k == w.k1 - 1;
-      if (last) commit(bars + B_QEMPTY);
+      if (!opens) values_done(u - 1, NARROW && mine);
+      first = k == w.k0 + (NARROW ? i : 0);
       masked = !all_seen(p, p0, p1, w.it.len, w.it.t.tile(k) * PR_T, PR_T);
+      if (NARROW) idle = !mine;
     }
+    if (!NARROW) idle = false;
+    commit(bars + B_QEMPTY);
+    return true;
+  };
+  while (w.next(p)) {
+    // the products before need not wait for this item's queries
+    if (!close()) goto done;
+    // what the second query tile's softmax left in S_1, and O_1, have been read
+    if (i == 1 && narrow && !pr_wait(dead, p, bars + B_TAKEN, taken++ & 1u, WHERE_MMA)) goto done;
+    if (!pr_wait(dead, p, bars + (E8 ? B_QREADY : B_QFULL), q_ph, WHERE_MMA)) goto done;
+    q_ph ^= 1u;
+    narrow = narrow_item(p, w.it);
+    if (!(narrow ? segment(std::true_type()) : segment(std::false_type()))) goto done;
   }
-  if (u > 0 && values(u - 1)) values_done(u - 1);
+  close();
 done:
   commit(bars + B_DRAIN + 8u * i);
   // even after giving up: nothing may run on when the tensor memory is freed
@@ -818,6 +846,16 @@ __device__ __forceinline__ void add_not_finite(const PagedParams& p, const Walk&
   }
 }
 
+// For 8-bit caches (128 registers) not inlined, so that the walk's state stays out of the registers of the
+// loop over tiles: the two pieces above 614 us instead of 639; with 16-bit ones the prompt takes 456
+// us that way, not 430.
+__device__ __noinline__ bool next_apart(const PagedParams& p, Walk* w) { return w->next(p); }
+template <bool E8>
+__device__ __forceinline__ bool next_segment(const PagedParams& p, Walk& w) {
+  if constexpr (E8) return next_apart(p, &w);
+  else return w.next(p);
+}
+
 template <class T, bool E8, int D>
 __device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uint32_t bars, const uint8_t* sm,
                            uint32_t tmem, volatile int* odd) {
@@ -831,17 +869,19 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uin
   const int toks = PR_T / p.group;
   const int my_tok = row / p.group, my_head = row - my_tok * p.group;
   float c = p.scale_log2;
-  uint32_t u = 0, o_ph = 0;
+  uint32_t u = 0, n = 0, o_ph = 0, others = 0;             // tiles, own tiles, segments, narrow ones
   const long long begin = w.x;
   if (threadIdx.x == 32 * W_SOFT) p.cut[blockIdx.x].u0 = -1;
-  for (int seg = 0; w.next(p); ++seg) {
+  for (int seg = 0; next_segment<E8>(p, w); ++seg) {
     if (seg == 0 && threadIdx.x == 32 * W_SOFT && w.u0 < begin)
       p.cut[blockIdx.x] = CutUnit{w.u0, w.count, w.it.row0, w.it.n, w.h, w.it.tok0};
-    const Item& it = w.it;
-    const int tok = it.tok0 + g * toks + my_tok;           // new token of this row
+    const typename std::conditional<E8, Item, Item&>::type it = w.it;
+    const int k0 = w.k0, k1 = w.k1;
+    const bool narrow = narrow_item(p, it);
+    const int tok = it.tok0 + (narrow ? 0 : g * toks) + my_tok;   // new token of this row
     const bool real = my_tok < toks && tok < it.n;
     const int pos = it.len - it.n + tok;
-    const int g0 = it.len - it.n + it.tok0 + g * toks;       // positions of the tile's real rows
+    const int g0 = it.len - it.n + it.tok0 + (narrow ? 0 : g * toks);   // positions of the tile's real rows
     const int g1 = min(g0 + toks, it.len) - 1;
     float m = -INFINITY, l = 0.f;
     // 8-bit caches: a weight meets its value's code as fp16(weight x scale x F), F = 2^f; f brings
@@ -849,20 +889,14 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uin
     // that its product with a scale below 2^27 is finite, and scales from 2^-100 on keep their bits.)
     float mv = -INFINITY, f = 0.f, F = 1.f;
     bool ready = false;                                    // every row of the warp has a reference
-    const bool idle = no_rows(p, it, g);
-    for (int k = w.k0; k < w.k1; ++k, ++u) {
+    const int k_first = k0 + (narrow ? g : 0);
+    for (int k = k0; k < k1; ++k, ++u) {
       const int key0 = it.t.tile(k) * PR_T;
       const bool masked = g1 >= g0 && !all_seen(p, g0, g1, it.len, key0, PR_T);
-      if (!pr_wait(dead, p, bars + B_S + 8u * g, u & 1u, WHERE_EPILOGUE)) return;
-      if (idle) {
-        if (lane == 0) {
-          mbar_arrive(bars + B_GO + 16u * g);
-          mbar_arrive(bars + B_GO + 16u * g + 8u);
-        }
-        continue;
-      }
+      if (narrow && ((k - k0) & 1) != g) continue;
+      if (!pr_wait(dead, p, bars + B_S + 8u * g, n & 1u, WHERE_EPILOGUE)) return;
       tc_fence_after();
-      if (E8 && k == w.k0) {
+      if (E8 && k == k_first) {
         const int ex = reinterpret_cast<const signed char*>(sm + Plan<E8, D>::QEXP)[(seg & 1) * 2 * PR_T + g * PR_T + row];
         c = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
       }
@@ -936,9 +970,9 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uin
             l *= factor;
             s_a *= factor;
             ready = __all_sync(0xffffffffu, m != -INFINITY);
-            if ((half != 0 || k > w.k0) && __any_sync(0xffffffffu, factor_o != 1.f)) {
+            if ((half != 0 || k > k_first) && __any_sync(0xffffffffu, factor_o != 1.f)) {
               if (half != 0) {
-                if (!pr_wait(dead, p, bars + B_HALF + 8u * g, u & 1u, WHERE_EPILOGUE)) return;
+                if (!pr_wait(dead, p, bars + B_HALF + 8u * g, n & 1u, WHERE_EPILOGUE)) return;
                 tc_fence_after();
               }
 #pragma unroll 1
@@ -967,12 +1001,44 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uin
         if (half == 0) s_a = sum;
         else l += s_a + sum;
       }
+      ++n;
     }
     if (!pr_wait(dead, p, bars + B_O + 8u * g, o_ph, WHERE_EPILOGUE)) return;
     o_ph ^= 1u;
-    if (idle) continue;
     tc_fence_after();
-    const float inv = l == 0.f ? 0.f : 1.f / l, inv_f = E8 ? pg_ex2(-f) : 1.f;
+    float mul = E8 ? pg_ex2(-f) : 1.f, mul_other = 0.f;
+    const bool other = narrow && w.k1 - w.k0 > 1;          // the second query tile had a key tile
+    if (narrow) {
+      // maximum, sum and factor of the second tile's rows go through S_1, which no product reads any more
+      // and none writes before B_TAKEN
+      uint32_t x[16];
+      if (g == 1) {
+        x[0] = __float_as_uint(m);
+        x[1] = __float_as_uint(l);
+        x[2] = __float_as_uint(f);
+#pragma unroll
+        for (int q = 3; q < 16; ++q) x[q] = 0u;
+        tc_st_32x32b_x16(scol, x);
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + B_OTHER);
+        continue;
+      }
+      if (!pr_wait(dead, p, bars + B_OTHER, others++ & 1u, WHERE_EPILOGUE)) return;
+      tc_fence_after();
+      if (other) {
+        tc_ld_32x32b_x16(scol + PR_T, x);
+        tc_wait_ld();
+        const float m1 = __uint_as_float(x[0]), top = fmaxf(m, m1), ref = top == -INFINITY ? 0.f : top;
+        const float a0 = pg_ex2(m - ref), a1 = pg_ex2(m1 - ref);
+        l = l * a0 + __uint_as_float(x[1]) * a1;
+        mul *= a0;
+        mul_other = E8 ? pg_ex2(-__uint_as_float(x[2])) * a1 : a1;
+        m = top;
+      }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     const float lse2 = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) + log2f(l) - SHIFT;
     const int head = w.h * p.group + my_head;
     const long long t = it.row0 + tok;
@@ -998,7 +1064,16 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uin
       tc_wait_ld();
       float f[32];
 #pragma unroll
-      for (int q = 0; q < 32; ++q) f[q] = (E8 ? __uint_as_float(v[q]) * inv_f : __uint_as_float(v[q])) * inv;
+      for (int q = 0; q < 32; ++q) f[q] = __uint_as_float(v[q]) * mul;
+      if (other) {
+        __syncwarp();
+        tc_ld_32x32b_x32(ocol + PR_T + 32u * a, v);
+        tc_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 32; ++q) f[q] = fmaf(__uint_as_float(v[q]), mul_other, f[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < 32; ++q) f[q] *= inv;
       if (add && real) add_not_finite<T, E8>(p, w, pos, 32 * a, f);
       __syncwarp();
       uint4 out[4];
@@ -1027,6 +1102,8 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uin
       else if (p.lse != nullptr) p.lse[t * p.heads_q + head] = lse2 * LN2;
     }
     tc_fence_before();
+    __syncwarp();
+    if (narrow && lane == 0) mbar_arrive(bars + B_TAKEN);
   }
 }
 
@@ -1064,6 +1141,8 @@ __global__ void __launch_bounds__(Plan<E8, D>::THREADS, 1)
       mbar_init(bars + B_DRAIN + 8u * g, 1);
     }
     for (int s = 0; s < 4; ++s) mbar_init(bars + B_TURN + 8u * s, 1);
+    mbar_init(bars + B_OTHER, 4);
+    mbar_init(bars + B_TAKEN, 4);
     mbar_init(bars + B_RKFULL, 1);
     mbar_init(bars + B_RKEMPTY, 4);
     mbar_init(bars + B_RVFULL, 1);
