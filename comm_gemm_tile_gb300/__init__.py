@@ -240,16 +240,33 @@ def _check(st: int, what: str):
 # ------------------------------------------------------------------ workspaces
 
 class Workspace:
-    """A device workspace, zero-filled once at (re)allocation as the library requires."""
+    """A device workspace, zero-filled once at (re)allocation as the library requires, before any stream uses
+    it.  A buffer that a captured call uses stays allocated when a larger one takes its place: the graph keeps
+    its address."""
 
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
         self.buf = None
+        self.kept = []             # buffers that graphs use
+        self.captured = False      # buf is one of them
+        self.filled = True         # False: allocated while capturing, so that only a replay would fill it
 
     def get(self, nbytes: int) -> torch.Tensor:
         nbytes = max(int(nbytes), 256)
+        capturing = torch._C._cuda_isCurrentStreamCapturing()
         if self.buf is None or self.buf.numel() < nbytes:
+            if self.captured:
+                self.kept.append(self.buf)
             self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+            self.captured, self.filled = False, not capturing
+            if not capturing:
+                torch.cuda.current_stream(self.device).synchronize()
+        if capturing:
+            self.captured = True
+        elif not self.filled:
+            self.buf.zero_()
+            torch.cuda.current_stream(self.device).synchronize()
+            self.filled = True
         return self.buf
 
 
@@ -716,7 +733,8 @@ def paged_attention(q, cache: KVCache, cu_q, kv_len, pages, *, causal: bool = Tr
     heads); cu_q, kv_len, pages as for kv_append.  The token at position p sees the keys
     j <= p (all of them with causal=False) that are among the last `window` (0: no window) or
     the first `sinks`.  max_q: an upper bound on a sequence's new tokens, if the caller knows
-    one.  Returns out, or (out, lse) with return_lse; rows that see nothing are 0 (-inf)."""
+    one.  Returns out, or (out, lse) with return_lse; rows that see nothing are 0 (-inf).
+    Calls that may run at the same time (on several streams) need a workspace each."""
     _need(isinstance(cache, KVCache), "cache is not a KVCache")
     lse = True if return_lse else None
     if stream is not None:

@@ -844,12 +844,11 @@ bool paged_layout(long long tokens, int group, int d, int batch, int sms, PagedL
   if (d != 64 && d != 128) return false;
   const bool prompt = may_be_prompt(tokens, group);
   const size_t rows = static_cast<size_t>(2) * sms * (prompt ? prompt_part_rows() : DC_MAX_ROWS);
-  const size_t units = std::max<size_t>(std::min(batch, DC_BATCH),
-                                        prompt ? prompt_entries(static_cast<int>(tokens), group, batch) : 0);
+  const size_t items = prompt ? prompt_entries(static_cast<int>(tokens), group, batch) : 0;
   L.turn_off = WS_HDR_BYTES;
   L.cut_off = L.turn_off + ((static_cast<size_t>(sms) * 4 + 255) & ~size_t(255));
   L.prefix_off = L.cut_off + ((static_cast<size_t>(sms) * sizeof(CutUnit) + 255) & ~size_t(255));
-  L.part_off = L.prefix_off + (((units + 1) * 8 + 255) & ~size_t(255));
+  L.part_off = L.prefix_off + (((items + 1) * 8 + 255) & ~size_t(255));
   L.lse_off = L.part_off + rows * d * 4;
   L.total = (L.lse_off + rows * 4 + 255) & ~size_t(255);
   return true;

@@ -31,7 +31,7 @@ struct PagedParams {
   float* part_lse;
   uint32_t* turn;                      // decode: CTAs that are done with the unit begun by each CTA; 0 between calls
   CutUnit* cut;                        // prompts: one for each CTA
-  long long* prefix;                   // tiles of the units before each sequence / item (see the kernels)
+  long long* prefix;                   // prompts: places of one head before each item
   long long wait_ns;
   float scale_log2;                    // softmax scale * log2(e)
   int heads_q, group;                  // query heads; of them per key head
