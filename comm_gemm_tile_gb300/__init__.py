@@ -683,7 +683,7 @@ class KVCache:
     """A paged key / value cache: k, v [n_pages x heads x page_size x d] (any strides with d
     contiguous, the same for both; a cache laid out [n_pages x page_size x heads x d] is passed
     as k.transpose(1, 2)) in bf16, fp16 or float8_e4m3fn, the latter with k_scale, v_scale
-    [n_pages x heads] fp32.  KVCache.empty allocates one."""
+    [n_pages x heads] fp32, not negative.  KVCache.empty allocates one."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         self._c, self._device = _bind().cache(k, v, k_scale, v_scale)   # the bytes of an mk_kv_cache

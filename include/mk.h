@@ -445,7 +445,7 @@ typedef struct {
 /* A paged cache: element e of slot s, head h, page g of k (and of v) is at
  * g * page_stride + h * head_stride + s * slot_stride + e.  dtype MK_BF16, MK_F16,
  * or MK_E4M3: then a value is its code times the scale of its page and head
- * (k_scale, v_scale: [n_pages x heads] fp32, else NULL).  page_size is a power
+ * (k_scale, v_scale: [n_pages x heads] fp32, not negative; else NULL).  page_size is a power
  * of two, 8 .. 256; rows are whole 16-byte pieces. */
 typedef struct {
   void *k, *v;
