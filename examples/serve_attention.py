@@ -28,9 +28,7 @@ class AttentionLayer:
         self.w_o = [draw(self.hq * d, hidden) for _ in range(ranks)]
         self.freqs, self.magnitude = mk.rope_freqs(d, device=device)
         dtype = torch.float8_e4m3fn if cache == "e4m3" else torch.bfloat16
-        slots = lambda: torch.zeros(pages, self.hk, page, d, device=device).to(dtype)
-        scales = lambda: torch.ones(pages, self.hk, device=device) if cache == "e4m3" else None
-        self.caches = [mk.KVCache(slots(), slots(), scales(), scales()) for _ in range(ranks)]
+        self.caches = [mk.KVCache.empty(pages, self.hk, page, d, dtype, device) for _ in range(ranks)]
 
     def __call__(self, x, cu_q, kv_len, pages, max_q):
         """x: [tokens x hidden], the new tokens of every sequence, which kv_len already counts."""
