@@ -8,7 +8,7 @@
 // serves up to 256 rows.  The list of all (item, head, key tile) of the batch is
 // cut into one equal run per CTA (one CTA per SM), wherever that falls: causal
 // items of any length and few long ones alike keep every SM busy to the end.
-// Items cut by a run's end leave fp32 partial rows for the join (mk_paged.cu).
+// Items cut by a run's end leave fp32 partial rows for the join (below).
 //
 // Roles of a CTA's warps:
 //   4-7, 8-11 softmax of query tile 0 / 1, one row a thread: the 128 scores of a
@@ -27,10 +27,10 @@
 // A prompt of 8192 tokens, 32 query heads on 8, d = 128, bf16, causal: 427 us, 1.29 PFLOP/s of what
 // the mask leaves (67 % of the burst rate of a plain product, 75 % of its rate under the power cap).
 // The tensor pipe is busy 61 % of the time; a key tile takes the softmax warps about as long as the
-// products (the exponentials alone half of that), and changing items 5 %.  Over 8-bit caches the same
-// loop is bound by issue slots and shared memory together: the codes' conversion adds 128 conversions a
-// scheduler and 96 KB of shared memory traffic to a key tile (two pieces of 1000 tokens after 15000 to
-// 30000: 614 us, 1.04 PFLOP/s; the same over a bf16 cache 520 us).
+// products (the exponentials alone half of that), and changing items 5 %.  Over 8-bit caches that
+// chain is longer (two scales a weight; 32 scores at a time, with 128 registers for sixteen warps) and
+// the turning warps' conversions and shared memory traffic run beside it: two pieces of 1000 tokens
+// after 15000 to 30000, 614 us, 1.04 PFLOP/s; the same over a bf16 cache 520 us.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
