@@ -619,11 +619,15 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _new(shape, dtype, device, stream):
-    """An output of a call on a given stream, taken from that stream's pool."""
+def _on(stream, device):
+    """A context in which outputs of a call on a given stream come from that stream's pool."""
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
-    with torch.cuda.stream(stream):
+    return torch.cuda.stream(stream)
+
+
+def _new(shape, dtype, device, stream):
+    with _on(stream, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
@@ -669,10 +673,14 @@ def rope(x, freqs, positions=None, *, start: int = 0, interleaved: bool = False,
     The first 2 * len(freqs) elements of every head are turned by positions[t] * freqs (or
     (start + t) * freqs) and scaled by magnitude; interleaved pairs neighbours instead of
     halves.  inverse=True is the gradient: rope(dy, ..., inverse=True) = dx.
-    Returns out (same shape and strides as x unless given; out=x works in place)."""
+    Returns out (unless given: of x's shape and memory order, dense; out=x works in place)."""
     if out is None:
         _need(isinstance(x, torch.Tensor), "x is not a tensor")
-        out = torch.empty_like(x) if stream is None else _new(x.shape, x.dtype, x.device, stream)
+        if stream is None:
+            out = torch.empty_like(x)
+        else:
+            with _on(stream, x.device):
+                out = torch.empty_like(x)
     st = _bind().rope(_address("mk_rope"), x, out, freqs, positions, start, interleaved, inverse, magnitude, _raw(stream))
     if st:
         _check(st, "mk_rope")
