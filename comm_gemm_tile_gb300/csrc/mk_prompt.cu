@@ -733,8 +733,9 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 // The weights 2^(c s + nref) of 32 scores as 16-bit pairs; returns their sum.  8-bit caches: scales
 // has those of the four groups of 8 keys, which c is multiplied by, and from 16 on those of their
-// values; the weight of a value is the weight times its scale and F, summed in sum_v.
-template <class T, bool E8>
+// values; the weight of a value is the weight times its scale and F, summed in sum_v.  ABOVE: the scores
+// went through above(), so c is 1 and the keys' scales are in them.
+template <class T, bool E8, bool ABOVE = false>
 __device__ __forceinline__ float weights(const uint32_t (&s)[32], uint32_t* w, float c, float nref, const float* scales,
                                          float F, float& sum_v) {
   const uint64_t nref2 = two(nref, nref);
@@ -744,7 +745,7 @@ __device__ __forceinline__ float weights(const uint32_t (&s)[32], uint32_t* w, f
   for (int g = 0; g < 4; ++g) {
     float cg = c, vg = 1.f;
     if (E8) {
-      cg *= scales[g];
+      if (!ABOVE) cg *= scales[g];
       if (cg == 0.f) cg = 1e-37f;              // a score of -infinity (masked) stays one
       vg = fminf(fmaxf(F * scales[16 + g], -3e38f), 3e38f);
     }
@@ -801,6 +802,153 @@ __device__ __forceinline__ void largest(const uint32_t (&s)[32], float c, const 
 __device__ __forceinline__ uint32_t below(int n, int a) {
   const int k = n - 32 * a;
   return k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u;
+}
+
+// The keys among 32 a .. 32 a + 31 of the tile at key0 that the row at position pos sees, as bits.
+__device__ __forceinline__ uint32_t seen_bits(const PagedParams& p, int pos, int len, int key0, int a) {
+  uint32_t see = below((p.causal ? min(len, pos + 1) : len) - key0, a);
+  if (p.window > 0) see &= ~below(pos - p.window + 1 - key0, a) | below(p.sinks - key0, a);
+  return see;
+}
+// O of a query tile, this thread's row, times f.
+template <int D>
+__device__ __forceinline__ void scale_output(uint32_t ocol, float f) {
+#pragma unroll 1
+  for (int a = 0; a < D / 16; ++a) {
+    uint32_t v[16];
+    tc_ld_32x32b_x16(ocol + 16u * a, v);
+    tc_wait_ld();
+#pragma unroll
+    for (int q = 0; q < 16; ++q) v[q] = __float_as_uint(__uint_as_float(v[q]) * f);
+    tc_st_32x32b_x16(ocol + 16u * a, v);
+  }
+}
+
+// Scores far from 0.  fma(s, c, -m) has in it what the rounding of m took off: 1/16 where |m| is 2^20, 64 at
+// 2^31, so that the weight of the largest score itself would be far from 1, or nothing, or past every limit
+// however often m moves.  From FAR on, the rest of a segment goes a slower way: m is moved to the largest
+// score of every half tile first, and the products are rounded before m is taken off, as m's own was: the
+// largest weight is 1 and none is larger.
+constexpr float FAR = 1048576.f;             // 2^20
+template <bool E8>
+__device__ __forceinline__ void above(uint32_t (&s)[32], float c, const float* scales, float m) {
+  const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    float cg = c;
+    if (E8) {
+      cg *= scales[g];
+      if (cg == 0.f) cg = 1e-37f;
+    }
+#pragma unroll
+    for (int q = 8 * g; q < 8 * g + 8; ++q)
+      s[q] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(s[q]), cg), ref));
+  }
+}
+// A row's state inside a segment: as the loop over its tiles left it, and as far_rest does.
+struct FarRow {
+  float m, l, s_a, f, F;
+  float vr;                                  // 8-bit: the largest log2 of a weight times its value's scale, next to m
+  float c;
+  uint32_t scol, ocol, u, n;
+  int k, side, k0, k1, first;                // next tile and half of it; the segment's tiles, this row's first one
+  int g, len, pos, g0, g1;
+  KeyTiles t;
+  bool real, narrow;
+};
+// The rest of a segment, once a row of the warp is far from 0.  (A function of its own, called outside the loop
+// over tiles, after a test where m moves: with the test for every half, or the call inside, the two pieces above
+// take 651 to 669 us in place of 618; without either 613.)
+template <class T, bool E8, int D>
+__device__ __noinline__ bool far_rest(const PagedParams& p, volatile int* dead, uint32_t bars, const uint8_t* sm,
+                                      FarRow* row) {
+  constexpr float SHIFT = std::is_same<T, __half>::value ? 7.f : 0.f;
+  FarRow r = *row;
+  const int lane = threadIdx.x & 31;
+  bool there = true;                         // the scores of tile k
+#pragma unroll 1
+  for (; r.k < r.k1; ++r.k, ++r.u) {
+    if (r.narrow && ((r.k - r.k0) & 1) != r.g) continue;
+    if (!there) {
+      if (!pr_wait(dead, p, bars + B_S + 8u * r.g, r.n & 1u, WHERE_EPILOGUE)) return false;
+      tc_fence_after();
+    }
+    there = false;
+    const int key0 = r.t.tile(r.k) * PR_T;
+    const bool cover = r.real && r.g1 >= r.g0 && !all_seen(p, r.g0, r.g1, r.len, key0, PR_T);
+#pragma unroll 1
+    for (; r.side < 2; ++r.side) {
+      const float* scales =
+          E8 ? reinterpret_cast<const float*>(sm + Plan<E8, D>::SCALES) + (r.u & 3u) * 32 + 8 * r.side : nullptr;
+      uint32_t s[32], wt[16];
+      auto get = [&](int a) {
+        tc_ld_32x32b_x32(r.scol + 64u * r.side + 32u * a, s);
+        tc_wait_ld_regs(s);
+        if (cover) {
+          const uint32_t see = seen_bits(p, r.pos, r.len, key0, 2 * r.side + a);
+#pragma unroll
+          for (int q = 0; q < 32; ++q)
+            if (!(see & (1u << q))) s[q] = 0xff800000u;        // -inf
+        }
+      };
+      float mn = r.m, factor = 1.f, factor_o = 1.f, none = -INFINITY;
+#pragma unroll 1
+      for (int a = 0; a < 2; ++a) {
+        get(a);
+        largest<E8>(s, r.c, E8 ? scales + 4 * a : scales, mn, none);
+      }
+      const float f_was = r.f;
+      if (E8) {
+        r.vr = r.m == -INFINITY ? -INFINITY : r.vr + (r.m - mn);
+#pragma unroll 1
+        for (int a = 0; a < 2; ++a) {
+          get(a);
+          above<E8>(s, r.c, scales + 4 * a, mn);
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int q = 8 * g; q < 8 * g + 8; ++q) top = fmaxf(top, __uint_as_float(s[q]));
+            r.vr = fmaxf(r.vr, top + __log2f(fabsf(scales[16 + 4 * a + g])));
+          }
+        }
+        r.f = fminf(fmaxf(2.f - r.vr, -126.f), 100.f);
+        r.F = pg_ex2(r.f);
+      }
+      if (r.l != 0.f || r.s_a != 0.f) {      // else O is nothing, or zeros
+        factor = pg_ex2(r.m - mn);
+        factor_o = E8 ? pg_ex2(r.m - mn + (r.f - f_was)) : factor;
+      }
+      r.m = mn;
+      r.l *= factor;
+      r.s_a *= factor;
+      if ((r.side != 0 || r.k > r.first) && __any_sync(0xffffffffu, factor_o != 1.f)) {
+        if (r.side != 0) {
+          if (!pr_wait(dead, p, bars + B_HALF + 8u * r.g, r.n & 1u, WHERE_EPILOGUE)) return false;
+          tc_fence_after();
+        }
+        scale_output<D>(r.ocol, factor_o);
+      }
+      float sum = 0.f, sum_v = 0.f;
+#pragma unroll 1
+      for (int a = 0; a < 2; ++a) {          // (the weights' columns are those of scores already read)
+        get(a);
+        above<E8>(s, r.c, E8 ? scales + 4 * a : scales, mn);
+        sum += weights<T, E8, true>(s, wt, 1.f, SHIFT, E8 ? scales + 4 * a : scales, r.F, sum_v);
+        tc_st_32x32b_x16(r.scol + 32u * r.side + 16u * a, wt);
+      }
+      tc_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + B_GO + 16u * r.g + 8u * r.side);
+      if (r.side == 0) r.s_a = sum;
+      else r.l += r.s_a + sum;
+    }
+    r.side = 0;
+    ++r.n;
+  }
+  *row = r;
+  return true;
 }
 
 // Pieces of four rows by row -> by place: lane i of four gets piece i of each of their rows.
@@ -890,7 +1038,9 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uin
     float mv = -INFINITY, f = 0.f, F = 1.f;
     bool ready = false;                                    // every row of the warp has a reference
     const int k_first = k0 + (narrow ? g : 0);
-    for (int k = k0; k < k1; ++k, ++u) {
+    int k = k0, from = 0;                                  // from: the half to go on with
+    float s_a = 0.f;                                       // the first half's sum
+    for (; k < k1; ++k, ++u) {
       const int key0 = it.t.tile(k) * PR_T;
       const bool masked = g1 >= g0 && !all_seen(p, g0, g1, it.len, key0, PR_T);
       if (narrow && ((k - k0) & 1) != g) continue;
@@ -903,7 +1053,7 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uin
       // Half the row at a time, its weights handed over once written: the products start on the
       // first while the second is being computed.  (One copy of this code for both halves, 64
       // scores in registers: with the whole row unrolled the instructions did not come fast enough.)
-      float s_a = 0.f;
+      s_a = 0.f;
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         const float* scales = E8 ? reinterpret_cast<const float*>(sm + Plan<E8, D>::SCALES) + (u & 3u) * 32 + 8 * half : nullptr;
@@ -919,10 +1069,7 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uin
         auto cover = [&](int a) {
           uint32_t (&s)[32] = sv[a & (HELD - 1)];
           if (masked && real) {
-            const int hi = (p.causal ? min(it.len, pos + 1) : it.len) - key0;
-            uint32_t see = below(hi, 2 * half + a);
-            if (p.window > 0)
-              see &= ~below(pos - p.window + 1 - key0, 2 * half + a) | below(p.sinks - key0, 2 * half + a);
+            const uint32_t see = seen_bits(p, pos, it.len, key0, 2 * half + a);
 #pragma unroll
             for (int q = 0; q < 32; ++q)
               if (!(see & (1u << q))) s[q] = 0xff800000u;          // -inf
@@ -945,7 +1092,8 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uin
           return sv[a & (HELD - 1)];
         };
         // No maximum is taken of a tile: the reference m, the largest of the first scores, stands as
-        // long as no sum of weights passes LIMIT, which bounds each weight too.
+        // long as no sum of weights passes LIMIT, which bounds each weight too.  Once m has moved (and is
+        // not FAR from 0) no sum of this half can: two passes at most.
         bool move = !ready;
         float sum;
         while (true) {
@@ -969,20 +1117,19 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uin
             if (E8) F = pg_ex2(f);
             l *= factor;
             s_a *= factor;
-            ready = __all_sync(0xffffffffu, m != -INFINITY);
+            ready = __all_sync(0xffffffffu, fabsf(m) < FAR);
             if ((half != 0 || k > k_first) && __any_sync(0xffffffffu, factor_o != 1.f)) {
               if (half != 0) {
                 if (!pr_wait(dead, p, bars + B_HALF + 8u * g, n & 1u, WHERE_EPILOGUE)) return;
                 tc_fence_after();
               }
-#pragma unroll 1
-              for (int a = 0; a < D / 16; ++a) {
-                uint32_t v[16];
-                tc_ld_32x32b_x16(ocol + 16u * a, v);
-                tc_wait_ld();
-#pragma unroll
-                for (int q = 0; q < 16; ++q) v[q] = __float_as_uint(__uint_as_float(v[q]) * factor_o);
-                tc_st_32x32b_x16(ocol + 16u * a, v);
+              scale_output<D>(ocol, factor_o);
+            }
+            if (!ready) {                                  // nothing seen yet, or far from 0
+              ready = __all_sync(0xffffffffu, m != -INFINITY);
+              if (__builtin_expect(__any_sync(0xffffffffu, fabsf(m) >= FAR && m != -INFINITY), 0)) {
+                from = half;
+                goto far;
               }
             }
           }
@@ -1002,6 +1149,17 @@ __device__ void pr_softmax(const PagedParams& p, Walk w, volatile int* dead, uin
         else l += s_a + sum;
       }
       ++n;
+    }
+    if (false) {
+    far:                                                   // the rest of the segment, from tile k on
+      FarRow r = {m, l, s_a, f, F, l == 0.f && s_a == 0.f ? -INFINITY : 2.f - f, c, scol, ocol, u, n, k, from, k0, k1,
+                  k_first, g, it.len, pos, g0, g1, it.t, real, narrow};
+      if (!far_rest<T, E8, D>(p, dead, bars, sm, &r)) return;
+      m = r.m;
+      l = r.l;
+      f = r.f;
+      u += k1 - k;                                         // (counted here: the same for every thread)
+      n += narrow ? (k1 - k + 1) >> 1 : k1 - k;
     }
     if (!pr_wait(dead, p, bars + B_O + 8u * g, o_ph, WHERE_EPILOGUE)) return;
     o_ph ^= 1u;
