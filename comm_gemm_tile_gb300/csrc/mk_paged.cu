@@ -294,7 +294,7 @@ __device__ __forceinline__ void consume(const PagedParams& p, const Segment& g, 
   const int p0 = g.len - g.n, p1 = g.len - 1, tiles = g.k1 - g.k0;
   // per column of S^T and O^T that this lane holds: query rows 8 q + 2 c and + 1
   float m[NQ][2], l[NQ][2];            // maximum and sum of the weights
-  float mv[NQ][2];                     // 8-bit: maximum of weight times value scale, O's reference
+  float mv[NQ][2];                     // 8-bit: log2 of the largest weight times value scale, next to m: O's reference
 #pragma unroll
   for (int q = 0; q < NQ; ++q)
 #pragma unroll
@@ -442,36 +442,49 @@ __device__ __forceinline__ void consume(const PagedParams& p, const Segment& g, 
       uint32_t pf[NQ][MT][2];
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
-        float top[2] = {-INFINITY, -INFINITY}, top_v[2] = {-INFINITY, -INFINITY};
+        // Scores are rounded products before the maximum is taken off, so that the largest weight is 1 however
+        // far from 0 they are (one fma would leave in the rounding of the maximum: 64 at 2^31).
+        float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const int e = x & 1, h = x >> 1;
-            if (E8) s[q][t][x] *= row_scale[q][e] * ks[2 * t + h];
+            s[q][t][x] = __fmul_rn(s[q][t][x], E8 ? row_scale[q][e] * ks[2 * t + h] : p.scale_log2);
             if (masked && !key_seen(p, pos[q][e], g.len, key0 + 16 * t + perm + 8 * h)) s[q][t][x] = -INFINITY;
             top[e] = fmaxf(top[e], s[q][t][x]);
-            if (E8) top_v[e] = fmaxf(top_v[e], s[q][t][x] + lv[2 * t + h]);
           }
-        float nref[2], alpha[2], rel[2];
+        float mref[2], alpha[2], rel[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
-          for (int y = 4; y < 32; y <<= 1) {
-            top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], y));
-            if (E8) top_v[e] = fmaxf(top_v[e], __shfl_xor_sync(0xffffffffu, top_v[e], y));
-          }
-          const float mn = fmaxf(m[q][e], E8 ? top[e] : top[e] * p.scale_log2);
-          const float mref = mn == -INFINITY ? 0.f : mn;
-          alpha[e] = pg_ex2(m[q][e] - mref);
+          for (int y = 4; y < 32; y <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], y));
+          const float mn = fmaxf(m[q][e], top[e]);
+          mref[e] = mn == -INFINITY ? 0.f : mn;
+          const float down = m[q][e] - mref[e];
+          alpha[e] = pg_ex2(down);
           m[q][e] = mn;
           l[q][e] *= alpha[e];
-          nref[e] = SHIFT - mref;
-          if (E8) {
-            const float mvn = fmaxf(mv[q][e], top_v[e]), vref = mvn == -INFINITY ? 0.f : mvn;
+          if (E8) mv[q][e] += down;
+        }
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) s[q][t][x] = __fsub_rn(s[q][t][x], mref[x & 1]);
+        if (E8) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top_v = -INFINITY;
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) top_v = fmaxf(top_v, s[q][t][2 * h + e] + lv[2 * t + h]);
+#pragma unroll
+            for (int y = 4; y < 32; y <<= 1) top_v = fmaxf(top_v, __shfl_xor_sync(0xffffffffu, top_v, y));
+            const float mvn = fmaxf(mv[q][e], top_v), vref = mvn == -INFINITY ? 0.f : mvn;
             alpha[e] = pg_ex2(mv[q][e] - vref);
             mv[q][e] = mvn;
-            rel[e] = mvn == -INFINITY ? 0.f : pg_ex2(mref - vref);
+            rel[e] = mvn == -INFINITY ? 0.f : pg_ex2(-vref);
           }
         }
         if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
@@ -486,7 +499,7 @@ __device__ __forceinline__ void consume(const PagedParams& p, const Segment& g, 
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const int e = x & 1;
-            w[x] = pg_ex2(E8 ? s[q][t][x] + nref[e] : fmaf(s[q][t][x], p.scale_log2, nref[e]));
+            w[x] = pg_ex2(HALF ? s[q][t][x] + SHIFT : s[q][t][x]);
             l[q][e] += w[x];
             if (E8) w[x] = w[x] == 0.f ? 0.f : w[x] * (vs[2 * t + (x >> 1)] * rel[e]);
           }
@@ -577,7 +590,7 @@ __device__ __forceinline__ void consume(const PagedParams& p, const Segment& g, 
         float* at = wk.ml + (warp * S::ROWS + 8 * q + 2 * c + e) * 3;
         at[0] = m[q][e];
         at[1] = l[q][e];
-        at[2] = !E8 ? 1.f : mv[q][e] == -INFINITY ? 0.f : pg_ex2(mv[q][e] - m[q][e]);
+        at[2] = !E8 ? 1.f : pg_ex2(mv[q][e]);
       }
   }
   auto barrier = [] { asm volatile("bar.sync 1, %0;" ::"n"(32 * S::WARPS) : "memory"); };
