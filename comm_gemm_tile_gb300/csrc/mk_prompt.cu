@@ -807,7 +807,8 @@ __device__ __forceinline__ uint32_t below(int n, int a) {
 // The keys among 32 a .. 32 a + 31 of the tile at key0 that the row at position pos sees, as bits.
 __device__ __forceinline__ uint32_t seen_bits(const PagedParams& p, int pos, int len, int key0, int a) {
   uint32_t see = below((p.causal ? min(len, pos + 1) : len) - key0, a);
-  if (p.window > 0) see &= ~below(pos - p.window + 1 - key0, a) | below(p.sinks - key0, a);
+  // (keys before pos - window + 1, in an order that no window overflows)
+  if (p.window > 0) see &= ~below(max(pos - key0 + 1, p.window) - p.window, a) | below(p.sinks - key0, a);
   return see;
 }
 // O of a query tile, this thread's row, times f.
