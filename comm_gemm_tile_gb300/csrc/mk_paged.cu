@@ -826,7 +826,7 @@ bool cache_map(CUtensorMap* m, const mk_kv_cache* c, const void* base, const voi
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c->d), static_cast<cuuint64_t>(c->page_size),
                               static_cast<cuuint64_t>(c->heads),
                               static_cast<cuuint64_t>(std::max(1LL, c->n_pages))};
-  // a stride of a dimension of one element says nothing, but the map wants it positive
+  // the stride of a dimension of one element may be 0 (view_of), but the map wants it positive
   const cuuint64_t row = static_cast<cuuint64_t>(c->d) * esz;
   const cuuint64_t strides[3] = {c->slot_stride > 0 ? static_cast<cuuint64_t>(c->slot_stride) * esz : row,
                                  c->head_stride > 0 ? static_cast<cuuint64_t>(c->head_stride) * esz : row,
@@ -906,6 +906,7 @@ mk_status mk_paged_attention(const void* q, void* out, float* lse, mk_dtype dtyp
   if (((q_token | q_head | o_token | o_head) * 2) & 15) return MK_ERR_INVALID;
   if (q_token < 0 || q_head < 0 || o_token < 0 || o_head < 0 || (reinterpret_cast<uintptr_t>(lse) & 3u))
     return MK_ERR_INVALID;
+  if ((o_token == 0 && tokens > 1) || (o_head == 0 && heads_q > 1)) return MK_ERR_INVALID;   // rows that share memory
   if (dev_sms <= 0) return MK_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   p.q = q;
@@ -934,8 +935,10 @@ mk_status mk_paged_attention(const void* q, void* out, float* lse, mk_dtype dtyp
   if (p.grid <= 0) return MK_ERR_UNSUPPORTED;
   // Which kernels: by the most new tokens a sequence can have.  A kernel that is launched alone
   // takes every sequence, whatever the hint was; of two, each takes its side of PG_DECODE_ROWS.
+  // Queries with a stride of 0 are the decode kernel's: the prompt kernel's tensor map has no such stride.
   const long long most = max_q > 0 ? std::min<long long>(max_q, tokens) : tokens;
-  const bool prompt = may_be_prompt(most, p.group);
+  const bool q_map = (q_token > 0 || tokens == 1) && (q_head > 0 || heads_q == 1);
+  const bool prompt = q_map && may_be_prompt(most, p.group);
   const bool decode = !prompt || (seqs->batch > 1 && most * seqs->batch != tokens);
   if (decode) {
     const int tile = d == 128 && !e8 ? Shape<__half, false, 128, 1>::KT : 64;

@@ -48,7 +48,9 @@ bool view_of(const mk_kv_cache* c, CacheView& out) {
   int lg = 0;
   while ((1 << lg) < c->page_size && lg < 30) ++lg;
   if (c->page_size < 8 || c->page_size > 256 || (1 << lg) != c->page_size) return false;
-  if (c->page_stride < 0 || c->head_stride < 0 || c->slot_stride < 0) return false;
+  if (c->page_stride < 0 || c->head_stride < 0 || c->slot_stride <= 0) return false;
+  // pages or heads that share their memory: appends would race, and a tensor map has no stride of 0
+  if ((c->page_stride == 0 && c->n_pages > 1) || (c->head_stride == 0 && c->heads > 1)) return false;
   if (c->n_pages > 0 && (!c->k || !c->v)) return false;
   if (c->dtype == MK_E4M3 && c->n_pages > 0 && (!c->k_scale || !c->v_scale)) return false;
   const uintptr_t a = reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v);
@@ -644,6 +646,10 @@ bool rotation_ok(const mk_rotation* r, int d, Rotation& out) {
 bool pieces_ok(const void* x, long long st, long long sh, int esz) {
   return !(reinterpret_cast<uintptr_t>(x) & 15u) && !((st * esz) & 15) && !((sh * esz) & 15);
 }
+// Whether rows that are written have memory of their own (expanded tensors do not).
+bool rows_apart(long long st, long long sh, long long tokens, int heads) {
+  return (st != 0 || tokens <= 1) && (sh != 0 || heads <= 1);
+}
 bool rows_vec(int d, int rot, int n) { return rot % (2 * n) == 0 && d % (2 * n) == 0; }
 
 }  // namespace
@@ -665,6 +671,7 @@ mk_status mk_rope(const void* x, void* y, mk_dtype dtype, long long tokens, int 
   if (tokens == 0 || heads == 0) return MK_OK;
   const int esz = dtype == MK_F32 ? 4 : 2;
   if (!x || !y || ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y)) & (esz - 1))) return MK_ERR_INVALID;
+  if (!rows_apart(y_token, y_head, tokens, heads)) return MK_ERR_INVALID;
   p.x = x;
   p.y = y;
   p.xs_t = x_token;
@@ -707,6 +714,7 @@ mk_status mk_kv_append(const mk_kv_cache* cache, const void* k, const void* v, m
   if (((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) | reinterpret_cast<uintptr_t>(q) |
         reinterpret_cast<uintptr_t>(q_out)) & 1u))
     return MK_ERR_INVALID;
+  if (q && !rows_apart(qo_token, qo_head, tokens, heads_q)) return MK_ERR_INVALID;
   p.x = q;
   p.y = q_out;
   p.xs_t = q_token;

@@ -401,7 +401,9 @@ size_t mk_mlp_trace_entries(int R, long long m, long long h, long long f_r, cons
  * decode step or the next piece of a prompt needs next to mk_ring_attention.
  * These entry points keep no epoch: a CUDA graph may capture them (with the
  * workspace, where they take one, reserved for the graph).  Strides count
- * elements; the last dimension (d) is contiguous.
+ * elements; the last dimension (d) is contiguous.  A stride of 0 (an expanded
+ * dimension) is for inputs: outputs and caches with one are refused unless that
+ * dimension has one element.
  *
  * Rotation: the pair (a, b) of a head at position p with frequency f becomes
  *   (a cos(p f) - b sin(p f), b cos(p f) + a sin(p f)) * magnitude.
