@@ -241,29 +241,27 @@ def _check(st: int, what: str):
 
 class Workspace:
     """A device workspace, zero-filled once at (re)allocation as the library requires, before any stream uses
-    it.  A buffer that a captured call uses stays allocated when a larger one takes its place: the graph keeps
-    its address."""
+    it.  A buffer stays allocated when a larger one takes its place, since calls in flight on any stream and
+    graphs keep its address; buffers at least double, so that those kept are no more than the last."""
 
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
         self.buf = None
-        self.kept = []             # buffers that graphs use
-        self.captured = False      # buf is one of them
+        self.kept = []             # outgrown buffers
         self.filled = True         # False: allocated while capturing, so that only a replay would fill it
 
     def get(self, nbytes: int) -> torch.Tensor:
         nbytes = max(int(nbytes), 256)
-        capturing = torch._C._cuda_isCurrentStreamCapturing()
         if self.buf is None or self.buf.numel() < nbytes:
-            if self.captured:
+            if self.buf is not None:
                 self.kept.append(self.buf)
+                nbytes = max(nbytes, 2 * self.buf.numel())
+            capturing = torch._C._cuda_isCurrentStreamCapturing()
             self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
-            self.captured, self.filled = False, not capturing
+            self.filled = not capturing
             if not capturing:
                 torch.cuda.current_stream(self.device).synchronize()
-        if capturing:
-            self.captured = True
-        elif not self.filled:
+        elif not self.filled and not torch._C._cuda_isCurrentStreamCapturing():
             self.buf.zero_()
             torch.cuda.current_stream(self.device).synchronize()
             self.filled = True
