@@ -8,7 +8,9 @@ The R virtual ranks of an op are R separate device buffers on one GPU.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import math
 import dataclasses
 import os
@@ -242,7 +244,9 @@ def _check(st: int, what: str):
 class Workspace:
     """A device workspace, zero-filled once at (re)allocation as the library requires, before any stream uses
     it.  A buffer stays allocated when a larger one takes its place, since calls in flight on any stream and
-    graphs keep its address; buffers at least double, so that those kept are no more than the last."""
+    graphs keep its address; buffers at least double, so that those kept are no more than the last.  A buffer made
+    while capturing is filled by every captured call that uses it, until a call outside has filled it: graphs may be
+    replayed in any order."""
 
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
@@ -250,21 +254,25 @@ class Workspace:
         self.kept = []             # outgrown buffers
         self.filled = True         # False: allocated while capturing, so that only a replay would fill it
 
-    def get(self, nbytes: int) -> torch.Tensor:
+    def get(self, nbytes: int, stream=None) -> torch.Tensor:
+        """A buffer of at least nbytes for a call on the given stream (None: the current one)."""
         nbytes = max(int(nbytes), 256)
-        if self.buf is None or self.buf.numel() < nbytes:
-            if self.buf is not None:
-                self.kept.append(self.buf)
-                nbytes = max(nbytes, 2 * self.buf.numel())
-            capturing = torch._C._cuda_isCurrentStreamCapturing()
-            self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+        large = self.buf is not None and self.buf.numel() >= nbytes
+        if large and self.filled:
+            return self.buf
+        capturing = torch._C._cuda_isCurrentStreamCapturing()
+        with contextlib.nullcontext() if stream is None else _on(stream, self.device):
+            capturing = capturing or torch._C._cuda_isCurrentStreamCapturing()
+            if large:
+                self.buf.zero_()
+            else:
+                if self.buf is not None:
+                    self.kept.append(self.buf)
+                    nbytes = max(nbytes, 2 * self.buf.numel())
+                self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
             self.filled = not capturing
             if not capturing:
                 torch.cuda.current_stream(self.device).synchronize()
-        elif not self.filled and not torch._C._cuda_isCurrentStreamCapturing():
-            self.buf.zero_()
-            torch.cuda.current_stream(self.device).synchronize()
-            self.filled = True
         return self.buf
 
 
@@ -297,7 +305,7 @@ def device_status(workspace: Workspace | None = None, stream=None, device=None):
     first = (MK_OK, 0)
     for w in spaces:
         detail = ctypes.c_longlong(0)
-        st = lib().mk_get_device_status(ctypes.c_void_p(w.get(256).data_ptr()),
+        st = lib().mk_get_device_status(ctypes.c_void_p(w.get(256, stream).data_ptr()),
                                         ctypes.c_void_p(_stream(stream, w.device)), ctypes.byref(detail))
         if first[0] == MK_OK:
             first = (int(st), int(detail.value))
@@ -323,7 +331,7 @@ def ag_gemm(a_shards, b, *, local_rank: int = 0, out_dtype=torch.bfloat16, a_gat
     nb = workspace_size(OP_AG_GEMM, R, m_r, n, k, cfg)
     if nb == 0:
         raise MkError(MK_ERR_INVALID, "mk_workspace_size(AG)")
-    buf = ws.get(nb)
+    buf = ws.get(nb, stream)
     st = lib().mk_ag_gemm(_ptrs(a_shards), b.data_ptr(), a_gathered.data_ptr(), c.data_ptr(),
                           _dt(c.dtype), R, local_rank, m_r, n, k, buf.data_ptr(), buf.numel(),
                           _cfgp(cfg), _stream(stream, dev))
@@ -337,7 +345,7 @@ def _rs_ar(fn, op, a, b, outs, R, m, n, k, cfg, workspace, stream, what):
     nb = workspace_size(op, R, m, n, k, cfg)
     if nb == 0:
         raise MkError(MK_ERR_INVALID, f"mk_workspace_size({what})")
-    buf = ws.get(nb)
+    buf = ws.get(nb, stream)
     st = fn(_ptrs(a), _ptrs(b), _ptrs(outs), _dt(outs[0].dtype), R, m, n, k, buf.data_ptr(),
             buf.numel(), _cfgp(cfg), _stream(stream, dev))
     _check(st, what)
@@ -470,7 +478,7 @@ def moe_dispatch_gemm(x, logits, w, *, E_loc: int, topk: int = 2, cap_rows: int 
     nb = moe_workspace_size(R, E_loc, topk, T, H, N, cap, cfg)
     if nb == 0:
         raise MkError(MK_ERR_INVALID, "mk_moe_workspace_size")
-    buf = ws.get(nb)
+    buf = ws.get(nb, stream)
     st = lib().mk_moe_dispatch_gemm(_ptrs(x), _ptrs(logits), _ptrs(w), R, E_loc, topk, T, H, N, cap,
                                     o["topk_idx"].data_ptr(), o["counts"].data_ptr(),
                                     _ptrs(o["recv_src"]), o["recv_counts"].data_ptr(),
@@ -508,7 +516,7 @@ def moe_combine(h, w2, gates, recv_src, counts, *, E_loc: int, topk: int = 2,
     nb = moe_combine_workspace_size(R, E_loc, topk, T, N, H, cap, cfg)
     if nb == 0:
         raise MkError(MK_ERR_INVALID, "mk_moe_combine_workspace_size")
-    buf = ws.get(nb)
+    buf = ws.get(nb, stream)
     st = lib().mk_moe_combine(_ptrs(h), _ptrs(w2), _ptrs(gates), _ptrs(recv_src), counts.data_ptr(),
                               R, E_loc, topk, T, N, H, cap, _ptrs(o["ret"]), _ptrs(o["out"]),
                               buf.data_ptr(), buf.numel(), _cfgp(cfg), _stream(stream, dev))
@@ -541,7 +549,7 @@ def mlp_ag_rs(x_shards, w1, w2, *, x_gathered=None, hid=None, y_blocks=None,
     nb = mlp_workspace_size(R, m, h, f_r, cfg)
     if nb == 0:
         raise MkError(MK_ERR_INVALID, "mk_mlp_workspace_size")
-    buf = ws.get(nb)
+    buf = ws.get(nb, stream)
     st = lib().mk_mlp_ag_rs(_ptrs(x_shards), _ptrs(w1), _ptrs(w2), R, m, h, f_r, x_gathered.data_ptr(),
                             _ptrs(hid), _ptrs(y_blocks), buf.data_ptr(), buf.numel(), _cfgp(cfg),
                             _stream(stream, dev))
@@ -575,7 +583,7 @@ def ring_attention(q, k, v, *, causal: bool = False, scale: float | None = None,
     nb = int(lib().mk_ring_attention_workspace_size(R, heads, s_r, d, int(causal), _cfgp(cfg)))
     if nb == 0:
         raise MkError(MK_ERR_INVALID, "mk_ring_attention_workspace_size")
-    buf = ws.get(nb)
+    buf = ws.get(nb, stream)
     st = lib().mk_ring_attention(_ptrs(q), _ptrs(k), _ptrs(v), R, heads, s_r, d, int(causal),
                                  float(scale), kr, vr, _ptrs(out), buf.data_ptr(), buf.numel(),
                                  _cfgp(cfg), _stream(stream, dev))
@@ -719,7 +727,7 @@ def kv_append(cache: KVCache, k, v, cu_q, kv_len, pages, *, q=None, freqs=None, 
     if q is not None and q_out is None and stream is not None:
         q_out = _new(q.shape, q.dtype, q.device, stream)
     st, q_out = _bind().append(_address("mk_kv_append"), cache._c, cache._device, k, v, cu_q, kv_len, pages, q, q_out,
-                               freqs, positions, interleaved, magnitude, (workspace or _default_ws.get(cache._device) or _ws(None, cache.k.device)).get(256),
+                               freqs, positions, interleaved, magnitude, (workspace or _default_ws.get(cache._device) or _ws(None, cache.k.device)).get(256, stream),
                                _raw(stream))
     if st:
         _check(st, "mk_kv_append")
@@ -750,10 +758,12 @@ def paged_attention(q, cache: KVCache, cu_q, kv_len, pages, *, causal: bool = Tr
         if return_lse:
             lse = _new(q.shape[:2], torch.float32, q.device, stream)
     c = cfg.c() if cfg is not None else None
+    get = (workspace or _default_paged_ws.get(cache._device) or _ws(None, cache.k.device, _default_paged_ws)).get
+    if stream is not None:
+        get = functools.partial(get, stream=stream)
     st, out, lse = _bind().attention(_address("mk_paged_attention"), _address("mk_paged_attention_workspace_size"),
-                                     (workspace or _default_paged_ws.get(cache._device) or
-                                      _ws(None, cache.k.device, _default_paged_ws)).get, q, cache._c, cache._device,
-                                     cu_q, kv_len, pages, causal, window, sinks, scale, max_q, out, lse,
+                                     get, q, cache._c, cache._device, cu_q, kv_len, pages, causal, window, sinks, scale,
+                                     max_q, out, lse,
                                      ctypes.addressof(c) if c is not None else None, _raw(stream))
     if st:
         _check(st, "mk_paged_attention")
