@@ -606,7 +606,7 @@ def _bind():
             raise RuntimeError("_mkbind.so is not built; run comm_gemm_tile_gb300/build.py "
                                "(or __graft_entry__.build())") from e
         _mkbind.setup((torch.bfloat16, torch.float32, torch.float16, FP8, torch.int32, torch.int64, torch.float64),
-                      torch._C._cuda_getCurrentRawStream, torch.empty)
+                      torch._C._cuda_getCurrentRawStream, torch.empty, torch._C._cuda_getDevice)
         _bound = _mkbind
     return _bound
 

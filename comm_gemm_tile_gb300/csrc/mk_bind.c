@@ -24,6 +24,7 @@ static PyObject *dtypes[7];        /* bf16, f32, f16, e4m3, i32, i64, f64 */
 static const int dtype_codes[7] = {MK_BF16, MK_F32, MK_F16, MK_E4M3, T_I32, T_I64, T_F64};
 static PyObject *raw_stream;       /* torch._C._cuda_getCurrentRawStream */
 static PyObject *empty;            /* torch.empty: 1.6 us; the method new_empty takes 5 */
+static PyObject *current_device;   /* torch._C._cuda_getDevice */
 
 static int refuse(const char *what) {
   PyErr_SetString(PyExc_ValueError, what);
@@ -143,6 +144,19 @@ static int read_seqs(PyObject *cu_q, PyObject *kv_len, PyObject *pages, int devi
   return 0;
 }
 
+/* A launch goes to the current device, whatever its pointers' and its stream's device. */
+static int check_device(int device) {
+  PyObject *v = PyObject_CallNoArgs(current_device);
+  if (!v) return -1;
+  const long now = PyLong_AsLong(v);
+  Py_DECREF(v);
+  if (PyErr_Occurred()) return -1;
+  if (now == device) return 0;
+  PyErr_Format(PyExc_ValueError, "the tensors are on device %d, and the current device is %ld: use torch.cuda.device(%d)",
+               device, now, device);
+  return -1;
+}
+
 static int read_stream(PyObject *stream, int device, mk_stream_t *s) {
   PyObject *v;
   if (stream == Py_None) {
@@ -225,7 +239,7 @@ static PyObject *bind_rope(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   if (read_rows(a[1], &x, "x", NULL, 0) || read_rows(a[2], &y, "out", &x, 1)) return NULL;
   NEED(x.dtype == MK_BF16 || x.dtype == MK_F16 || x.dtype == MK_F32, "unsupported dtype: bf16, fp16 or fp32");
   NEED(x.shape[1] < (1 << 30) && x.shape[2] < (1 << 30), "x is too large");
-  if (read_rotation(a[3], a[4], a[5], a[6], a[7], a[8], x.shape[0], x.device, &r) ||
+  if (check_device(x.device) || read_rotation(a[3], a[4], a[5], a[6], a[7], a[8], x.shape[0], x.device, &r) ||
       read_stream(a[9], x.device, &s))
     return NULL;
   rope_fn fn = (rope_fn)PyLong_AsVoidPtr(a[0]);
@@ -259,7 +273,7 @@ static PyObject *bind_append(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   NEED(k.shape[1] == c->heads && k.shape[2] == c->d, "k and v do not fit the cache's heads and d");
   NEED((k.dtype == MK_BF16 || k.dtype == MK_F16) && (c->dtype == k.dtype || c->dtype == MK_E4M3) && k.device == dev,
        "k and v do not have the cache's type or device");
-  if (read_seqs(a[5], a[6], a[7], dev, &s)) return NULL;
+  if (check_device(dev) || read_seqs(a[5], a[6], a[7], dev, &s)) return NULL;
   const int has_q = a[8] != Py_None, turn = a[10] != Py_None;
   NEED(turn || !has_q, "q is only rotated: give freqs with it");
   if (turn && read_rotation(a[10], a[11], Py_False, a[12], Py_False, a[13], k.shape[0], dev, &r)) return NULL;
@@ -312,7 +326,7 @@ static PyObject *bind_attention(PyObject *self, PyObject *const *a, Py_ssize_t n
   NEED(c->dtype != MK_E4M3 || q.dtype == MK_BF16, "an 8-bit cache takes bf16 queries");
   NEED(q.shape[2] == c->d, "q's d is not the cache's");
   NEED(q.shape[1] < (1 << 30), "q has too many heads");
-  if (read_seqs(a[6], a[7], a[8], dev, &s)) return NULL;
+  if (check_device(dev) || read_seqs(a[6], a[7], a[8], dev, &s)) return NULL;
   const int causal = PyObject_IsTrue(a[9]);
   const long long window = PyLong_AsLongLong(a[10]), sinks = PyLong_AsLongLong(a[11]), max_q = PyLong_AsLongLong(a[13]);
   const double scale = a[12] == Py_None ? 1.0 / sqrt((double)c->d) : PyFloat_AsDouble(a[12]);
@@ -353,13 +367,14 @@ end:
   return result;
 }
 
-/* setup(dtypes in the order of `dtypes`, raw_stream, empty) */
+/* setup(dtypes in the order of `dtypes`, raw_stream, empty, current_device) */
 static PyObject *bind_setup(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   (void)self;
-  NEED(n == 3 && PyTuple_Check(a[0]) && PyTuple_GET_SIZE(a[0]) == 7, "setup: (7 dtypes, two functions)");
+  NEED(n == 4 && PyTuple_Check(a[0]) && PyTuple_GET_SIZE(a[0]) == 7, "setup: (7 dtypes, three functions)");
   for (int i = 0; i < 7; ++i) Py_XSETREF(dtypes[i], Py_NewRef(PyTuple_GET_ITEM(a[0], i)));
   Py_XSETREF(raw_stream, Py_NewRef(a[1]));
   Py_XSETREF(empty, Py_NewRef(a[2]));
+  Py_XSETREF(current_device, Py_NewRef(a[3]));
   Py_RETURN_NONE;
 }
 
