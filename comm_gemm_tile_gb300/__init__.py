@@ -697,11 +697,17 @@ class KVCache:
     """A paged key / value cache: k, v [n_pages x heads x page_size x d] (any strides with d
     contiguous, the same for both; a cache laid out [n_pages x page_size x heads x d] is passed
     as k.transpose(1, 2)) in bf16, fp16 or float8_e4m3fn, the latter with k_scale, v_scale
-    [n_pages x heads] fp32, not negative.  KVCache.empty allocates one."""
+    [n_pages x heads] fp32, not negative.  KVCache.empty allocates one.  The tensors are the
+    cache's for good: a larger one is another KVCache."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         self._c, self._device = _bind().cache(k, v, k_scale, v_scale)   # the bytes of an mk_kv_cache
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._tensors = k, v, k_scale, v_scale
+
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    k_scale = property(lambda self: self._tensors[2])
+    v_scale = property(lambda self: self._tensors[3])
 
     @staticmethod
     def empty(n_pages: int, heads: int, page_size: int, d: int, dtype=torch.bfloat16, device="cuda"):
