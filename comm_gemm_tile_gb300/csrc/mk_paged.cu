@@ -173,15 +173,17 @@ __device__ __forceinline__ long long sequence_tiles(const PagedParams& p, int b)
   return ((rows + ROWS - 1) / ROWS) * key_tiles<KT>(p, len - n, len - 1, len).count();
 }
 
+// Returns the number of tiles that it has begun to load.
 template <int KT, bool E8, int D, int NQ>
-__device__ void dc_producer(const PagedParams& p, const long long* pre, volatile int* dead, uint32_t full, uint32_t empty,
+__device__ uint32_t dc_producer(const PagedParams& p, const long long* pre, volatile int* dead, uint32_t full, uint32_t empty,
                             uint32_t ring, int stages, long long x, long long end) {
   constexpr int TILE = KT * D * (E8 ? 1 : 2), ROWS = 8 * NQ;
   const int lane = threadIdx.x & 31;
   const int box = min(p.c.page_size, KT), boxes = KT / box;
   int b = warp_last_le(p.s.batch, 0, [&](int i) { return pre[i] * p.c.heads <= x ? 0 : 1; });
   int st = 0;
-  uint32_t ph = 0;
+  uint32_t ph = 0, loads = 0;
+  const uint32_t stop = stop_at(p);
   while (x < end) {
     while (pre[b + 1] * p.c.heads <= x) ++b;
     const Segment g = segment_at<KT, ROWS>(p, pre, b, x, end);
@@ -211,7 +213,8 @@ __device__ void dc_producer(const PagedParams& p, const long long* pre, volatile
         if (k + batch < g.k1) next = pages_of(k + batch);
       }
       const int page = __shfl_sync(0xffffffffu, pages, at * boxes + (lane % boxes));
-      if (!__all_sync(0xffffffffu, pg_wait(dead, p, empty + 8u * st, ph ^ 1u, WHERE_PRODUCER))) return;
+      if (!__all_sync(0xffffffffu, pg_wait(dead, p, empty + 8u * st, ph ^ 1u, WHERE_PRODUCER))) return loads;
+      if (loads == stop) return loads;
       const uint32_t bar = full + 8u * st;
       if (lane == 0) mbar_arrive_expect_tx(bar, 2u * TILE);
       __syncwarp();
@@ -225,6 +228,7 @@ __device__ void dc_producer(const PagedParams& p, const long long* pre, volatile
         for (int a = 0; a < ATOMS; ++a)
           tma_load_4d(dst + a * (KT * 128u), lane < 16 ? &p.tmK : &p.tmV, bar, 64 * a, slot, g.h, page);
       }
+      ++loads;
       if (++st == stages) {
         st = 0;
         ph ^= 1u;
@@ -232,6 +236,7 @@ __device__ void dc_producer(const PagedParams& p, const long long* pre, volatile
     }
     x += g.k1 - g.k0;
   }
+  return loads;
 }
 
 // The first tile of a segment that is a warp's: the run's tiles are dealt to the warps in turn.
@@ -776,8 +781,9 @@ __global__ void __launch_bounds__(Shape<T, E8, D, NQ>::THREADS, 1)
   long long x = deal.start(blockIdx.x);
   const long long end = deal.start(blockIdx.x + 1);
   if (warp == S::WARPS) {
-    dc_producer<KT, E8, D, NQ>(p, pre, dead, full, empty, ring, S::STAGES, x, end);
+    const uint32_t loads = dc_producer<KT, E8, D, NQ>(p, pre, dead, full, empty, ring, S::STAGES, x, end);
     __syncwarp();
+    pg_drain(p, full, S::STAGES, loads);
   } else {
     int b = warp_last_le(batch, 0, [&](int i) { return pre[i] * p.c.heads <= x ? 0 : 1; });
     uint32_t done = 0;                   // tiles of the run before this segment
@@ -789,10 +795,6 @@ __global__ void __launch_bounds__(Shape<T, E8, D, NQ>::THREADS, 1)
       done += g.k1 - g.k0;
       x += g.k1 - g.k0;
     }
-  }
-  if (*dead) {   // loads whose barrier nobody waited for may still be landing
-    const uint64_t t0 = globaltimer_ns();
-    while (globaltimer_ns() - t0 < 50000ull) __nanosleep(1000);
   }
 }
 
@@ -924,6 +926,7 @@ mk_status mk_paged_attention(const void* q, void* out, float* lse, mk_dtype dtyp
   p.part = reinterpret_cast<float*>(ws + L.part_off);
   p.part_lse = reinterpret_cast<float*>(ws + L.lse_off);
   p.wait_ns = default_wait_ns(cfg);
+  p.inject = cfg ? cfg->inject : 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.heads_q = heads_q;
   p.group = heads_q / cache->heads;

@@ -39,6 +39,7 @@ struct PagedParams {
   int map_pages;                       // pages in the tensor maps; a load from this page reads zeros
   int rows_lo, rows_hi;                // sequences with this many packed rows (tokens x group) are this launch's
   int grid;
+  int inject;                          // test only: 1 = the first CTA's loader stops after two tiles
 };
 
 // The keys a sequence's rows see, in tiles of KT keys: tiles 0 .. sink-1 (the
@@ -96,9 +97,12 @@ __device__ __forceinline__ int part_slot(int i, bool begins) { return 2 * i + (b
 
 // ------------------------------------------------------------------ bounded waits
 // No CTA of these kernels waits for another, so giving up is a CTA's own
-// affair: a word in shared memory, after which every wait returns at once.
+// affair: a word in shared memory, after which every wait returns at once.  What is
+// in flight then (loads, products) is still waited for, by the warp that issued it.
+constexpr uint64_t DRAIN_NS = 1000000000ull;
 __device__ __forceinline__ bool pg_wait_slow(volatile int* dead, const PagedParams& p, uint32_t bar, uint32_t parity,
                                              int where) {
+  if (*dead) return false;
   const uint64_t t0 = globaltimer_ns();
   uint32_t it = 0;
   while (!mbar_try_wait(bar, parity)) {
@@ -119,6 +123,26 @@ __device__ __forceinline__ bool pg_wait(volatile int* dead, const PagedParams& p
                                         int where) {
   if (mbar_try_wait(bar, parity)) return true;
   return pg_wait_loop(dead, p, bar, parity, where);
+}
+
+// The tile before which a CTA's loader stops (compared for every tile: worked out there, decode steps took 1 % more).
+__device__ __forceinline__ uint32_t stop_at(const PagedParams& p) {
+  return p.inject == 1 && blockIdx.x == 0 ? 2u : 0xffffffffu;
+}
+
+// The last `stages` of `count` loads that a warp issued, load i on barrier bar + 8 (i % stages): each is its barrier's
+// latest phase, so that its parity cannot be mistaken.
+__device__ __forceinline__ void pg_drain(const PagedParams& p, uint32_t bar, uint32_t stages, uint32_t count) {
+  for (uint32_t i = count > stages ? count - stages : 0u; i < count; ++i) {
+    const uint32_t at = bar + 8u * (i % stages), parity = (i / stages) & 1u;
+    if (mbar_try_wait(at, parity)) continue;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(at, parity))
+      if (globaltimer_ns() - t0 > DRAIN_NS) {
+        seq_error(p.hdr, MK_ERR_TIMEOUT, WHERE_PRODUCER, blockIdx.x);
+        return;
+      }
+  }
 }
 
 __device__ __forceinline__ float pg_ex2(float x) {

@@ -78,6 +78,7 @@ __device__ __forceinline__ uint32_t idesc(int n, bool b_mn, bool half) {
 // Waits of a whole warp, which agrees by vote.
 __device__ __noinline__ bool pr_wait_loop(volatile int* dead, const PagedParams& p, uint32_t bar, uint32_t parity,
                                           int where) {
+  if (__any_sync(0xffffffffu, *dead)) return false;
   const uint64_t t0 = globaltimer_ns();
   uint32_t it = 0;
   while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
@@ -278,13 +279,18 @@ __device__ __forceinline__ void load_tile(const PagedParams& p, const CUtensorMa
   __syncwarp();
 }
 
+// Loads begun: tiles of keys, of values, queries.
+struct Loads {
+  uint32_t k, v, q;
+};
 // Warp 1: K, and after an item's first K tile its queries; 8-bit caches: V too.
 template <bool E8, int D>
-__device__ void pr_load(const PagedParams& p, Walk w, volatile int* dead, uint32_t bars, uint32_t base) {
+__device__ void pr_load(const PagedParams& p, Walk w, volatile int* dead, uint32_t bars, uint32_t base, Loads& begun) {
   using P = Plan<E8, D>;
   const int lane = threadIdx.x & 31;
   const int toks = PR_T / p.group;
-  uint32_t u = 0, q_ph = 0;
+  const uint32_t stop = stop_at(p);
+  uint32_t u = 0;
   while (w.next(p)) {
     const Pages g(p, w.it);
     if (lane == 0 && ((w.it.len - 1) >> p.c.page_log2) >= p.s.max_pages)
@@ -293,6 +299,7 @@ __device__ void pr_load(const PagedParams& p, Walk w, volatile int* dead, uint32
     for (int k = w.k0; k < w.k1; ++k, ++u) {
       const int tile = w.it.t.tile(k), page = next;
       if (k + 1 < w.k1) next = g.of(p, w.it, w.it.t.tile(k + 1), lane);
+      if (u == stop) return;
       if (E8) {
         if (!pr_wait(dead, p, bars + B_RKEMPTY, (u & 1u) ^ 1u, WHERE_PRODUCER)) return;
         load_tile<E8, D>(p, &p.tmK, base + P::RK, bars + B_RKFULL, g, tile, page, w.h, lane);
@@ -301,9 +308,10 @@ __device__ void pr_load(const PagedParams& p, Walk w, volatile int* dead, uint32
         if (!pr_wait(dead, p, bars + B_KEMPTY + 8u * st, ph ^ 1u, WHERE_PRODUCER)) return;
         load_tile<E8, D>(p, &p.tmK, base + P::K + st * P::TILE, bars + B_KFULL + 8u * st, g, tile, page, w.h, lane);
       }
+      ++begun.k;
       if (k == w.k0) {
-        if (!pr_wait(dead, p, bars + B_QEMPTY, q_ph ^ 1u, WHERE_PRODUCER)) return;
-        q_ph ^= 1u;
+        if (!pr_wait(dead, p, bars + B_QEMPTY, (begun.q & 1u) ^ 1u, WHERE_PRODUCER)) return;
+        ++begun.q;
         if (lane == 0) {
           const int second = narrow_item(p, w.it) ? 0 : toks;
           mbar_arrive_expect_tx(bars + B_QFULL, 2u * toks * p.group * D * 2u);
@@ -319,6 +327,7 @@ __device__ void pr_load(const PagedParams& p, Walk w, volatile int* dead, uint32
       if (E8) {
         if (!pr_wait(dead, p, bars + B_RVEMPTY, (u & 1u) ^ 1u, WHERE_PRODUCER)) return;
         load_tile<E8, D>(p, &p.tmV, base + P::RV, bars + B_RVFULL, g, tile, page, w.h, lane);
+        ++begun.v;
       }
     }
   }
@@ -378,7 +387,7 @@ __device__ __forceinline__ bool any_not_finite(const uint8_t* tile, int lane) {
 // cleared one segment ahead; this warp is at most four segments ahead of the rows' last read.
 template <class T, int D>
 __device__ void pr_load_v(const PagedParams& p, Walk w, volatile int* dead, uint32_t bars, uint32_t base, uint8_t* sm,
-                          volatile int* odd) {
+                          volatile int* odd, Loads& begun) {
   using P = Plan<false, D>;
   const int lane = threadIdx.x & 31;
   uint32_t u = 0;
@@ -395,6 +404,7 @@ __device__ void pr_load_v(const PagedParams& p, Walk w, volatile int* dead, uint
       const uint32_t st = u % PR_ST, ph = (u / PR_ST) & 1u;
       if (!pr_wait(dead, p, bars + B_VEMPTY + 8u * st, ph ^ 1u, WHERE_PRODUCER)) return;
       load_tile<false, D>(p, &p.tmV, base + P::V + st * P::TILE, bars + B_VFULL + 8u * st, g, number, page, w.h, lane);
+      ++begun.v;
       if (!all_seen(p, p0, p1, w.it.len, key0, PR_T)) {
         if (!pr_wait(dead, p, bars + B_VFULL + 8u * st, ph, WHERE_COPY)) return;
         uint8_t* tile = sm + P::V + st * P::TILE;
@@ -701,7 +711,7 @@ done:
   {
     const uint64_t t0 = globaltimer_ns();
     while (!__all_sync(0xffffffffu, mbar_try_wait(bars + B_DRAIN + 8u * i, 0)))
-      if (globaltimer_ns() - t0 > static_cast<uint64_t>(p.wait_ns)) break;
+      if (globaltimer_ns() - t0 > DRAIN_NS) break;
   }
 }
 
@@ -865,6 +875,7 @@ __device__ __noinline__ bool far_rest(const PagedParams& p, volatile int* dead, 
                                       FarRow* row) {
   constexpr float SHIFT = std::is_same<T, __half>::value ? 7.f : 0.f;
   FarRow r = *row;
+  tc_wait_st();                              // before a wait that may run out
   const int lane = threadIdx.x & 31;
   bool there = true;                         // the scores of tile k
 #pragma unroll 1
@@ -1345,20 +1356,28 @@ __global__ void __launch_bounds__(Plan<E8, D>::THREADS, 1)
     if (warp >= W_SOFT && warp < W_SOFT + 8) {
       pr_softmax<T, E8, D>(p, w, dead, bars, sm, tmem, odd);
     } else {
-      if (warp == W_LOAD) pr_load<E8, D>(p, w, dead, bars, base);
+      if (warp == W_LOAD) {
+        Loads begun = {0, 0, 0};
+        pr_load<E8, D>(p, w, dead, bars, base, begun);
+        __syncwarp();
+        pg_drain(p, bars + (E8 ? B_RKFULL : B_KFULL), E8 ? 1 : PR_ST, begun.k);
+        pg_drain(p, bars + B_QFULL, 1, begun.q);
+        pg_drain(p, bars + B_RVFULL, 1, begun.v);
+      }
       else if (warp == W_MMA || warp == W_MMA1)
         pr_mma<T, E8, D>(p, w, dead, bars, base, tmem, warp == W_MMA1);
-      else if (!E8 && warp == W_LOADV) pr_load_v<T, D>(p, w, dead, bars, base, sm, odd);
+      else if (!E8 && warp == W_LOADV) {
+        Loads begun = {0, 0, 0};
+        pr_load_v<T, D>(p, w, dead, bars, base, sm, odd, begun);
+        __syncwarp();
+        pg_drain(p, bars + B_VFULL, PR_ST, begun.v);
+      }
       else if (E8 && warp == W_LOADV) pr_scales<D>(p, w, dead, bars, sm, odd);
       else if (E8 && warp >= W_TURN) pr_turn<D>(p, w, dead, bars, sm, odd);
     }
     __syncwarp();
   }
   tc_fence_before();
-  if (threadIdx.x == 0 && *dead) {   // loads whose barrier nobody waited for may still be landing
-    const uint64_t t0 = globaltimer_ns();
-    while (globaltimer_ns() - t0 < 50000ull) __nanosleep(1000);
-  }
   __syncthreads();
   if (warp == W_MMA) {
     tc_fence_after();

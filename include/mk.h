@@ -100,7 +100,8 @@ typedef struct {
   int mode;                 /* mk_mode                                                  */
   long long wait_limit_ns;  /* bound on every device-side wait (default 2e9 ns)        */
   int inject;               /* test only: 1 = one copy-in chunk never signals ready;
-                               2 = one partial tile never signals ready                */
+                               2 = one partial tile never signals ready; paged
+                               attention: 1 = one CTA stops loading after two tiles    */
   int reduce;               /* RS / AR with n_reduce_ctas == 0: 0 = default: 4 for an AR
                                    with at most 2048 partial tiles (output tiles x R, i.e.
                                    256 MiB of staging) when wire == 0 and split_k <= 1,
@@ -501,7 +502,9 @@ size_t mk_paged_attention_workspace_size(long long tokens, int heads_q, int head
  * and sets the device status (MK_ERR_INVALID, MK_ERR_CAPACITY).
  * The workspace needs no clearing except once before its first use, and must
  * not be shared with the collective entry points above.  cfg (may be NULL):
- * max_ctas and wait_limit_ns apply. */
+ * max_ctas, wait_limit_ns and inject apply.  After a wait has run out (device
+ * status MK_ERR_TIMEOUT) some rows of out and lse are undefined; the workspace
+ * serves the next call. */
 mk_status mk_paged_attention(const void *q, void *out, float *lse, mk_dtype dtype, long long tokens,
                              int heads_q, long long q_token, long long q_head, long long o_token,
                              long long o_head, const mk_kv_cache *cache, const mk_seq_batch *seqs,
