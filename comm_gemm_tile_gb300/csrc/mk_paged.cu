@@ -111,6 +111,13 @@ __device__ __forceinline__ uint32_t turn8x8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
+// x, or 3e38 where that is less; NaN stays NaN.  (A scale over the reference of weight times scale is past fp32's range
+// where weights below 2^-118 stand beside it: their product is ordinary, so the factor must not be infinite.)
+__device__ __forceinline__ float at_most_large(float x) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(3e38f));
+  return y;
+}
 __device__ __forceinline__ uint32_t f16x2(float a, float b) { return Piece<__half>::pack(a, b); }
 // Byte offset of 16-byte piece ch of key row `key` in a tile: rows of 128 bytes
 // (16-bit types: d / 64 such atoms, one after the other) or of 64 bytes, with
@@ -489,7 +496,7 @@ __device__ __forceinline__ void consume(const PagedParams& p, const Segment& g, 
             const float mvn = fmaxf(mv[q][e], top_v), vref = mvn == -INFINITY ? 0.f : mvn;
             alpha[e] = pg_ex2(mv[q][e] - vref);
             mv[q][e] = mvn;
-            rel[e] = mvn == -INFINITY ? 0.f : pg_ex2(-vref);
+            rel[e] = mvn == -INFINITY ? 0.f : at_most_large(pg_ex2(-vref));
           }
         }
         if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
@@ -506,7 +513,7 @@ __device__ __forceinline__ void consume(const PagedParams& p, const Segment& g, 
             const int e = x & 1;
             w[x] = pg_ex2(HALF ? s[q][t][x] + SHIFT : s[q][t][x]);
             l[q][e] += w[x];
-            if (E8) w[x] = w[x] == 0.f ? 0.f : w[x] * (vs[2 * t + (x >> 1)] * rel[e]);
+            if (E8) w[x] = w[x] == 0.f ? 0.f : w[x] * at_most_large(vs[2 * t + (x >> 1)] * rel[e]);
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h)
