@@ -672,14 +672,38 @@ def rope_freqs(rot: int, *, base: float = 10000.0, scaling: str | None = None, f
     return f.to(device), magnitude
 
 
+class _Rope(torch.autograd.Function):
+    """rope under autograd: the gradient is the inverse rotation, through rope again, so that it has one too."""
+
+    @staticmethod
+    def forward(ctx, x, freqs, positions, how, stream):
+        y = rope(x, freqs, positions, **how, stream=stream)
+        ctx.how = how
+        ctx.save_for_backward(freqs, positions)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        freqs, positions = ctx.saved_tensors
+        if dy.stride(-1) != 1:      # the gradient of a sum, for one, is expanded
+            dy = dy.contiguous()
+        # (autograd runs this on the stream that was current in forward, and orders it)
+        return rope(dy, freqs, positions, **{**ctx.how, "inverse": not ctx.how["inverse"]}), None, None, None, None
+
+
 def rope(x, freqs, positions=None, *, start: int = 0, interleaved: bool = False, inverse: bool = False,
          magnitude: float = 1.0, out=None, stream=None):
     """Rotary positions.  x: [tokens x heads x d] (bf16, fp16 or fp32, any strides with d
     contiguous; a [heads x s x d] tensor of ring_attention is passed as x.transpose(0, 1)).
     The first 2 * len(freqs) elements of every head are turned by positions[t] * freqs (or
     (start + t) * freqs) and scaled by magnitude; interleaved pairs neighbours instead of
-    halves.  inverse=True is the gradient: rope(dy, ..., inverse=True) = dx.
+    halves.  inverse=True is the gradient: rope(dy, ..., inverse=True) = dx; where x requires a
+    gradient, autograd takes it (not through an `out` of the caller's: that is refused).
     Returns out (unless given: of x's shape and memory order, dense; out=x works in place)."""
+    if torch.is_grad_enabled() and getattr(x, "requires_grad", False):
+        _need(out is None, "x requires a gradient: rope cannot write it to a given out")
+        return _Rope.apply(x, freqs, positions, dict(start=start, interleaved=interleaved, inverse=inverse,
+                                                     magnitude=magnitude), stream)
     if out is None:
         _need(isinstance(x, torch.Tensor), "x is not a tensor")
         if stream is None:
