@@ -3,7 +3,9 @@
  * attribute look-ups in Python take the host (rope: 16 us of Python against 4 us in the library),
  * so their arguments are read here.  The functions take the entry point's address from the ctypes
  * library, so that whatever build of it is in use is the one that is called.
- * CPython C API only: tensors are read through their Python methods. */
+ * CPython C API only: tensors are read through their Python methods.  The interpreter's lock is given up for the
+ * library's call, which waits where the GPU's queue is full: the arguments, and with them the memory that the call
+ * reads, stay referenced by the caller. */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <math.h>
@@ -244,8 +246,12 @@ static PyObject *bind_rope(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     return NULL;
   rope_fn fn = (rope_fn)PyLong_AsVoidPtr(a[0]);
   if (!fn) return NULL;
-  return PyLong_FromLong(fn(x.ptr, y.ptr, (mk_dtype)x.dtype, x.shape[0], (int)x.shape[1], (int)x.shape[2], x.stride[0],
-                            x.stride[1], y.stride[0], y.stride[1], &r, s));
+  mk_status e;
+  Py_BEGIN_ALLOW_THREADS
+  e = fn(x.ptr, y.ptr, (mk_dtype)x.dtype, x.shape[0], (int)x.shape[1], (int)x.shape[2], x.stride[0], x.stride[1],
+         y.stride[0], y.stride[1], &r, s);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(e);
 }
 
 static int read_cache(PyObject *bytes, PyObject *device, const mk_kv_cache **c, int *dev) {
@@ -295,10 +301,13 @@ static PyObject *bind_append(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   {
     append_fn fn = (append_fn)PyLong_AsVoidPtr(a[0]);
     if (!fn) goto fail;
-    const mk_status e = fn(c, k.ptr, v.ptr, (mk_dtype)k.dtype, k.shape[0], k.stride[0], k.stride[1], v.stride[0],
-                           v.stride[1], has_q ? q.ptr : NULL, has_q ? o.ptr : NULL, has_q ? (int)q.shape[1] : 0,
-                           has_q ? q.stride[0] : 0, has_q ? q.stride[1] : 0, has_q ? o.stride[0] : 0,
-                           has_q ? o.stride[1] : 0, &s, turn ? &r : NULL, w.ptr, (size_t)w.shape[0], st);
+    mk_status e;
+    Py_BEGIN_ALLOW_THREADS
+    e = fn(c, k.ptr, v.ptr, (mk_dtype)k.dtype, k.shape[0], k.stride[0], k.stride[1], v.stride[0], v.stride[1],
+           has_q ? q.ptr : NULL, has_q ? o.ptr : NULL, has_q ? (int)q.shape[1] : 0, has_q ? q.stride[0] : 0,
+           has_q ? q.stride[1] : 0, has_q ? o.stride[0] : 0, has_q ? o.stride[1] : 0, &s, turn ? &r : NULL, w.ptr,
+           (size_t)w.shape[0], st);
+    Py_END_ALLOW_THREADS
     return Py_BuildValue("(iN)", (int)e, has_q ? out : (Py_DECREF(out), Py_NewRef(Py_None)));
   }
 fail:
@@ -355,9 +364,12 @@ static PyObject *bind_attention(PyObject *self, PyObject *const *a, Py_ssize_t n
     if (!ws || read_tensor(ws, &w, "workspace") || read_stream(a[17], dev, &st)) goto end;
     attention_fn fn = (attention_fn)PyLong_AsVoidPtr(a[0]);
     if (!fn) goto end;
-    const mk_status e = fn(q.ptr, o.ptr, (float *)l.ptr, (mk_dtype)q.dtype, q.shape[0], (int)q.shape[1], q.stride[0],
-                           q.stride[1], o.stride[0], o.stride[1], c, &s, (float)scale, causal, (int)window, (int)sinks,
-                           (int)max_q, w.ptr, (size_t)w.shape[0], (const mk_config *)cfg, st);
+    mk_status e;
+    Py_BEGIN_ALLOW_THREADS
+    e = fn(q.ptr, o.ptr, (float *)l.ptr, (mk_dtype)q.dtype, q.shape[0], (int)q.shape[1], q.stride[0], q.stride[1],
+           o.stride[0], o.stride[1], c, &s, (float)scale, causal, (int)window, (int)sinks, (int)max_q, w.ptr,
+           (size_t)w.shape[0], (const mk_config *)cfg, st);
+    Py_END_ALLOW_THREADS
     result = Py_BuildValue("(iOO)", (int)e, out, lse);
   }
 end:
