@@ -209,8 +209,6 @@ __device__ uint32_t dc_producer(const PagedParams& p, const long long* pre, vola
       if (keys_seen(p, g.len - g.n, g.len - 1, g.len, key, box)) seq_error(p.hdr, MK_ERR_INVALID, WHERE_PRODUCER, g.b);
       return p.map_pages;
     };
-    if (lane == 0 && ((g.len - 1) >> p.c.page_log2) >= p.s.max_pages)
-      seq_error(p.hdr, MK_ERR_CAPACITY, WHERE_PRODUCER, g.b);
     const int batch = 32 / boxes;
     int pages = 0, next = pages_of(g.k0);
     for (int k = g.k0, at = batch; k < g.k1; ++k, ++at) {
@@ -782,7 +780,7 @@ __global__ void __launch_bounds__(Shape<T, E8, D, NQ>::THREADS, 1)
   for (int b = blockIdx.x; b < batch; b += gridDim.x) {   // sequences without a key: nothing is seen
     int n, len, row0;
     if (pre[b + 1] == pre[b] && sequence_of(p, b, n, len, row0) && rows_are_ours(p, n))
-      no_keys<T, D>(p, row0, n, S::THREADS);
+      no_keys<T, D>(p, b, row0, n, S::THREADS);
   }
   if (static_cast<int>(blockIdx.x) >= deal.c) return;
   long long x = deal.start(blockIdx.x);
@@ -941,6 +939,8 @@ mk_status mk_paged_attention(const void* q, void* out, float* lse, mk_dtype dtyp
   p.window = window;
   p.sinks = sinks;
   p.map_pages = static_cast<int>(std::max(1LL, cache->n_pages));
+  // (and so far below 2^31 that the ends of tiles and boxes after it are ints)
+  p.len_max = static_cast<int>(std::min(static_cast<long long>(p.s.max_pages) << p.c.page_log2, 0x7fffffffLL - 8192));
   p.grid = grid_cap(cfg);
   if (p.grid <= 0) return MK_ERR_UNSUPPORTED;
   // Which kernels: by the most new tokens a sequence can have.  A kernel that is launched alone

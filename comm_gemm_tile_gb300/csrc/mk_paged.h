@@ -36,6 +36,7 @@ struct PagedParams {
   float scale_log2;                    // softmax scale * log2(e)
   int heads_q, group;                  // query heads; of them per key head
   int causal, window, sinks;
+  int len_max;                         // tokens that the page table has room for
   int map_pages;                       // pages in the tensor maps; a load from this page reads zeros
   int rows_lo, rows_hi;                // sequences with this many packed rows (tokens x group) are this launch's
   int grid;
@@ -155,19 +156,26 @@ constexpr float LN2 = 0.69314718055994530942f;
 
 // ------------------------------------------------------------------ rows and values
 
+// A sequence's tokens; a length that the page table has no room for counts as none, so that no work or index
+// comes of it.
+__device__ __forceinline__ int length_of(const PagedParams& p, int b) {
+  const int len = p.s.kv_len[b];
+  return len > 0 && len <= p.len_max ? len : 0;
+}
 __device__ __forceinline__ bool sequence_of(const PagedParams& p, int b, int& n, int& len, int& row0) {
   row0 = p.s.cu_q[b];
   n = min(p.s.cu_q[b + 1], p.s.tokens) - row0;
-  len = p.s.kv_len[b];
+  len = length_of(p, b);
   return row0 >= 0 && n > 0;
 }
 __device__ __forceinline__ bool rows_are_ours(const PagedParams& p, int n) {
   const long long rows = static_cast<long long>(n) * p.group;
   return rows >= p.rows_lo && rows <= p.rows_hi;
 }
-// The rows of n tokens from row0 see nothing: out = 0, lse = -inf (by a whole block).
+// The rows of n tokens from row0, of sequence b, see nothing: out = 0, lse = -inf (by a whole block).
 template <class T, int D>
-__device__ __forceinline__ void no_keys(const PagedParams& p, int row0, int n, int threads) {
+__device__ __forceinline__ void no_keys(const PagedParams& p, int b, int row0, int n, int threads) {
+  if (threadIdx.x == 0 && p.s.kv_len[b] > p.len_max) seq_error(p.hdr, MK_ERR_CAPACITY, WHERE_PRODUCER, b);
   const long long pieces = static_cast<long long>(n) * p.heads_q * (D / 8);
   for (long long i = threadIdx.x; i < pieces; i += threads) {
     const long long r = i / (D / 8);

@@ -118,7 +118,7 @@ __device__ __forceinline__ bool item_of(const PagedParams& p, int e, int b, Item
   it.b = b;
   it.row0 = p.s.cu_q[b];
   it.n = min(p.s.cu_q[b + 1], p.s.tokens) - it.row0;
-  it.len = p.s.kv_len[b];
+  it.len = length_of(p, b);
   const int j = e - (it.row0 / per + b);
   if (it.row0 < 0 || it.n <= 0 || j < 0 || static_cast<long long>(j) * per >= it.n) return false;
   const long long rows = static_cast<long long>(it.n) * p.group;
@@ -293,8 +293,6 @@ __device__ void pr_load(const PagedParams& p, Walk w, volatile int* dead, uint32
   uint32_t u = 0;
   while (w.next(p)) {
     const Pages g(p, w.it);
-    if (lane == 0 && ((w.it.len - 1) >> p.c.page_log2) >= p.s.max_pages)
-      seq_error(p.hdr, MK_ERR_CAPACITY, WHERE_PRODUCER, w.it.b);
     int next = g.of(p, w.it, w.it.t.tile(w.k0), lane);
     for (int k = w.k0; k < w.k1; ++k, ++u) {
       const int tile = w.it.t.tile(k), page = next;
@@ -1349,7 +1347,7 @@ __global__ void __launch_bounds__(Plan<E8, D>::THREADS, 1)
     const int b = warp_last_le(p.s.batch, e, [&](int i) { return p.s.cu_q[i] / per + i; });
     Item it;
     if (b >= 0 && item_of(p, e, b, it))
-      no_keys<T, D>(p, it.row0 + it.tok0, min(per, it.n - it.tok0), P::THREADS);
+      no_keys<T, D>(p, b, it.row0 + it.tok0, min(per, it.n - it.tok0), P::THREADS);
   }
   if (static_cast<int>(blockIdx.x) < deal.c) {
     const Walk w(p, entries, deal);

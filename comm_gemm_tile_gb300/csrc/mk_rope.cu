@@ -438,11 +438,11 @@ __device__ __forceinline__ void quant_block(const RowsParams& p, float* tc, floa
       int page = -1, lo = 0, hi = 0, tok = 0, fresh = 0;
       if (b >= 0) {
         const int c0 = p.s.cu_q[b], c1 = min(p.s.cu_q[b + 1], p.s.tokens);
-        const int len = p.s.kv_len[b], first = len - (c1 - c0);
+        const long long len = p.s.kv_len[b], first = len - (c1 - c0);
         const int number = piece - ((c0 >> p.c.page_log2) + 2 * b);
-        const long long lp = (max(first, 0) >> p.c.page_log2) + number;
-        const long long from = max(static_cast<long long>(first), lp << p.c.page_log2);
-        const long long to = min(static_cast<long long>(len), (lp + 1) << p.c.page_log2);
+        const long long lp = (max(first, 0LL) >> p.c.page_log2) + number;
+        const long long from = max(first, lp << p.c.page_log2);
+        const long long to = min(len, (lp + 1) << p.c.page_log2);
         if (first < 0 && number == 0 && c1 > c0) seq_error(p.hdr, MK_ERR_CAPACITY, WHERE_COPY, b);
         if (c0 >= 0 && c1 > c0 && from < to) {
           page = cache_page(p, b, from);

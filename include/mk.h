@@ -498,8 +498,9 @@ size_t mk_paged_attention_workspace_size(long long tokens, int heads_q, int head
  * the values (to fp16 over 8-bit caches).
  * max_q: no sequence has more new tokens than this (0: not known).  It chooses
  * kernels; a wrong value costs time, not results.  Sequence lengths stay on the
- * device.  A page outside the cache or a length past the table reads as zeros
- * and sets the device status (MK_ERR_INVALID, MK_ERR_CAPACITY).
+ * device.  A page outside the cache reads as zeros, the rows of a sequence whose
+ * length is past its table (or 2^31 - 8192) see nothing, and either sets the
+ * device status (MK_ERR_INVALID, MK_ERR_CAPACITY).
  * The workspace needs no clearing except once before its first use, and must
  * not be shared with the collective entry points above.  cfg (may be NULL):
  * max_ctas, wait_limit_ns and inject apply.  After a wait has run out (device
