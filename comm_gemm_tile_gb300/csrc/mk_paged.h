@@ -162,11 +162,15 @@ __device__ __forceinline__ int length_of(const PagedParams& p, int b) {
   const int len = p.s.kv_len[b];
   return len > 0 && len <= p.len_max ? len : 0;
 }
-__device__ __forceinline__ bool sequence_of(const PagedParams& p, int b, int& n, int& len, int& row0) {
+// Its new tokens: rows of the call's arrays, whatever cu_q holds.
+__device__ __forceinline__ int new_tokens(const PagedParams& p, int b, int& row0) {
   row0 = p.s.cu_q[b];
-  n = min(p.s.cu_q[b + 1], p.s.tokens) - row0;
+  return row0 < 0 ? 0 : max(min(p.s.cu_q[b + 1], p.s.tokens), 0) - row0;
+}
+__device__ __forceinline__ bool sequence_of(const PagedParams& p, int b, int& n, int& len, int& row0) {
+  n = new_tokens(p, b, row0);
   len = length_of(p, b);
-  return row0 >= 0 && n > 0;
+  return n > 0;
 }
 __device__ __forceinline__ bool rows_are_ours(const PagedParams& p, int n) {
   const long long rows = static_cast<long long>(n) * p.group;

@@ -116,11 +116,10 @@ struct Item {
 __device__ __forceinline__ bool item_of(const PagedParams& p, int e, int b, Item& it) {
   const int per = 2 * (PR_T / p.group);
   it.b = b;
-  it.row0 = p.s.cu_q[b];
-  it.n = min(p.s.cu_q[b + 1], p.s.tokens) - it.row0;
+  it.n = new_tokens(p, b, it.row0);
   it.len = length_of(p, b);
   const int j = e - (it.row0 / per + b);
-  if (it.row0 < 0 || it.n <= 0 || j < 0 || static_cast<long long>(j) * per >= it.n) return false;
+  if (it.n <= 0 || j < 0 || static_cast<long long>(j) * per >= it.n) return false;
   const long long rows = static_cast<long long>(it.n) * p.group;
   if (rows < p.rows_lo || rows > p.rows_hi) return false;
   it.tok0 = j * per;
