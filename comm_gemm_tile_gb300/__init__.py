@@ -752,7 +752,8 @@ def kv_append(cache: KVCache, k, v, cu_q, kv_len, pages, *, q=None, freqs=None, 
     (all int32, on the device).  A token's rotary position is its position in the sequence
     unless `positions` gives another; freqs=None stores k as it is.  8-bit caches are
     quantised with a power-of-two scale for each page and head (see include/mk.h).
-    Returns q_out (None without q).  Tokens without a slot set the device status."""
+    Returns q_out (None without q).  Tokens without a slot set the device status.  For serving:
+    no gradient comes through it (rope has one)."""
     _need(isinstance(cache, KVCache), "cache is not a KVCache")
     if q is not None and q_out is None and stream is not None:
         q_out = _new(q.shape, q.dtype, q.device, stream)
@@ -777,7 +778,8 @@ def paged_attention(q, cache: KVCache, cu_q, kv_len, pages, *, causal: bool = Tr
     heads); cu_q, kv_len, pages as for kv_append.  The token at position p sees the keys
     j <= p (all of them with causal=False) that are among the last `window` (0: no window) or
     the first `sinks`.  max_q: an upper bound on a sequence's new tokens, if the caller knows
-    one.  Returns out, or (out, lse) with return_lse; rows that see nothing are 0 (-inf).
+    one.  Returns out, or (out, lse) with return_lse; rows that see nothing are 0 (-inf).  For
+    serving: no gradient comes through it.
     Calls that may run at the same time (on several streams) need a workspace each."""
     _need(isinstance(cache, KVCache), "cache is not a KVCache")
     lse = True if return_lse else None

@@ -10,7 +10,8 @@
 //     lengths: every CTA finds its run from the lengths, so the host needs none
 //     of them and a call can be captured into a graph;
 //   * one warp issues a TMA load per page and 128 bytes of row into a ring of
-//     32- or 64-key stages (128 KB), so a page's end inside a tile costs nothing;
+//     32- or 64-key stages (192 KB; 128 KB with two column groups), so a page's end inside a tile
+//     costs nothing;
 //   * twelve warps take the tiles in turn, each with its own running maximum, sum and accumulator.
 //     They compute the transposes, S^T = K Q^T and O^T += V^T P^T (mma.sync m16n8k16): keys and
 //     elements fill the 16 rows of the instruction and the 8 query rows its 8 columns, so with
@@ -22,15 +23,15 @@
 //     log2 sums; the last of their CTAs to be done joins them, in the order of
 //     the runs, so the result does not depend on which one it is.  (A second,
 //     programmatically dependent launch for that took 3 to 5 us more a call.)
-// 128 sequences of 100 to 32000 tokens, 64 query heads on 8, d = 128, e4m3: 705 us, 5.9 TB/s (87 %
-// of a plain copy's rate).  48 windows of 4096 tokens, 8 heads, d = 64, fp16: 85 us, 4.7 TB/s, of
-// which the start (lengths, page table, first loads) and the uneven end take about 15.  One sequence of
-// 2000 tokens: 12.5 us in a graph, all of it latency: lengths, page ids, loads, and the join.
+// 128 sequences of 100 to 32000 tokens, 64 query heads on 8, d = 128, e4m3: 714 us, 5.9 TB/s (86 %
+// of a plain copy's rate).  48 windows of 4096 tokens, 8 heads, d = 64, fp16: 85.5 us, 4.6 TB/s.  One sequence of
+// 2000 tokens: 12.7 us in a graph, all of it latency: lengths, page ids, loads, and the join.
 // 8-bit caches: codes become fp16, exactly (the fp8 form of mma.sync does the same conversions
 // inside, with more instructions); the query row is scaled by a power of two to fit fp16 (bf16 has
 // fewer bits), the key scale multiplies the scores, the value scale the weights, and those
 // products have a running maximum of their own: a small weight of a page with a large scale keeps
-// its bits.
+// its bits.  With two column groups, d = 128, what a lane holds does not fit its 168 registers
+// (276 bytes of spills): 16 packed rows take 182 us below, where the bytes alone are 77.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -850,9 +851,9 @@ bool cache_map(CUtensorMap* m, const mk_kv_cache* c, const void* base, const voi
 
 // Packed rows (new tokens times query heads of a key head) up to which a sequence is the decode
 // kernel's: that kernel reads the keys once per 16 rows, the prompt kernel computes 256 at a time.
-// 16 sequences of 16000 tokens, 8 key heads, d = 128, decode / prompt kernel: 16 rows bf16 198 / 189
-// us, e4m3 174 / 201; 20 rows 357 / 191 and 307 / 203; 64 rows bf16 669 / 194.  Of 1000 tokens, bf16:
-// 16 rows 45 / 48, 20 rows 61 / 50.
+// 16 sequences of 16000 tokens, 8 key heads, d = 128, decode / prompt kernel: 16 rows bf16 196 / 188
+// us, e4m3 182 / 196; 20 rows 356 / 192 and 327 / 196; 64 rows 669 / 194 and 620 / 194.  Of 1000 tokens,
+// bf16: 16 rows 47 / 49, 20 rows 61 / 54.
 constexpr int PG_DECODE_ROWS = 16;
 
 struct PagedLayout {
@@ -954,7 +955,7 @@ mk_status mk_paged_attention(const void* q, void* out, float* lse, mk_dtype dtyp
     const int tile = d == 128 && !e8 ? Shape<__half, false, 128, 1>::KT : 64;
     // 8 packed rows to a unit where no sequence has more, else 16: the keys are read once for either,
     // but 8 rows as 16 take twice the MMAs, on eight warps (128 sequences of up to 32000 tokens, e4m3,
-    // 8 rows: 705 us, as 16: 1112; 48 windows of 4096, fp16, 4 rows: 85 and 96)
+    // 8 rows: 724 us alone, as 16: 1184; 48 windows of 4096, fp16, 4 rows: 103 and 114)
     const int nq = most * p.group <= 8 ? 1 : 2;
     if (!cache_map(&p.tmK, cache, cache->k, ws, tile, true) || !cache_map(&p.tmV, cache, cache->v, ws, tile, true))
       return MK_ERR_CUDA;

@@ -24,13 +24,13 @@
 //             multiply the scores and the weights), and an item's queries, each row times a
 //             power of two; warp 2 brings the scales
 //
-// A prompt of 8192 tokens, 32 query heads on 8, d = 128, bf16, causal: 427 us, 1.29 PFLOP/s of what
+// A prompt of 8192 tokens, 32 query heads on 8, d = 128, bf16, causal: 428 us, 1.28 PFLOP/s of what
 // the mask leaves (67 % of the burst rate of a plain product, 75 % of its rate under the power cap).
 // The tensor pipe is busy 61 % of the time; a key tile takes the softmax warps about as long as the
 // products (the exponentials alone half of that), and changing items 5 %.  Over 8-bit caches that
-// chain is longer (two scales a weight; 32 scores at a time, with 128 registers for sixteen warps) and
-// the turning warps' conversions and shared memory traffic run beside it: two pieces of 1000 tokens
-// after 15000 to 30000, 614 us, 1.04 PFLOP/s; the same over a bf16 cache 520 us.
+// chain is longer (two scales a weight; 32 scores at a time, since all sixteen warps have 128 registers)
+// and the turning warps' conversions and shared memory traffic run beside it: two pieces of 1000 tokens
+// after 15000 to 30000, 614 to 620 us, 1.04 PFLOP/s; the same over a bf16 cache 500 us.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -223,7 +223,7 @@ struct Walk {
 
 // A narrow item has rows for one query tile only (short sequences, ends of prompts): both query tiles are
 // that one, each takes every other key tile of a segment, and the softmax warps of the first merge the two
-// results.  16 sequences of 16000 tokens, 8 key heads, d = 128, 32 rows: bf16 192 us (5.5 TB/s), e4m3 199;
+// results.  16 sequences of 16000 tokens, 8 key heads, d = 128, 32 rows: bf16 192 us (5.5 TB/s), e4m3 196;
 // with the second query tile left idle 203 and 258.
 __device__ __forceinline__ bool narrow_item(const PagedParams& p, const Item& it) {
   return it.tok0 + PR_T / p.group >= it.n;

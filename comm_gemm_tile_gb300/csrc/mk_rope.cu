@@ -9,8 +9,9 @@
 // Angles: p f in fp32 would be off by p f 2^-24 (0.06 rad at p = 10^6).  Here
 // f / 2 pi is taken as a 64-bit fraction of a turn and multiplied by the
 // integer p modulo 2^64, which drops whole turns exactly; the upper 32 bits,
-// as a signed fraction of a half turn, go through sincospif: about 1e-7 rad at
-// any position.  A block computes the cosines and sines of its tokens once,
+// as a signed fraction of a half turn, go through sincospif: about 1e-7 rad, and
+// p times the error of the fraction, which is that of two 64-bit products and of
+// its 64 bits: 2^-52 p f + 2^-62 p.  A block computes the cosines and sines of its tokens once,
 // in shared memory, for all their heads.
 //
 // Both kernels move each value once and are bound by memory (large calls) or
@@ -273,7 +274,7 @@ struct Unit {
       row[o1] = Piece<T>::of(b[0]);
     }
   }
-  __device__ __forceinline__ void copy(T* row, int o0, int o1) const {   // the bits as they are
+  __device__ __forceinline__ void copy(T* row, int o0, int o1) const {   // the values as they are
     if constexpr (VEC) {
       *reinterpret_cast<uint4*>(row + o0) = w0;
       *reinterpret_cast<uint4*>(row + o1) = w1;
@@ -564,8 +565,8 @@ __global__ void __launch_bounds__(RP_THREADS, 3) mk_append8_kernel(const __grid_
 
 // How a call's rows are split: about 1024 units a block (4 a thread, all in
 // flight), so several tokens where they are small, and several blocks a token
-// where it is large; few tokens (a decode step) get 256 units a block, to be
-// spread over more SMs.  Rows of at most RP_TABLE angles a block.  With 256 / 1024
+// where it is large; calls with less than 304 such blocks, two for each of 152 SMs,
+// (a decode step) get 256 units a block, to be spread over more SMs.  Rows of at most RP_TABLE angles a block.  With 256 / 1024
 // units, calls in a graph: 16 tokens x 40 heads x 128 2.5 / 3.1 us, an append
 // for 64 sequences 3.4 / 3.9 us; 32768 tokens x 8 heads, forward and gradient,
 // 78 / 56 us, an append of 18000 tokens to an 8-bit cache 107 / 78 us.

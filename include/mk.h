@@ -410,8 +410,9 @@ size_t mk_mlp_trace_entries(int R, long long m, long long h, long long f_r, cons
  *   (a cos(p f) - b sin(p f), b cos(p f) + a sin(p f)) * magnitude.
  * Pair i is (x[i], x[i + rot/2]), or (x[2i], x[2i+1]) with interleaved != 0;
  * elements rot .. d-1 are copied.  inverse != 0 turns by -p f: the gradient of
- * the rotation with respect to x.  Angles are exact to about 1e-7 at any
- * position; the arithmetic is fp32, rounded once. */
+ * the rotation with respect to x.  An angle is within about 1e-7 of p f, up to
+ * |p f| near 2^28, and 2^-52 |p f| + 2^-62 |p| beyond (the frequency's own bits);
+ * the arithmetic is fp32, rounded once. */
 typedef struct {
   const double *freqs;     /* [rot / 2], device                                      */
   const void *positions;   /* [tokens] int32 or int64, device; NULL: the token's own  */
