@@ -253,8 +253,8 @@ def _run_own(s):
             got.update(dw=dw, dx=dx)
         return got
     if c["op"] == "route":
-        how = dict(normalize=c["normalize"], scale=c["scale"], mask=s["mask"])
-        got = mk.moe_route(s["logits"], c["top_k"], **how)
+        how = dict(normalize=c["normalize"], scale=c["scale"])
+        got = mk.moe_route(s["logits"], c["top_k"], mask=s["mask"], **how)
         out = {name: got[name] for name in ("topk_idx", "gates", "counts", "balance_loss", "z_loss")}
         if c["gradient"]:
             out["dlogits"] = mk.moe_route_backward(s["logits"], got, s["dgates"], s["dbalance"], s["dz"], **how)
