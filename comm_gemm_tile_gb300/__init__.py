@@ -120,6 +120,15 @@ class _Cache(ctypes.Structure):
                 ("d", ctypes.c_int), ("page_size", ctypes.c_int)]
 
 
+class _Rows(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("token", ctypes.c_longlong), ("head", ctypes.c_longlong)]
+
+
+class _W4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p),
+                ("n", ctypes.c_longlong), ("k", ctypes.c_longlong), ("group", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
 class use_library:
     """Context manager: every op of this module calls the given library (for
     example the bounds-checking LIB_DEBUG_PATH) instead of libmk.so."""
@@ -202,6 +211,21 @@ def load_library(path: str) -> ctypes.CDLL:
     L.mk_paged_attention.restype = i
     L.mk_paged_attention.argtypes = [vp, vp, vp, i, ll, i, ll, ll, ll, ll, P(_Cache), P(_Seqs), f32, i, i, i, i,
                                      vp, sz, P(_Cfg), vp]
+    rows = P(_Rows)
+    L.mk_rms_norm.restype = i
+    L.mk_rms_norm.argtypes = [rows, rows, vp, rows, rows, vp, i, i, i, ll, i, i, f32, vp]
+    L.mk_rms_norm_backward_workspace_size.restype = sz
+    L.mk_rms_norm_backward_workspace_size.argtypes = [ll, i, i]
+    L.mk_rms_norm_backward.restype = i
+    L.mk_rms_norm_backward.argtypes = [rows, rows, rows, vp, rows, vp, i, i, ll, i, i, f32, vp, sz, vp]
+    L.mk_moe_route_workspace_size.restype = sz
+    L.mk_moe_route_workspace_size.argtypes = [ll, i]
+    L.mk_moe_route.restype = i
+    L.mk_moe_route.argtypes = [vp, i, ll, i, ll, i, i, f32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.mk_moe_route_backward.restype = i
+    L.mk_moe_route_backward.argtypes = [vp, i, ll, i, ll, i, i, f32, vp, vp, vp, vp, vp, vp, vp, ll, vp]
+    L.mk_w4_gemm.restype = i
+    L.mk_w4_gemm.argtypes = [vp, ll, P(_W4), vp, ll, i, i, ll, vp]
     return L
 
 
@@ -605,7 +629,8 @@ def _bind():
         except ImportError as e:
             raise RuntimeError("_mkbind.so is not built; run comm_gemm_tile_gb300/build.py "
                                "(or __graft_entry__.build())") from e
-        _mkbind.setup((torch.bfloat16, torch.float32, torch.float16, FP8, torch.int32, torch.int64, torch.float64),
+        _mkbind.setup((torch.bfloat16, torch.float32, torch.float16, FP8, torch.int32, torch.int64, torch.float64,
+                       torch.uint8, torch.bool),
                       torch._C._cuda_getCurrentRawStream, torch.empty, torch._C._cuda_getDevice)
         _bound = _mkbind
     return _bound
@@ -802,8 +827,225 @@ def paged_attention(q, cache: KVCache, cu_q, kv_len, pages, *, causal: bool = Tr
     return (out, lse) if return_lse else out
 
 
+# ------------------------------------------------------------------ norm, router, 4-bit weights
+
+def _on_given(stream, x):
+    """A context in which the outputs and scratch of a call come from the pool of the stream it is given."""
+    if stream is None:
+        return contextlib.nullcontext()
+    _need(isinstance(x, torch.Tensor) and x.is_cuda, "the first argument is not a CUDA tensor")
+    return _on(stream, x.device)
+
+
+def _getter(workspace, stream):
+    return None if workspace is None else functools.partial(workspace.get, stream=stream)
+
+
+def _wants_gradient(*tensors):
+    return torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in tensors)
+
+
+def _rows_gradient(g):
+    """A gradient as the calls read it: the one of a sum, for one, is expanded."""
+    return g if g is None or g.stride(-1) == 1 else g.contiguous()
+
+
+class _RmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps, stream):
+        ctx.set_materialize_grads(False)
+        y = rms_norm(x, weight, residual=residual, eps=eps, stream=stream)
+        ctx.eps, ctx.residual = eps, residual is not None
+        ctx.save_for_backward(y[1] if ctx.residual else x, weight)
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dh=None):
+        h, weight = ctx.saved_tensors
+        dx = dh
+        dw = None
+        if dy is not None:       # (autograd runs this on the stream that was current in forward, and orders it)
+            dx, dw = rms_norm_backward(_rows_gradient(dy), h, weight, dh=_rows_gradient(dh), eps=ctx.eps,
+                                       weight_gradient=ctx.needs_input_grad[1])
+        return dx, dw, dx if ctx.residual else None, None, None
+
+
+def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, out_dtype=None, out=None, scale_out=None, h_out=None,
+             stream=None):
+    """Root-mean-square norm of every row: y = h / sqrt(mean(h^2) + eps) * weight with h = x, or with
+    a residual h = x + residual rounded to x's type (the residual stream that goes on).
+
+    x, residual: [rows x n] or [tokens x heads x n] (bf16, fp16 or fp32, any strides with n
+    contiguous, n <= 16384); weight: [n] of x's type or fp32, None for ones.  out_dtype: x's type,
+    or float8_e4m3fn: then a row's scale is max(amax / 448, 2^-100) and y is the codes of
+    y / scale, an operand of ag_gemm whose rows of c are multiplied by scale.
+    Returns y, followed by scale (8 bits) and h (with a residual).  Outputs may be given: out,
+    scale_out, h_out (h_out=residual updates the stream in place).  Where x, weight or residual
+    requires a gradient, autograd takes it (not through an 8-bit output or outputs of the
+    caller's: those are refused)."""
+    e4m3 = out_dtype == FP8
+    _need(out_dtype is None or e4m3 or out_dtype == getattr(x, "dtype", None), "out_dtype is x's type or float8_e4m3fn")
+    if _wants_gradient(x, weight, residual):
+        _need(not e4m3, "an input requires a gradient: an 8-bit output has none")
+        _need(out is None and h_out is None, "an input requires a gradient: rms_norm cannot write to a given out")
+        return _RmsNorm.apply(x, weight, residual, eps, stream)
+    with _on_given(stream, x):
+        st, y, scale, h = _bind().rms_norm(_address("mk_rms_norm"), x, residual, weight, out, scale_out, h_out, e4m3, eps,
+                                           _raw(stream))
+    if st:
+        _check(st, "mk_rms_norm")
+    if residual is not None:
+        return (y, scale, h) if e4m3 else (y, h)
+    return (y, scale) if e4m3 else y
+
+
+def rms_norm_backward(dy, h, weight=None, *, dh=None, eps: float = 1e-6, weight_gradient: bool = True, out=None,
+                      workspace: Workspace | None = None, stream=None):
+    """The gradient of rms_norm: (dx, dweight) for dy, the gradient of y, and dh, that of the h it returned.
+
+    h: what was normalised (x, or the returned h).  dx is the gradient of x and of the residual
+    alike (out: where to write it, dy and dh too).  dweight is None without a weight or with
+    weight_gradient=False.  Scratch comes from the stream's memory unless a workspace is given
+    (calls that may run at the same time need one each)."""
+    wants = True if weight is not None and weight_gradient else None
+    with _on_given(stream, dy):
+        st, dx, dw = _bind().rms_norm_backward(_address("mk_rms_norm_backward"),
+                                               _address("mk_rms_norm_backward_workspace_size"),
+                                               _getter(workspace, stream), dy, dh, h, weight, out, wants, eps, _raw(stream))
+    if st:
+        _check(st, "mk_rms_norm_backward")
+    return dx, dw
+
+
+_ROUTE = ("topk_idx", "gates", "counts", "tokens", "balance_loss", "z_loss")
+
+
+class _MoeRoute(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, topk, how, mask, workspace, stream):
+        ctx.set_materialize_grads(False)
+        r = moe_route(logits, topk, mask=mask, workspace=workspace, stream=stream, **how)
+        ctx.how = how
+        ctx.save_for_backward(logits, r["topk_idx"], r["counts"], r["tokens"])
+        ctx.mark_non_differentiable(r["topk_idx"], r["counts"], r["tokens"])
+        return tuple(r[name] for name in _ROUTE)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, _idx, dgates, _counts, _tokens, dbalance, dz):
+        logits, idx, counts, tokens = ctx.saved_tensors
+        if dgates is None and dbalance is None and dz is None:
+            return (None,) * 6
+        route = {"topk_idx": idx, "counts": counts, "tokens": tokens}
+        if dgates is not None:
+            dgates = dgates.contiguous()
+        return moe_route_backward(logits, route, dgates, dbalance, dz, **ctx.how), None, None, None, None, None
+
+
+def moe_route(logits, topk: int, *, normalize: bool = True, scale: float = 1.0, mask=None, out=None,
+              workspace: Workspace | None = None, stream=None):
+    """Expert choice for the tokens of logits [T x E] (fp32, bf16 or fp16; E <= 256, topk <= 8).
+
+    Returns a dict: topk_idx [T x topk] int32, the experts moe_dispatch_gemm chooses for these
+    logits; gates [T x topk] fp32 for moe_combine: scale * softmax(logits) of those, over their
+    sum if normalize; counts [E] int32, the tokens of each expert; tokens, how many count (N); and
+    balance_loss = E * sum_e counts_e / (topk N) * mean p_e and z_loss = mean logsumexp^2 (fp32).
+    mask [T] bool: False leaves a token out (ids -1, gates 0, counted nowhere), as tokens whose
+    logits are all -inf are; an expert with a logit of -inf is not chosen.  `out` may pass
+    preallocated buffers.  Where logits requires a gradient, autograd takes that of the gates and
+    both losses (not into buffers of the caller's: those are refused)."""
+    o = out or {}
+    if _wants_gradient(logits):
+        _need(not o, "logits requires a gradient: moe_route cannot write to given outputs")
+        return dict(zip(_ROUTE, _MoeRoute.apply(logits, topk, dict(normalize=normalize, scale=scale), mask, workspace, stream)))
+    with _on_given(stream, logits):
+        st, *got = _bind().route(_address("mk_moe_route"), _address("mk_moe_route_workspace_size"), _getter(workspace, stream),
+                                 logits, topk, normalize, scale, mask, tuple(o.get(name) for name in _ROUTE), _raw(stream))
+    if st:
+        _check(st, "mk_moe_route")
+    return dict(zip(_ROUTE, got))
+
+
+def moe_route_backward(logits, route, dgates=None, dbalance=None, dz=None, *, normalize: bool = True, scale: float = 1.0,
+                       out=None, stream=None):
+    """The gradient of moe_route with respect to the logits, for the gradients of its gates [T x topk],
+    balance_loss and z_loss (fp32 on the device; None: none).  route: what moe_route returned for these logits,
+    normalize and scale as it had them.  The counts are constants."""
+    with _on_given(stream, logits):
+        st, dl = _bind().route_backward(_address("mk_moe_route_backward"), logits, route["topk_idx"], route["counts"],
+                                        route["tokens"], dgates, dbalance, dz, normalize, scale, out, _raw(stream))
+    if st:
+        _check(st, "mk_moe_route_backward")
+    return dl
+
+
+class W4Weight:
+    """A matrix of 4-bit weights [n x k], W[i][j] = scales[i][j / group] * (code[i][j] - zeros[i][j / group]):
+    codes [n x k / 2] uint8 (the code of an even j in the lower four bits), scales and zeros [n x k / group]
+    bf16 or fp16, all contiguous; without zeros 8 takes their place.  Groups have 32, 64 or 128 weights.
+    W4Weight.quantize makes one."""
+
+    def __init__(self, codes, scales, zeros=None):
+        self._w, self._device = _bind().w4(codes, scales, zeros)   # the bytes of an mk_w4_weight
+        self._tensors = codes, scales, zeros
+
+    codes = property(lambda self: self._tensors[0])
+    scales = property(lambda self: self._tensors[1])
+    zeros = property(lambda self: self._tensors[2])
+
+    @staticmethod
+    def pack(w, *, group: int = 128, symmetric: bool = True, dtype=torch.bfloat16):
+        """(codes, scales, zeros) of w [n x k], on its device: by group, symmetric scale amax / 7 and codes 1 .. 15
+        around 8, else scale (max - min) / 15 and the zero point of the least weight."""
+        _need(w.dim() == 2 and group in (32, 64, 128) and w.shape[1] % group == 0, "w must be [n x k], k whole groups of 32, 64 or 128")
+        _need(dtype in (torch.bfloat16, torch.float16), "scales are bf16 or fp16")
+        f = w.detach().float().view(w.shape[0], -1, group)
+        if symmetric:
+            scale, zero = f.abs().amax(dim=-1) / 7, None
+        else:
+            lo, hi = f.amin(dim=-1).clamp_max(0), f.amax(dim=-1).clamp_min(0)
+            scale = (hi - lo) / 15
+        scale = scale.to(dtype)
+        by = torch.where(scale == 0, torch.inf, scale.float())[..., None]
+        if not symmetric:
+            zero = (-lo / by[..., 0]).round().clamp(0, 15).to(dtype)
+        code = (f / by).round() + (8 if symmetric else zero.float()[..., None])
+        code = code.clamp(0, 15).to(torch.uint8).view(w.shape[0], -1, 2)
+        return code[..., 0] | (code[..., 1] << 4), scale, zero
+
+    @staticmethod
+    def quantize(w, *, group: int = 128, symmetric: bool = True, dtype=torch.bfloat16):
+        """The 4-bit form of w [n x k] (once, when a model is loaded: plain tensor operations)."""
+        return W4Weight(*W4Weight.pack(w, group=group, symmetric=symmetric, dtype=dtype))
+
+    def dequantize(self, dtype=None):
+        """W [n x k] in the scales' type, or another (plain tensor operations): for checks, or for the 16-bit
+        products of prompts."""
+        c, s, z = self._tensors
+        code = torch.stack((c & 15, c >> 4), dim=-1).view(c.shape[0], s.shape[1], -1).float()
+        w = (code - (8.0 if z is None else z.float()[..., None])) * s.float()[..., None]
+        return w.flatten(1).to(dtype or s.dtype)
+
+
+def w4_gemm(x, w: W4Weight, *, out_dtype=None, out=None, stream=None):
+    """y = x @ W^T for the rows of a decode step: x [m x k] of the weight's 16-bit type, y [m x n] in it or fp32
+    (out_dtype).  Codes are multiplied as whole numbers, groups scaled and summed in fp32, y is rounded once.
+    Any m is taken; for prompts the 16-bit products are faster.  For serving: an x that requires a gradient is
+    refused."""
+    _need(isinstance(w, W4Weight), "w is not a W4Weight")
+    _need(out_dtype in (None, torch.float32) or out_dtype == getattr(x, "dtype", None), "out_dtype is x's type or fp32")
+    _need(not _wants_gradient(x), "x requires a gradient: w4_gemm has none (use torch.no_grad)")
+    with _on_given(stream, x):
+        st, y = _bind().w4_gemm(_address("mk_w4_gemm"), x, w._w, w._device, out, out_dtype == torch.float32, _raw(stream))
+    if st:
+        _check(st, "mk_w4_gemm")
+    return y
+
+
 __all__ = ["Config", "MkError", "Workspace", "ag_gemm", "gemm_rs", "gemm_ar", "device_status",
            "workspace_size", "lib", "status_string", "MODE_FUSED", "MODE_GEMM_ONLY",
            "MODE_UNFUSED", "moe_dispatch_gemm", "moe_workspace_size", "moe_combine",
            "moe_combine_workspace_size", "mlp_ag_rs", "mlp_workspace_size", "ring_attention", "rope_freqs", "rope",
-           "KVCache", "kv_append", "paged_attention", "paged_attention_workspace_size"]
+           "KVCache", "kv_append", "paged_attention", "paged_attention_workspace_size", "rms_norm", "rms_norm_backward",
+           "moe_route", "moe_route_backward", "W4Weight", "w4_gemm"]

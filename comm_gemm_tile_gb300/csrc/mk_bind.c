@@ -1,5 +1,5 @@
-/* mk_bind.c -- the checks and the marshalling of the rotary, cache and paged attention calls, for
- * Python.  The calls of a decode step take the GPU a few microseconds, less than ctypes and
+/* mk_bind.c -- the checks and the marshalling of the rotary, cache, paged attention, norm, router
+ * and 4-bit weight calls, for Python.  The calls of a decode step take the GPU a few microseconds, less than ctypes and
  * attribute look-ups in Python take the host (rope: 16 us of Python against 4 us in the library),
  * so their arguments are read here.  The functions take the entry point's address from the ctypes
  * library, so that whatever build of it is in use is the one that is called.
@@ -19,11 +19,12 @@ typedef struct {
   int device, dims;
   long long shape[4], stride[4];
 } tensor;
-enum { T_I32 = 16, T_I64 = 17, T_F64 = 18, T_OTHER = 19 };
+enum { T_I32 = 16, T_I64 = 17, T_F64 = 18, T_OTHER = 19, T_U8 = 20, T_BOOL = 21 };
+enum { N_DTYPES = 9 };
 
 static PyObject *s_data_ptr, *s_dtype, *s_shape, *s_stride, *s_get_device, *s_device, *s_kw;
-static PyObject *dtypes[7];        /* bf16, f32, f16, e4m3, i32, i64, f64 */
-static const int dtype_codes[7] = {MK_BF16, MK_F32, MK_F16, MK_E4M3, T_I32, T_I64, T_F64};
+static PyObject *dtypes[N_DTYPES];  /* bf16, f32, f16, e4m3, i32, i64, f64, u8, bool */
+static const int dtype_codes[N_DTYPES] = {MK_BF16, MK_F32, MK_F16, MK_E4M3, T_I32, T_I64, T_F64, T_U8, T_BOOL};
 static PyObject *raw_stream;       /* torch._C._cuda_getCurrentRawStream */
 static PyObject *empty;            /* torch.empty: 1.6 us; the method new_empty takes 5 */
 static PyObject *current_device;   /* torch._C._cuda_getDevice */
@@ -46,7 +47,7 @@ static int read_tensor(PyObject *t, tensor *o, const char *name) {
   p = PyObject_GetAttr(t, s_dtype);
   if (!p) return -1;
   o->dtype = T_OTHER;
-  for (int i = 0; i < 7; ++i)
+  for (int i = 0; i < N_DTYPES; ++i)
     if (p == dtypes[i]) o->dtype = dtype_codes[i];
   Py_DECREF(p);
   p = PyObject_CallMethodNoArgs(t, s_get_device);
@@ -379,11 +380,398 @@ end:
   return result;
 }
 
+/* ------------------------------------------------------------------ norm, router, 4-bit weights */
+
+static PyObject *new_tensor(PyObject *shape, PyObject *dtype, PyObject *like) {      /* steals shape */
+  PyObject *device = shape ? PyObject_GetAttr(like, s_device) : NULL;
+  PyObject *args[3] = {shape, dtype, device};
+  PyObject *r = device ? PyObject_Vectorcall(empty, args, 1, s_kw) : NULL;
+  Py_XDECREF(shape);
+  Py_XDECREF(device);
+  return r;
+}
+static PyObject *dtype_object(int code) {
+  for (int i = 0; i < N_DTYPES; ++i)
+    if (dtype_codes[i] == code) return dtypes[i];
+  return NULL;
+}
+
+/* [rows x n] or [tokens x heads x n] rows of a norm, as three dimensions. */
+static int read_norm_rows(PyObject *t, tensor *o, const char *name, const tensor *like) {
+  if (read_tensor(t, o, name)) return -1;
+  if ((o->dims != 2 && o->dims != 3) || o->device < 0) {
+    PyErr_Format(PyExc_ValueError, "%s must be a [rows x n] or [tokens x heads x n] CUDA tensor", name);
+    return -1;
+  }
+  if (o->dims == 2) {
+    o->shape[2] = o->shape[1];
+    o->stride[2] = o->stride[1];
+    o->shape[1] = 1;
+    o->stride[1] = 0;
+  }
+  if (o->stride[2] != 1 && o->shape[2] != 1) {
+    PyErr_Format(PyExc_ValueError, "%s's last dimension must be contiguous", name);
+    return -1;
+  }
+  if (like && (o->device != like->device || o->dims != like->dims || o->shape[0] != like->shape[0] ||
+               o->shape[1] != like->shape[1] || o->shape[2] != like->shape[2])) {
+    PyErr_Format(PyExc_ValueError, "%s's shape or device is not that of the others", name);
+    return -1;
+  }
+  if (o->shape[1] >= (1 << 30) || o->shape[2] >= (1 << 30)) return refuse("the rows are too large");
+  if (o->shape[0] <= 1) o->stride[0] = 0;
+  if (o->shape[1] <= 1) o->stride[1] = 0;
+  return 0;
+}
+static mk_rows rows_arg(const tensor *t) {
+  mk_rows r = {t->ptr, t->stride[0], t->stride[1]};
+  return r;
+}
+static int read_same_rows(PyObject *t, tensor *o, const char *name, const tensor *like) {
+  if (read_norm_rows(t, o, name, like)) return -1;
+  if (o->dtype == like->dtype) return 0;
+  PyErr_Format(PyExc_ValueError, "%s's type is not that of the others", name);
+  return -1;
+}
+
+/* A contiguous tensor of the given type and shape (dims of them; -1: any). */
+static int read_plain(PyObject *t, tensor *o, const char *name, int dtype, int device, int dims, const long long *shape) {
+  if (read_tensor(t, o, name)) return -1;
+  int good = o->dtype == dtype && o->device == device && o->dims == dims;
+  long long n = 1;
+  for (int i = dims - 1; i >= 0 && good; --i) {
+    if (shape[i] >= 0 && o->shape[i] != shape[i]) good = 0;
+    if (n > 0 && o->shape[i] > 1 && o->stride[i] != n) good = 0;       /* (strides of nothing say nothing) */
+    n *= o->shape[i];
+  }
+  if (good) return 0;
+  PyErr_Format(PyExc_ValueError, "%s must be contiguous and have the type, shape and device that the call says", name);
+  return -1;
+}
+
+static int read_weight(PyObject *w, tensor *o, const tensor *x) {
+  o->ptr = NULL;
+  o->dtype = x->dtype;
+  if (w == Py_None) return 0;
+  if (read_tensor(w, o, "weight")) return -1;
+  if (o->dims != 1 || o->shape[0] != x->shape[2] || (o->stride[0] != 1 && o->shape[0] > 1) || o->device != x->device ||
+      (o->dtype != x->dtype && o->dtype != MK_F32))
+    return refuse("weight must be a contiguous [n] vector of the rows' type or fp32, on their device");
+  return 0;
+}
+
+typedef mk_status (*norm_fn)(const mk_rows *, const mk_rows *, const void *, const mk_rows *, const mk_rows *, float *,
+                             mk_dtype, mk_dtype, mk_dtype, long long, int, int, float, mk_stream_t);
+/* rms_norm(fn, x, residual, weight, out, scale_out, h_out, e4m3, eps, stream) -> (status, out, scale, h) */
+static PyObject *bind_norm(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  (void)self;
+  NEED(n == 10, "rms_norm: 10 arguments");
+  tensor x, r, w, y, h, sc;
+  mk_stream_t st;
+  if (read_norm_rows(a[1], &x, "x", NULL)) return NULL;
+  NEED(x.dtype == MK_BF16 || x.dtype == MK_F16 || x.dtype == MK_F32, "unsupported dtype: bf16, fp16 or fp32");
+  NEED(x.shape[2] >= 1, "rows of no elements have no norm");
+  const int has_r = a[2] != Py_None, e4m3 = PyObject_IsTrue(a[7]);
+  if (has_r && read_same_rows(a[2], &r, "residual", &x)) return NULL;
+  NEED(has_r || a[6] == Py_None, "h_out is x + residual: give a residual with it");
+  NEED(e4m3 || a[5] == Py_None, "only 8-bit outputs have scales");
+  const double eps = PyFloat_AsDouble(a[8]);
+  if (PyErr_Occurred() || read_weight(a[3], &w, &x) || check_device(x.device) || read_stream(a[9], x.device, &st)) return NULL;
+  PyObject *out = NULL, *scale = NULL, *ho = NULL, *result = NULL;
+  const int odt = e4m3 ? MK_E4M3 : x.dtype;
+  out = a[4] == Py_None ? new_tensor(PyObject_GetAttr(a[1], s_shape), dtype_object(odt), a[1]) : Py_NewRef(a[4]);
+  if (!out || read_norm_rows(out, &y, "out", &x)) goto end;
+  if (y.dtype != odt) {
+    refuse("out's type is not the output's");
+    goto end;
+  }
+  sc.ptr = NULL;
+  if (e4m3) {
+    const long long shape[2] = {x.shape[0], x.shape[1]};
+    scale = a[5] == Py_None
+                ? new_tensor(x.dims == 3 ? Py_BuildValue("(LL)", shape[0], shape[1]) : Py_BuildValue("(L)", shape[0]), dtypes[1], a[1])
+                : Py_NewRef(a[5]);
+    if (!scale || read_plain(scale, &sc, "scale_out", MK_F32, x.device, x.dims - 1, shape)) goto end;
+  }
+  if (has_r) {
+    ho = a[6] == Py_None ? new_tensor(PyObject_GetAttr(a[1], s_shape), dtype_object(x.dtype), a[1]) : Py_NewRef(a[6]);
+    if (!ho || read_same_rows(ho, &h, "h_out", &x)) goto end;
+  }
+  {
+    norm_fn fn = (norm_fn)PyLong_AsVoidPtr(a[0]);
+    if (!fn) goto end;
+    const mk_rows xr = rows_arg(&x), yr = rows_arg(&y);
+    mk_rows rr, hr;
+    if (has_r) {
+      rr = rows_arg(&r);
+      hr = rows_arg(&h);
+    }
+    mk_status e;
+    Py_BEGIN_ALLOW_THREADS
+    e = fn(&xr, has_r ? &rr : NULL, w.ptr, &yr, has_r ? &hr : NULL, (float *)sc.ptr, (mk_dtype)x.dtype, (mk_dtype)w.dtype,
+           (mk_dtype)odt, x.shape[0], (int)x.shape[1], (int)x.shape[2], (float)eps, st);
+    Py_END_ALLOW_THREADS
+    result = Py_BuildValue("(iOOO)", (int)e, out, scale ? scale : Py_None, ho ? ho : Py_None);
+  }
+end:
+  Py_XDECREF(out);
+  Py_XDECREF(scale);
+  Py_XDECREF(ho);
+  return result;
+}
+
+/* Scratch of a call: from the given get(bytes), or memory of the call's stream. */
+static PyObject *scratch(PyObject *get, size_t bytes, PyObject *like) {
+  if (get == Py_None) return new_tensor(Py_BuildValue("(n)", (Py_ssize_t)bytes), dtype_object(T_U8), like);
+  PyObject *b = PyLong_FromSize_t(bytes), *r = b ? PyObject_CallOneArg(get, b) : NULL;
+  Py_XDECREF(b);
+  return r;
+}
+
+typedef size_t (*norm_size_fn)(long long, int, int);
+typedef mk_status (*norm_grad_fn)(const mk_rows *, const mk_rows *, const mk_rows *, const void *, const mk_rows *, void *,
+                                  mk_dtype, mk_dtype, long long, int, int, float, void *, size_t, mk_stream_t);
+/* rms_norm_backward(fn, size_fn, get_workspace or None, dy, dh, h, weight, dx, dweight (True to make one, None, or a
+ * tensor), eps, stream) -> (status, dx, dweight) */
+static PyObject *bind_norm_grad(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  (void)self;
+  NEED(n == 11, "rms_norm_backward: 11 arguments");
+  tensor dy, dh, h, w, dx, dw, ws;
+  mk_stream_t st;
+  if (read_norm_rows(a[5], &h, "h", NULL)) return NULL;
+  NEED(h.dtype == MK_BF16 || h.dtype == MK_F16 || h.dtype == MK_F32, "unsupported dtype: bf16, fp16 or fp32");
+  NEED(h.shape[2] >= 1, "rows of no elements have no norm");
+  if (read_same_rows(a[3], &dy, "dy", &h)) return NULL;
+  const int has_dh = a[4] != Py_None;
+  if (has_dh && read_same_rows(a[4], &dh, "dh", &h)) return NULL;
+  const double eps = PyFloat_AsDouble(a[9]);
+  if (PyErr_Occurred() || read_weight(a[6], &w, &h) || check_device(h.device) || read_stream(a[10], h.device, &st)) return NULL;
+  NEED(w.ptr || a[8] == Py_None, "there is no gradient of a weight without a weight");
+  PyObject *out = NULL, *dwo = NULL, *space = NULL, *result = NULL;
+  out = a[7] == Py_None ? new_tensor(PyObject_GetAttr(a[5], s_shape), dtype_object(h.dtype), a[5]) : Py_NewRef(a[7]);
+  if (!out || read_same_rows(out, &dx, "dx", &h)) goto end;
+  dw.ptr = ws.ptr = NULL;
+  ws.shape[0] = 0;
+  if (a[8] != Py_None) {
+    const long long shape[1] = {h.shape[2]};
+    dwo = a[8] == Py_True ? new_tensor(Py_BuildValue("(L)", shape[0]), dtype_object(w.dtype), a[5]) : Py_NewRef(a[8]);
+    if (!dwo || read_plain(dwo, &dw, "dweight", w.dtype, h.device, 1, shape)) goto end;
+    const size_t need = ((norm_size_fn)PyLong_AsVoidPtr(a[1]))(h.shape[0], (int)h.shape[1], (int)h.shape[2]);
+    if (need == 0) {
+      result = Py_BuildValue("(iOO)", (int)MK_ERR_INVALID, Py_None, Py_None);
+      goto end;
+    }
+    space = scratch(a[2], need, a[5]);
+    if (!space || read_tensor(space, &ws, "workspace")) goto end;
+  }
+  {
+    norm_grad_fn fn = (norm_grad_fn)PyLong_AsVoidPtr(a[0]);
+    if (!fn) goto end;
+    const mk_rows yr = rows_arg(&dy), hr = rows_arg(&h), xr = rows_arg(&dx);
+    mk_rows sr;
+    if (has_dh) sr = rows_arg(&dh);
+    mk_status e;
+    Py_BEGIN_ALLOW_THREADS
+    e = fn(&yr, has_dh ? &sr : NULL, &hr, w.ptr, &xr, dw.ptr, (mk_dtype)h.dtype, (mk_dtype)w.dtype, h.shape[0],
+           (int)h.shape[1], (int)h.shape[2], (float)eps, ws.ptr, (size_t)ws.shape[0], st);
+    Py_END_ALLOW_THREADS
+    result = Py_BuildValue("(iOO)", (int)e, out, dwo ? dwo : Py_None);
+  }
+end:
+  Py_XDECREF(out);
+  Py_XDECREF(dwo);
+  Py_XDECREF(space);
+  return result;
+}
+
+/* A [rows x n] matrix with contiguous rows. */
+static int read_matrix(PyObject *t, tensor *o, const char *name) {
+  if (read_tensor(t, o, name)) return -1;
+  if (o->dims != 2 || o->device < 0 || (o->stride[1] != 1 && o->shape[1] > 1)) {
+    PyErr_Format(PyExc_ValueError, "%s must be a CUDA matrix with contiguous rows", name);
+    return -1;
+  }
+  if (o->shape[0] <= 1) o->stride[0] = o->shape[1];
+  return 0;
+}
+static int logits_dtype(const tensor *t) {
+  return t->dtype == MK_F32 || t->dtype == MK_BF16 || t->dtype == MK_F16 ? 0 : refuse("logits must be fp32, bf16 or fp16");
+}
+
+typedef size_t (*route_size_fn)(long long, int);
+typedef mk_status (*route_fn)(const void *, mk_dtype, long long, int, long long, int, int, float, const unsigned char *, int *,
+                              float *, int *, int *, float *, float *, void *, size_t, mk_stream_t);
+/* route(fn, size_fn, get_workspace or None, logits, topk, normalize, scale, mask, (six outputs or None each), stream)
+ * -> (status, topk_idx, gates, counts, tokens, balance_loss, z_loss) */
+static PyObject *bind_route(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  (void)self;
+  NEED(n == 10 && PyTuple_Check(a[8]) && PyTuple_GET_SIZE(a[8]) == 6, "route: 10 arguments");
+  tensor l, m, ws, t[6];
+  mk_stream_t st;
+  if (read_matrix(a[3], &l, "logits") || logits_dtype(&l)) return NULL;
+  const long long topk = PyLong_AsLongLong(a[4]);
+  const int normalize = PyObject_IsTrue(a[5]);
+  const double scale = PyFloat_AsDouble(a[6]);
+  if (PyErr_Occurred()) return NULL;
+  NEED(l.shape[1] >= 1 && l.shape[1] < (1 << 30) && topk >= 1 && topk <= l.shape[1] && topk <= 8,
+       "topk must be between 1 and the experts, at most 8");
+  m.ptr = NULL;
+  if (a[7] != Py_None) {
+    const long long shape[1] = {l.shape[0]};
+    if (read_plain(a[7], &m, "mask (bool, one for each token)", T_BOOL, l.device, 1, shape)) return NULL;
+  }
+  if (check_device(l.device) || read_stream(a[9], l.device, &st)) return NULL;
+  static const char *names[6] = {"topk_idx", "gates", "counts", "tokens", "balance_loss", "z_loss"};
+  static const int types[6] = {T_I32, MK_F32, T_I32, T_I32, MK_F32, MK_F32}, dims[6] = {2, 2, 1, 0, 0, 0};
+  const long long pairs[2] = {l.shape[0], topk}, experts[1] = {l.shape[1]};
+  PyObject *o[6] = {NULL}, *space = NULL, *result = NULL;
+  for (int i = 0; i < 6; ++i) {
+    PyObject *given = PyTuple_GET_ITEM(a[8], i);
+    const long long *shape = i < 2 ? pairs : experts;
+    if (given != Py_None) o[i] = Py_NewRef(given);
+    else
+      o[i] = new_tensor(i < 2 ? Py_BuildValue("(LL)", pairs[0], pairs[1]) : i == 2 ? Py_BuildValue("(L)", experts[0]) : PyTuple_New(0),
+                        dtype_object(types[i]), a[3]);
+    if (!o[i] || read_plain(o[i], &t[i], names[i], types[i], l.device, dims[i], shape)) goto end;
+  }
+  ws.ptr = NULL;
+  ws.shape[0] = 0;
+  if (l.shape[0] > MK_ROUTE_SMALL) {
+    const size_t need = ((route_size_fn)PyLong_AsVoidPtr(a[1]))(l.shape[0], (int)l.shape[1]);
+    if (need > 0) {                      /* (0: the call refuses the sizes) */
+      space = scratch(a[2], need, a[3]);
+      if (!space || read_tensor(space, &ws, "workspace")) goto end;
+    }
+  }
+  {
+    route_fn fn = (route_fn)PyLong_AsVoidPtr(a[0]);
+    if (!fn) goto end;
+    mk_status e;
+    Py_BEGIN_ALLOW_THREADS
+    e = fn(l.ptr, (mk_dtype)l.dtype, l.shape[0], (int)l.shape[1], l.stride[0], (int)topk, normalize, (float)scale,
+           (const unsigned char *)m.ptr, (int *)t[0].ptr, (float *)t[1].ptr, (int *)t[2].ptr, (int *)t[3].ptr,
+           (float *)t[4].ptr, (float *)t[5].ptr, ws.ptr, (size_t)ws.shape[0], st);
+    Py_END_ALLOW_THREADS
+    result = Py_BuildValue("(iOOOOOO)", (int)e, o[0], o[1], o[2], o[3], o[4], o[5]);
+  }
+end:
+  for (int i = 0; i < 6; ++i) Py_XDECREF(o[i]);
+  Py_XDECREF(space);
+  return result;
+}
+
+typedef mk_status (*route_grad_fn)(const void *, mk_dtype, long long, int, long long, int, int, float, const int *, const int *,
+                                   const int *, const float *, const float *, const float *, void *, long long, mk_stream_t);
+/* route_backward(fn, logits, topk_idx, counts, tokens, dgates, dbalance, dz, normalize, scale, out, stream)
+ * -> (status, dlogits) */
+static PyObject *bind_route_grad(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  (void)self;
+  NEED(n == 12, "route_backward: 12 arguments");
+  tensor l, idx, counts, tokens, g[3], dl;
+  mk_stream_t st;
+  if (read_matrix(a[1], &l, "logits") || logits_dtype(&l)) return NULL;
+  NEED(l.shape[1] < (1 << 30), "too many experts");
+  const long long any[2] = {l.shape[0], -1}, experts[1] = {l.shape[1]};
+  if (read_plain(a[2], &idx, "topk_idx", T_I32, l.device, 2, any) ||
+      read_plain(a[3], &counts, "counts", T_I32, l.device, 1, experts) ||
+      read_plain(a[4], &tokens, "tokens", T_I32, l.device, 0, experts))
+    return NULL;
+  NEED(idx.shape[1] >= 1 && idx.shape[1] <= 8, "topk_idx has no or too many experts for a token");
+  const long long pairs[2] = {l.shape[0], idx.shape[1]};
+  static const char *names[3] = {"dgates", "dbalance", "dz"};
+  for (int i = 0; i < 3; ++i) {
+    g[i].ptr = NULL;
+    if (a[5 + i] != Py_None && read_plain(a[5 + i], &g[i], names[i], MK_F32, l.device, i ? 0 : 2, pairs)) return NULL;
+  }
+  const int normalize = PyObject_IsTrue(a[8]);
+  const double scale = PyFloat_AsDouble(a[9]);
+  if (PyErr_Occurred() || check_device(l.device) || read_stream(a[11], l.device, &st)) return NULL;
+  PyObject *out = a[10] == Py_None ? new_tensor(PyObject_GetAttr(a[1], s_shape), dtype_object(l.dtype), a[1]) : Py_NewRef(a[10]);
+  PyObject *result = NULL;
+  if (!out || read_matrix(out, &dl, "out")) goto end;
+  if (dl.dtype != l.dtype || dl.device != l.device || dl.shape[0] != l.shape[0] || dl.shape[1] != l.shape[1]) {
+    refuse("out's type, shape or device is not that of the logits");
+    goto end;
+  }
+  {
+    route_grad_fn fn = (route_grad_fn)PyLong_AsVoidPtr(a[0]);
+    if (!fn) goto end;
+    mk_status e;
+    Py_BEGIN_ALLOW_THREADS
+    e = fn(l.ptr, (mk_dtype)l.dtype, l.shape[0], (int)l.shape[1], l.stride[0], (int)idx.shape[1], normalize, (float)scale,
+           (const int *)idx.ptr, (const int *)counts.ptr, (const int *)tokens.ptr, (const float *)g[0].ptr,
+           (const float *)g[1].ptr, (const float *)g[2].ptr, dl.ptr, dl.stride[0], st);
+    Py_END_ALLOW_THREADS
+    result = Py_BuildValue("(iO)", (int)e, out);
+  }
+end:
+  Py_XDECREF(out);
+  return result;
+}
+
+/* w4(codes, scales, zeros or None) -> (the bytes of an mk_w4_weight, device) */
+static PyObject *bind_w4(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  (void)self;
+  NEED(n == 3, "w4: 3 arguments");
+  tensor c, s, z;
+  if (read_tensor(a[0], &c, "codes") || read_tensor(a[1], &s, "scales")) return NULL;
+  NEED(c.dtype == T_U8 && c.dims == 2 && c.device >= 0, "codes must be a [n x k / 2] uint8 CUDA tensor");
+  NEED((c.shape[1] <= 1 || c.stride[1] == 1) && (c.shape[0] <= 1 || c.stride[0] == c.shape[1]), "codes must be contiguous");
+  NEED(s.dtype == MK_BF16 || s.dtype == MK_F16, "scales must be bf16 or fp16");
+  const long long groups = s.dims == 2 ? s.shape[1] : 0;
+  NEED(groups > 0 && 2 * c.shape[1] % groups == 0, "scales must be [n x k / group]");
+  const long long group = 2 * c.shape[1] / groups, shape[2] = {c.shape[0], groups};
+  NEED(group == 32 || group == 64 || group == 128, "groups must have 32, 64 or 128 weights");
+  if (read_plain(a[1], &s, "scales", s.dtype, c.device, 2, shape)) return NULL;
+  z.ptr = NULL;
+  if (a[2] != Py_None && read_plain(a[2], &z, "zeros", s.dtype, c.device, 2, shape)) return NULL;
+  const mk_w4_weight w = {c.ptr, s.ptr, z.ptr, c.shape[0], 2 * c.shape[1], (int)group, s.dtype};
+  return Py_BuildValue("(y#i)", (const char *)&w, (Py_ssize_t)sizeof(w), c.device);
+}
+
+typedef mk_status (*w4_fn)(const void *, long long, const mk_w4_weight *, void *, long long, mk_dtype, mk_dtype, long long,
+                           mk_stream_t);
+/* w4_gemm(fn, x, weight, device, out, fp32, stream) -> (status, out) */
+static PyObject *bind_w4_gemm(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  (void)self;
+  NEED(n == 7, "w4_gemm: 7 arguments");
+  tensor x, y;
+  mk_stream_t st;
+  if (read_matrix(a[1], &x, "x")) return NULL;
+  NEED(PyBytes_Check(a[2]) && PyBytes_GET_SIZE(a[2]) == (Py_ssize_t)sizeof(mk_w4_weight), "not a 4-bit weight");
+  const mk_w4_weight *w = (const mk_w4_weight *)PyBytes_AS_STRING(a[2]);
+  const int dev = (int)PyLong_AsLong(a[3]), f32 = PyObject_IsTrue(a[5]);
+  if (PyErr_Occurred()) return NULL;
+  NEED(x.dtype == w->dtype && x.device == dev, "x does not have the weight's type or device");
+  NEED(x.shape[1] == w->k, "x's rows are not as long as the weight's");
+  if (check_device(dev) || read_stream(a[6], dev, &st)) return NULL;
+  const int odt = f32 ? MK_F32 : x.dtype;
+  PyObject *out = a[4] == Py_None ? new_tensor(Py_BuildValue("(LL)", x.shape[0], w->n), dtype_object(odt), a[1]) : Py_NewRef(a[4]);
+  PyObject *result = NULL;
+  if (!out || read_matrix(out, &y, "out")) goto end;
+  if (y.dtype != odt || y.device != dev || y.shape[0] != x.shape[0] || y.shape[1] != w->n) {
+    refuse("out's type, shape or device does not fit");
+    goto end;
+  }
+  {
+    w4_fn fn = (w4_fn)PyLong_AsVoidPtr(a[0]);
+    if (!fn) goto end;
+    mk_status e;
+    Py_BEGIN_ALLOW_THREADS
+    e = fn(x.ptr, x.stride[0], w, y.ptr, y.stride[0], (mk_dtype)x.dtype, (mk_dtype)odt, x.shape[0], st);
+    Py_END_ALLOW_THREADS
+    result = Py_BuildValue("(iO)", (int)e, out);
+  }
+end:
+  Py_XDECREF(out);
+  return result;
+}
+
 /* setup(dtypes in the order of `dtypes`, raw_stream, empty, current_device) */
 static PyObject *bind_setup(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   (void)self;
-  NEED(n == 4 && PyTuple_Check(a[0]) && PyTuple_GET_SIZE(a[0]) == 7, "setup: (7 dtypes, three functions)");
-  for (int i = 0; i < 7; ++i) Py_XSETREF(dtypes[i], Py_NewRef(PyTuple_GET_ITEM(a[0], i)));
+  NEED(n == 4 && PyTuple_Check(a[0]) && PyTuple_GET_SIZE(a[0]) == N_DTYPES, "setup: (9 dtypes, three functions)");
+  for (int i = 0; i < N_DTYPES; ++i) Py_XSETREF(dtypes[i], Py_NewRef(PyTuple_GET_ITEM(a[0], i)));
   Py_XSETREF(raw_stream, Py_NewRef(a[1]));
   Py_XSETREF(empty, Py_NewRef(a[2]));
   Py_XSETREF(current_device, Py_NewRef(a[3]));
@@ -395,6 +783,12 @@ static PyMethodDef methods[] = {{"setup", (PyCFunction)(void (*)(void))bind_setu
                                 {"rope", (PyCFunction)(void (*)(void))bind_rope, METH_FASTCALL, NULL},
                                 {"append", (PyCFunction)(void (*)(void))bind_append, METH_FASTCALL, NULL},
                                 {"attention", (PyCFunction)(void (*)(void))bind_attention, METH_FASTCALL, NULL},
+                                {"rms_norm", (PyCFunction)(void (*)(void))bind_norm, METH_FASTCALL, NULL},
+                                {"rms_norm_backward", (PyCFunction)(void (*)(void))bind_norm_grad, METH_FASTCALL, NULL},
+                                {"route", (PyCFunction)(void (*)(void))bind_route, METH_FASTCALL, NULL},
+                                {"route_backward", (PyCFunction)(void (*)(void))bind_route_grad, METH_FASTCALL, NULL},
+                                {"w4", (PyCFunction)(void (*)(void))bind_w4, METH_FASTCALL, NULL},
+                                {"w4_gemm", (PyCFunction)(void (*)(void))bind_w4_gemm, METH_FASTCALL, NULL},
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mkbind", NULL, -1, methods, NULL, NULL, NULL, NULL};
 

@@ -83,7 +83,6 @@ constexpr int RP_TOKENS = 64;          // tokens of a block at most
 constexpr int RP_FREQS = 256;          // frequencies at most
 constexpr int AP_CHUNK = 32;           // tokens of a page whose angles are in the table at once
 constexpr int AP_HEADS = 4;            // heads of a block of the 8-bit append: 8 warps, k and v each
-constexpr float E4M3_MAX = 448.f;
 
 // A thread's place in a block's work (token, row, unit of the row; or token, frequency): found by
 // multiplication and counted up from there.
@@ -393,12 +392,6 @@ __global__ void __launch_bounds__(RP_THREADS, VEC ? 4 : 1) mk_rows_kernel(const 
 
 // ------------------------------------------------------------------ 8-bit cache
 
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  uint16_t lo, hi;   // to nearest even; past 448 saturates, NaN stays NaN
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
-}
 __device__ __forceinline__ float2 e4m3_pair(uint32_t two) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));

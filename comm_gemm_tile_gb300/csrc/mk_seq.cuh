@@ -61,6 +61,16 @@ __device__ __forceinline__ int warp_last_le(int n, int t, Key key) {
   return lo;
 }
 
+constexpr float E4M3_MAX = 448.f;
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  uint16_t two;      // to nearest even; past 448 saturates, NaN stays NaN
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(b), "f"(a));
+  return two;
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
+}
+
 // 16 bytes of a row as fp32 values, and back (one rounding, to nearest even).
 template <class T> struct Piece;
 template <> struct Piece<float> {

@@ -514,6 +514,100 @@ mk_status mk_paged_attention(const void *q, void *out, float *lse, mk_dtype dtyp
                              void *workspace, size_t ws_bytes, const mk_config *cfg,
                              mk_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * What stands around the products of a layer: the norm of its rows, the choice
+ * of experts, and products with 4-bit weights.  These entry points set no device
+ * status and keep nothing between calls: a workspace is scratch of the call alone, needs no clearing, and a
+ * CUDA graph may capture them.  Strides count elements. */
+
+/* [tokens x heads x n] rows, the last dimension contiguous; any token and head
+ * strides, 0 (an expanded dimension) for inputs only. */
+typedef struct {
+  void *p;
+  long long token, head;
+} mk_rows;
+
+/* Root-mean-square norm over the n elements of each row:
+ *   h = x, or x + residual rounded to dtype;  r = 1 / sqrt(mean(h^2) + eps);  y = h * r * weight
+ * x, residual, h: dtype (MK_BF16, MK_F16, MK_F32).  residual and h go together (both
+ * NULL: the norm of x); h may be residual or x.  weight: [n] of weight_dtype (dtype or MK_F32),
+ * NULL for ones.  y: out_dtype = dtype, or MK_E4M3: then scale[token * heads + head]
+ * = max(amax / 448, 2^-100) over the row's finite |y| and the codes are y / scale (to
+ * nearest even; infinities saturate, NaN stays NaN).  fp32 arithmetic, each output
+ * rounded once; sums of squares past fp32's range come out right.  n <= 16384, eps > 0,
+ * tokens * heads below 2^31.  Rows of whole 16-byte pieces (base, strides, n) move
+ * 16 bytes at a time, others element by element. */
+mk_status mk_rms_norm(const mk_rows *x, const mk_rows *residual, const void *weight, const mk_rows *y,
+                      const mk_rows *h, float *scale, mk_dtype dtype, mk_dtype weight_dtype,
+                      mk_dtype out_dtype, long long tokens, int heads, int n, float eps,
+                      mk_stream_t stream);
+
+/* Workspace bytes for mk_rms_norm_backward with a dweight (0 on bad arguments). */
+size_t mk_rms_norm_backward_workspace_size(long long tokens, int heads, int n);
+
+/* The gradient of y = norm(h) for dy, and of h itself for dh (NULL: none):
+ *   g = dy * weight;  dx = r g - h r^3 mean(g h) + dh;  dweight = sum over rows of dy h r
+ * dx (dtype) is the gradient of x and of the residual alike; it may be dy or dh.
+ * dweight: [n] of weight_dtype, or NULL; its sums are fp32 in a fixed order (the
+ * workspace holds them). */
+mk_status mk_rms_norm_backward(const mk_rows *dy, const mk_rows *dh, const mk_rows *h,
+                               const void *weight, const mk_rows *dx, void *dweight, mk_dtype dtype,
+                               mk_dtype weight_dtype, long long tokens, int heads, int n, float eps,
+                               void *workspace, size_t ws_bytes, mk_stream_t stream);
+
+/* Workspace bytes for mk_moe_route (0 on bad arguments).  Calls of up to
+ * MK_ROUTE_SMALL tokens take none: their workspace may be NULL. */
+#define MK_ROUTE_SMALL 64
+size_t mk_moe_route_workspace_size(long long T, int E);
+
+/* Expert choice and its losses for T tokens with logits [T x E] (MK_F32, MK_BF16, MK_F16;
+ * rows `row` elements apart).  With p = softmax(logits):
+ *   topk_idx [T x topk]  the experts with the largest logits, largest first, ties to
+ *                        the lower id: what mk_moe_dispatch_gemm chooses
+ *   gates [T x topk]     scale * p of those, over their sum if normalize: what
+ *                        mk_moe_combine takes
+ *   counts [E]           tokens of each expert
+ *   tokens [1]           N, the tokens that count
+ *   balance_loss [1]     E * sum_e counts_e / (topk N) * (mean over the N tokens of p_e)
+ *   z_loss [1]           mean over the N tokens of (log sum_e exp(logit_e))^2
+ * An expert with a logit of -inf is never chosen: slots left over get id -1 and gate 0.  Tokens
+ * that mask leaves out ([T] bytes, 0: left out; NULL: none is) and tokens without an
+ * expert get ids -1 and gates 0 and count nowhere; with N = 0 both losses are 0.
+ * E <= 256, 1 <= topk <= min(8, E).  fp32 sums in a fixed order. */
+mk_status mk_moe_route(const void *logits, mk_dtype dtype, long long T, int E, long long row,
+                       int topk, int normalize, float scale, const unsigned char *mask, int *topk_idx,
+                       float *gates, int *counts, int *tokens, float *balance_loss, float *z_loss,
+                       void *workspace, size_t ws_bytes, mk_stream_t stream);
+
+/* dlogits [T x E] (dtype, rows dl_row elements apart): the gradient of
+ *   sum(gates * dgates) + dbalance * balance_loss + dz * z_loss
+ * with the counts held constant.  topk_idx, counts, tokens as mk_moe_route wrote them;
+ * dgates [T x topk], dbalance [1], dz [1] fp32 on the device, each NULL for none. */
+mk_status mk_moe_route_backward(const void *logits, mk_dtype dtype, long long T, int E, long long row,
+                                int topk, int normalize, float scale, const int *topk_idx,
+                                const int *counts, const int *tokens, const float *dgates,
+                                const float *dbalance, const float *dz, void *dlogits,
+                                long long dl_row, mk_stream_t stream);
+
+/* A matrix of 4-bit weights, [n x k] (K-major, as the fp8 operands):
+ *   W[i][j] = scales[i][j / group] * (code[i][j] - zeros[i][j / group])
+ * codes: [n x k / 2] bytes, the code of an even j in the lower four bits; scales, zeros:
+ * [n x k / group] of dtype (MK_BF16 or MK_F16); zeros NULL: 8 everywhere.  group is 32,
+ * 64 or 128 and divides k.  codes 16-byte aligned. */
+typedef struct {
+  const void *codes, *scales, *zeros;
+  long long n, k;
+  int group, dtype;
+} mk_w4_weight;
+
+/* y = x @ W^T for a few rows: x [m x k] of w->dtype (rows x_row elements apart, whole
+ * 16-byte pieces), y [m x n] of the same type or MK_F32.  Codes are multiplied as whole
+ * numbers, groups are scaled and summed in fp32, y is rounded once.  A row of x that
+ * holds an infinity gives infinities or NaN.  Built for the
+ * rows of a decode step; any m is taken, 64 rows at a time. */
+mk_status mk_w4_gemm(const void *x, long long x_row, const mk_w4_weight *w, void *y, long long y_row,
+                     mk_dtype dtype, mk_dtype out_dtype, long long m, mk_stream_t stream);
+
 /* Synchronises `stream`, then reads and clears the device status word of a
  * workspace: MK_OK, MK_ERR_TIMEOUT or MK_ERR_CAPACITY (or MK_ERR_CUDA if the
  * stream itself reports an error).  `detail` (may be NULL) receives a code
