@@ -14,8 +14,7 @@
 // rows a block), a whole block for long ones.
 //
 // A sum of squares that leaves fp32's range is taken again from h 2^-80 (rows
-// with values past 1e16 or so; with h 2^80 where eps leaves tiny ones room):
-// r is kept as r1 r2, r1 that power of two.
+// with values past 1e16 or so; with h 2^80 where eps leaves tiny ones room).
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -28,7 +27,7 @@ namespace {
 
 constexpr int NM_MAX = 16384;          // elements of a row at most
 constexpr int NM_THREADS = 256;        // threads of a block that has several rows
-constexpr int NM_PARTS = 304;          // blocks, and partial sums of a column, of the gradient at most
+constexpr int NM_PARTS = 456;          // blocks, and partial sums of a column, of the gradient at most
 constexpr float NM_LEAST = 7.888609052210118e-31f;   // 2^-100, the least scale of 8-bit rows
 
 struct RowsOf {
@@ -124,18 +123,38 @@ __device__ __forceinline__ float over_row(float v, int lanes, float (*buf)[32], 
   return v;
 }
 
-// r = r1 r2 of a row whose sum of squares is ss; where fp32 did not hold it, from again(r1) = the sum of (h r1)^2.
-// Rows of one warp go the second way together; a row's numbers do not depend on its neighbours'.
-template <class Again>
-__device__ __forceinline__ void inverse_root(float ss, int n, float eps, float& r1, float& r2, Again again) {
-  const bool high = !(ss <= 1e36f), low = eps < 1e-30f && ss < 1e-30f * n;
-  r1 = high ? 8.271806125530277e-25f : low ? 1.2089258196146292e24f : 1.f;     // 2^-80, 2^80
-  if (__any_sync(0xffffffffu, high || low)) {
-    const float scaled = again(r1);
-    if (high || low) ss = scaled;
+// Two sums over a row at once.
+template <bool WIDE>
+__device__ __forceinline__ float2 over_row2(float2 v, int lanes, float2 (*buf)[32], int& turn) {
+  const int width = WIDE ? 32 : lanes;
+  for (int o = width >> 1; o > 0; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
   }
-  r2 = 1.f / sqrtf(ss / n + eps * r1 * r1);
+  if (WIDE) {
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    if (lane == 0) buf[turn][threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = lane < warps ? buf[turn][lane] : make_float2(0.f, 0.f);
+    turn ^= 1;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+      v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    }
+  }
+  return v;
 }
+
+// Whether fp32 did not hold a row's sum of squares: high (or not a number), or low where eps does not cover it.
+__device__ __forceinline__ bool sum_high(float ss) { return !(ss <= 1e36f); }
+__device__ __forceinline__ bool sum_low(float ss, int n, float eps) { return eps < 1e-30f && ss < 1e-30f * n; }
+// r of a row whose sum of squares is ss; of (h by)^2 where that is not 1.  (A product of the two factors near fp32's
+// least numbers, for rows past 1e38, keeps 21 bits.)
+__device__ __forceinline__ float inverse_root(float ss, int n, float eps, float by) {
+  return by / sqrtf(ss / n + eps * by * by);
+}
+constexpr float NM_DOWN = 8.271806125530277e-25f, NM_UP = 1.2089258196146292e24f;       // 2^-80, 2^80
 
 template <class T, bool VEC, int U, bool WIDE, bool OUT8>
 __global__ void __launch_bounds__(WIDE ? 1024 : NM_THREADS) mk_norm_kernel(const __grid_constant__ NormParams p) {
@@ -194,8 +213,15 @@ __global__ void __launch_bounds__(WIDE ? 1024 : NM_THREADS) mk_norm_kernel(const
       }
       return over_row<WIDE, false>(s, p.lanes, buf, turn);
     };
-    float r1, r2;
-    inverse_root(squares(1.f), p.n, p.eps, r1, r2, squares);
+    float ss = squares(1.f), by = 1.f;
+    // rows of one warp go the second way together; a row's numbers do not depend on its neighbours'
+    const bool high = sum_high(ss), low = sum_low(ss, p.n, p.eps);
+    if (__any_sync(0xffffffffu, high || low)) {
+      by = high ? NM_DOWN : low ? NM_UP : 1.f;
+      const float scaled = squares(by);
+      ss = high || low ? scaled : ss;
+    }
+    const float r = inverse_root(ss, p.n, p.eps, by);
     float inv = 1.f;
     if (OUT8) {
       float top = 0.f;
@@ -208,7 +234,7 @@ __global__ void __launch_bounds__(WIDE ? 1024 : NM_THREADS) mk_norm_kernel(const
         weights<T, VEC>(p, i, w);
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-          const float a = fabsf(f[e] * r1 * r2 * w[e]);
+          const float a = fabsf(f[e] * r * w[e]);
           if (a < INFINITY) top = fmaxf(top, a);
         }
       }
@@ -227,7 +253,7 @@ __global__ void __launch_bounds__(WIDE ? 1024 : NM_THREADS) mk_norm_kernel(const
       b[u].get(f);
       weights<T, VEC>(p, i, w);
 #pragma unroll
-      for (int e = 0; e < N; ++e) f[e] = f[e] * r1 * r2 * w[e] * inv;
+      for (int e = 0; e < N; ++e) f[e] = OUT8 ? f[e] * r * w[e] * inv : f[e] * r * w[e];
       if constexpr (!OUT8) {
         b[u].set(f);
         b[u].store(y, i);
@@ -243,133 +269,192 @@ __global__ void __launch_bounds__(WIDE ? 1024 : NM_THREADS) mk_norm_kernel(const
 }
 
 // The gradient.  A block has every gridDim.x-th set of rows; a thread's columns are the same in all of them, so that it
-// adds their dy u in its own places of shared memory, [U N / 4][threads] x 4 floats (or [U][threads] single ones).
-// The blocks' sums are added in the order of their numbers by mk_norm_columns_kernel: the same bits every time.
-template <class T, bool VEC, int U, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? 1024 : NM_THREADS) mk_norm_grad_kernel(const __grid_constant__ NormParams p) {
+// adds their dy u in registers.  The blocks' sums are added in the order of their numbers by
+// mk_norm_columns_kernel: the same bits every time.
+//
+// Whole pieces come through shared memory, S sets of rows ahead (cp.async: no registers while they are on their way);
+// a thread copies what it reads itself, so that no barrier is needed.  Single elements are loaded as they are used.
+// Both sums of a row go over its threads at once: one barrier a row.
+template <class T, bool VEC, int U>
+struct GradShape {
+  static constexpr int THREADS = !VEC ? 1024 : U == 2 ? NM_THREADS : sizeof(T) == 4 ? 1024 : 512;   // of a wide row at most
+  static constexpr int BLOCKS = VEC && U == 2 ? 3 : 1;      // of an SM at least
+};
+
+template <class T, bool VEC, int U, bool WIDE, int S>
+__global__ void __launch_bounds__(WIDE ? GradShape<T, VEC, U>::THREADS : NM_THREADS, GradShape<T, VEC, U>::BLOCKS)
+    mk_norm_grad_kernel(const __grid_constant__ NormParams p) {
   using B = Bit<T, VEC>;
-  constexpr int N = B::N, Q = N >= 4 ? N / 4 : 1;
-  extern __shared__ __align__(16) float acc[];
-  __shared__ float buf[2][32];
+  constexpr int N = B::N;
+  extern __shared__ __align__(16) uint4 ring[];              // [S][h, dy, dh][U][threads]
+  __shared__ float2 buf[2][32];
   int turn = 0;
   const int t = WIDE ? threadIdx.x : threadIdx.x & (p.lanes - 1);
   const unsigned per = WIDE ? 1 : NM_THREADS / p.lanes, mine = WIDE ? 0 : threadIdx.x / p.lanes;
-  float4* acc4 = reinterpret_cast<float4*>(acc);
+  const unsigned step = gridDim.x * per;
+  const int tensors = p.r.p != nullptr ? 3 : 2;
   griddep_launch_dependents();
-  if (p.part != nullptr) {
+  float acc[U * N], wr[U * N];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+  for (int u = 0; u < U; ++u) {
+    float w[N];
 #pragma unroll
-      for (int q = 0; q < Q; ++q) {
-        if (VEC) acc4[(u * Q + q) * blockDim.x + threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
-        else acc[u * blockDim.x + threadIdx.x] = 0.f;
-      }
+    for (int e = 0; e < N; ++e) w[e] = 0.f;
+    if (t + u * p.lanes < p.pieces) weights<T, VEC>(p, t + u * p.lanes, w);
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      acc[u * N + e] = 0.f;
+      wr[u * N + e] = w[e];
+    }
   }
-  for (unsigned base = blockIdx.x * per; base < p.rows; base += gridDim.x * per) {
+  auto place = [&](int stage, int which, int u) -> uint4* {
+    return ring + ((stage * tensors + which) * U + u) * blockDim.x + threadIdx.x;
+  };
+  auto fetch = [&](unsigned base, int into) {
+    if constexpr (VEC) {
+      const unsigned row = base + mine;
+      if (base < p.rows && row < p.rows) {
+        const char* h = row_of(p.h, row, p.heads);
+        const char* d = row_of(p.x, row, p.heads);
+        const char* g = tensors == 3 ? row_of(p.r, row, p.heads) : nullptr;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = t + u * p.lanes;
+          if (i >= p.pieces) continue;
+          cp_async_16(smem_u32(place(into, 0, u)), h + 16 * i);
+          cp_async_16(smem_u32(place(into, 1, u)), d + 16 * i);
+          if (tensors == 3) cp_async_16(smem_u32(place(into, 2, u)), g + 16 * i);
+        }
+      }
+      cp_async_commit();
+    }
+  };
+  unsigned ahead = blockIdx.x * per;
+  int fill = 0, stage = 0;
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) {
+    fetch(ahead, fill++);
+    ahead += step;
+  }
+  for (unsigned base = blockIdx.x * per; base < p.rows; base += step) {
+    fetch(ahead, fill);
+    ahead = ahead < p.rows ? ahead + step : ahead;           // (stays below 2^32)
+    fill = fill + 1 == S ? 0 : fill + 1;
+    cp_async_wait<S - 1>();
     const unsigned row = base + mine;
     const bool real = row < p.rows;
-    B h[U], d[U];
-    if (real) {
-      const char* hr = row_of(p.h, row, p.heads);
-      const char* dr = row_of(p.x, row, p.heads);
+    // whole pieces are read where they lie, twice; single elements are held
+    B single[VEC ? 1 : 2 * U];
+    if constexpr (!VEC) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int i = t + u * p.lanes;
-        if (i < p.pieces) {
-          h[u].load(hr, i);
-          d[u].load(dr, i);
-        } else {
-          h[u].zero();
-          d[u].zero();
+        single[2 * u].zero();
+        single[2 * u + 1].zero();
+        if (real && i < p.pieces) {
+          single[2 * u].load(row_of(p.h, row, p.heads), i);
+          single[2 * u + 1].load(row_of(p.x, row, p.heads), i);
         }
       }
-    } else {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        h[u].zero();
-        d[u].zero();
-      }
     }
-    auto squares = [&](float by) {
-      float s = 0.f;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float f[N];
-        h[u].get(f);
-#pragma unroll
-        for (int e = 0; e < N; ++e) s = fmaf(f[e] * by, f[e] * by, s);
+    auto read = [&](int u, float (&f)[N], float (&g)[N]) {
+      B h, d;
+      if constexpr (VEC) {
+        h.zero();
+        d.zero();
+        if (real && t + u * p.lanes < p.pieces) {
+          h.w = *place(stage, 0, u);
+          d.w = *place(stage, 1, u);
+        }
+      } else {
+        h = single[2 * u];
+        d = single[2 * u + 1];
       }
-      return over_row<WIDE, false>(s, p.lanes, buf, turn);
+      h.get(f);
+      d.get(g);
     };
-    float r1, r2;
-    inverse_root(squares(1.f), p.n, p.eps, r1, r2, squares);
-    float dot = 0.f;
+    // the sums of h^2 and of g h; mean(g u) is the second times r / n
+    auto sums = [&](float by, float gby) {
+      float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = t + u * p.lanes;
-      if (i >= p.pieces) continue;
-      float f[N], g[N], w[N];
-      h[u].get(f);
-      d[u].get(g);
-      weights<T, VEC>(p, i, w);
+      for (int u = 0; u < U; ++u) {
+        float f[N], g[N];
+        read(u, f, g);
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        f[e] = f[e] * r1 * r2;
-        dot = fmaf(g[e] * w[e], f[e], dot);
-      }
-      if (p.part != nullptr && real) {
-        if constexpr (VEC) {
-#pragma unroll
-          for (int q = 0; q < Q; ++q) {
-            float4 a = acc4[(u * Q + q) * blockDim.x + threadIdx.x];
-            a.x = fmaf(g[4 * q], f[4 * q], a.x);
-            a.y = fmaf(g[4 * q + 1], f[4 * q + 1], a.y);
-            a.z = fmaf(g[4 * q + 2], f[4 * q + 2], a.z);
-            a.w = fmaf(g[4 * q + 3], f[4 * q + 3], a.w);
-            acc4[(u * Q + q) * blockDim.x + threadIdx.x] = a;
-          }
-        } else {
-          float& a = acc[u * blockDim.x + threadIdx.x];
-          a = fmaf(g[0], f[0], a);
+        for (int e = 0; e < N; ++e) {
+          s.x = fmaf(f[e] * by, f[e] * by, s.x);
+          s.y = fmaf(g[e] * wr[u * N + e], f[e] * gby, s.y);
         }
       }
+      return over_row2<WIDE>(s, p.lanes, buf, turn);
+    };
+    float2 s = sums(1.f, 1.f);
+    float by = 1.f;
+    const bool high = sum_high(s.x), low = sum_low(s.x, p.n, p.eps), far = high || low || !(fabsf(s.y) <= 1e36f);
+    const bool again = __any_sync(0xffffffffu, far);
+    if (again) {
+      by = high ? NM_DOWN : low ? NM_UP : 1.f;
+      const float scaled = sums(by, 1.f).x;
+      s.x = high || low ? scaled : s.x;
     }
-    dot = over_row<WIDE, false>(dot, p.lanes, buf, turn) / p.n;
-    if (!real) continue;
-    char* dx = row_of(p.y, row, p.heads);
-    const char* dh = p.r.p != nullptr ? row_of(p.r, row, p.heads) : nullptr;
+    const float r = inverse_root(s.x, p.n, p.eps, by);
+    float dot = s.y * r / p.n;
+    if (again) {                                             // sums of g u: u is at most sqrt(n)
+      const float of_u = sums(1.f, r).y / p.n;
+      dot = far ? of_u : dot;
+    }
+    if (real) {
+      char* dx = row_of(p.y, row, p.heads);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = t + u * p.lanes;
-      if (i >= p.pieces) continue;
-      float f[N], g[N], w[N];
-      h[u].get(f);
-      d[u].get(g);
-      weights<T, VEC>(p, i, w);
+      for (int u = 0; u < U; ++u) {
+        const int i = t + u * p.lanes;
+        if (i >= p.pieces) continue;
+        float f[N], g[N];
+        read(u, f, g);
 #pragma unroll
-      for (int e = 0; e < N; ++e) f[e] = (g[e] * w[e] - f[e] * r1 * r2 * dot) * r1 * r2;
-      if (dh != nullptr) {
-        B a;
-        a.load(dh, i);
-        a.get(g);
+        for (int e = 0; e < N; ++e) {
+          f[e] *= r;
+          acc[u * N + e] = fmaf(g[e], f[e], acc[u * N + e]);
+          f[e] = fmaf(-f[e], dot, g[e] * wr[u * N + e]) * r;
+        }
+        if (tensors == 3) {
+          B a;
+          if constexpr (VEC) a.w = *place(stage, 2, u);
+          else a.load(row_of(p.r, row, p.heads), i);
+          a.get(g);
 #pragma unroll
-        for (int e = 0; e < N; ++e) f[e] += g[e];
+          for (int e = 0; e < N; ++e) f[e] += g[e];
+        }
+        B out;
+        out.set(f);
+        out.store(dx, i);
       }
-      d[u].set(f);
-      d[u].store(dx, i);
     }
+    stage = stage + 1 == S ? 0 : stage + 1;
   }
   if (p.part == nullptr) return;
-  // the block's rows that were handled side by side, in order
-  __syncthreads();
   float* out = p.part + static_cast<long long>(blockIdx.x) * p.n;
-  for (int c = threadIdx.x; c < p.n; c += blockDim.x) {
+  if (WIDE) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = t + u * p.lanes;
+      if (i >= p.pieces) continue;
+#pragma unroll
+      for (int e = 0; e < N; ++e) out[i * N + e] = acc[u * N + e];
+    }
+    return;
+  }
+  // the rows that were handled side by side, in order
+  float* sums = reinterpret_cast<float*>(ring);              // [U N][threads]
+  cp_async_wait<0>();
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < U * N; ++i) sums[i * NM_THREADS + threadIdx.x] = acc[i];
+  __syncthreads();
+  for (int c = threadIdx.x; c < p.n; c += NM_THREADS) {
     const int i = c / N, e = c % N, u = i / p.lanes, tt = i % p.lanes;
     float s = 0.f;
-    for (unsigned g = 0; g < per; ++g) {
-      const int at = g * p.lanes + tt;
-      s += VEC ? acc[4 * ((u * Q + e / 4) * blockDim.x + at) + e % 4] : acc[u * blockDim.x + at];
-    }
+    for (unsigned g = 0; g < per; ++g) s += sums[(u * N + e) * NM_THREADS + g * p.lanes + tt];
     out[c] = s;
   }
 }
@@ -426,6 +511,19 @@ Split split_row(int pieces, long long rows, bool vec) {
   return s;
 }
 
+// The gradient's: two pieces a thread, four in rows of more than 512.
+Split split_grad(int pieces, bool vec) {
+  Split s;
+  s.u = vec ? (pieces > 2 * NM_THREADS ? 4 : 2) : pieces > 4096 ? 16 : 4;
+  const int need = (pieces + s.u - 1) / s.u;
+  s.wide = need > 32;
+  s.lanes = 1;
+  if (s.wide) s.lanes = (need + 31) / 32 * 32;
+  else
+    while (s.lanes < need) s.lanes *= 2;
+  return s;
+}
+
 int grad_blocks(long long rows, const Split& s) {
   const long long per = s.wide ? 1 : NM_THREADS / s.lanes;
   return static_cast<int>(std::min<long long>(ceil_div_ll(rows, per), NM_PARTS));
@@ -440,17 +538,19 @@ cudaError_t launch_norm(const NormParams& p, const Split& s, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <class T, bool VEC, int U>
+template <class T, bool VEC, int U, int S>
 cudaError_t launch_grad(const NormParams& p, const Split& s, cudaStream_t st) {
   const int threads = s.wide ? s.lanes : NM_THREADS;
-  const size_t smem = p.part ? sizeof(float) * U * Bit<T, VEC>::N * threads : 0;
-  const int grid = grad_blocks(p.rows, s);
-  auto k = s.wide ? mk_norm_grad_kernel<T, VEC, U, true> : mk_norm_grad_kernel<T, VEC, U, false>;
-  if (smem > 48 * 1024) {
+  size_t smem = VEC ? sizeof(uint4) * S * (p.r.p ? 3 : 2) * U * threads : 0;
+  if (!s.wide) smem = std::max(smem, sizeof(float) * U * Bit<T, VEC>::N * threads);
+  auto k = mk_norm_grad_kernel<T, VEC, U, true, S>;
+  if constexpr (U == (VEC ? 2 : 4))                          // (more a thread: rows of more than a warp)
+    if (!s.wide) k = mk_norm_grad_kernel<T, VEC, U, false, S>;
+  if (smem > 40 * 1024) {                                     // (48 KB with what the kernel declares itself)
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  k<<<grid, threads, smem, st>>>(p);
+  k<<<grad_blocks(p.rows, s), threads, smem, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -461,11 +561,13 @@ cudaError_t launch_norm(const NormParams& p, const Split& s, bool vec, cudaStrea
   return s.u == 4 ? launch_norm<T, false, 4, OUT8>(p, s, st) : launch_norm<T, false, 16, OUT8>(p, s, st);
 }
 
+// Shared memory: 24 KB a set of rows and block with two pieces a thread (three sets, three blocks of an SM), 48 to
+// 192 KB with four (two sets up to 512 threads, one beyond).
 template <class T>
 cudaError_t launch_grad(const NormParams& p, const Split& s, bool vec, cudaStream_t st) {
-  if (vec) return s.u == 1 ? launch_grad<T, true, 1>(p, s, st) : launch_grad<T, true, 4>(p, s, st);
-  if (s.u == 1) return launch_grad<T, false, 1>(p, s, st);
-  return s.u == 4 ? launch_grad<T, false, 4>(p, s, st) : launch_grad<T, false, 16>(p, s, st);
+  if (!vec) return s.u == 4 ? launch_grad<T, false, 4, 1>(p, s, st) : launch_grad<T, false, 16, 1>(p, s, st);
+  if (s.u == 2) return launch_grad<T, true, 2, 3>(p, s, st);
+  return s.lanes <= 512 ? launch_grad<T, true, 4, 2>(p, s, st) : launch_grad<T, true, 4, 1>(p, s, st);
 }
 
 bool sizes_ok(mk_dtype dtype, mk_dtype weight_dtype, long long tokens, int heads, int n, float eps) {
@@ -571,7 +673,7 @@ mk_status mk_rms_norm_backward(const mk_rows* dy, const mk_rows* dh, const mk_ro
   p.n = n;
   p.eps = eps;
   p.pieces = vec ? n / N : n;
-  const Split s = split_row(p.pieces, p.rows, vec);
+  const Split s = split_grad(p.pieces, vec);
   p.lanes = s.lanes;
   cudaError_t e;
   if (dtype == MK_BF16) e = launch_grad<__nv_bfloat16>(p, s, vec, st);
