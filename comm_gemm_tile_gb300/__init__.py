@@ -224,8 +224,10 @@ def load_library(path: str) -> ctypes.CDLL:
     L.mk_moe_route.argtypes = [vp, i, ll, i, ll, i, i, f32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     L.mk_moe_route_backward.restype = i
     L.mk_moe_route_backward.argtypes = [vp, i, ll, i, ll, i, i, f32, vp, vp, vp, vp, vp, vp, vp, ll, vp]
+    L.mk_w4_gemm_scratch_size.restype = sz
+    L.mk_w4_gemm_scratch_size.argtypes = [P(_W4), ll]
     L.mk_w4_gemm.restype = i
-    L.mk_w4_gemm.argtypes = [vp, ll, P(_W4), vp, ll, i, i, ll, vp]
+    L.mk_w4_gemm.argtypes = [vp, ll, P(_W4), vp, ll, i, i, ll, vp, sz, vp, sz, P(_Cfg), vp]
     return L
 
 
@@ -1028,16 +1030,22 @@ class W4Weight:
         return w.flatten(1).to(dtype or s.dtype)
 
 
-def w4_gemm(x, w: W4Weight, *, out_dtype=None, out=None, stream=None):
+def w4_gemm(x, w: W4Weight, *, out_dtype=None, out=None, cfg: Config | None = None, workspace: Workspace | None = None,
+            stream=None):
     """y = x @ W^T for the rows of a decode step: x [m x k] of the weight's 16-bit type, y [m x n] in it or fp32
     (out_dtype).  Codes are multiplied as whole numbers, groups scaled and summed in fp32, y is rounded once.
-    Any m is taken; for prompts the 16-bit products are faster.  For serving: an x that requires a gradient is
-    refused."""
+    Any m is taken; for long prompts the 16-bit products are faster.  For serving: an x that requires a gradient is
+    refused.  More than 8 rows take scratch from the stream's memory; a wait that runs out there sets the device status."""
     _need(isinstance(w, W4Weight), "w is not a W4Weight")
     _need(out_dtype in (None, torch.float32) or out_dtype == getattr(x, "dtype", None), "out_dtype is x's type or fp32")
     _need(not _wants_gradient(x), "x requires a gradient: w4_gemm has none (use torch.no_grad)")
+    c = cfg.c() if cfg is not None else None
+    get = (workspace or _default_ws.get(w._device) or _ws(None, w.codes.device)).get
+    if stream is not None:
+        get = functools.partial(get, stream=stream)
     with _on_given(stream, x):
-        st, y = _bind().w4_gemm(_address("mk_w4_gemm"), x, w._w, w._device, out, out_dtype == torch.float32, _raw(stream))
+        st, y = _bind().w4_gemm(_address("mk_w4_gemm"), _address("mk_w4_gemm_scratch_size"), get, x, w._w, w._device, out,
+                                out_dtype == torch.float32, ctypes.addressof(c) if c is not None else None, _raw(stream))
     if st:
         _check(st, "mk_w4_gemm")
     return y

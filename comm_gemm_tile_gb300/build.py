@@ -22,7 +22,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmk.so")
 LIB_DEBUG = os.path.join(HERE, "libmk_debug.so")
 SOURCES = ["mk_api.cu", "mk_fused.cu", "mk_moe.cu", "mk_combine.cu", "mk_attn.cu", "mk_noalloc.cu",
-           "mk_rope.cu", "mk_paged.cu", "mk_prompt.cu", "mk_norm.cu", "mk_route.cu", "mk_w4.cu"]
+           "mk_rope.cu", "mk_paged.cu", "mk_prompt.cu", "mk_norm.cu", "mk_route.cu", "mk_w4.cu",
+           "mk_w4_tiles.cu"]
 BIND = os.path.join(HERE, "_mkbind.so")
 BIND_SOURCE = os.path.join(CSRC, "mk_bind.c")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

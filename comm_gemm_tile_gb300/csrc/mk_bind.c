@@ -729,41 +729,55 @@ static PyObject *bind_w4(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   return Py_BuildValue("(y#i)", (const char *)&w, (Py_ssize_t)sizeof(w), c.device);
 }
 
+typedef size_t (*w4_size_fn)(const mk_w4_weight *, long long);
 typedef mk_status (*w4_fn)(const void *, long long, const mk_w4_weight *, void *, long long, mk_dtype, mk_dtype, long long,
-                           mk_stream_t);
-/* w4_gemm(fn, x, weight, device, out, fp32, stream) -> (status, out) */
+                           void *, size_t, void *, size_t, const mk_config *, mk_stream_t);
+/* w4_gemm(fn, size_fn, get_workspace, x, weight, device, out, fp32, config address, stream) -> (status, out) */
 static PyObject *bind_w4_gemm(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   (void)self;
-  NEED(n == 7, "w4_gemm: 7 arguments");
-  tensor x, y;
+  NEED(n == 10, "w4_gemm: 10 arguments");
+  tensor x, y, sc, ws;
   mk_stream_t st;
-  if (read_matrix(a[1], &x, "x")) return NULL;
-  NEED(PyBytes_Check(a[2]) && PyBytes_GET_SIZE(a[2]) == (Py_ssize_t)sizeof(mk_w4_weight), "not a 4-bit weight");
-  const mk_w4_weight *w = (const mk_w4_weight *)PyBytes_AS_STRING(a[2]);
-  const int dev = (int)PyLong_AsLong(a[3]), f32 = PyObject_IsTrue(a[5]);
+  if (read_matrix(a[3], &x, "x")) return NULL;
+  NEED(PyBytes_Check(a[4]) && PyBytes_GET_SIZE(a[4]) == (Py_ssize_t)sizeof(mk_w4_weight), "not a 4-bit weight");
+  const mk_w4_weight *w = (const mk_w4_weight *)PyBytes_AS_STRING(a[4]);
+  const int dev = (int)PyLong_AsLong(a[5]), f32 = PyObject_IsTrue(a[7]);
+  void *cfg = a[8] == Py_None ? NULL : PyLong_AsVoidPtr(a[8]);
   if (PyErr_Occurred()) return NULL;
   NEED(x.dtype == w->dtype && x.device == dev, "x does not have the weight's type or device");
   NEED(x.shape[1] == w->k, "x's rows are not as long as the weight's");
-  if (check_device(dev) || read_stream(a[6], dev, &st)) return NULL;
+  if (check_device(dev) || read_stream(a[9], dev, &st)) return NULL;
   const int odt = f32 ? MK_F32 : x.dtype;
-  PyObject *out = a[4] == Py_None ? new_tensor(Py_BuildValue("(LL)", x.shape[0], w->n), dtype_object(odt), a[1]) : Py_NewRef(a[4]);
-  PyObject *result = NULL;
+  PyObject *out = a[6] == Py_None ? new_tensor(Py_BuildValue("(LL)", x.shape[0], w->n), dtype_object(odt), a[3]) : Py_NewRef(a[6]);
+  PyObject *space = NULL, *status = NULL, *result = NULL;
   if (!out || read_matrix(out, &y, "out")) goto end;
   if (y.dtype != odt || y.device != dev || y.shape[0] != x.shape[0] || y.shape[1] != w->n) {
     refuse("out's type, shape or device does not fit");
     goto end;
   }
+  sc.ptr = ws.ptr = NULL;
+  sc.shape[0] = ws.shape[0] = 0;
   {
+    const size_t need = ((w4_size_fn)PyLong_AsVoidPtr(a[1]))(w, x.shape[0]);
+    if (need > 0) {
+      space = scratch(Py_None, need, a[3]);
+      if (!space || read_tensor(space, &sc, "scratch")) goto end;
+      status = PyObject_CallFunction(a[2], "i", 256);
+      if (!status || read_tensor(status, &ws, "workspace")) goto end;
+    }
     w4_fn fn = (w4_fn)PyLong_AsVoidPtr(a[0]);
     if (!fn) goto end;
     mk_status e;
     Py_BEGIN_ALLOW_THREADS
-    e = fn(x.ptr, x.stride[0], w, y.ptr, y.stride[0], (mk_dtype)x.dtype, (mk_dtype)odt, x.shape[0], st);
+    e = fn(x.ptr, x.stride[0], w, y.ptr, y.stride[0], (mk_dtype)x.dtype, (mk_dtype)odt, x.shape[0], sc.ptr,
+           (size_t)sc.shape[0], ws.ptr, (size_t)ws.shape[0], (const mk_config *)cfg, st);
     Py_END_ALLOW_THREADS
     result = Py_BuildValue("(iO)", (int)e, out);
   }
 end:
   Py_XDECREF(out);
+  Py_XDECREF(space);
+  Py_XDECREF(status);
   return result;
 }
 

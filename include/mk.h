@@ -516,9 +516,9 @@ mk_status mk_paged_attention(const void *q, void *out, float *lse, mk_dtype dtyp
 
 /* ---------------------------------------------------------------------------
  * What stands around the products of a layer: the norm of its rows, the choice
- * of experts, and products with 4-bit weights.  These entry points set no device
- * status and keep nothing between calls: a workspace is scratch of the call alone, needs no clearing, and a
- * CUDA graph may capture them.  Strides count elements. */
+ * of experts, and products with 4-bit weights.  These entry points keep
+ * nothing between calls, and a CUDA graph may capture them.  Where no other use is given, a
+ * workspace is scratch of the call alone and needs no clearing.  Strides count elements. */
 
 /* [tokens x heads x n] rows, the last dimension contiguous; any token and head
  * strides, 0 (an expanded dimension) for inputs only. */
@@ -600,13 +600,23 @@ typedef struct {
   int group, dtype;
 } mk_w4_weight;
 
+/* Scratch bytes for mk_w4_gemm (0 for up to 8 rows, and on bad arguments). */
+size_t mk_w4_gemm_scratch_size(const mk_w4_weight *w, long long m);
+
 /* y = x @ W^T for a few rows: x [m x k] of w->dtype (rows x_row elements apart, whole
  * 16-byte pieces), y [m x n] of the same type or MK_F32.  Codes are multiplied as whole
  * numbers, groups are scaled and summed in fp32, y is rounded once.  A row of x that
- * holds an infinity gives infinities or NaN.  Built for the
- * rows of a decode step; any m is taken, 64 rows at a time. */
+ * holds an infinity gives infinities or NaN.  Built for the rows of a decode step; more
+ * are taken 64 at a time (m below 2^24, and m n k below 2^49 or so).
+ * More than 8 rows take scratch (256-byte aligned, of the call alone, no clearing) and a
+ * workspace of 256 bytes, zero-filled once, which holds the device status and nothing else:
+ * MK_ERR_TIMEOUT if a bounded wait ran out, after which y is undefined.  Both may be NULL for
+ * fewer.  cfg (may be NULL): max_ctas, wait_limit_ns and inject (1: one CTA does not
+ * load its last step) apply. */
 mk_status mk_w4_gemm(const void *x, long long x_row, const mk_w4_weight *w, void *y, long long y_row,
-                     mk_dtype dtype, mk_dtype out_dtype, long long m, mk_stream_t stream);
+                     mk_dtype dtype, mk_dtype out_dtype, long long m, void *scratch,
+                     size_t scratch_bytes, void *workspace, size_t ws_bytes, const mk_config *cfg,
+                     mk_stream_t stream);
 
 /* Synchronises `stream`, then reads and clears the device status word of a
  * workspace: MK_OK, MK_ERR_TIMEOUT or MK_ERR_CAPACITY (or MK_ERR_CUDA if the

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import comm_gemm_tile_gb300 as mk
-from bind_util import Fake, library, stand_in
+from bind_util import Fake, FakeWorkspace, library, stand_in
 from comm_gemm_tile_gb300 import build as mkbuild
 
 GOOD = 0x10000
@@ -95,17 +95,29 @@ def weight(**kw):
 
 
 def test_w4_refusals(L):
-    def call(x=GOOD, x_row=256, w=weight(), y=GOOD, y_row=40, dtype=mk.MK_BF16, odt=mk.MK_BF16, m=4):
-        return L.mk_w4_gemm(x, x_row, ref(w), y, y_row, dtype, odt, m, None)
+    size = L.mk_w4_gemm_scratch_size(ref(weight()), 9)
+    assert size > 0 and L.mk_w4_gemm_scratch_size(ref(weight()), 8) == 0
+    assert L.mk_w4_gemm_scratch_size(ref(weight(k=0)), 9) == 0 == L.mk_w4_gemm_scratch_size(ref(weight()), -1)
+
+    def call(x=GOOD, x_row=256, w=weight(), y=GOOD, y_row=40, dtype=mk.MK_BF16, odt=mk.MK_BF16, m=4, scratch=None,
+             scratch_bytes=0, ws=None, ws_bytes=0, cfg=None):
+        return L.mk_w4_gemm(x, x_row, ref(w), y, y_row, dtype, odt, m, scratch, scratch_bytes, ws, ws_bytes,
+                            ref(cfg.c() if cfg else None), None)
 
     assert call(m=0) == mk.MK_OK == call(w=weight(n=0))
     for bad in (dict(x=None), dict(x=GOOD + 8), dict(x_row=260), dict(w=None), dict(y=None), dict(y=GOOD + 1), dict(y_row=39),
                 dict(dtype=mk.MK_F32), dict(dtype=mk.MK_F16), dict(odt=mk.MK_F16), dict(odt=mk.MK_E4M3), dict(m=-1),
-                dict(m=1 << 40), dict(odt=mk.MK_F32, y=GOOD + 2), dict(w=weight(codes=None)), dict(w=weight(scales=None)),
+                dict(m=1 << 24), dict(odt=mk.MK_F32, y=GOOD + 2), dict(w=weight(codes=None)), dict(w=weight(scales=None)),
                 dict(w=weight(codes=GOOD + 8)), dict(w=weight(scales=GOOD + 1)), dict(w=weight(zeros=GOOD + 1)),
                 dict(w=weight(group=16)), dict(w=weight(group=256)), dict(w=weight(k=0)), dict(w=weight(k=288)),
-                dict(w=weight(n=-1)), dict(w=weight(n=1 << 31)), dict(w=weight(dtype=mk.MK_F32))):
+                dict(w=weight(n=-1)), dict(w=weight(n=1 << 31)), dict(w=weight(dtype=mk.MK_F32)),
+                dict(w=weight(n=(1 << 31) - 1, k=1 << 29)), dict(cfg=mk.Config(mode=1)), dict(cfg=mk.Config(operand=1)),
+                dict(cfg=mk.Config(max_ctas=-1))):
         assert call(**bad) == mk.MK_ERR_INVALID, bad
+    more = dict(m=9, scratch=GOOD, scratch_bytes=size, ws=GOOD, ws_bytes=256)
+    for bad in (dict(scratch=None), dict(scratch=GOOD + 64), dict(scratch_bytes=size - 1), dict(ws=None), dict(ws=GOOD + 8),
+                dict(ws_bytes=255)):
+        assert call(**{**more, **bad}) == mk.MK_ERR_INVALID, bad
 
 
 # ------------------------------------------------------------------ the Python calls, on stand-ins for CUDA tensors
@@ -134,7 +146,7 @@ def calls(device=0):
         lambda: mk.rms_norm_backward(t(4, 64, **d), t(4, 64, **d), t(64, **d), weight_gradient=False, out=t(4, 64, **d)),
         lambda: mk.moe_route(t(10, 64, dtype=F32, **d), 2, out=route(device)),
         lambda: mk.moe_route_backward(t(10, 64, **d), route(device), out=t(10, 64, **d)),
-        lambda: mk.w4_gemm(t(3, 256, **d), w4(device), out=t(3, 40, **d)),
+        lambda: mk.w4_gemm(t(3, 256, **d), w4(device), out=t(3, 40, **d), workspace=FakeWorkspace(device)),
     ]
 
 
@@ -142,7 +154,7 @@ def calls(device=0):
 def launches(monkeypatch, tmp_path):
     mkbuild.build()
     lib = library(tmp_path, "#include <unistd.h>\nstatic int n, slow; int entry(void) { ++n; if (slow) usleep(300000); return 0; }"
-                            "int count(void) { return n; } void wait(void) { slow = 1; } unsigned long size(void) { return 256; }")
+                            "int count(void) { return n; } void wait(void) { slow = 1; } unsigned long size(void) { return 0; }")
     yield lambda current: stand_in(monkeypatch, lib.entry, lib.size, current), lib
     monkeypatch.undo()
     mk._bound = None

@@ -146,6 +146,24 @@ def test_streams_and_graphs():
     assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
 
 
+def test_a_wait_that_runs_out_is_reported():
+    """One CTA stops loading: its waits end, the call returns, and the next one serves."""
+    x, w = problem(16, 300, 4096, 128, True, BF, seed=12)
+    want = mk.w4_gemm(x, w)
+    ws = mk.Workspace()
+    mk.w4_gemm(x, w, cfg=mk.Config(wait_limit_ns=20_000_000, inject=1), workspace=ws)
+    assert mk.device_status(ws)[0] == mk.MK_ERR_TIMEOUT
+    assert torch.equal(mk.w4_gemm(x, w, workspace=ws), want) and mk.device_status(ws)[0] == mk.MK_OK
+
+
+@pytest.mark.parametrize("ctas", [1, 3, 7, 64])
+def test_any_number_of_ctas(ctas):
+    """Runs that hold many tiles, one, or a part: the joins differ, the sums' tolerance does not."""
+    for m, n, k, group in ((9, 260, 1152, 128), (40, 700, 640, 64), (33, 129, 96, 32)):
+        x, w = problem(m, n, k, group, True, HF, seed=13)
+        check(x, w, F32, cfg=mk.Config(max_ctas=ctas))
+
+
 def test_a_gradient_is_refused():
     x, w = problem(2, 32, 64, 32, False, BF)
     x.requires_grad_()
