@@ -6,8 +6,8 @@
 // tokens' 128 k in shared memory (A from tensor memory, M = 128, N = NT tokens, one
 // accumulator for each group of the half); then thread r of two more warpgroups adds the
 // accumulators of its lane, times its scales, to its sums of half the tokens in registers.
-// Nothing is rounded to 16 bits but the output.  Each half has two places for its numbers, one or two for its
-// accumulators in tensor memory, and a warp that issues its products (a look at a barrier takes 150
+// Nothing is rounded to 16 bits but the output.  Each half has two or three places for its numbers, one or two for
+// its accumulators in tensor memory, and a warp that issues its products (a look at a barrier takes 150
 // cycles, a half's eight products of 64 tokens 350); codes and x come through rings of their own.
 //
 // Three launches.  w4_order_kernel copies x with each 8 values in the order in
@@ -88,15 +88,16 @@ struct Tile {
   static constexpr int SC = 6, SX = NT == 64 ? 6 : 8;        // stages: steps of codes, halves of x
   static constexpr int XS = SC * C, BARS = XS + SX * X;
   static constexpr int SMEM = 1024 + BARS + 512;
-  static constexpr uint32_t A = 0, D = 256;                  // columns of tensor memory
-  static constexpr int DP = GPC * NT <= 64 ? 4 : 2;          // places of accumulators
-  static_assert(D + DP * GPC * NT <= 512, "tensor memory");
+  static constexpr int DP = GPC * NT <= 64 ? 4 : 2;          // places of accumulators, and of a half's numbers
+  static constexpr int AP = (512 - DP * GPC * NT) / 128 > 3 ? 3 : (512 - DP * GPC * NT) / 128;
+  static constexpr uint32_t A = 0, D = AP * 128;             // columns of tensor memory
+  static_assert(D + DP * GPC * NT <= 512 && AP >= 2, "tensor memory");
   static_assert(SMEM <= 232448, "shared memory");
 };
 constexpr int WT_THREADS = 640;        // warps 0-7 codes, 8-15 sums, 16 loads codes, 17 loads x, 18 and 19 products
 // barriers (byte offsets)
-constexpr uint32_t B_CFULL = 0, B_CEMPTY = 64, B_XFULL = 128, B_XEMPTY = 192, B_AFULL = 256, B_AEMPTY = 288, B_DFULL = 320,
-                   B_DEMPTY = 352, B_TMEM = 384, B_DEAD = 388;
+constexpr uint32_t B_CFULL = 0, B_CEMPTY = 64, B_XFULL = 128, B_XEMPTY = 192, B_AFULL = 256, B_AEMPTY = 304, B_DFULL = 352,
+                   B_DEMPTY = 384, B_TMEM = 416, B_DEAD = 420;
 
 __device__ __noinline__ bool wt_wait_slow(volatile int* dead, const TileParams& p, uint32_t bar, uint32_t parity, int where) {
   if (*dead) return false;
@@ -118,7 +119,13 @@ __device__ __noinline__ bool wt_wait_slow(volatile int* dead, const TileParams& 
 __device__ __forceinline__ bool wt_wait(volatile int* dead, const TileParams& p, uint32_t bar, uint32_t parity, int where) {
   return mbar_test_wait(bar, parity) || wt_wait_slow(dead, p, bar, parity, where);
 }
-// Several barriers: looked at together, waited for one by one.
+// Two or three barriers: looked at together, waited for one by one.
+__device__ __forceinline__ bool wt_wait_warp(volatile int* dead, const TileParams& p, uint32_t bar0, uint32_t parity0, uint32_t bar1,
+                                             uint32_t parity1, int where) {
+  const bool a = mbar_test_wait(bar0, parity0), b = mbar_test_wait(bar1, parity1);
+  if (__all_sync(0xffffffffu, a && b)) return true;
+  return __all_sync(0xffffffffu, wt_wait(dead, p, bar0, parity0, where) && wt_wait(dead, p, bar1, parity1, where));
+}
 __device__ __forceinline__ bool wt_wait_warp(volatile int* dead, const TileParams& p, uint32_t bar0, uint32_t parity0, uint32_t bar1,
                                              uint32_t parity1, uint32_t bar2, uint32_t parity2, int where) {
   const bool a = mbar_test_wait(bar0, parity0), b = mbar_test_wait(bar1, parity1), c = mbar_test_wait(bar2, parity2);
@@ -142,7 +149,7 @@ __device__ __forceinline__ void wt_drain(const TileParams& p, uint32_t bar, uint
 template <class T, int NT, int GPC, bool ZEROS>
 __global__ void __launch_bounds__(WT_THREADS, 1) mk_w4_tiles_kernel(const __grid_constant__ TileParams p) {
   using L = Tile<NT, GPC, ZEROS>;
-  constexpr int SC = L::SC, SX = L::SX, DP = L::DP;
+  constexpr int SC = L::SC, SX = L::SX, DP = L::DP, AP = L::AP;
   constexpr bool HALF = std::is_same<T, __half>::value;
   constexpr uint32_t IDESC = idesc_bf16_f32(WT_ROWS, NT, false, false) & (HALF ? ~((1u << 7) | (1u << 10)) : ~0u);
   extern __shared__ uint8_t raw[];
@@ -161,7 +168,7 @@ __global__ void __launch_bounds__(WT_THREADS, 1) mk_w4_tiles_kernel(const __grid
       mbar_init(bars + B_XFULL + 8 * i, 1);
       mbar_init(bars + B_XEMPTY + 8 * i, 8);                 // the warps that add what came of it
     }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2 * AP; ++i) {
       mbar_init(bars + B_AFULL + 8 * i, 4);
       mbar_init(bars + B_AEMPTY + 8 * i, 1);
     }
@@ -187,16 +194,18 @@ __global__ void __launch_bounds__(WT_THREADS, 1) mk_w4_tiles_kernel(const __grid
     const uint32_t ta = tmem + L::A + h * 64 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     for (int i = 0; i < count; ++i) {
       const int s = i % SC;
-      if (!wt_wait_warp(dead, p, bars + B_CFULL + 8 * s, (i / SC) & 1, WHERE_COPY)) break;
+      const int place = i % AP;
+      const uint32_t to = bars + 8 * (h + 2 * place), at = ta + 128 * place;
+      // (a place's first use waits for the phase before the first, which has ended)
+      if (!wt_wait_warp(dead, p, bars + B_CFULL + 8 * s, (i / SC) & 1, to + B_AEMPTY, (i / AP + 1) & 1, WHERE_COPY)) break;
+      tc_fence_after();
       // the 128-byte swizzle of the codes' tile: 16-byte piece q of row r lies at q ^ (r & 7)
       const uint8_t* w = smem + s * L::C + r * 128;
       uint4 v[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const uint4*>(w + 16 * ((4 * h + q) ^ (r & 7)));
-      const uint32_t to = bars + 8 * (h + 2 * (i & 1)), at = ta + 128 * (i & 1);
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + B_CEMPTY + 8 * s);
-      bool alive = true;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint32_t o[32];
@@ -212,14 +221,8 @@ __global__ void __launch_bounds__(WT_THREADS, 1) mk_w4_tiles_kernel(const __grid
             for (int f = 0; f < 4; ++f) o[16 * q + 4 * e + f] = four[f];
           }
         }
-        if (half == 0) {
-          alive = i < 2 || wt_wait_warp(dead, p, to + B_AEMPTY, (i / 2 - 1) & 1, WHERE_COPY);
-          if (!alive) break;
-          tc_fence_after();
-        }
         tc_st_32x32b_x32(at + 32 * half, o);
       }
-      if (!alive) break;
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -227,7 +230,7 @@ __global__ void __launch_bounds__(WT_THREADS, 1) mk_w4_tiles_kernel(const __grid
     }
   } else if (warp < 16) {
     // ---------------------------------------------------------------- sums, of half the tokens
-    constexpr int TOK = NT / 2, CH = TOK < 16 ? 8 : 16;
+    constexpr int TOK = NT / 2;
     const int r = threadIdx.x & 127, t0 = warp < 12 ? 0 : TOK;
     const uint32_t td = tmem + L::D + t0 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     uint64_t acc[TOK / 2];                                   // two tokens each
@@ -282,54 +285,47 @@ __global__ void __launch_bounds__(WT_THREADS, 1) mk_w4_tiles_kernel(const __grid
         of_row();
       }
       scales(ends ? 0 : c + 1);                              // (the first of a tile once more after the last)
-      bool alive = true;
+      const int x0 = 2 * i % SX, place0 = 2 * i % DP;        // (of the first half; the second's come after them)
+      const uint32_t full = bars + B_DFULL + 8 * place0, turn = 2 * i / DP & 1, xfull = bars + B_XFULL + 8 * x0;
+      if (!wt_wait_warp(dead, p, full, turn, full + 8, turn, WHERE_EPILOGUE)) break;
+      if (ZEROS && !wt_wait_warp(dead, p, xfull, 2 * i / SX & 1, xfull + 8, 2 * i / SX & 1, WHERE_EPILOGUE)) break;   // (there already)
+      tc_fence_after();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int x = (2 * i + h) % SX, place = (2 * i + h) % DP;
-        const uint32_t turn = (2 * i + h) / DP & 1;
-        const uint32_t full = bars + B_DFULL + 8 * place, xfull = bars + B_XFULL + 8 * x;
-        if (ZEROS)                                           // (x is there already: the products waited for it)
-          alive = alive && wt_wait_warp(dead, p, full, turn, xfull, ((2 * i + h) / SX) & 1, full, turn, WHERE_EPILOGUE);
-        else
-          alive = alive && wt_wait_warp(dead, p, full, turn, WHERE_EPILOGUE);
-        if (!alive) break;
-        tc_fence_after();
-        if (threadIdx.x == 8 * 32) mbar_arrive(bars + B_AEMPTY + 8 * (h + 2 * (i & 1)));
 #pragma unroll
         for (int q = 0; q < GPC; ++q) {
           const uint64_t s = two(fs[h * GPC + q], fs[h * GPC + q]), z = two(fz[h * GPC + q], fz[h * GPC + q]);
+          uint32_t d[TOK];
+          const uint32_t from = td + ((place0 + h) * GPC + q) * NT;
+          if constexpr (TOK == 32) tc_ld_32x32b_x32(from, d);
+          else if constexpr (TOK == 16) tc_ld_32x32b_x16(from, d);
+          else tc_ld_32x32b_x8(from, d);
+          tc_wait_ld();
 #pragma unroll
-          for (int b = 0; b < TOK; b += CH) {
-            uint32_t d[CH];
-            if constexpr (CH == 16) tc_ld_32x32b_x16(td + (place * GPC + q) * NT + b, d);
-            else tc_ld_32x32b_x8(td + (place * GPC + q) * NT + b, d);
-            tc_wait_ld();
+          for (int e = 0; e < TOK; ++e) asm volatile("" : "+r"(d[e]));     // no use of them before the wait
+          const ulonglong2* sx = reinterpret_cast<const ulonglong2*>(smem + L::XS + (x0 + h) * L::X + NT * 256 + (q * NT + t0) * 4);
 #pragma unroll
-            for (int e = 0; e < CH; ++e) asm volatile("" : "+r"(d[e]));     // no use of them before the wait
-            if (q == GPC - 1 && b + CH == TOK) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bars + B_DEMPTY + 8 * place);
+          for (int e = 0; e < TOK / 2; e += 2) {
+            uint64_t lo = two(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1]));
+            uint64_t hi = two(__uint_as_float(d[2 * e + 2]), __uint_as_float(d[2 * e + 3]));
+            if (ZEROS) {
+              const ulonglong2 t = sx[e / 2];
+              lo = fma2(z, t.x, lo);
+              hi = fma2(z, t.y, hi);
             }
-            const ulonglong2* sx = reinterpret_cast<const ulonglong2*>(smem + L::XS + x * L::X + NT * 256 + (q * NT + t0 + b) * 4);
-#pragma unroll
-            for (int e = 0; e < CH / 2; e += 2) {
-              uint64_t lo = two(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1]));
-              uint64_t hi = two(__uint_as_float(d[2 * e + 2]), __uint_as_float(d[2 * e + 3]));
-              if (ZEROS) {
-                const ulonglong2 t = sx[e / 2];
-                lo = fma2(z, t.x, lo);
-                hi = fma2(z, t.y, hi);
-              }
-              acc[b / 2 + e] = fma2(s, lo, acc[b / 2 + e]);
-              acc[b / 2 + e + 1] = fma2(s, hi, acc[b / 2 + e + 1]);
-            }
+            acc[e] = fma2(s, lo, acc[e]);
+            acc[e + 1] = fma2(s, hi, acc[e + 1]);
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars + B_XEMPTY + 8 * x);
+        if (h == 1) tc_fence_before();
       }
-      if (!alive) break;
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bars + B_DEMPTY + 8 * place0);
+        mbar_arrive(bars + B_DEMPTY + 8 * place0 + 8);
+        mbar_arrive(bars + B_XEMPTY + 8 * x0);
+        mbar_arrive(bars + B_XEMPTY + 8 * x0 + 8);
+      }
       if (ends || i + 1 == count) {
         // all of a tile, or the run's part of it: that at the run's beginning first, another second
         const int m0 = tile / row_tiles * NT + t0;
@@ -404,9 +400,9 @@ __global__ void __launch_bounds__(WT_THREADS, 1) mk_w4_tiles_kernel(const __grid
     const int h = warp - 18;
     int i = 0;
     for (; i < count; ++i) {
-      const int j = 2 * i + h, s = j % SX, place = h + 2 * (i & 1), to = j % DP;
+      const int j = 2 * i + h, s = j % SX, place = h + 2 * (i % AP), to = j % DP;
       const uint32_t xfull = bars + B_XFULL + 8 * s, afull = bars + B_AFULL + 8 * place;
-      const uint32_t xp = (j / SX) & 1, ap = (i / 2) & 1;
+      const uint32_t xp = (j / SX) & 1, ap = (i / AP) & 1;
       // (a place's first use waits for the phase before the first, which has ended)
       if (!wt_wait_warp(dead, p, xfull, xp, afull, ap, bars + B_DEMPTY + 8 * to, (j / DP + 1) & 1, WHERE_MMA)) break;
       tc_fence_after();
@@ -418,6 +414,7 @@ __global__ void __launch_bounds__(WT_THREADS, 1) mk_w4_tiles_kernel(const __grid
           constexpr int PER = 8 / GPC;                       // products of a group
           tc_mma_bf16_ts(d + ks / PER * NT, a + 8 * ks, b + ((ks / 4 * (NT * 128) + ks % 4 * 32) >> 4), IDESC, ks % PER != 0);
         }
+        tc_commit(bars + B_AEMPTY + 8 * place);
         tc_commit(bars + B_DFULL + 8 * to);
       }
       __syncwarp();
