@@ -831,10 +831,13 @@ def paged_attention(q, cache: KVCache, cu_q, kv_len, pages, *, causal: bool = Tr
 
 # ------------------------------------------------------------------ norm, router, 4-bit weights
 
+_NULL = contextlib.nullcontext()
+
+
 def _on_given(stream, x):
     """A context in which the outputs and scratch of a call come from the pool of the stream it is given."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _NULL
     _need(isinstance(x, torch.Tensor) and x.is_cuda, "the first argument is not a CUDA tensor")
     return _on(stream, x.device)
 
@@ -844,7 +847,10 @@ def _getter(workspace, stream):
 
 
 def _wants_gradient(*tensors):
-    return torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in tensors)
+    for t in tensors:
+        if getattr(t, "requires_grad", False):
+            return torch.is_grad_enabled()
+    return False
 
 
 def _rows_gradient(g):
@@ -921,6 +927,7 @@ def rms_norm_backward(dy, h, weight=None, *, dh=None, eps: float = 1e-6, weight_
 
 
 _ROUTE = ("topk_idx", "gates", "counts", "tokens", "balance_loss", "z_loss")
+_NONE = (None,) * len(_ROUTE)
 
 
 class _MoeRoute(torch.autograd.Function):
@@ -963,7 +970,7 @@ def moe_route(logits, topk: int, *, normalize: bool = True, scale: float = 1.0, 
         return dict(zip(_ROUTE, _MoeRoute.apply(logits, topk, dict(normalize=normalize, scale=scale), mask, workspace, stream)))
     with _on_given(stream, logits):
         st, *got = _bind().route(_address("mk_moe_route"), _address("mk_moe_route_workspace_size"), _getter(workspace, stream),
-                                 logits, topk, normalize, scale, mask, tuple(o.get(name) for name in _ROUTE), _raw(stream))
+                                 logits, topk, normalize, scale, mask, tuple(map(o.get, _ROUTE)) if o else _NONE, _raw(stream))
     if st:
         _check(st, "mk_moe_route")
     return dict(zip(_ROUTE, got))

@@ -382,13 +382,27 @@ end:
 
 /* ------------------------------------------------------------------ norm, router, 4-bit weights */
 
-static PyObject *new_tensor(PyObject *shape, PyObject *dtype, PyObject *like) {      /* steals shape */
-  PyObject *device = shape ? PyObject_GetAttr(like, s_device) : NULL;
+static PyObject *new_tensor(PyObject *shape, PyObject *dtype, PyObject *device) {      /* steals shape */
   PyObject *args[3] = {shape, dtype, device};
-  PyObject *r = device ? PyObject_Vectorcall(empty, args, 1, s_kw) : NULL;
+  PyObject *r = shape && device ? PyObject_Vectorcall(empty, args, 1, s_kw) : NULL;
   Py_XDECREF(shape);
-  Py_XDECREF(device);
   return r;
+}
+static int pointer_of(PyObject *t, tensor *o) {
+  PyObject *p = PyObject_CallMethodNoArgs(t, s_data_ptr);
+  if (!p) return -1;
+  o->ptr = PyLong_AsVoidPtr(p);
+  Py_DECREF(p);
+  return PyErr_Occurred() ? -1 : 0;
+}
+/* What a new contiguous tensor of like's shape and the given type is (like: three dimensions). */
+static int read_new_rows(PyObject *t, tensor *o, const tensor *like, int dtype) {
+  *o = *like;
+  o->dtype = dtype;
+  o->stride[2] = 1;
+  o->stride[1] = o->shape[1] > 1 ? o->shape[2] : 0;
+  o->stride[0] = o->shape[0] > 1 ? o->shape[1] * o->shape[2] : 0;
+  return pointer_of(t, o);
 }
 static PyObject *dtype_object(int code) {
   for (int i = 0; i < N_DTYPES; ++i)
@@ -477,10 +491,10 @@ static PyObject *bind_norm(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   NEED(e4m3 || a[5] == Py_None, "only 8-bit outputs have scales");
   const double eps = PyFloat_AsDouble(a[8]);
   if (PyErr_Occurred() || read_weight(a[3], &w, &x) || check_device(x.device) || read_stream(a[9], x.device, &st)) return NULL;
-  PyObject *out = NULL, *scale = NULL, *ho = NULL, *result = NULL;
+  PyObject *out = NULL, *scale = NULL, *ho = NULL, *result = NULL, *device = PyObject_GetAttr(a[1], s_device);
   const int odt = e4m3 ? MK_E4M3 : x.dtype;
-  out = a[4] == Py_None ? new_tensor(PyObject_GetAttr(a[1], s_shape), dtype_object(odt), a[1]) : Py_NewRef(a[4]);
-  if (!out || read_norm_rows(out, &y, "out", &x)) goto end;
+  out = a[4] == Py_None ? new_tensor(PyObject_GetAttr(a[1], s_shape), dtype_object(odt), device) : Py_NewRef(a[4]);
+  if (!out || (a[4] == Py_None ? read_new_rows(out, &y, &x, odt) : read_norm_rows(out, &y, "out", &x))) goto end;
   if (y.dtype != odt) {
     refuse("out's type is not the output's");
     goto end;
@@ -489,13 +503,13 @@ static PyObject *bind_norm(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   if (e4m3) {
     const long long shape[2] = {x.shape[0], x.shape[1]};
     scale = a[5] == Py_None
-                ? new_tensor(x.dims == 3 ? Py_BuildValue("(LL)", shape[0], shape[1]) : Py_BuildValue("(L)", shape[0]), dtypes[1], a[1])
+                ? new_tensor(x.dims == 3 ? Py_BuildValue("(LL)", shape[0], shape[1]) : Py_BuildValue("(L)", shape[0]), dtypes[1], device)
                 : Py_NewRef(a[5]);
-    if (!scale || read_plain(scale, &sc, "scale_out", MK_F32, x.device, x.dims - 1, shape)) goto end;
+    if (!scale || (a[5] == Py_None ? pointer_of(scale, &sc) : read_plain(scale, &sc, "scale_out", MK_F32, x.device, x.dims - 1, shape))) goto end;
   }
   if (has_r) {
-    ho = a[6] == Py_None ? new_tensor(PyObject_GetAttr(a[1], s_shape), dtype_object(x.dtype), a[1]) : Py_NewRef(a[6]);
-    if (!ho || read_same_rows(ho, &h, "h_out", &x)) goto end;
+    ho = a[6] == Py_None ? new_tensor(PyObject_GetAttr(a[1], s_shape), dtype_object(x.dtype), device) : Py_NewRef(a[6]);
+    if (!ho || (a[6] == Py_None ? read_new_rows(ho, &h, &x, x.dtype) : read_same_rows(ho, &h, "h_out", &x))) goto end;
   }
   {
     norm_fn fn = (norm_fn)PyLong_AsVoidPtr(a[0]);
@@ -517,15 +531,25 @@ end:
   Py_XDECREF(out);
   Py_XDECREF(scale);
   Py_XDECREF(ho);
+  Py_XDECREF(device);
   return result;
 }
 
 /* Scratch of a call: from the given get(bytes), or memory of the call's stream. */
-static PyObject *scratch(PyObject *get, size_t bytes, PyObject *like) {
-  if (get == Py_None) return new_tensor(Py_BuildValue("(n)", (Py_ssize_t)bytes), dtype_object(T_U8), like);
-  PyObject *b = PyLong_FromSize_t(bytes), *r = b ? PyObject_CallOneArg(get, b) : NULL;
-  Py_XDECREF(b);
-  return r;
+static PyObject *scratch(PyObject *get, size_t bytes, PyObject *device, tensor *o) {
+  PyObject *r;
+  if (get == Py_None) {
+    r = new_tensor(Py_BuildValue("(n)", (Py_ssize_t)bytes), dtype_object(T_U8), device);
+    o->shape[0] = (long long)bytes;
+    if (r && !pointer_of(r, o)) return r;
+  } else {
+    PyObject *b = PyLong_FromSize_t(bytes);
+    r = b ? PyObject_CallOneArg(get, b) : NULL;
+    Py_XDECREF(b);
+    if (r && !read_tensor(r, o, "workspace")) return r;
+  }
+  Py_XDECREF(r);
+  return NULL;
 }
 
 typedef size_t (*norm_size_fn)(long long, int, int);
@@ -547,22 +571,22 @@ static PyObject *bind_norm_grad(PyObject *self, PyObject *const *a, Py_ssize_t n
   const double eps = PyFloat_AsDouble(a[9]);
   if (PyErr_Occurred() || read_weight(a[6], &w, &h) || check_device(h.device) || read_stream(a[10], h.device, &st)) return NULL;
   NEED(w.ptr || a[8] == Py_None, "there is no gradient of a weight without a weight");
-  PyObject *out = NULL, *dwo = NULL, *space = NULL, *result = NULL;
-  out = a[7] == Py_None ? new_tensor(PyObject_GetAttr(a[5], s_shape), dtype_object(h.dtype), a[5]) : Py_NewRef(a[7]);
-  if (!out || read_same_rows(out, &dx, "dx", &h)) goto end;
+  PyObject *out = NULL, *dwo = NULL, *space = NULL, *result = NULL, *device = PyObject_GetAttr(a[5], s_device);
+  out = a[7] == Py_None ? new_tensor(PyObject_GetAttr(a[5], s_shape), dtype_object(h.dtype), device) : Py_NewRef(a[7]);
+  if (!out || (a[7] == Py_None ? read_new_rows(out, &dx, &h, h.dtype) : read_same_rows(out, &dx, "dx", &h))) goto end;
   dw.ptr = ws.ptr = NULL;
   ws.shape[0] = 0;
   if (a[8] != Py_None) {
     const long long shape[1] = {h.shape[2]};
-    dwo = a[8] == Py_True ? new_tensor(Py_BuildValue("(L)", shape[0]), dtype_object(w.dtype), a[5]) : Py_NewRef(a[8]);
-    if (!dwo || read_plain(dwo, &dw, "dweight", w.dtype, h.device, 1, shape)) goto end;
+    dwo = a[8] == Py_True ? new_tensor(Py_BuildValue("(L)", shape[0]), dtype_object(w.dtype), device) : Py_NewRef(a[8]);
+    if (!dwo || (a[8] == Py_True ? pointer_of(dwo, &dw) : read_plain(dwo, &dw, "dweight", w.dtype, h.device, 1, shape))) goto end;
     const size_t need = ((norm_size_fn)PyLong_AsVoidPtr(a[1]))(h.shape[0], (int)h.shape[1], (int)h.shape[2]);
     if (need == 0) {
       result = Py_BuildValue("(iOO)", (int)MK_ERR_INVALID, Py_None, Py_None);
       goto end;
     }
-    space = scratch(a[2], need, a[5]);
-    if (!space || read_tensor(space, &ws, "workspace")) goto end;
+    space = scratch(a[2], need, device, &ws);
+    if (!space) goto end;
   }
   {
     norm_grad_fn fn = (norm_grad_fn)PyLong_AsVoidPtr(a[0]);
@@ -579,6 +603,7 @@ static PyObject *bind_norm_grad(PyObject *self, PyObject *const *a, Py_ssize_t n
   }
 end:
   Py_XDECREF(out);
+  Py_XDECREF(device);
   Py_XDECREF(dwo);
   Py_XDECREF(space);
   return result;
@@ -624,23 +649,24 @@ static PyObject *bind_route(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   static const char *names[6] = {"topk_idx", "gates", "counts", "tokens", "balance_loss", "z_loss"};
   static const int types[6] = {T_I32, MK_F32, T_I32, T_I32, MK_F32, MK_F32}, dims[6] = {2, 2, 1, 0, 0, 0};
   const long long pairs[2] = {l.shape[0], topk}, experts[1] = {l.shape[1]};
-  PyObject *o[6] = {NULL}, *space = NULL, *result = NULL;
+  PyObject *o[6] = {NULL}, *space = NULL, *result = NULL, *device = PyObject_GetAttr(a[3], s_device);
   for (int i = 0; i < 6; ++i) {
     PyObject *given = PyTuple_GET_ITEM(a[8], i);
     const long long *shape = i < 2 ? pairs : experts;
     if (given != Py_None) o[i] = Py_NewRef(given);
     else
       o[i] = new_tensor(i < 2 ? Py_BuildValue("(LL)", pairs[0], pairs[1]) : i == 2 ? Py_BuildValue("(L)", experts[0]) : PyTuple_New(0),
-                        dtype_object(types[i]), a[3]);
-    if (!o[i] || read_plain(o[i], &t[i], names[i], types[i], l.device, dims[i], shape)) goto end;
+                        dtype_object(types[i]), device);
+    if (!o[i] || (given == Py_None ? pointer_of(o[i], &t[i]) : read_plain(o[i], &t[i], names[i], types[i], l.device, dims[i], shape)))
+      goto end;
   }
   ws.ptr = NULL;
   ws.shape[0] = 0;
   if (l.shape[0] > MK_ROUTE_SMALL) {
     const size_t need = ((route_size_fn)PyLong_AsVoidPtr(a[1]))(l.shape[0], (int)l.shape[1]);
     if (need > 0) {                      /* (0: the call refuses the sizes) */
-      space = scratch(a[2], need, a[3]);
-      if (!space || read_tensor(space, &ws, "workspace")) goto end;
+      space = scratch(a[2], need, device, &ws);
+      if (!space) goto end;
     }
   }
   {
@@ -657,6 +683,7 @@ static PyObject *bind_route(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 end:
   for (int i = 0; i < 6; ++i) Py_XDECREF(o[i]);
   Py_XDECREF(space);
+  Py_XDECREF(device);
   return result;
 }
 
@@ -686,9 +713,16 @@ static PyObject *bind_route_grad(PyObject *self, PyObject *const *a, Py_ssize_t 
   const int normalize = PyObject_IsTrue(a[8]);
   const double scale = PyFloat_AsDouble(a[9]);
   if (PyErr_Occurred() || check_device(l.device) || read_stream(a[11], l.device, &st)) return NULL;
-  PyObject *out = a[10] == Py_None ? new_tensor(PyObject_GetAttr(a[1], s_shape), dtype_object(l.dtype), a[1]) : Py_NewRef(a[10]);
-  PyObject *result = NULL;
-  if (!out || read_matrix(out, &dl, "out")) goto end;
+  PyObject *device = PyObject_GetAttr(a[1], s_device), *result = NULL;
+  PyObject *out = a[10] == Py_None ? new_tensor(PyObject_GetAttr(a[1], s_shape), dtype_object(l.dtype), device) : Py_NewRef(a[10]);
+  if (!out) goto end;
+  if (a[10] == Py_None) {
+    dl = l;
+    dl.stride[0] = l.shape[1];
+    if (pointer_of(out, &dl)) goto end;
+  } else if (read_matrix(out, &dl, "out")) {
+    goto end;
+  }
   if (dl.dtype != l.dtype || dl.device != l.device || dl.shape[0] != l.shape[0] || dl.shape[1] != l.shape[1]) {
     refuse("out's type, shape or device is not that of the logits");
     goto end;
@@ -706,6 +740,7 @@ static PyObject *bind_route_grad(PyObject *self, PyObject *const *a, Py_ssize_t 
   }
 end:
   Py_XDECREF(out);
+  Py_XDECREF(device);
   return result;
 }
 
@@ -748,9 +783,17 @@ static PyObject *bind_w4_gemm(PyObject *self, PyObject *const *a, Py_ssize_t n) 
   NEED(x.shape[1] == w->k, "x's rows are not as long as the weight's");
   if (check_device(dev) || read_stream(a[9], dev, &st)) return NULL;
   const int odt = f32 ? MK_F32 : x.dtype;
-  PyObject *out = a[6] == Py_None ? new_tensor(Py_BuildValue("(LL)", x.shape[0], w->n), dtype_object(odt), a[3]) : Py_NewRef(a[6]);
-  PyObject *space = NULL, *status = NULL, *result = NULL;
-  if (!out || read_matrix(out, &y, "out")) goto end;
+  PyObject *device = PyObject_GetAttr(a[3], s_device), *space = NULL, *status = NULL, *result = NULL;
+  PyObject *out = a[6] == Py_None ? new_tensor(Py_BuildValue("(LL)", x.shape[0], w->n), dtype_object(odt), device) : Py_NewRef(a[6]);
+  if (!out) goto end;
+  if (a[6] == Py_None) {
+    y = x;
+    y.dtype = odt;
+    y.shape[1] = y.stride[0] = w->n;
+    if (pointer_of(out, &y)) goto end;
+  } else if (read_matrix(out, &y, "out")) {
+    goto end;
+  }
   if (y.dtype != odt || y.device != dev || y.shape[0] != x.shape[0] || y.shape[1] != w->n) {
     refuse("out's type, shape or device does not fit");
     goto end;
@@ -760,8 +803,8 @@ static PyObject *bind_w4_gemm(PyObject *self, PyObject *const *a, Py_ssize_t n) 
   {
     const size_t need = ((w4_size_fn)PyLong_AsVoidPtr(a[1]))(w, x.shape[0]);
     if (need > 0) {
-      space = scratch(Py_None, need, a[3]);
-      if (!space || read_tensor(space, &sc, "scratch")) goto end;
+      space = scratch(Py_None, need, device, &sc);
+      if (!space) goto end;
       status = PyObject_CallFunction(a[2], "i", 256);
       if (!status || read_tensor(status, &ws, "workspace")) goto end;
     }
@@ -778,6 +821,7 @@ end:
   Py_XDECREF(out);
   Py_XDECREF(space);
   Py_XDECREF(status);
+  Py_XDECREF(device);
   return result;
 }
 

@@ -1,6 +1,7 @@
 // mk_internal.h -- definitions shared by the host launchers and the kernels.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -202,6 +203,17 @@ bool make_map_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uin
 bool encode_map(CUtensorMap* m, CUtensorMapDataType type, int rank, void* base, const cuuint64_t* dims,
                 const cuuint64_t* strides, const cuuint32_t* box, const cuuint32_t* steps, CUtensorMapSwizzle swizzle);
 long long default_wait_ns(const mk_config* cfg);
+
+// Lets a kernel have that much dynamic shared memory, once a device (`done`: a static of the caller, one bit a device).
+template <class Kernel>
+cudaError_t allow_smem(Kernel* kernel, size_t bytes, std::atomic<unsigned>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 32 && (done.load(std::memory_order_relaxed) >> dev & 1u))) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess && dev < 32) done.fetch_or(1u << dev, std::memory_order_relaxed);
+  return e;
+}
 
 // Launches kernel(a) as a programmatic dependent of the previous launch on s:
 // the kernel must wait (griddepcontrol.wait) before it reads that launch's

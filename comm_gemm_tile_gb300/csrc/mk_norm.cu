@@ -544,10 +544,12 @@ cudaError_t launch_grad(const NormParams& p, const Split& s, cudaStream_t st) {
   size_t smem = VEC ? sizeof(uint4) * S * (p.r.p ? 3 : 2) * U * threads : 0;
   if (!s.wide) smem = std::max(smem, sizeof(float) * U * Bit<T, VEC>::N * threads);
   auto k = mk_norm_grad_kernel<T, VEC, U, true, S>;
+  static std::atomic<unsigned> done[2];
   if constexpr (U == (VEC ? 2 : 4))                          // (more a thread: rows of more than a warp)
     if (!s.wide) k = mk_norm_grad_kernel<T, VEC, U, false, S>;
-  if (smem > 40 * 1024) {                                     // (48 KB with what the kernel declares itself)
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (VEC) {
+    constexpr size_t most = sizeof(uint4) * S * 3 * U * (S == 2 ? 512 : GradShape<T, VEC, U>::THREADS);
+    const cudaError_t e = allow_smem(k, most, done[s.wide]);
     if (e != cudaSuccess) return e;
   }
   k<<<grad_blocks(p.rows, s), threads, smem, st>>>(p);

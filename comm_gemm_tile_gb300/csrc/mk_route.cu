@@ -11,11 +11,16 @@
 //   balance           dl_e += db E / N p_e (f_e - sum_j p_j f_j)
 //   z                 dl_e += dz 2 lse p_e / N
 //
-// A warp has a token, a lane a run of PER neighbouring experts, so that the
-// lowest lane of equal logits is the lowest expert.  Per-expert sums stay in the
-// lanes' registers, are added over a block's warps in shared memory and over the
-// blocks by a second launch, always in the same order.
-#include <algorithm>
+// A warp has a token (and the next one's logits on their way), a lane a run of PER neighbouring
+// experts, so that the lowest lane of equal logits is the lowest expert.  Per-expert
+// sums of p stay in the lanes' registers, are added over a block's warps in shared
+// memory and over the blocks by a second launch, always in the same order.  (Counts
+// are whole numbers: shared memory's atomics do for them.)
+//
+// Choosing: at most two experts, by as many rounds of the largest key over the warp.
+// More: K rounds over the lanes' largest keys alone give a bound that at least K
+// keys reach, and few more; those are gathered one to a lane, and each counts the ones
+// before it.  #include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -25,9 +30,12 @@ namespace mk {
 
 namespace {
 
-constexpr int RT_WARPS = 8;
+constexpr int RT_WARPS = 32;           // 131072 tokens, 256 experts: 114 us with the gradient; blocks of 16 warps 121, of 8 130
 constexpr int RT_THREADS = 32 * RT_WARPS;
-constexpr int RT_BLOCKS = 304;         // blocks of a call at most
+constexpr int RT_BLOCKS = 152;         // blocks of a call at most
+constexpr int RS_WARPS = 32;           // of a block that adds the blocks' sums
+constexpr int RG_WARPS = 8;            // the gradient's
+constexpr int RG_THREADS = 32 * RG_WARPS;
 
 struct RouteParams {
   const char* logits;
@@ -68,119 +76,180 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// A lane's logits of a token; -inf past the last expert.
-template <class T, int PER>
-__device__ __forceinline__ void load_logits(const RouteParams& p, int t, float (&v)[PER]) {
-  const T* row = reinterpret_cast<const T*>(p.logits + t * p.row);
-  const int e0 = (threadIdx.x & 31) * PER;
-#pragma unroll
-  for (int j = 0; j < PER; ++j) v[j] = e0 + j < p.E ? Piece<T>::one(row[e0 + j]) : -INFINITY;
+// Both losses and N from the sums over tokens: b of counts times p, z of lse^2.
+__device__ __forceinline__ void write_losses(const RouteParams& p, float b, float z, int n) {
+  const float in = n > 0 ? 1.f / n : 0.f;
+  *p.balance = b * in * in * (static_cast<float>(p.E) / p.K);
+  *p.z = z * in;
+  *p.tokens = n;
 }
 
-__device__ void finish(const RouteParams& p, const float* sp, const int* sc, float z, int n, float* scratch) {
-  // sp, sc: [E] sums of p and counts; by the whole block
-  const float f = n > 0 ? 1.f / (static_cast<float>(p.K) * n) : 0.f, in = n > 0 ? 1.f / n : 0.f;
-  float b = 0.f;
-  for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
-    b += sc[e] * f * (sp[e] * in);
-    p.counts[e] = sc[e];
+// exp(x), x <= 0: off by about |x| 2^-24 and 4 2^-24 of itself.
+__device__ __forceinline__ float exp_of(float x) { return __expf(x); }
+
+// A lane's logits of a token, as they lie; -inf past the last expert.
+template <class T, int PER>
+struct Logits {
+  static constexpr int BYTES = PER * static_cast<int>(sizeof(T));
+  T v[PER];
+  __device__ __forceinline__ void load(const RouteParams& p, int t) {
+    const T* row = reinterpret_cast<const T*>(p.logits + t * p.row) + (threadIdx.x & 31) * PER;
+    const int left = p.E - (threadIdx.x & 31) * PER;
+    if (p.vec && BYTES >= 4) {                               // all of a lane's, or none
+      if (left >= PER) {
+        if constexpr (BYTES == 4) copy(__ldg(reinterpret_cast<const uint32_t*>(row)));
+        else if constexpr (BYTES == 8) copy(__ldg(reinterpret_cast<const uint2*>(row)));
+        else
+#pragma unroll
+          for (int i = 0; i < BYTES / 16; ++i) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(row) + i);
+            memcpy(reinterpret_cast<char*>(v) + 16 * i, &w, 16);
+          }
+      } else {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) v[j] = Piece<T>::of(-INFINITY);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) v[j] = j < left ? row[j] : Piece<T>::of(-INFINITY);
+    }
   }
-  b = warp_sum(b);
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = b;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    b = 0.f;
-    for (unsigned w = 0; w < blockDim.x / 32; ++w) b += scratch[w];
-    *p.balance = b * p.E;
-    *p.z = z * in;
-    *p.tokens = n;
+  template <class W>
+  __device__ __forceinline__ void copy(const W& w) { memcpy(v, &w, sizeof(W)); }
+  __device__ __forceinline__ void get(float (&f)[PER]) const {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) f[j] = Piece<T>::one(v[j]);
   }
-}
+};
 
 template <class T, int PER>
 __global__ void __launch_bounds__(RT_THREADS) mk_route_kernel(const __grid_constant__ RouteParams p) {
   __shared__ float s_p[RT_WARPS][32 * PER];
-  __shared__ int s_c[RT_WARPS][32 * PER];
+  __shared__ int s_c[32 * PER];
+  __shared__ uint2 s_list[RT_WARPS][32];             // keys and experts that may be among the chosen
   __shared__ float s_z[RT_WARPS];
   __shared__ int s_n[RT_WARPS];
   __shared__ float scratch[RT_WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = lane * PER;
+  const uint32_t before = (1u << lane) - 1u;
   griddep_launch_dependents();
+  for (int e = threadIdx.x; e < 32 * PER; e += RT_THREADS) s_c[e] = 0;
+  __syncthreads();
   float psum[PER];
-  int cnt[PER];
 #pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    psum[j] = 0.f;
-    cnt[j] = 0;
-  }
+  for (int j = 0; j < PER; ++j) psum[j] = 0.f;
   float z = 0.f;
   int n = 0;
-  for (int t = blockIdx.x * RT_WARPS + warp; t < p.T; t += gridDim.x * RT_WARPS) {
-    int my_idx = -1;
-    float my_gate = 0.f;
-    if (p.mask == nullptr || p.mask[t] != 0) {
+  const int step = gridDim.x * RT_WARPS;
+  int t = blockIdx.x * RT_WARPS + warp;
+  Logits<T, PER> next;
+  bool next_real = false;
+  auto ahead = [&](int t) {
+    next_real = t < p.T && (p.mask == nullptr || p.mask[t] != 0);
+    if (next_real) next.load(p, t);
+  };
+  ahead(t);
+  for (; t < p.T; t += step) {
+    const Logits<T, PER> now = next;
+    const bool real = next_real;
+    ahead(t > p.T - step ? p.T : t + step);        // (t + step may pass 2^31)
+    int id = -1, slot = lane;                        // this lane's chosen expert, and its place among them
+    float w = 0.f;                                   // exp(its logit - the largest)
+    if (real) {
       float v[PER];
       uint32_t k[PER];
-      load_logits<T, PER>(p, t, v);
+      now.get(v);
 #pragma unroll
       for (int j = 0; j < PER; ++j) k[j] = key_of(v[j]);
-      float top = 0.f, chosen = 0.f;
-      for (int r = 0; r < p.K; ++r) {
-        uint32_t m = k[0];
+      uint32_t most = k[0];
 #pragma unroll
-        for (int j = 1; j < PER; ++j) m = max(m, k[j]);
-        const uint32_t best = __reduce_max_sync(0xffffffffu, m);
-        if (best <= KEY_NONE) break;                     // no expert left
-        const int owner = __ffs(__ballot_sync(0xffffffffu, m == best)) - 1;
-        int at = 0;
-        if (lane == owner) {
-#pragma unroll
-          for (int j = PER - 1; j >= 0; --j)
-            if (k[j] == best) at = j;
-#pragma unroll
-          for (int j = 0; j < PER; ++j)
-            if (j == at) {
-              k[j] = 0;
-              ++cnt[j];
-            }
+      for (int j = 1; j < PER; ++j) most = max(most, k[j]);
+      const uint32_t first = __reduce_max_sync(0xffffffffu, most);
+      const float top = value_of(first);
+      bool rounds = p.K <= 2;
+      if (!rounds) {
+        uint32_t m = most, bound = first;
+        for (int r = 1; r < p.K; ++r) {
+          if (m == bound) m = 0;
+          bound = __reduce_max_sync(0xffffffffu, m);
         }
-        at = __shfl_sync(0xffffffffu, e0 + at, owner);
-        const float value = value_of(best);
-        if (r == 0) top = value;
-        const float w = expf(value - top);
-        chosen += w;
-        if (lane == r) {
-          my_idx = at;
-          my_gate = w;
+        bound = max(bound, KEY_NONE + 1);
+        int count = 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+          const uint32_t vote = __ballot_sync(0xffffffffu, k[j] >= bound);
+          const int at = count + __popc(vote & before);
+          if (k[j] >= bound && at < 32) s_list[warp][at] = make_uint2(k[j], e0 + j);
+          count += __popc(vote);
+        }
+        rounds = count > 32;                         // (many equal logits)
+        if (!rounds) {
+          __syncwarp();
+          const uint2 mine = lane < count ? s_list[warp][lane] : make_uint2(0, 0);
+          int larger = 0;
+          for (int i = 0; i < count; ++i) {
+            const uint2 o = s_list[warp][i];         // the same for every lane
+            larger += o.x > mine.x || (o.x == mine.x && o.y < mine.y);
+          }
+          __syncwarp();                              // the list has been read
+          // the places left over when fewer than K experts have a logit are the lanes' past the list
+          slot = lane < count ? larger : lane;
+          if (lane < count && larger < p.K) {
+            id = mine.y;
+            w = exp_of(value_of(mine.x) - top);
+          }
         }
       }
-      if (__shfl_sync(0xffffffffu, my_idx, 0) >= 0) {
+      if (rounds) {
+        for (int r = 0; r < p.K; ++r) {
+          uint32_t m = k[0];
+#pragma unroll
+          for (int j = 1; j < PER; ++j) m = max(m, k[j]);
+          const uint32_t best = __reduce_max_sync(0xffffffffu, m);
+          if (best <= KEY_NONE) break;               // no expert left
+          const int owner = __ffs(__ballot_sync(0xffffffffu, m == best)) - 1;
+          int at = 0;
+          if (lane == owner) {
+#pragma unroll
+            for (int j = PER - 1; j >= 0; --j)
+              if (k[j] == best) at = j;
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+              if (j == at) k[j] = 0;
+          }
+          at = __shfl_sync(0xffffffffu, e0 + at, owner);
+          if (lane == r) {
+            id = at;
+            w = exp_of(value_of(best) - top);
+          }
+        }
+      }
+      if (first > KEY_NONE) {
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-          v[j] = expf(v[j] - top);
+          v[j] = exp_of(v[j] - top);
           sum += v[j];
         }
         sum = warp_sum(sum);
-        const float inv = 1.f / sum;
+        const float inv = __fdividef(1.f, sum);
 #pragma unroll
-        for (int j = 0; j < PER; ++j) psum[j] += v[j] * inv;
-        const float lse = top + logf(sum);
-        z += lse * lse;
+        for (int j = 0; j < PER; ++j) psum[j] = fmaf(v[j], inv, psum[j]);
+        const float lse = top + __logf(sum);         // (sum is 1 .. 256: off by 3 2^-24)
+        z = fmaf(lse, lse, z);
         ++n;
-        my_gate = my_gate / (p.normalize ? chosen : sum) * p.scale;
+        w = (p.normalize ? __fdividef(w, warp_sum(w)) : w * inv) * p.scale;
+        if (id >= 0) atomicAdd(&s_c[id], 1);
       }
     }
-    if (lane < p.K) {
-      p.idx[static_cast<long long>(t) * p.K + lane] = my_idx;
-      p.gates[static_cast<long long>(t) * p.K + lane] = my_gate;
+    if (slot < p.K) {
+      p.idx[static_cast<long long>(t) * p.K + slot] = id;
+      p.gates[static_cast<long long>(t) * p.K + slot] = w;
     }
+    if (t > p.T - step) break;
   }
 #pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    s_p[warp][e0 + j] = psum[j];
-    s_c[warp][e0 + j] = cnt[j];
-  }
+  for (int j = 0; j < PER; ++j) s_p[warp][e0 + j] = psum[j];
   if (lane == 0) {
     s_z[warp] = z;
     s_n[warp] = n;
@@ -189,18 +258,13 @@ __global__ void __launch_bounds__(RT_THREADS) mk_route_kernel(const __grid_const
   float* part = p.part + static_cast<long long>(blockIdx.x) * (2 * p.E + 2);
   for (int e = threadIdx.x; e < p.E; e += RT_THREADS) {
     float a = 0.f;
-    int c = 0;
 #pragma unroll
-    for (int w = 0; w < RT_WARPS; ++w) {
-      a += s_p[w][e];
-      c += s_c[w][e];
-    }
+    for (int w = 0; w < RT_WARPS; ++w) a += s_p[w][e];
     if (gridDim.x == 1) {
       s_p[0][e] = a;
-      s_c[0][e] = c;
     } else {
       part[e] = a;
-      reinterpret_cast<int*>(part)[p.E + e] = c;
+      reinterpret_cast<int*>(part)[p.E + e] = s_c[e];
     }
   }
   z = 0.f;
@@ -210,113 +274,203 @@ __global__ void __launch_bounds__(RT_THREADS) mk_route_kernel(const __grid_const
     z += s_z[w];
     n += s_n[w];
   }
-  if (gridDim.x == 1) {
-    __syncthreads();
-    finish(p, s_p[0], s_c[0], z, n, scratch);
-  } else if (threadIdx.x == 0) {
-    part[2 * p.E] = z;
-    reinterpret_cast<int*>(part)[2 * p.E + 1] = n;
+  if (gridDim.x > 1) {
+    if (threadIdx.x == 0) {
+      part[2 * p.E] = z;
+      reinterpret_cast<int*>(part)[2 * p.E + 1] = n;
+    }
+    return;
+  }
+  // one block: the losses at once
+  __syncthreads();
+  float b = 0.f;
+  for (int e = threadIdx.x; e < p.E; e += RT_THREADS) {
+    b += s_p[0][e] * s_c[e];
+    p.counts[e] = s_c[e];
+  }
+  b = warp_sum(b);
+  if (lane == 0) scratch[warp] = b;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    b = 0.f;
+#pragma unroll
+    for (int w = 0; w < RT_WARPS; ++w) b += scratch[w];
+    write_losses(p, b, z, n);
   }
 }
 
-// One block: the blocks' sums in order, then the losses.
-__global__ void __launch_bounds__(1024) mk_route_sums_kernel(const __grid_constant__ RouteParams p) {
-  __shared__ float s_p[4][256 + 2];
-  __shared__ int s_c[4][256 + 2];
-  __shared__ float scratch[32];
-  const int e = threadIdx.x & 255, q = threadIdx.x >> 8, width = 2 * p.E + 2;
+// The blocks' sums, in order: a cluster of blocks with 32 experts each, whose shares of the balance loss meet in
+// the first.
+__global__ void __launch_bounds__(32 * RS_WARPS) mk_route_sums_kernel(const __grid_constant__ RouteParams p) {
+  __shared__ float s_p[RS_WARPS][32];
+  __shared__ int s_c[RS_WARPS][32];
+  __shared__ float share[8];                         // in the first block: every block's
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane, width = 2 * p.E + 2;
   griddep_wait();
   float a = 0.f;
   int c = 0;
   if (e < p.E) {
-#pragma unroll 4
-    for (int b = q; b < p.blocks; b += 4) {
+#pragma unroll 5
+    for (int b = warp; b < p.blocks; b += RS_WARPS) {
       a += p.part[static_cast<long long>(b) * width + e];
       c += reinterpret_cast<const int*>(p.part)[static_cast<long long>(b) * width + p.E + e];
     }
-    s_p[q][e] = a;
-    s_c[q][e] = c;
   }
+  s_p[warp][lane] = a;
+  s_c[warp][lane] = c;
   float z = 0.f;
   int n = 0;
-  if (threadIdx.x < 32) {
-    for (int b = threadIdx.x; b < p.blocks; b += 32) {
+  if (blockIdx.x == 0 && warp == 1) {
+#pragma unroll 5
+    for (int b = lane; b < p.blocks; b += 32) {
       z += p.part[static_cast<long long>(b) * width + 2 * p.E];
       n += reinterpret_cast<const int*>(p.part)[static_cast<long long>(b) * width + 2 * p.E + 1];
     }
     z = warp_sum(z);
     n = __reduce_add_sync(0xffffffffu, n);
-    if (threadIdx.x == 0) {
-      s_p[0][256] = z;
-      s_c[0][256] = n;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    a = 0.f;
+    c = 0;
+#pragma unroll
+    for (int w = 0; w < RS_WARPS; ++w) {
+      a += s_p[w][lane];
+      c += s_c[w][lane];
     }
+    if (e < p.E) p.counts[e] = c;
+    const float b = warp_sum(a * c);
+    if (lane == 0) st_shared_cluster_f32(mapa_shared(smem_u32(&share[blockIdx.x]), 0), b);
+    __syncwarp();
   }
-  __syncthreads();
-  if (threadIdx.x < p.E) {
-    s_p[0][e] = s_p[0][e] + s_p[1][e] + s_p[2][e] + s_p[3][e];
-    s_c[0][e] = s_c[0][e] + s_c[1][e] + s_c[2][e] + s_c[3][e];
+  cluster_sync_all();
+  if (blockIdx.x == 0 && threadIdx.x == 32) {
+    float b = 0.f;
+    for (unsigned w = 0; w < gridDim.x; ++w) b += share[w];
+    write_losses(p, b, z, n);
   }
-  __syncthreads();
-  finish(p, s_p[0], s_c[0], s_p[0][256], s_c[0][256], scratch);
 }
 
 template <class T, int PER>
-__global__ void __launch_bounds__(RT_THREADS) mk_route_grad_kernel(const __grid_constant__ RouteParams p) {
+__global__ void __launch_bounds__(RG_THREADS) mk_route_grad_kernel(const __grid_constant__ RouteParams p) {
+  __shared__ __align__(16) float s_add[RG_WARPS][32 * PER];      // what the chosen experts get besides
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = lane * PER;
   const int n = max(1, *p.tokens);
   const float db = p.dbalance ? *p.dbalance * (static_cast<float>(p.E) / n) : 0.f;
   const float dz = p.dz ? *p.dz * (2.f / n) : 0.f;
   float f[PER];
 #pragma unroll
-  for (int j = 0; j < PER; ++j)
+  for (int j = 0; j < PER; ++j) {
     f[j] = p.dbalance && e0 + j < p.E ? p.counts[e0 + j] / (static_cast<float>(p.K) * n) : 0.f;
-  for (int t = blockIdx.x * RT_WARPS + warp; t < p.T; t += gridDim.x * RT_WARPS) {
-    T* out = reinterpret_cast<T*>(p.dl + t * p.dl_row);
-    const int id = lane < p.K ? p.idx[static_cast<long long>(t) * p.K + lane] : -1;
+    s_add[warp][e0 + j] = 0.f;
+  }
+  __syncwarp();
+  const int step = gridDim.x * RG_WARPS;
+  int t = blockIdx.x * RG_WARPS + warp;
+  Logits<T, PER> next;
+  int next_id = -1;
+  float next_dg = 0.f;
+  auto ahead = [&](int t) {
+    next_id = -1;
+    if (t >= p.T) return;
+    next.load(p, t);
+    if (lane < p.K) {
+      next_id = p.idx[static_cast<long long>(t) * p.K + lane];
+      if (p.dgates != nullptr) next_dg = p.dgates[static_cast<long long>(t) * p.K + lane];
+    }
+  };
+  ahead(t);
+  for (; t < p.T; t += step) {
+    const Logits<T, PER> now = next;
+    int id = next_id;
+    float dg = next_dg * p.scale;
+    ahead(t > p.T - step ? p.T : t + step);        // (t + step may pass 2^31)
+    const bool real = __shfl_sync(0xffffffffu, id, 0) >= 0;
     float d[PER];
 #pragma unroll
     for (int j = 0; j < PER; ++j) d[j] = 0.f;
-    if (__shfl_sync(0xffffffffu, id, 0) >= 0) {
+    if (real) {
       float v[PER];
-      load_logits<T, PER>(p, t, v);
+      now.get(v);
       float top = v[0];
 #pragma unroll
       for (int j = 1; j < PER; ++j) top = fmaxf(top, v[j]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      top = value_of(__reduce_max_sync(0xffffffffu, key_of(top)));
       float sum = 0.f, pf = 0.f;
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
-        v[j] = expf(v[j] - top);
+        v[j] = exp_of(v[j] - top);
         sum += v[j];
         pf = fmaf(v[j], f[j], pf);
       }
-      sum = warp_sum(sum);
-      pf = warp_sum(pf);
-      const float inv = 1.f / sum, lse = top + logf(sum);
-      float dg = 0.f, w = 0.f;                       // of lane k's chosen expert
-      if (p.dgates != nullptr && id >= 0 && id < p.E) {
-        dg = p.dgates[static_cast<long long>(t) * p.K + lane] * p.scale;
-        w = expf(Piece<T>::one(reinterpret_cast<const T*>(p.logits + t * p.row)[id]) - top);
+      const bool chosen = p.dgates != nullptr && id >= 0 && id < p.E;
+      float w = 0.f;                                 // exp(logit - top) of this lane's chosen expert
+      if (chosen) w = exp_of(Piece<T>::one(reinterpret_cast<const T*>(p.logits + t * p.row)[id]) - top);
+      else dg = 0.f;
+      float own = w;                                 // of the chosen ones together
+      float dot = w * dg;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        pf += __shfl_xor_sync(0xffffffffu, pf, o);
       }
-      const float share = w / (p.normalize ? warp_sum(w) : sum);
-      const float dot = warp_sum(share * dg);
-      const float mine = share * (p.normalize ? dg - dot : dg);
-      const float all = (p.normalize || p.dgates == nullptr ? 0.f : -dot) - db * pf * inv + dz * lse;
+      if (p.dgates != nullptr) {
 #pragma unroll
-      for (int j = 0; j < PER; ++j) d[j] = v[j] * inv * (fmaf(db, f[j], all));
-      if (p.dgates != nullptr)
-        for (int k = 0; k < p.K; ++k) {
-          const int at = __shfl_sync(0xffffffffu, id, k) - e0;
-          const float c = __shfl_sync(0xffffffffu, mine, k);
-#pragma unroll
-          for (int j = 0; j < PER; ++j)
-            if (j == at) d[j] += c;
+        for (int o = 4; o > 0; o >>= 1) {            // (lanes below K <= 8)
+          own += __shfl_xor_sync(0xffffffffu, own, o);
+          dot += __shfl_xor_sync(0xffffffffu, dot, o);
         }
-    }
+      }
+      const float inv = __fdividef(1.f, sum), lse = top + __logf(sum);
+      const float part = p.normalize ? __fdividef(1.f, __shfl_sync(0xffffffffu, own, 0)) : inv;
+      dot = __shfl_sync(0xffffffffu, dot, 0) * part;
+      const float mine = w * part * (p.normalize ? dg - dot : dg);
+      const float all = (p.normalize || p.dgates == nullptr ? 0.f : -dot) - db * pf * inv + dz * lse;
+      if (p.dgates != nullptr) {
+        if (chosen) s_add[warp][id] = mine;          // (a token's experts differ)
+        __syncwarp();
+      }
 #pragma unroll
-    for (int j = 0; j < PER; ++j)
-      if (e0 + j < p.E) out[e0 + j] = Piece<T>::of(d[j]);
+      for (int j = 0; j < PER; ++j) d[j] = v[j] * inv * fmaf(db, f[j], all);
+      if (p.dgates != nullptr) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) d[j] += s_add[warp][e0 + j];
+        __syncwarp();
+        if (chosen) s_add[warp][id] = 0.f;
+        __syncwarp();
+      }
+    }
+    T* out = reinterpret_cast<T*>(p.dl + t * p.dl_row) + e0;
+    const int left = p.E - e0;
+    constexpr int BYTES = Logits<T, PER>::BYTES;
+    if (p.vec && BYTES >= 4) {
+      if (left >= PER) {
+        T o[PER];
+#pragma unroll
+        for (int j = 0; j < PER; ++j) o[j] = Piece<T>::of(d[j]);
+        if constexpr (BYTES == 4) {
+          uint32_t w;
+          memcpy(&w, o, 4);
+          *reinterpret_cast<uint32_t*>(out) = w;
+        } else if constexpr (BYTES == 8) {
+          uint2 w;
+          memcpy(&w, o, 8);
+          *reinterpret_cast<uint2*>(out) = w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < BYTES / 16; ++i) {
+            uint4 w;
+            memcpy(&w, reinterpret_cast<char*>(o) + 16 * i, 16);
+            reinterpret_cast<uint4*>(out)[i] = w;
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < PER; ++j)
+        if (j < left) out[j] = Piece<T>::of(d[j]);
+    }
+    if (t > p.T - step) break;
   }
 }
 
@@ -328,8 +482,13 @@ int route_blocks(long long T) {
 }
 
 template <class T, int PER>
-cudaError_t launch_route(const RouteParams& p, bool grad, cudaStream_t s) {
-  if (grad) mk_route_grad_kernel<T, PER><<<p.blocks, RT_THREADS, 0, s>>>(p);
+cudaError_t launch_route(RouteParams p, bool grad, cudaStream_t s) {
+  // whole pieces of PER logits, where every row has them
+  const uintptr_t piece = PER * sizeof(T) < 16 ? PER * sizeof(T) : 16;
+  uintptr_t lie = reinterpret_cast<uintptr_t>(p.logits) | (p.T > 1 ? static_cast<uintptr_t>(p.row) : 0);
+  if (grad) lie |= reinterpret_cast<uintptr_t>(p.dl) | (p.T > 1 ? static_cast<uintptr_t>(p.dl_row) : 0);
+  p.vec = p.E % PER == 0 && !(lie & (piece - 1));
+  if (grad) mk_route_grad_kernel<T, PER><<<p.blocks, RG_THREADS, 0, s>>>(p);
   else mk_route_kernel<T, PER><<<p.blocks, RT_THREADS, 0, s>>>(p);
   return cudaGetLastError();
 }
@@ -397,7 +556,21 @@ mk_status mk_moe_route(const void* logits, mk_dtype dtype, long long T, int E, l
   p.scale = scale;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = launch_route(p, dtype, false, s);
-  if (e == cudaSuccess && p.blocks > 1) e = launch_dependent(mk_route_sums_kernel, dim3(1), dim3(1024), s, p);
+  if (e == cudaSuccess && p.blocks > 1) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : 8);
+    cfg.blockDim = dim3(32 * RS_WARPS);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cfg.gridDim.x;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, mk_route_sums_kernel, p);
+  }
   return e == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }
 
@@ -429,7 +602,7 @@ mk_status mk_moe_route_backward(const void* logits, mk_dtype dtype, long long T,
   p.K = topk;
   p.normalize = normalize != 0;
   p.scale = scale;
-  p.blocks = static_cast<int>(std::min<long long>(ceil_div_ll(T, RT_WARPS), 4 * RT_BLOCKS));
+  p.blocks = static_cast<int>(std::min<long long>(ceil_div_ll(T, RG_WARPS), 4 * RT_BLOCKS));
   const cudaError_t e = launch_route(p, dtype, true, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }

@@ -496,7 +496,8 @@ template <class T, int NT, int GPC, bool ZEROS>
 cudaError_t launch_products(const TileParams& p, cudaStream_t s) {
   using L = Tile<NT, GPC, ZEROS>;
   auto k = mk_w4_tiles_kernel<T, NT, GPC, ZEROS>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+  static std::atomic<unsigned> done{0};
+  const cudaError_t e = allow_smem(k, L::SMEM, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.ctas));
