@@ -12,6 +12,9 @@
 // thread's own codes are its operands as they come, and x is read in the same order.  A block
 // has 16 rows of the matrix; its warps share out k in pieces of 128, a thread 16 bytes
 // (32 codes) of two rows of each, loaded one piece ahead, and add their sums in shared memory, in order.
+// 8192 x 8192, groups of 128, one token: 12.7 us in a graph, 2.7 TB/s.  More pieces ahead or two tiles of rows a
+// block cost registers and with them warps (13.2 to 14.6 us); a ring of shared memory 19.4.
+// Columns past the last token hold another token's x and are dropped.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -24,8 +27,8 @@ namespace {
 
 constexpr int W4_WARPS = 8;
 constexpr int W4_THREADS = 32 * W4_WARPS;
-constexpr int W4_ROWS = 16;
 constexpr int W4_TOKENS = 8;
+constexpr int W4_ROWS = 16;
 
 template <class T>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -39,109 +42,101 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// What a thread has of a piece: the words of its two rows by group, x of its token, scales and zero points.
-template <class T, int GPC>
+// What a thread has of a piece: the words of its two rows by group, scales and zero points.
+template <class T, int GPC, bool ZEROS>
 struct Step {
-  uint32_t a[4], b[4];
-  uint4 x[4];
-  T sa[GPC], sb[GPC], za[GPC], zb[GPC];
+  uint32_t w[2][4];
+  T s[2][GPC], z[2][ZEROS ? GPC : 1];
 };
 
-// WPG: words of a thread in a group (4, 2, 1 for groups of 128, 64, 32).
-template <class T, int WPG, bool ZEROS>
+// WPG: words of a thread in a group (4, 2, 1 for groups of 128, 64, 32).  WHOLE: k is whole pieces.
+template <class T, int WPG, bool ZEROS, bool WHOLE>
 __global__ void __launch_bounds__(W4_THREADS) mk_w4_kernel(const __grid_constant__ W4Params p) {
   constexpr int GPC = 4 / WPG;                       // groups of a piece
   __shared__ float red[W4_WARPS][W4_TOKENS][W4_ROWS + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, j = lane & 3;
   const int n0 = blockIdx.x * W4_ROWS;
-  const int ra = min(n0 + r, p.n - 1), rb = min(n0 + r + 8, p.n - 1);      // rows past the last repeat it
-  const uint8_t* ca = p.codes + static_cast<long long>(ra) * (p.k / 2);
-  const uint8_t* cb = p.codes + static_cast<long long>(rb) * (p.k / 2);
-  const long long ga = static_cast<long long>(ra) * p.groups, gb = static_cast<long long>(rb) * p.groups;
-  const T* scales = static_cast<const T*>(p.scales);
-  const T* zeros = static_cast<const T*>(p.zeros);
-  const char* x = p.x + (r < p.m ? r : 0) * p.x_row;
-  auto load = [&](int c, Step<T, GPC>& o) {
+  const uint8_t* codes[2];
+  const T *scales[2], *zeros[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int row = min(n0 + 8 * t + r, p.n - 1);    // rows past the last repeat it
+    codes[t] = p.codes + static_cast<long long>(row) * (p.k / 2) + j * (WPG * 4);
+    scales[t] = static_cast<const T*>(p.scales) + static_cast<long long>(row) * p.groups;
+    zeros[t] = static_cast<const T*>(p.zeros) + static_cast<long long>(row) * p.groups;
+  }
+  const char* x = p.x + min(r, p.m - 1) * p.x_row + j * (WPG * 16);
+  const int pieces = (p.k + W4_PIECE - 1) / W4_PIECE;
+  auto load = [&](int c, Step<T, GPC, ZEROS>& o) {
+    if (WHOLE && c >= pieces) return;
 #pragma unroll
     for (int g = 0; g < GPC; ++g) {
-      const int group = c * GPC + g, k0 = group * (WPG * 32) + j * (WPG * 8);      // this thread's codes of the group
-      const bool real = group < p.groups;
-      const uint8_t *a = ca + k0 / 2, *b = cb + k0 / 2;
-      if constexpr (WPG == 4) {
-        uint4 u = make_uint4(0, 0, 0, 0), v = u;
-        if (real) {
-          u = ld_nc_v4(a);
-          v = ld_nc_v4(b);
-        }
-        o.a[0] = u.x; o.a[1] = u.y; o.a[2] = u.z; o.a[3] = u.w;
-        o.b[0] = v.x; o.b[1] = v.y; o.b[2] = v.z; o.b[3] = v.w;
-      } else if constexpr (WPG == 2) {
-        uint2 u = make_uint2(0, 0), v = u;
-        if (real) {
-          u = __ldg(reinterpret_cast<const uint2*>(a));
-          v = __ldg(reinterpret_cast<const uint2*>(b));
-        }
-        o.a[2 * g] = u.x; o.a[2 * g + 1] = u.y;
-        o.b[2 * g] = v.x; o.b[2 * g + 1] = v.y;
-      } else {
-        o.a[g] = real ? __ldg(reinterpret_cast<const uint32_t*>(a)) : 0;
-        o.b[g] = real ? __ldg(reinterpret_cast<const uint32_t*>(b)) : 0;
-      }
-      o.sa[g] = real ? scales[ga + group] : Piece<T>::of(0.f);
-      o.sb[g] = real ? scales[gb + group] : Piece<T>::of(0.f);
-      if (ZEROS) {
-        o.za[g] = real ? zeros[ga + group] : Piece<T>::of(0.f);
-        o.zb[g] = real ? zeros[gb + group] : Piece<T>::of(0.f);
-      }
+      const int group = c * GPC + g;
+      const bool real = WHOLE || group < p.groups;
 #pragma unroll
-      for (int w = 0; w < WPG; ++w) {
-        o.x[g * WPG + w] = make_uint4(0, 0, 0, 0);
-        if (real && r < p.m) o.x[g * WPG + w] = __ldg(reinterpret_cast<const uint4*>(x) + (k0 / 8 + w));
+      for (int t = 0; t < 2; ++t) {
+        const uint8_t* a = codes[t] + group * (WPG * 16);
+        if constexpr (WPG == 4) {
+          const uint4 u = real ? ld_nc_v4(a) : make_uint4(0, 0, 0, 0);
+          o.w[t][0] = u.x; o.w[t][1] = u.y; o.w[t][2] = u.z; o.w[t][3] = u.w;
+        } else if constexpr (WPG == 2) {
+          const uint2 u = real ? __ldg(reinterpret_cast<const uint2*>(a)) : make_uint2(0, 0);
+          o.w[t][2 * g] = u.x; o.w[t][2 * g + 1] = u.y;
+        } else {
+          o.w[t][g] = real ? __ldg(reinterpret_cast<const uint32_t*>(a)) : 0;
+        }
+        o.s[t][g] = real ? scales[t][group] : Piece<T>::of(0.f);
+        if constexpr (ZEROS) o.z[t][g] = real ? zeros[t][group] : Piece<T>::of(0.f);
       }
     }
   };
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  Step<T, GPC> next;
-  load(warp, next);
-  for (int c = warp; c * W4_PIECE < p.k; c += W4_WARPS) {
-    const Step<T, GPC> now = next;
-    load(c + W4_WARPS, next);
+  auto multiply = [&](int c, const Step<T, GPC, ZEROS>& now) {
 #pragma unroll
     for (int g = 0; g < GPC; ++g) {
+      const int group = c * GPC + g;
       float part[4] = {0.f, 0.f, 0.f, 0.f}, ones[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int w = g * WPG; w < (g + 1) * WPG; ++w) {
-        uint32_t a[4], b[4], xs[4];
-        Codes<T>::pairs(now.a[w], a);
-        Codes<T>::pairs(now.b[w], b);
-        x_pairs(now.x[w], xs);
+      for (int w = 0; w < WPG; ++w) {
+        uint32_t xs[4], a[4], b[4];
+        const uint4 v = WHOLE || group < p.groups ? __ldg(reinterpret_cast<const uint4*>(x + group * (WPG * 64)) + w) : make_uint4(0, 0, 0, 0);
+        x_pairs(v, xs);
+        Codes<T>::pairs(now.w[0][g * WPG + w], a);
+        Codes<T>::pairs(now.w[1][g * WPG + w], b);
         mma<T>(part, a[0], b[0], a[1], b[1], xs[0], xs[1]);
         mma<T>(part, a[2], b[2], a[3], b[3], xs[2], xs[3]);
-        if (ZEROS) {
+        if constexpr (ZEROS) {
           constexpr uint32_t I = Codes<T>::ONES;
           mma<T>(ones, I, I, I, I, xs[0], xs[1]);
           mma<T>(ones, I, I, I, I, xs[2], xs[3]);
         }
       }
-      if (ZEROS) {
-        const float oa = 8.f - Piece<T>::one(now.za[g]), ob = 8.f - Piece<T>::one(now.zb[g]);
+      if constexpr (ZEROS) {
+        const float oa = 8.f - Piece<T>::one(now.z[0][g]), ob = 8.f - Piece<T>::one(now.z[1][g]);
         part[0] = fmaf(oa, ones[0], part[0]);
         part[1] = fmaf(oa, ones[1], part[1]);
         part[2] = fmaf(ob, ones[2], part[2]);
         part[3] = fmaf(ob, ones[3], part[3]);
       }
-      const float fa = Piece<T>::one(now.sa[g]), fb = Piece<T>::one(now.sb[g]);
+      const float fa = Piece<T>::one(now.s[0][g]), fb = Piece<T>::one(now.s[1][g]);
       acc[0] = fmaf(fa, part[0], acc[0]);
       acc[1] = fmaf(fa, part[1], acc[1]);
       acc[2] = fmaf(fb, part[2], acc[2]);
       acc[3] = fmaf(fb, part[3], acc[3]);
     }
+  };
+  Step<T, GPC, ZEROS> next;
+  if (warp < pieces) load(warp, next);
+  for (int c = warp; c < pieces; c += W4_WARPS) {
+    const Step<T, GPC, ZEROS> now = next;
+    load(c + W4_WARPS, next);
+    multiply(c, now);
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) red[warp][2 * j + (e & 1)][r + 8 * (e >> 1)] = acc[e];
   __syncthreads();
   const int row = threadIdx.x % W4_ROWS, t = threadIdx.x / W4_ROWS;
-  if (t >= W4_TOKENS || n0 + row >= p.n || t >= p.m) return;
+  if (t >= p.m || t >= W4_TOKENS || n0 + row >= p.n) return;
   float s = 0.f;
 #pragma unroll
   for (int w = 0; w < W4_WARPS; ++w) s += red[w][t][row];
@@ -150,12 +145,16 @@ __global__ void __launch_bounds__(W4_THREADS) mk_w4_kernel(const __grid_constant
 
 // ------------------------------------------------------------------ host
 
-template <class T, int WPG>
+template <class T, int WPG, bool ZEROS>
 cudaError_t launch_w4(const W4Params& p, cudaStream_t s) {
   const unsigned grid = static_cast<unsigned>(ceil_div_ll(p.n, W4_ROWS));
-  if (p.zeros) mk_w4_kernel<T, WPG, true><<<grid, W4_THREADS, 0, s>>>(p);
-  else mk_w4_kernel<T, WPG, false><<<grid, W4_THREADS, 0, s>>>(p);
+  if (p.k % W4_PIECE == 0) mk_w4_kernel<T, WPG, ZEROS, true><<<grid, W4_THREADS, 0, s>>>(p);
+  else mk_w4_kernel<T, WPG, ZEROS, false><<<grid, W4_THREADS, 0, s>>>(p);
   return cudaGetLastError();
+}
+template <class T, int WPG>
+cudaError_t launch_w4(const W4Params& p, cudaStream_t s) {
+  return p.zeros ? launch_w4<T, WPG, true>(p, s) : launch_w4<T, WPG, false>(p, s);
 }
 template <class T>
 cudaError_t launch_w4(const W4Params& p, int group, cudaStream_t s) {
@@ -191,7 +190,7 @@ using namespace mk;
 extern "C" {
 
 size_t mk_w4_gemm_scratch_size(const mk_w4_weight* w, long long m) {
-  if (!weight_ok(w, m) || m < W4_TILE_TOKENS || w->n == 0) return 0;
+  if (!weight_ok(w, m) || !w4_use_tiles(sizes_of(w, m), w->group) || w->n == 0) return 0;
   return w4_tiles_scratch(sizes_of(w, m), w->group);
 }
 
@@ -218,7 +217,7 @@ mk_status mk_w4_gemm(const void* x, long long x_row, const mk_w4_weight* w, void
   p.y_row = osz * y_row;
   p.out_f32 = out_dtype == MK_F32;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (m >= W4_TILE_TOKENS) {
+  if (w4_use_tiles(p, w->group)) {
     if (!scratch || (reinterpret_cast<uintptr_t>(scratch) & 255u) || scratch_bytes < w4_tiles_scratch(p, w->group)) return MK_ERR_INVALID;
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) || ws_bytes < WS_HDR_BYTES) return MK_ERR_INVALID;
     return launch_w4_tiles(p, dtype, w->group, scratch, static_cast<uint32_t*>(workspace), cfg, s);

@@ -18,11 +18,14 @@ struct W4Params {
 
 constexpr int W4_PIECE = 128;          // k of a step
 
-// Tokens from which on mk_w4_tiles.cu serves a call.
-#ifndef W4_TT
-#define W4_TT 9
-#endif
-constexpr int W4_TILE_TOKENS = W4_TT;
+// Whether mk_w4_tiles.cu serves a call: more than 8 tokens, and fewer where small groups make the other way's scales
+// dear and the matrix is large enough for three launches (graphs, us, mma.sync / tcgen05, one token: groups of 32,
+// 1024 x 2048 4.5 / 6.6, 3584 x 8192 16.8 / 12.8, 28672 x 8192 90 / 53; of 64 with zero points 8192 x 8192 18.2 / 17.3,
+// 28672 x 8192 52 / 46; of 128 without, 34 / 42).
+inline bool w4_use_tiles(const W4Params& p, int group) {
+  const long long weights = static_cast<long long>(p.n) * p.k;
+  return p.m > 8 || (group == 32 && weights >= (1LL << 24)) || (group == 64 && weights >= (1LL << 27));
+}
 size_t w4_tiles_scratch(const W4Params& p, int group);
 mk_status launch_w4_tiles(const W4Params& p, mk_dtype dtype, int group, void* scratch, uint32_t* hdr, const mk_config* cfg,
                           cudaStream_t s);

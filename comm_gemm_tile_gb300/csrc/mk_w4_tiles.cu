@@ -40,7 +40,7 @@ struct TileParams {
   float* part;                         // [CTAs x 2 x NT x 128]
   int sums_pitch;
   unsigned each, over;
-  int whole_steps;                     // k is whole steps, and their scales lie on whole words
+  int whole_scales;                    // rows of scales are whole 16-byte pieces
   int ctas, steps, row_tiles, tok_tiles, NT;   // steps: of a tile
   long long wait_ns;
   int inject;
@@ -238,53 +238,78 @@ __global__ void __launch_bounds__(WT_THREADS, 1) mk_w4_tiles_kernel(const __grid
     for (int e = 0; e < TOK / 2; ++e) acc[e] = 0;
     unsigned tile = u0 / steps, c = u0 - tile * steps;
     int row = tile % row_tiles * WT_ROWS + r, first = 0;
-    // a step's scales and zero points, loaded a step ahead; rows past the last repeat it
-    union alignas(4 * GPC) Step {
-      uint32_t w[GPC];
-      T v[2 * GPC];
-      __device__ __forceinline__ Step() {}
-    };
-    Step sc, ze;
+    // Scales and zero points, of rows past the last those of the last: 8 groups (PER steps) at once, loaded as many ahead
+    // (a load of each step's own takes the load unit as long: every row has a line of its own); or, where rows of scales
+    // are not whole 16-byte pieces, each step's, a step ahead.
+    constexpr int PER = 4 / GPC;
+    uint4 sc, sc_next, ze, ze_next;
     const T *ps, *pz;
     auto of_row = [&] {
       const long long at = static_cast<long long>(min(row, p.w.n - 1)) * p.w.groups;
       ps = static_cast<const T*>(p.w.scales) + at;
       pz = static_cast<const T*>(p.w.zeros) + at;
     };
-    auto scales = [&](unsigned c) {
-      if (p.whole_steps) {
-        sc = *reinterpret_cast<const Step*>(ps + c * (2 * GPC));
-        if (ZEROS) ze = *reinterpret_cast<const Step*>(pz + c * (2 * GPC));
+    auto ahead = [&](unsigned c) {                           // the step's or its block's
+      if (p.whole_scales) {
+        sc_next = __ldg(reinterpret_cast<const uint4*>(ps) + c / PER);
+        if (ZEROS) ze_next = __ldg(reinterpret_cast<const uint4*>(pz) + c / PER);
       } else {
+        T v[8], u[8];
 #pragma unroll
-        for (int q = 0; q < 2 * GPC; ++q) {
+        for (int q = 0; q < 8; ++q) {
           const int g = c * (2 * GPC) + q;
-          sc.v[q] = g < p.w.groups ? ps[g] : Piece<T>::of(0.f);
-          if (ZEROS) ze.v[q] = g < p.w.groups ? pz[g] : Piece<T>::of(0.f);
+          const bool real = q < 2 * GPC && g < p.w.groups;
+          v[q] = real ? ps[g] : Piece<T>::of(0.f);
+          u[q] = ZEROS && real ? pz[g] : Piece<T>::of(0.f);
         }
+        memcpy(&sc_next, v, 16);
+        memcpy(&ze_next, u, 16);
       }
     };
     of_row();
-    scales(c);
+    ahead(c);
+    bool fresh = true;                                       // sc_next is this step's
     for (int i = 0; i < count; ++i) {
-      float fs[2 * GPC], fz[2 * GPC];
-#pragma unroll
-      for (int q = 0; q < GPC; ++q) {                        // not converted where they are loaded: that would wait
-        asm volatile("" : "+r"(sc.w[q]));
-        if (ZEROS) asm volatile("" : "+r"(ze.w[q]));
-      }
-#pragma unroll
-      for (int q = 0; q < 2 * GPC; ++q) {
-        fs[q] = Piece<T>::one(sc.v[q]);
-        fz[q] = ZEROS ? 8.f - Piece<T>::one(ze.v[q]) : 0.f;
-      }
       const bool ends = c + 1 == steps;
       const int row_now = row;
+      if (fresh) {
+        sc = sc_next;
+        ze = ze_next;
+      }
       if (ends) {
         row = (tile + 1) % row_tiles * WT_ROWS + r;
         of_row();
       }
-      scales(ends ? 0 : c + 1);                              // (the first of a tile once more after the last)
+      const unsigned after = ends ? 0 : c + 1, place_in = p.whole_scales ? c % PER : 0;
+      // the next step's, if they are not in hand; what is loaded last is not used
+      const bool had = fresh;
+      fresh = ends || !p.whole_scales || after % PER == 0;
+      if (p.whole_scales) {
+        if (had || ends) ahead(ends ? 0 : min(c / PER * PER + PER, steps - 1));
+      } else {
+        ahead(after);
+      }
+      float fs[2 * GPC], fz[2 * GPC];
+      {
+        uint32_t w[4] = {sc.x, sc.y, sc.z, sc.w}, y[4] = {ze.x, ze.y, ze.z, ze.w};
+        if (GPC == 1) {
+          w[0] = place_in == 0 ? w[0] : place_in == 1 ? w[1] : place_in == 2 ? w[2] : w[3];
+          y[0] = place_in == 0 ? y[0] : place_in == 1 ? y[1] : place_in == 2 ? y[2] : y[3];
+        } else if (GPC == 2 && place_in == 1) {
+          w[0] = w[2];
+          w[1] = w[3];
+          y[0] = y[2];
+          y[1] = y[3];
+        }
+        T v[2 * GPC], u[2 * GPC];
+        memcpy(v, w, sizeof(v));
+        memcpy(u, y, sizeof(u));
+#pragma unroll
+        for (int q = 0; q < 2 * GPC; ++q) {
+          fs[q] = Piece<T>::one(v[q]);
+          fz[q] = ZEROS ? 8.f - Piece<T>::one(u[q]) : 0.f;
+        }
+      }
       const int x0 = 2 * i % SX, place0 = 2 * i % DP;        // (of the first half; the second's come after them)
       const uint32_t full = bars + B_DFULL + 8 * place0, turn = 2 * i / DP & 1, xfull = bars + B_XFULL + 8 * x0;
       if (!wt_wait_warp(dead, p, full, turn, full + 8, turn, WHERE_EPILOGUE)) break;
@@ -331,12 +356,19 @@ __global__ void __launch_bounds__(WT_THREADS, 1) mk_w4_tiles_kernel(const __grid
         const int m0 = tile / row_tiles * NT + t0;
         const bool whole = ends && i - first + 1 == p.steps;
         float* out = p.part + ((static_cast<long long>(blockIdx.x) * 2 + (first == 0 ? 0 : 1)) * NT + t0) * WT_ROWS + r;
+        char* y = p.w.y + m0 * p.w.y_row + static_cast<long long>(row_now) * (p.w.out_f32 ? 4 : 2);
+        const int tokens = row_now < p.w.n ? p.w.m - m0 : 0;
 #pragma unroll
         for (int e = 0; e < TOK; ++e) {
           float v[2];
           split(acc[e / 2], v[0], v[1]);
-          if (!whole) out[e * WT_ROWS] = v[e & 1];
-          else if (m0 + e < p.w.m && row_now < p.w.n) w4_store<T>(p.w, m0 + e, row_now, v[e & 1]);
+          if (!whole) {
+            out[e * WT_ROWS] = v[e & 1];
+          } else if (e < tokens) {
+            if (p.w.out_f32) *reinterpret_cast<float*>(y) = v[e & 1];
+            else *reinterpret_cast<T*>(y) = Piece<T>::of(v[e & 1]);
+            y += p.w.y_row;
+          }
         }
 #pragma unroll
         for (int e = 0; e < TOK / 2; ++e) acc[e] = 0;
@@ -559,8 +591,7 @@ mk_status launch_w4_tiles(const W4Params& w, mk_dtype dtype, int group, void* sc
   p.each = all / p.ctas;
   p.over = all % p.ctas;
   p.NT = l.NT;
-  const uintptr_t lie = reinterpret_cast<uintptr_t>(w.scales) | reinterpret_cast<uintptr_t>(w.zeros);
-  p.whole_steps = w.k % WT_STEP == 0 && !(lie & (2 * WT_STEP / group - 1));
+  p.whole_scales = w.groups % 8 == 0 && !((reinterpret_cast<uintptr_t>(w.scales) | reinterpret_cast<uintptr_t>(w.zeros)) & 15u);
   p.wait_ns = default_wait_ns(cfg);
   p.inject = cfg ? cfg->inject : 0;
   {

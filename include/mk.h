@@ -600,7 +600,7 @@ typedef struct {
   int group, dtype;
 } mk_w4_weight;
 
-/* Scratch bytes for mk_w4_gemm (0 for up to 8 rows, and on bad arguments). */
+/* Scratch bytes for mk_w4_gemm (0: the call takes none, or the arguments are bad). */
 size_t mk_w4_gemm_scratch_size(const mk_w4_weight *w, long long m);
 
 /* y = x @ W^T for a few rows: x [m x k] of w->dtype (rows x_row elements apart, whole
@@ -608,10 +608,10 @@ size_t mk_w4_gemm_scratch_size(const mk_w4_weight *w, long long m);
  * numbers, groups are scaled and summed in fp32, y is rounded once.  A row of x that
  * holds an infinity gives infinities or NaN.  Built for the rows of a decode step; more
  * are taken 64 at a time (m below 2^24, and m n k below 2^49 or so).
- * More than 8 rows take scratch (256-byte aligned, of the call alone, no clearing) and a
- * workspace of 256 bytes, zero-filled once, which holds the device status and nothing else:
- * MK_ERR_TIMEOUT if a bounded wait ran out, after which y is undefined.  Both may be NULL for
- * fewer.  cfg (may be NULL): max_ctas, wait_limit_ns and inject (1: one CTA does not
+ * Calls that take scratch (all of more than 8 rows; 256-byte aligned, of the call alone, no
+ * clearing) also take a workspace of 256 bytes, zero-filled once, which holds the device status
+ * and nothing else: MK_ERR_TIMEOUT if a bounded wait ran out, after which y is undefined.
+ * Both may be NULL for the others.  cfg (may be NULL): max_ctas, wait_limit_ns and inject (1: one CTA does not
  * load its last step) apply. */
 mk_status mk_w4_gemm(const void *x, long long x_row, const mk_w4_weight *w, void *y, long long y_row,
                      mk_dtype dtype, mk_dtype out_dtype, long long m, void *scratch,
