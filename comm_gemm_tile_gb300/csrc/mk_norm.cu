@@ -465,22 +465,25 @@ struct ColumnParams {
   int n, parts, dtype;
 };
 
-// Column sums of part [parts x n]: a block has 32 columns, its 8 warps every 8th part.
-__global__ void __launch_bounds__(256) mk_norm_columns_kernel(const __grid_constant__ ColumnParams p) {
-  __shared__ float sums[8][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+// Column sums of part [parts x n]: a block has 32 columns, its 32 warps every 32nd part, all in flight at once.
+constexpr int NC_WARPS = 32;
+__global__ void __launch_bounds__(32 * NC_WARPS) mk_norm_columns_kernel(const __grid_constant__ ColumnParams p) {
+  __shared__ float sums[NC_WARPS][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.x * 32;
   griddep_wait();
   float s = 0.f;
-  if (c < p.n) {
-#pragma unroll 8
-    for (int i = warp; i < p.parts; i += 8) s += p.part[static_cast<long long>(i) * p.n + c];
+  if (c0 + lane < p.n) {
+#pragma unroll 15
+    for (int i = warp; i < p.parts; i += NC_WARPS) s += p.part[static_cast<long long>(i) * p.n + c0 + lane];
   }
   sums[warp][lane] = s;
   __syncthreads();
-  if (warp != 0 || c >= p.n) return;
-  s = 0.f;
+  // warp w adds column w's
+  s = sums[lane][warp];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s += sums[i][lane];
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const int c = c0 + warp;
+  if (lane != 0 || c >= p.n) return;
   if (p.dtype == MK_F32) static_cast<float*>(p.out)[c] = s;
   else if (p.dtype == MK_BF16) static_cast<__nv_bfloat16*>(p.out)[c] = __float2bfloat16_rn(s);
   else static_cast<__half*>(p.out)[c] = __float2half_rn(s);
@@ -607,6 +610,7 @@ mk_status mk_rms_norm(const mk_rows* x, const mk_rows* residual, const void* wei
   if (out_dtype != dtype && out_dtype != MK_E4M3) return MK_ERR_INVALID;
   if (!x || !y || (residual == nullptr) != (h == nullptr)) return MK_ERR_INVALID;
   if (tokens == 0 || heads == 0) return MK_OK;
+  if (h && h->p == y->p) return MK_ERR_INVALID;             // one would be written over the other
   const int esz = size_of(dtype), N = 16 / esz;
   bool vec = n % N == 0;
   NormParams p;
@@ -684,7 +688,7 @@ mk_status mk_rms_norm_backward(const mk_rows* dy, const mk_rows* dh, const mk_ro
   if (e != cudaSuccess) return MK_ERR_CUDA;
   if (!dweight) return MK_OK;
   ColumnParams c = {p.part, dweight, n, grad_blocks(p.rows, s), weight_dtype};
-  e = launch_dependent(mk_norm_columns_kernel, dim3((n + 31) / 32), dim3(256), st, c);
+  e = launch_dependent(mk_norm_columns_kernel, dim3((n + 31) / 32), dim3(32 * NC_WARPS), st, c);
   return e == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }
 

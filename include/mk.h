@@ -530,7 +530,7 @@ typedef struct {
 /* Root-mean-square norm over the n elements of each row:
  *   h = x, or x + residual rounded to dtype;  r = 1 / sqrt(mean(h^2) + eps);  y = h * r * weight
  * x, residual, h: dtype (MK_BF16, MK_F16, MK_F32).  residual and h go together (both
- * NULL: the norm of x); h may be residual or x.  weight: [n] of weight_dtype (dtype or MK_F32),
+ * NULL: the norm of x); h may be residual or x, not y.  weight: [n] of weight_dtype (dtype or MK_F32),
  * NULL for ones.  y: out_dtype = dtype, or MK_E4M3: then scale[token * heads + head]
  * = max(amax / 448, 2^-100) over the row's finite |y| and the codes are y / scale (to
  * nearest even; infinities saturate, NaN stays NaN).  fp32 arithmetic, each output

@@ -40,7 +40,7 @@ def test_norm_refusals(L):
     e4 = dict(odt=mk.MK_E4M3)
     for bad in (dict(x=None), dict(y=None), dict(x=rows(None)), dict(x=rows(GOOD + 1)), dict(y=rows(GOOD + 1)),
                 dict(residual=rows()), dict(h=rows()), dict(residual=rows(GOOD + 1), h=rows()),
-                dict(residual=rows(), h=rows(None)), dict(residual=rows(), h=rows(token=0)), dict(y=rows(token=0)),
+                dict(residual=rows(), h=rows(None)), dict(residual=rows(), h=rows()), dict(residual=rows(), h=rows(2 * GOOD, token=0)), dict(y=rows(token=0)),
                 dict(y=rows(head=0)), dict(weight=GOOD + 1), dict(weight=GOOD + 2, wdt=mk.MK_F32), dict(dtype=mk.MK_E4M3),
                 dict(dtype=9), dict(wdt=mk.MK_F16), dict(odt=mk.MK_F32), dict(odt=9), e4, dict(e4, scale=GOOD + 2),
                 dict(tokens=-1), dict(tokens=1 << 31), dict(tokens=1 << 20, heads=1 << 11), dict(heads=-1), dict(n=0),

@@ -93,6 +93,28 @@ def test_heads_and_strides(dtype):
     check(one.expand(9, 5, 64), w, residual=draw((9, 1, 64), dtype, 8).expand(9, 5, 64))
 
 
+def test_weights_off_whole_pieces():
+    w = draw((513,), BF, 50)[1:]
+    x, r, dy = draw((20, 512), BF, 51), draw((20, 512), BF, 52), draw((20, 512), BF, 53)
+    check(x, w, residual=r)
+    check(x, w, e4m3=True)
+    gradient_check(x, w, dy)
+    assert torch.allclose(mk.rms_norm(x, w).float(), mk.rms_norm(x, w.clone()).float(), rtol=2.0 ** -7, atol=0)
+
+
+def test_rows_far_apart():
+    """Rows more than 2^31 bytes from each other."""
+    big = torch.empty(3, (1 << 30) + 64, dtype=BF, device="cuda")
+    x = big[:, :64]
+    x.copy_(draw((3, 64), BF, 54))
+    w = draw((64,), F32, 55)
+    y = check(x, w, out=big[:, 1 << 30:])[0]
+    assert torch.equal(y, mk.rms_norm(x.contiguous(), w))
+    dx, dw = mk.rms_norm_backward(y, x, w)
+    want = mk.rms_norm_backward(y.contiguous(), x.contiguous(), w)
+    assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
+
+
 def test_the_stream_in_place_and_equal_forms():
     x, r, w = draw((50, 512), BF, 9), draw((50, 512), BF, 10), draw((512,), BF, 11)
     y, h = mk.rms_norm(x, w, residual=r)
@@ -167,7 +189,7 @@ def gradient_check(h, w, dy, dh=None, eps=1e-6, got=None):
         return dx, dw
     t = (dy.double() * u).flatten(0, -2)
     want, rows = t.sum(dim=0), t.shape[0]
-    # a column's sum: rows of a block in order, then at most 456 blocks, 8 at a time
+    # a column's sum: rows of a block in order, then at most 456 blocks, 32 at a time
     assert bool(((dw.double() - want).abs() <= half_step(want, w.dtype)
                  + (SUM + (rows / 300 + 64) * 2.0 ** -24) * t.abs().sum(dim=0)).all())
     return dx, dw
@@ -255,6 +277,7 @@ def test_autograd():
     dx, dw = mk.rms_norm_backward(dy, want_h, w, dh=dh)
     for leaf, want in zip(leaves, (dx, dw, dx)):
         assert torch.equal(leaf.grad, want)
+    assert leaves[0].grad.data_ptr() != leaves[2].grad.data_ptr()
     # only one of the outputs used; a sum's gradient is expanded; only the weight wants one
     leaf = x.clone().requires_grad_()
     mk.rms_norm(leaf, w, residual=r)[1].sum().backward()

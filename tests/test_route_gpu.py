@@ -139,6 +139,26 @@ def test_strides():
         assert bool((room[:, :5] == 9).all()) and bool((room[:, 5 + logits.shape[1]:] == 9).all())
 
 
+def test_rows_far_apart():
+    big = torch.empty(3, (1 << 29) + 32, device="cuda")
+    logits = big[:, :32]
+    logits.copy_(draw((3, 32), F32, 40))
+    got, _ = check(logits, 3)
+    dg = draw((3, 3), F32, 41)
+    dl = mk.moe_route_backward(logits, got, dg, out=big[:, 1 << 29:])
+    assert torch.equal(dl, mk.moe_route_backward(logits.contiguous(), got, dg))
+
+
+def test_equal_logits_of_many_experts():
+    """More equal logits than a warp has lanes, of 16-bit types too: rounds instead of lists, the same choice."""
+    for dtype in (F32, BF):
+        for E in (64, 130, 256):
+            logits = draw((90, E), F32, 42).round().to(dtype)
+            logits[::4] = 2.0
+            check(logits, 8)
+            gradient_check(logits, 8, normalize=False)
+
+
 def test_the_dispatch_chooses_the_same():
     R, T, E, K, H, N = 2, 300, 16, 4, 64, 64
     logits = draw((R * T, E), F32, 8).bfloat16().float()     # ties

@@ -52,7 +52,7 @@ def check(x, w, dtype=None, **kw):
 
 # tokens: one, a column group's edges, both sides of every tile; rows and k odd, small, several pieces a warp
 SIZES = [(1, 1, 1), (1, 16, 1), (2, 17, 2), (3, 100, 3), (7, 33, 5), (8, 640, 8), (9, 129, 9), (16, 333, 4), (17, 64, 17),
-         (31, 250, 2), (33, 50, 3), (64, 200, 6), (65, 48, 2), (130, 90, 3), (1, 3584, 16)]
+         (31, 250, 2), (33, 50, 3), (64, 200, 6), (65, 48, 2), (130, 90, 3), (1, 3584, 16), (10, 20, 1), (40, 129, 1), (3, 8192, 65)]
 
 
 @pytest.mark.parametrize("dtype", [BF, HF])
