@@ -102,6 +102,44 @@ def test_weights_off_whole_pieces():
     assert torch.allclose(mk.rms_norm(x, w).float(), mk.rms_norm(x, w.clone()).float(), rtol=2.0 ** -7, atol=0)
 
 
+def between(rows, n, gap, off, dtype, fill):
+    """[rows, n] inside of a buffer of `fill`: `gap` elements between rows, the first `off` elements into it; the buffer,
+    and where it is not the rows."""
+    buf = torch.full((off + rows * (n + gap) + 9,), fill, dtype=dtype, device="cuda")
+    view = buf[off:off + rows * (n + gap)].view(rows, n + gap)[:, :n]
+    rest = torch.ones(buf.shape, dtype=torch.bool, device="cuda")
+    rest[off:off + rows * (n + gap)].view(rows, n + gap)[:, :n] = False
+    return view, buf, rest
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("rows,n", [(1, 16), (1, 1001), (7, 17), (9, 31), (40, 129), (310, 130), (700, 1001), (320, 4095),
+                                    (5, 8191), (310, 16383)])
+@pytest.mark.parametrize("gap,off,apart", [(0, 0, 0), (0, 3, 0), (1, 1, 0), (5, 8, 8), (2, 0, 1), (11, 5, 7)])
+def test_rows_that_begin_inside_of_pieces(rows, n, gap, off, apart, dtype):
+    """Rows that begin anywhere in 16 bytes, NaN between them, alike in all tensors (apart 0 or 8) and not; what lies
+    between the rows of the outputs stays."""
+    nan = float("nan")
+    x, r, dy = (between(rows, n, gap, off, dtype, nan)[0].copy_(draw((rows, n), dtype, 70 + i)) for i in range(3))
+    y, ybuf, yrest = between(rows, n, gap, off + apart, dtype, 7)
+    h, hbuf, hrest = between(rows, n, gap, off, dtype, 7)
+    c, cbuf, crest = between(rows, n, gap, off, E4, 7)
+    w = between(1, n, 0, 1, dtype, nan)[0][0].copy_(draw((n,), dtype, 73))
+    check(x, w, residual=r, out=y, h_out=h)
+    check(x, w.float(), out=y)
+    check(x, w, residual=r, out=c, h_out=h, e4m3=True)
+    check(x, None, out=c, e4m3=True)
+    got = mk.rms_norm_backward(dy, x, w, dh=r, out=y)
+    gradient_check(x, w, dy, dh=r, got=got)
+    gradient_check(x, w, dy, got=mk.rms_norm_backward(dy, x, w, out=y))
+    stays = torch.full((), 7, dtype=E4, device="cuda").view(torch.uint8)
+    assert bool((ybuf[yrest] == 7).all()) and bool((hbuf[hrest] == 7).all())
+    assert bool((cbuf.view(torch.uint8)[crest] == stays).all())
+    own, stream = dy.clone(), r.clone()                       # in place
+    gradient_check(x, w, dy, dh=r, got=mk.rms_norm_backward(own, x, w, dh=r.clone(), out=own))
+    assert torch.equal(mk.rms_norm(x.clone(), w, residual=stream, h_out=stream)[1], h) and torch.equal(stream, h)
+
+
 def test_rows_far_apart():
     """Rows more than 2^31 bytes from each other."""
     big = torch.empty(3, (1 << 30) + 64, dtype=BF, device="cuda")
@@ -189,7 +227,7 @@ def gradient_check(h, w, dy, dh=None, eps=1e-6, got=None):
         return dx, dw
     t = (dy.double() * u).flatten(0, -2)
     want, rows = t.sum(dim=0), t.shape[0]
-    # a column's sum: rows of a block in order, then at most 456 blocks, 32 at a time
+    # a column's sum: rows of a block in order, then at most 456 blocks, 8 at a time
     assert bool(((dw.double() - want).abs() <= half_step(want, w.dtype)
                  + (SUM + (rows / 300 + 64) * 2.0 ** -24) * t.abs().sum(dim=0)).all())
     return dx, dw
