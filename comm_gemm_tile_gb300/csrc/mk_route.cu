@@ -20,7 +20,15 @@
 // Choosing: at most two experts, by as many rounds of the largest key over the warp.
 // More: K rounds over the lanes' largest keys alone give a bound that at least K
 // keys reach, and few more; those are gathered one to a lane, and each counts the ones
-// before it.  #include <algorithm>
+// before it.  (32768 tokens, us, rounds and gathered: 64 experts K 1 13.1 and 14.0,
+// 2 14.5 and 14.6, 3 15.6 and 14.7, 8 23.3 and 17.6; 256 experts 1 16.8 and 18.8, 2 19.5
+// and 19.4, 3 21.9 and 19.7, 8 36.1 and 22.4.)
+//
+// What bounds it: 131072 tokens of 256 bf16 logits, 8 chosen: 67 us for 76 MB (1.1 TB/s), at 3.3 instructions
+// a cycle and SM of the 4 that it can start: the exponentials, the keys and the choice of
+// 487 warp instructions a token.  The gradient: 48 us for 143 MB, 3 TB/s.
+#include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 
@@ -84,8 +92,68 @@ __device__ __forceinline__ void write_losses(const RouteParams& p, float b, floa
   *p.tokens = n;
 }
 
-// exp(x), x <= 0: off by about |x| 2^-24 and 4 2^-24 of itself.
-__device__ __forceinline__ float exp_of(float x) { return __expf(x); }
+// The largest of a warp's values; NaN if there is one.
+__device__ __forceinline__ float warp_max(float v) {
+  float m;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
+// exp(x), x <= 0: off by about |x| 2^-24 and 4 2^-24 of itself, 0 below 2^-126.  log(x) and 1 / x, x >= 1.
+__device__ __forceinline__ float exp2_of(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float LOG2_E = 1.4426950408889634f, LN_2 = 0.6931471805599453f;
+__device__ __forceinline__ float exp_of(float x) { return exp2_of(x * LOG2_E); }
+__device__ __forceinline__ float log_of(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y * LN_2;
+}
+__device__ __forceinline__ float inverse(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// v[j] = exp(v[j] - top) and their sum: pairs where there are any.
+template <int PER>
+__device__ __forceinline__ float exps(float (&v)[PER], float top) {
+  if constexpr (PER == 1) {
+    v[0] = exp_of(v[0] - top);
+    return v[0];
+  } else {
+    const uint64_t less = two(-top, -top), log2_e = two(LOG2_E, LOG2_E);
+    uint64_t sum = 0;
+#pragma unroll
+    for (int j = 0; j < PER; j += 2) {
+      float a, b;
+      split(mul2(add2(two(v[j], v[j + 1]), less), log2_e), a, b);
+      v[j] = exp2_of(a);
+      v[j + 1] = exp2_of(b);
+      sum = add2(sum, two(v[j], v[j + 1]));
+    }
+    float a, b;
+    split(sum, a, b);
+    return a + b;
+  }
+}
+// s[j] += by v[j]
+template <int PER>
+__device__ __forceinline__ void add_times(float (&s)[PER], const float (&v)[PER], float by) {
+  if constexpr (PER == 1) {
+    s[0] = fmaf(v[0], by, s[0]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < PER; j += 2) split(fma2(two(v[j], v[j + 1]), two(by, by), two(s[j], s[j + 1])), s[j], s[j + 1]);
+  }
+}
 
 // A lane's logits of a token, as they lie; -inf past the last expert.
 template <class T, int PER>
@@ -122,11 +190,44 @@ struct Logits {
   }
 };
 
+// The largest K of a warp's values (numbers, or keys), the lowest expert of equal ones first: lane r gets the r-th's
+// expert and value.  Those not above `none` are not chosen.
+__device__ __forceinline__ uint32_t most_of(uint32_t a, uint32_t b) { return max(a, b); }
+__device__ __forceinline__ float most_of(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ uint32_t warp_most(uint32_t a) { return __reduce_max_sync(0xffffffffu, a); }
+__device__ __forceinline__ float warp_most(float a) { return warp_max(a); }
+template <int PER, class W>
+__device__ __forceinline__ void choose(W (&k)[PER], int K, W none, int lane, int& id, W& value) {
+  for (int r = 0; r < K; ++r) {
+    W m = k[0];
+#pragma unroll
+    for (int j = 1; j < PER; ++j) m = most_of(m, k[j]);
+    const W best = warp_most(m);
+    if (!(best > none)) return;                      // no expert left
+    const int owner = __ffs(__ballot_sync(0xffffffffu, m == best)) - 1;
+    int at = 0;
+    if (lane == owner) {
+#pragma unroll
+      for (int j = PER - 1; j >= 0; --j)
+        if (k[j] == best) at = j;
+#pragma unroll
+      for (int j = 0; j < PER; ++j)
+        if (j == at) k[j] = none;
+    }
+    at = __shfl_sync(0xffffffffu, lane * PER + at, owner);
+    if (lane == r) {
+      id = at;
+      value = best;
+    }
+  }
+}
+
 template <class T, int PER>
 __global__ void __launch_bounds__(RT_THREADS) mk_route_kernel(const __grid_constant__ RouteParams p) {
   __shared__ float s_p[RT_WARPS][32 * PER];
   __shared__ int s_c[32 * PER];
-  __shared__ uint2 s_list[RT_WARPS][32];             // keys and experts that may be among the chosen
+  __shared__ __align__(16) float s_value[RT_WARPS][32];      // logits that may be among the chosen,
+  __shared__ int s_expert[RT_WARPS][32];                     // in the order of their experts
   __shared__ float s_z[RT_WARPS];
   __shared__ int s_n[RT_WARPS];
   __shared__ float scratch[RT_WARPS];
@@ -154,91 +255,85 @@ __global__ void __launch_bounds__(RT_THREADS) mk_route_kernel(const __grid_const
     const bool real = next_real;
     ahead(t > p.T - step ? p.T : t + step);        // (t + step may pass 2^31)
     int id = -1, slot = lane;                        // this lane's chosen expert, and its place among them
-    float w = 0.f;                                   // exp(its logit - the largest)
+    float w = 0.f;                                   // its gate
     if (real) {
       float v[PER];
-      uint32_t k[PER];
       now.get(v);
+      float most = v[0];
 #pragma unroll
-      for (int j = 0; j < PER; ++j) k[j] = key_of(v[j]);
-      uint32_t most = k[0];
+      for (int j = 1; j < PER; ++j) most = max_nan(most, v[j]);
+      const float first = warp_max(most);
+      float top = first, chosen = -INFINITY;
+      bool rounds = p.K <= 2, any = first > -INFINITY;
+      if (first != first) {                          // by the keys, in whose order NaN has a place
+        uint32_t k[PER], key = 0;
 #pragma unroll
-      for (int j = 1; j < PER; ++j) most = max(most, k[j]);
-      const uint32_t first = __reduce_max_sync(0xffffffffu, most);
-      const float top = value_of(first);
-      bool rounds = p.K <= 2;
-      if (!rounds) {
-        uint32_t m = most, bound = first;
+        for (int j = 0; j < PER; ++j) k[j] = key_of(v[j]);
+        choose<PER>(k, p.K, KEY_NONE, lane, id, key);
+        top = value_of(__shfl_sync(0xffffffffu, key, 0));
+        chosen = id >= 0 ? value_of(key) : -INFINITY;
+        any = __shfl_sync(0xffffffffu, id, 0) >= 0;
+        rounds = false;
+      } else if (!rounds) {
+        float m = most, bound = first;
         for (int r = 1; r < p.K; ++r) {
-          if (m == bound) m = 0;
-          bound = __reduce_max_sync(0xffffffffu, m);
+          if (m == bound) m = -INFINITY;
+          bound = warp_max(m);
         }
-        bound = max(bound, KEY_NONE + 1);
-        int count = 0;
+        bound = fmaxf(bound, -FLT_MAX);
+        int own = 0;
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-          const uint32_t vote = __ballot_sync(0xffffffffu, k[j] >= bound);
-          const int at = count + __popc(vote & before);
-          if (k[j] >= bound && at < 32) s_list[warp][at] = make_uint2(k[j], e0 + j);
-          count += __popc(vote);
+        for (int j = 0; j < PER; ++j) own += v[j] >= bound;
+        int upto = own;                              // with the lanes' before
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+          const int a = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += a;
         }
+        const int count = __shfl_sync(0xffffffffu, upto, 31);
         rounds = count > 32;                         // (many equal logits)
         if (!rounds) {
+          int at = upto - own;
+#pragma unroll
+          for (int j = 0; j < PER; ++j)
+            if (v[j] >= bound) {
+              s_value[warp][at] = v[j];
+              s_expert[warp][at++] = e0 + j;
+            }
+          if (lane >= count) s_value[warp][lane] = -INFINITY;
           __syncwarp();
-          const uint2 mine = lane < count ? s_list[warp][lane] : make_uint2(0, 0);
-          int larger = 0;
-          for (int i = 0; i < count; ++i) {
-            const uint2 o = s_list[warp][i];         // the same for every lane
-            larger += o.x > mine.x || (o.x == mine.x && o.y < mine.y);
+          const float mine = s_value[warp][lane] + 0.f;      // (-0 is +0's equal)
+          int larger = __popc(__match_any_sync(0xffffffffu, __float_as_uint(mine)) & before);
+          for (int i = 0; i < count; i += 4) {
+            const float4 o = *reinterpret_cast<const float4*>(&s_value[warp][i]);      // the same for every lane
+            larger += o.x > mine;
+            larger += o.y > mine;
+            larger += o.z > mine;
+            larger += o.w > mine;
           }
-          __syncwarp();                              // the list has been read
           // the places left over when fewer than K experts have a logit are the lanes' past the list
           slot = lane < count ? larger : lane;
           if (lane < count && larger < p.K) {
-            id = mine.y;
-            w = exp_of(value_of(mine.x) - top);
+            id = s_expert[warp][lane];
+            chosen = mine;
           }
+          __syncwarp();                              // the list has been read
         }
       }
       if (rounds) {
-        for (int r = 0; r < p.K; ++r) {
-          uint32_t m = k[0];
+        float k[PER];
 #pragma unroll
-          for (int j = 1; j < PER; ++j) m = max(m, k[j]);
-          const uint32_t best = __reduce_max_sync(0xffffffffu, m);
-          if (best <= KEY_NONE) break;               // no expert left
-          const int owner = __ffs(__ballot_sync(0xffffffffu, m == best)) - 1;
-          int at = 0;
-          if (lane == owner) {
-#pragma unroll
-            for (int j = PER - 1; j >= 0; --j)
-              if (k[j] == best) at = j;
-#pragma unroll
-            for (int j = 0; j < PER; ++j)
-              if (j == at) k[j] = 0;
-          }
-          at = __shfl_sync(0xffffffffu, e0 + at, owner);
-          if (lane == r) {
-            id = at;
-            w = exp_of(value_of(best) - top);
-          }
-        }
+        for (int j = 0; j < PER; ++j) k[j] = v[j];
+        choose<PER>(k, p.K, -INFINITY, lane, id, chosen);
       }
-      if (first > KEY_NONE) {
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-          v[j] = exp_of(v[j] - top);
-          sum += v[j];
-        }
-        sum = warp_sum(sum);
-        const float inv = __fdividef(1.f, sum);
-#pragma unroll
-        for (int j = 0; j < PER; ++j) psum[j] = fmaf(v[j], inv, psum[j]);
-        const float lse = top + __logf(sum);         // (sum is 1 .. 256: off by 3 2^-24)
+      if (any) {
+        const float sum = warp_sum(exps<PER>(v, top)), inv = inverse(sum);
+        add_times<PER>(psum, v, inv);
+        const float lse = top + log_of(sum);         // (sum is 1 .. 256: off by 3 2^-24)
         z = fmaf(lse, lse, z);
         ++n;
-        w = (p.normalize ? __fdividef(w, warp_sum(w)) : w * inv) * p.scale;
+        w = id >= 0 ? exp_of(chosen - top) : 0.f;
+        w *= (p.normalize ? inverse(warp_sum(w)) : inv) * p.scale;
         if (id >= 0) atomicAdd(&s_c[id], 1);
       }
     }
@@ -394,15 +489,11 @@ __global__ void __launch_bounds__(RG_THREADS) mk_route_grad_kernel(const __grid_
       now.get(v);
       float top = v[0];
 #pragma unroll
-      for (int j = 1; j < PER; ++j) top = fmaxf(top, v[j]);
-      top = value_of(__reduce_max_sync(0xffffffffu, key_of(top)));
-      float sum = 0.f, pf = 0.f;
+      for (int j = 1; j < PER; ++j) top = max_nan(top, v[j]);
+      top = warp_max(top);
+      float sum = exps<PER>(v, top), pf = 0.f;
 #pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        v[j] = exp_of(v[j] - top);
-        sum += v[j];
-        pf = fmaf(v[j], f[j], pf);
-      }
+      for (int j = 0; j < PER; ++j) pf = fmaf(v[j], f[j], pf);
       const bool chosen = p.dgates != nullptr && id >= 0 && id < p.E;
       float w = 0.f;                                 // exp(logit - top) of this lane's chosen expert
       if (chosen) w = exp_of(Piece<T>::one(reinterpret_cast<const T*>(p.logits + t * p.row)[id]) - top);
@@ -421,8 +512,8 @@ __global__ void __launch_bounds__(RG_THREADS) mk_route_grad_kernel(const __grid_
           dot += __shfl_xor_sync(0xffffffffu, dot, o);
         }
       }
-      const float inv = __fdividef(1.f, sum), lse = top + __logf(sum);
-      const float part = p.normalize ? __fdividef(1.f, __shfl_sync(0xffffffffu, own, 0)) : inv;
+      const float inv = inverse(sum), lse = top + log_of(sum);
+      const float part = p.normalize ? inverse(__shfl_sync(0xffffffffu, own, 0)) : inv;
       dot = __shfl_sync(0xffffffffu, dot, 0) * part;
       const float mine = w * part * (p.normalize ? dg - dot : dg);
       const float all = (p.normalize || p.dgates == nullptr ? 0.f : -dot) - db * pf * inv + dz * lse;
@@ -476,6 +567,8 @@ __global__ void __launch_bounds__(RG_THREADS) mk_route_grad_kernel(const __grid_
 
 // ------------------------------------------------------------------ host
 
+// Up to MK_ROUTE_SMALL tokens one block, which writes the losses itself: 64 tokens 5.2 us (96: 6.2, and 5.6 by many
+// blocks and a second launch; 256: 12.0 and 5.3).
 int route_blocks(long long T) {
   if (T <= MK_ROUTE_SMALL) return 1;
   return static_cast<int>(std::min<long long>(ceil_div_ll(T, RT_WARPS), RT_BLOCKS));

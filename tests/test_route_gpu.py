@@ -126,6 +126,31 @@ def test_nan_stays_with_its_token():
     assert bool(got["balance_loss"].isnan()) and bool(got["z_loss"].isnan())
 
 
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("experts", [24, 200])
+@pytest.mark.parametrize("topk", [1, 2, 3, 8])
+def test_where_nan_stands(topk, experts, dtype):
+    """NaN is above every logit and NaN with a sign below every one, as the dispatch has it: ids as integers would order them."""
+    logits = draw((40, experts), dtype, 61)
+    logits[3, 5] = float("nan")
+    logits[4, 7] = logits[4, 2] = logits[4, 19] = float("nan")
+    logits[5, 1] = -logits[3, 5]
+    logits[6] = -logits[3, 5]
+    logits[7] = float("nan")
+    logits[8, :20] = -INF
+    logits[8, 1] = float("nan")
+    got = mk.moe_route(logits, topk)
+    key = logits.float().view(torch.int32).long()
+    key = torch.where(key < 0, -(key & 0x7fffffff), key)
+    value, idx = torch.sort(key, dim=-1, descending=True, stable=True)
+    want = torch.where(value[:, :topk] > -0x7f800000, idx[:, :topk], -1)
+    assert torch.equal(got["topk_idx"].long(), want)          # (16-bit types lose NaN's sign when it is negated)
+    assert int(got["tokens"]) == int((want[:, 0] >= 0).sum()) and torch.equal(got["counts"].long(), torch.bincount(want[want >= 0], minlength=experts))
+    for t in (0, 20, 39):
+        clean = mk.moe_route(logits[t:t + 1], topk)
+        assert torch.equal(got["gates"][t:t + 1], clean["gates"])
+
+
 def test_strides():
     big = draw((150, 100), BF, 7)
     for logits in (big[:, 3:67], big[::2, :64], big[:1].expand(90, 100)[:, :50]):
