@@ -17,16 +17,16 @@
 // memory and over the blocks by a second launch, always in the same order.  (Counts
 // are whole numbers: shared memory's atomics do for them.)
 //
-// Choosing: at most two experts, by as many rounds of the largest key over the warp.
-// More: K rounds over the lanes' largest keys alone give a bound that at least K
-// keys reach, and few more; those are gathered one to a lane, and each counts the ones
-// before it.  (32768 tokens, us, rounds and gathered: 64 experts K 1 13.1 and 14.0,
-// 2 14.5 and 14.6, 3 15.6 and 14.7, 8 23.3 and 17.6; 256 experts 1 16.8 and 18.8, 2 19.5
-// and 19.4, 3 21.9 and 19.7, 8 36.1 and 22.4.)
+// Choosing: at most two experts, by as many rounds of the largest logit over the warp.
+// More: K rounds over the lanes' largest alone give a bound that at least K logits
+// reach, and few more; those are gathered one to a lane, in the order of the experts, and
+// each counts the larger ones.  (32768 tokens, us, rounds and gathered, of an earlier form of both: 64 experts K 1 13.1
+// and 14.0, 2 14.5 and 14.6, 3 15.6 and 14.7, 8 23.3 and 17.6; 256 experts 1 16.8 and 18.8, 2 19.5 and 19.4,
+// 3 21.9 and 19.7, 8 36.1 and 22.4.)
 //
-// What bounds it: 131072 tokens of 256 bf16 logits, 8 chosen: 67 us for 76 MB (1.1 TB/s), at 3.3 instructions
-// a cycle and SM of the 4 that it can start: the exponentials, the keys and the choice of
-// 487 warp instructions a token.  The gradient: 48 us for 143 MB, 3 TB/s.
+// What bounds it: 131072 tokens of 256 fp32 logits, a tenth of them masked, 8 chosen: 58 us for 129 MB (2.2 TB/s), at 3.3
+// instructions a cycle and SM of the 4 that it can start, some 420 a token; more warps do not fit the
+// registers.  The gradient: 47 us for 268 MB, 84 % of a copy's rate.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -82,6 +82,28 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+
+// Two and four sums over a warp: halves of it (quarters) take one each after the first exchange.
+__device__ __forceinline__ void warp_sums(float& a, float& b) {
+  const bool up = threadIdx.x & 16;
+  float v = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  a = __shfl_sync(0xffffffffu, v, 0);
+  b = __shfl_sync(0xffffffffu, v, 16);
+}
+__device__ __forceinline__ void warp_sums(float& a, float& b, float& c, float& d) {
+  const bool up = threadIdx.x & 16, right = threadIdx.x & 8;
+  const float v = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, 16);
+  const float w = (up ? d : c) + __shfl_xor_sync(0xffffffffu, up ? c : d, 16);
+  float u = (right ? w : v) + __shfl_xor_sync(0xffffffffu, right ? v : w, 8);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+  a = __shfl_sync(0xffffffffu, u, 0);
+  b = __shfl_sync(0xffffffffu, u, 16);
+  c = __shfl_sync(0xffffffffu, u, 8);
+  d = __shfl_sync(0xffffffffu, u, 24);
 }
 
 // Both losses and N from the sums over tokens: b of counts times p, z of lse^2.
@@ -276,7 +298,9 @@ __global__ void __launch_bounds__(RT_THREADS) mk_route_kernel(const __grid_const
         rounds = false;
       } else if (!rounds) {
         float m = most, bound = first;
-        for (int r = 1; r < p.K; ++r) {
+#pragma unroll
+        for (int r = 1; r < MOE_MAX_TOPK; ++r) {
+          if (r >= p.K) break;
           if (m == bound) m = -INFINITY;
           bound = warp_max(m);
         }
@@ -327,13 +351,15 @@ __global__ void __launch_bounds__(RT_THREADS) mk_route_kernel(const __grid_const
         choose<PER>(k, p.K, -INFINITY, lane, id, chosen);
       }
       if (any) {
-        const float sum = warp_sum(exps<PER>(v, top)), inv = inverse(sum);
+        w = id >= 0 ? exp_of(chosen - top) : 0.f;
+        float sum = exps<PER>(v, top), own = w;      // own: of the chosen ones together
+        warp_sums(sum, own);
+        const float inv = inverse(sum);
         add_times<PER>(psum, v, inv);
         const float lse = top + log_of(sum);         // (sum is 1 .. 256: off by 3 2^-24)
         z = fmaf(lse, lse, z);
         ++n;
-        w = id >= 0 ? exp_of(chosen - top) : 0.f;
-        w *= (p.normalize ? inverse(warp_sum(w)) : inv) * p.scale;
+        w *= (p.normalize ? inverse(own) : inv) * p.scale;
         if (id >= 0) atomicAdd(&s_c[id], 1);
       }
     }
@@ -500,21 +526,11 @@ __global__ void __launch_bounds__(RG_THREADS) mk_route_grad_kernel(const __grid_
       else dg = 0.f;
       float own = w;                                 // of the chosen ones together
       float dot = w * dg;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        pf += __shfl_xor_sync(0xffffffffu, pf, o);
-      }
-      if (p.dgates != nullptr) {
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) {            // (lanes below K <= 8)
-          own += __shfl_xor_sync(0xffffffffu, own, o);
-          dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        }
-      }
+      if (p.dgates != nullptr) warp_sums(sum, pf, own, dot);
+      else warp_sums(sum, pf);
       const float inv = inverse(sum), lse = top + log_of(sum);
-      const float part = p.normalize ? inverse(__shfl_sync(0xffffffffu, own, 0)) : inv;
-      dot = __shfl_sync(0xffffffffu, dot, 0) * part;
+      const float part = p.normalize ? inverse(own) : inv;
+      dot *= part;
       const float mine = w * part * (p.normalize ? dg - dot : dg);
       const float all = (p.normalize || p.dgates == nullptr ? 0.f : -dot) - db * pf * inv + dz * lse;
       if (p.dgates != nullptr) {
