@@ -551,10 +551,17 @@ __global__ void __launch_bounds__(WIDE ? GradShape<T, WAY, U>::THREADS : NM_THRE
     for (int u = 0; u < U; ++u) {
       const int i = t + u * p.lanes;
       if (i >= rs.pieces) continue;
+      if constexpr (WAY == PIECES) {                         // (single stores, 32 bytes apart: 2048 x 4096 20 us for 16)
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const int c = i * N - rs.before + e;
-        if (WAY != SHIFTED || static_cast<unsigned>(c) < static_cast<unsigned>(p.n)) out[c] = acc[u * N + e];
+        for (int e = 0; e < N; e += 4)
+          *reinterpret_cast<float4*>(out + i * N + e) =
+              make_float4(acc[u * N + e], acc[u * N + e + 1], acc[u * N + e + 2], acc[u * N + e + 3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const int c = i * N - rs.before + e;
+          if (WAY != SHIFTED || static_cast<unsigned>(c) < static_cast<unsigned>(p.n)) out[c] = acc[u * N + e];
+        }
       }
     }
     return;
@@ -580,22 +587,23 @@ struct ColumnParams {
   int n, parts, dtype;
 };
 
-// Column sums of part [parts x n]: a block has 32 columns, its 8 warps every 8th part (32 warps: no faster).
-__global__ void __launch_bounds__(256) mk_norm_columns_kernel(const __grid_constant__ ColumnParams p) {
-  __shared__ float sums[8][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+// Column sums of part [parts x n]: a block has 32 columns, each of its warps every 8th part, or, past 64 parts, every
+// 32nd (us of both kernels with 8 and 32 warps: 8 parts of 8192 columns 7.2 and 7.4, 456 of 4096 16.4 and 11.7).
+__global__ void __launch_bounds__(1024) mk_norm_columns_kernel(const __grid_constant__ ColumnParams p) {
+  __shared__ float sums[32][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, c = blockIdx.x * 32 + lane;
   griddep_wait();
   float s = 0.f;
   if (c < p.n) {
 #pragma unroll 8
-    for (int i = warp; i < p.parts; i += 8) s += p.part[static_cast<long long>(i) * p.n + c];
+    for (int i = warp; i < p.parts; i += warps) s += p.part[static_cast<long long>(i) * p.n + c];
   }
   sums[warp][lane] = s;
   __syncthreads();
   if (warp != 0 || c >= p.n) return;
   s = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) s += sums[i][lane];
+#pragma unroll 8
+  for (int i = 0; i < warps; ++i) s += sums[i][lane];
   if (p.dtype == MK_F32) static_cast<float*>(p.out)[c] = s;
   else if (p.dtype == MK_BF16) static_cast<__nv_bfloat16*>(p.out)[c] = __float2bfloat16_rn(s);
   else static_cast<__half*>(p.out)[c] = __float2half_rn(s);
@@ -637,12 +645,16 @@ Split split_grad(int pieces, Way way) {
   return s;
 }
 
-// Blocks for rows (of a class, where there are several): of at least two sets of rows, since every block leaves sums of
-// all columns (bf16, us, least one, two, four sets: 16 x 8192 9.2, 10.5, 13.9; 304 x 8192 19.7, 13.8, 15.5; 1216 x 4096
-// 20.4, 20.1, 15.6).
-int grad_blocks(long long rows, const Split& s, unsigned classes) {
+// Blocks for rows (of a class, where there are several): no more than run at once (three of an SM, or what its shared
+// memory holds of rows of four pieces a thread: 32768 x 8192, bf16, 304 blocks 242 us, 456 274; 16384 x 4095, whose rows are
+// 160 threads', 167 and 134), of at least two sets of rows, since
+// every block leaves sums of all columns (us, least one, two, four sets: 16 x 8192 6.1, 7.2, 10.0; 304 x 8192 11.8, 8.9,
+// 11.0; 1000 x 128 5.4, 5.9, 7.2; 1216 x 4096 16.3, 16.4, 12.2, with 32 warps for the columns 11.7 for two).
+int grad_blocks(long long rows, const Split& s, Way way, unsigned classes) {
   const long long per = s.wide ? 1 : NM_THREADS / s.lanes, mine = ceil_div_ll(rows, classes);
-  return static_cast<int>(std::min<long long>(ceil_div_ll(mine, 2 * per), NM_PARTS / classes) * classes);
+  const int room = way == ELEMENTS || s.u == 2 ? 3 : static_cast<int>(227 * 1024 / (sizeof(uint4) * 2 * 3 * 4 * s.lanes + 2048));
+  const int most = NM_PARTS / 3 * std::max(1, std::min(3, room));
+  return static_cast<int>(std::min<long long>(ceil_div_ll(mine, 2 * per), most / classes) * classes);
 }
 
 template <class T, Way WAY, int U, bool OUT8>
@@ -671,7 +683,7 @@ cudaError_t launch_grad(const NormParams& p, const Split& s, cudaStream_t st) {
     const cudaError_t e = allow_smem(k, most, done[s.wide]);
     if (e != cudaSuccess) return e;
   }
-  k<<<grad_blocks(p.rows, s, p.classes), threads, smem, st>>>(p);
+  k<<<grad_blocks(p.rows, s, WAY, p.classes), threads, smem, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -844,8 +856,8 @@ mk_status mk_rms_norm_backward(const mk_rows* dy, const mk_rows* dh, const mk_ro
   else e = launch_grad<float>(p, s, way, st);
   if (e != cudaSuccess) return MK_ERR_CUDA;
   if (!dweight) return MK_OK;
-  ColumnParams c = {p.part, dweight, n, grad_blocks(p.rows, s, p.classes), weight_dtype};
-  e = launch_dependent(mk_norm_columns_kernel, dim3((n + 31) / 32), dim3(256), st, c);
+  ColumnParams c = {p.part, dweight, n, grad_blocks(p.rows, s, way, p.classes), weight_dtype};
+  e = launch_dependent(mk_norm_columns_kernel, dim3((n + 31) / 32), dim3(c.parts > 64 ? 1024 : 256), st, c);
   return e == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }
 

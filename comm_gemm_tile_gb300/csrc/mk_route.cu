@@ -20,9 +20,8 @@
 // Choosing: at most two experts, by as many rounds of the largest logit over the warp.
 // More: K rounds over the lanes' largest alone give a bound that at least K logits
 // reach, and few more; those are gathered one to a lane, in the order of the experts, and
-// each counts the larger ones.  (32768 tokens, us, rounds and gathered, of an earlier form of both: 64 experts K 1 13.1
-// and 14.0, 2 14.5 and 14.6, 3 15.6 and 14.7, 8 23.3 and 17.6; 256 experts 1 16.8 and 18.8, 2 19.5 and 19.4,
-// 3 21.9 and 19.7, 8 36.1 and 22.4.)
+// each counts the larger ones.  (32768 tokens, us, rounds and gathered: 64 experts K 1 11.6 and 13.3, 2 12.7 and 14.0,
+// 3 13.3 and 14.0, 8 18.9 and 16.0; 256 experts 1 14.2 and 17.3, 2 16.4 and 17.5, 3 18.4 and 17.4, 8 30.1 and 19.6.)
 //
 // What bounds it: 131072 tokens of 256 fp32 logits, a tenth of them masked, 8 chosen: 58 us for 129 MB (2.2 TB/s), at 3.3
 // instructions a cycle and SM of the 4 that it can start, some 420 a token; more warps do not fit the

@@ -227,7 +227,7 @@ def gradient_check(h, w, dy, dh=None, eps=1e-6, got=None):
         return dx, dw
     t = (dy.double() * u).flatten(0, -2)
     want, rows = t.sum(dim=0), t.shape[0]
-    # a column's sum: rows of a block in order, then at most 456 blocks, 8 at a time
+    # a column's sum: rows of a block in order, then at most 456 blocks, 8 or (past 64) 32 at a time, then those
     assert bool(((dw.double() - want).abs() <= half_step(want, w.dtype)
                  + (SUM + (rows / 300 + 64) * 2.0 ** -24) * t.abs().sum(dim=0)).all())
     return dx, dw
