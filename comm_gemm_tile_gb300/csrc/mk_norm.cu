@@ -654,7 +654,8 @@ int grad_blocks(long long rows, const Split& s, Way way, unsigned classes) {
   const long long per = s.wide ? 1 : NM_THREADS / s.lanes, mine = ceil_div_ll(rows, classes);
   const int room = way == ELEMENTS || s.u == 2 ? 3 : static_cast<int>(227 * 1024 / (sizeof(uint4) * 2 * 3 * 4 * s.lanes + 2048));
   const int most = NM_PARTS / 3 * std::max(1, std::min(3, room));
-  return static_cast<int>(std::min<long long>(ceil_div_ll(mine, 2 * per), most / classes) * classes);
+  // (a whole number of each class; with fewer rows than classes one block a row, since the workspace has room for no more)
+  return static_cast<int>(std::min<long long>(rows, std::min<long long>(ceil_div_ll(mine, 2 * per), most / classes) * classes));
 }
 
 template <class T, Way WAY, int U, bool OUT8>

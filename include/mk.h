@@ -535,8 +535,9 @@ typedef struct {
  * = max(amax / 448, 2^-100) over the row's finite |y| and the codes are y / scale (to
  * nearest even; infinities saturate, NaN stays NaN).  fp32 arithmetic, each output
  * rounded once; sums of squares past fp32's range come out right.  n <= 16384, eps > 0,
- * tokens * heads below 2^31.  Rows of whole 16-byte pieces (base, strides, n) move
- * 16 bytes at a time, others element by element. */
+ * tokens * heads below 2^31.  Rows move 16 bytes at a time where they are whole 16-byte
+ * pieces (base, strides, n), or begin alike inside of 16 bytes in all tensors of dtype and lie
+ * one stride apart; others element by element. */
 mk_status mk_rms_norm(const mk_rows *x, const mk_rows *residual, const void *weight, const mk_rows *y,
                       const mk_rows *h, float *scale, mk_dtype dtype, mk_dtype weight_dtype,
                       mk_dtype out_dtype, long long tokens, int heads, int n, float eps,

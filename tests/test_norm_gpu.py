@@ -354,6 +354,24 @@ def test_the_same_bits_every_time():
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
+class Guarded:
+    """A workspace of exactly the bytes that are asked for, with others behind it."""
+    def get(self, size, stream=None):
+        self.size, self.buffer = size, torch.full((size + 4096 * 1024,), 77, dtype=torch.uint8, device="cuda")
+        return self.buffer[:size]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows", [1, 2, 3, 5, 7, 8, 9, 15, 17, 100, 1000])
+@pytest.mark.parametrize("n", [1, 33, 64, 1001, 4096, 9001])
+def test_the_workspace_is_no_larger_than_asked(rows, n, dtype):
+    """Partial sums stay in it, also where there are fewer rows than places for a row to begin in 16 bytes."""
+    h, dy, w = draw((rows, n), dtype, 80), draw((rows, n), dtype, 81), draw((n,), dtype, 82)
+    ws = Guarded()
+    gradient_check(h, w, dy, got=mk.rms_norm_backward(dy, h, w, workspace=ws))
+    assert bool((ws.buffer[ws.size:] == 77).all())
+
+
 def test_streams_graphs_and_workspaces():
     x, r, w, dy = draw((600, 512), BF, 45), draw((600, 512), BF, 46), draw((512,), BF, 47), draw((600, 512), BF, 48)
     want = mk.rms_norm(x, w, residual=r)
