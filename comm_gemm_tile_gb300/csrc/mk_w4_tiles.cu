@@ -204,8 +204,6 @@ __global__ void __launch_bounds__(WT_THREADS, 1) mk_w4_tiles_kernel(const __grid
       uint4 v[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const uint4*>(w + 16 * ((4 * h + q) ^ (r & 7)));
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + B_CEMPTY + 8 * s);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint32_t o[32];
@@ -226,7 +224,12 @@ __global__ void __launch_bounds__(WT_THREADS, 1) mk_w4_tiles_kernel(const __grid
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(to + B_AFULL);
+      // The codes' place is free only now that they have been used: released behind the loads, which were still on their
+      // way, it was filled again before they came.
+      if (lane == 0) {
+        mbar_arrive(bars + B_CEMPTY + 8 * s);
+        mbar_arrive(to + B_AFULL);
+      }
     }
   } else if (warp < 16) {
     // ---------------------------------------------------------------- sums, of half the tokens
@@ -270,6 +273,11 @@ __global__ void __launch_bounds__(WT_THREADS, 1) mk_w4_tiles_kernel(const __grid
     ahead(c);
     bool fresh = true;                                       // sc_next is this step's
     for (int i = 0; i < count; ++i) {
+      // (the sums of the step before have been used, by every lane)
+      if (ZEROS && i > 0 && lane == 0) {
+        mbar_arrive(bars + B_XEMPTY + 8 * (2 * (i - 1) % SX));
+        mbar_arrive(bars + B_XEMPTY + 8 * (2 * (i - 1) % SX) + 8);
+      }
       const bool ends = c + 1 == steps;
       const int row_now = row;
       if (fresh) {
@@ -348,8 +356,10 @@ __global__ void __launch_bounds__(WT_THREADS, 1) mk_w4_tiles_kernel(const __grid
       if (lane == 0) {
         mbar_arrive(bars + B_DEMPTY + 8 * place0);
         mbar_arrive(bars + B_DEMPTY + 8 * place0 + 8);
-        mbar_arrive(bars + B_XEMPTY + 8 * x0);
-        mbar_arrive(bars + B_XEMPTY + 8 * x0 + 8);
+        if (!ZEROS) {
+          mbar_arrive(bars + B_XEMPTY + 8 * x0);
+          mbar_arrive(bars + B_XEMPTY + 8 * x0 + 8);
+        }
       }
       if (ends || i + 1 == count) {
         // all of a tile, or the run's part of it: that at the run's beginning first, another second

@@ -72,6 +72,20 @@ def test_long_rows(m, group, k):
     check(x, w, F32)
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("zeros", [True, False])
+@pytest.mark.parametrize("m,n,k,group", [(9, 4104, 8320, 32), (40, 4104, 8320, 32), (40, 4224, 8192, 64), (40, 4104, 8320, 128)])
+def test_cold_matrices(m, n, k, group, zeros, dtype):
+    """Many steps a CTA with everything out of the caches, so that loads of scales hold up the sums and fill the rings."""
+    x, w = problem(m, n, k, group, zeros, dtype, seed=15)
+    want, size = formula(x, w)
+    flush = torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+    for _ in range(12):
+        flush.add_(1)
+        y = mk.w4_gemm(x, w, out_dtype=F32)
+        assert bool(((y.double() - want).abs() <= (k / 16 + k // group + 32) * 2.0 ** -22 * size).all())
+
+
 def test_whole_numbers_are_exact():
     """Small whole numbers: every product and sum is exact in fp32, so the bits are those of the 64-bit sums."""
     g = torch.Generator().manual_seed(8)
