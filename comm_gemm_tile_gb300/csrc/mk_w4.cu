@@ -7,13 +7,17 @@
 // by its scale in fp32: nothing is rounded before the output.  Zero points enter
 // as (8 - z) sum_k x[m][k] of the group, from one more product with ones.
 //
-// Here: up to 8 tokens (more go to mk_w4_tiles.cu).  The products are mma.sync m16n8k16 with
-// weights as the 16 rows and tokens as the 8 columns.  They sum over k in any order, so a
-// thread's own codes are its operands as they come, and x is read in the same order.  A block
+// Here: few tokens, up to 8, 16 or 32 (more, and large matrices, go to mk_w4_tiles.cu).  The products are mma.sync
+// m16n8k16 with weights as the 16 rows and 8 tokens as the columns, one for each 8 of them.  They sum over k in any
+// order, so a thread's own codes are its operands as they come, and x is read in the same order.  A block
 // has 16 rows of the matrix; its warps share out k in pieces of 128, a thread 16 bytes
 // (32 codes) of two rows of each, loaded one piece ahead, and add their sums in shared memory, in order.
-// 8192 x 8192, groups of 128, one token: 12.7 us in a graph, 2.7 TB/s.  More pieces ahead or two tiles of rows a
-// block cost registers and with them warps (13.2 to 14.6 us); a ring of shared memory 19.4.
+//
+// What bounds it: instructions, some 170 of a warp for 16 x 128 weights (28672 x 8192, groups of 128, one token: 35 us,
+// 3.4 TB/s), and at small matrices how many pieces a warp has one after the other: the warps of an SM are shared by as many blocks as
+// leave the fewest (1024 x 8192, one token, weights out of L2: 9.0 us with 8 warps a block, 5.0 with 32; 2432 x 16384 16.5 and 7.9;
+// 8192 x 8192, groups of 64 with zero points 24 and 18).  More pieces ahead or two tiles of rows a
+// block cost registers and with them warps; a ring of shared memory took half as long again.
 // Columns past the last token hold another token's x and are dropped.
 #include <algorithm>
 #include <cmath>
@@ -25,8 +29,10 @@ namespace mk {
 
 namespace {
 
-constexpr int W4_WARPS = 8;
-constexpr int W4_THREADS = 32 * W4_WARPS;
+// Warps of an SM, and of a block at most, for TILES times 8 tokens: 64, 80, 102 or 128 registers a thread.
+template <int WPG, bool ZEROS, int TILES>
+constexpr int W4_WARPS = TILES == 1 ? (ZEROS || WPG == 1 ? 24 : 32) : TILES == 2 ? (ZEROS ? 20 : 24) : 16;
+constexpr int W4_SMS = 152;
 constexpr int W4_TOKENS = 8;
 constexpr int W4_ROWS = 16;
 
@@ -49,11 +55,26 @@ struct Step {
   T s[2][GPC], z[2][ZEROS ? GPC : 1];
 };
 
-// WPG: words of a thread in a group (4, 2, 1 for groups of 128, 64, 32).  WHOLE: k is whole pieces.
-template <class T, int WPG, bool ZEROS, bool WHOLE>
-__global__ void __launch_bounds__(W4_THREADS) mk_w4_kernel(const __grid_constant__ W4Params p) {
+// 1, 2 or 4 neighbouring scales.
+template <class T, int N>
+__device__ __forceinline__ void read_groups(const T* p, T (&v)[N]) {
+  if constexpr (N == 1) v[0] = *p;
+  else if constexpr (N == 2) {
+    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p));
+    memcpy(v, &w, 4);
+  } else {
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+    memcpy(v, &w, 8);
+  }
+}
+
+// WPG: words of a thread in a group (4, 2, 1 for groups of 128, 64, 32).  WHOLE: k is whole pieces, whose scales
+// (and zero points) lie on 8, 4 or 2 bytes.
+template <class T, int WPG, bool ZEROS, bool WHOLE, int TILES>
+__global__ void __launch_bounds__(32 * W4_WARPS<WPG, ZEROS, TILES>) mk_w4_kernel(const __grid_constant__ W4Params p) {
   constexpr int GPC = 4 / WPG;                       // groups of a piece
-  __shared__ float red[W4_WARPS][W4_TOKENS][W4_ROWS + 1];
+  __shared__ float red[W4_WARPS<WPG, ZEROS, TILES>][TILES * W4_TOKENS][W4_ROWS + 1];
+  const int warps = blockDim.x >> 5;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, j = lane & 3;
   const int n0 = blockIdx.x * W4_ROWS;
   const uint8_t* codes[2];
@@ -65,7 +86,9 @@ __global__ void __launch_bounds__(W4_THREADS) mk_w4_kernel(const __grid_constant
     scales[t] = static_cast<const T*>(p.scales) + static_cast<long long>(row) * p.groups;
     zeros[t] = static_cast<const T*>(p.zeros) + static_cast<long long>(row) * p.groups;
   }
-  const char* x = p.x + min(r, p.m - 1) * p.x_row + j * (WPG * 16);
+  const char* x[TILES];
+#pragma unroll
+  for (int i = 0; i < TILES; ++i) x[i] = p.x + min(8 * i + r, p.m - 1) * p.x_row + j * (WPG * 16);
   const int pieces = (p.k + W4_PIECE - 1) / W4_PIECE;
   auto load = [&](int c, Step<T, GPC, ZEROS>& o) {
     if (WHOLE && c >= pieces) return;
@@ -85,72 +108,126 @@ __global__ void __launch_bounds__(W4_THREADS) mk_w4_kernel(const __grid_constant
         } else {
           o.w[t][g] = real ? __ldg(reinterpret_cast<const uint32_t*>(a)) : 0;
         }
-        o.s[t][g] = real ? scales[t][group] : Piece<T>::of(0.f);
-        if constexpr (ZEROS) o.z[t][g] = real ? zeros[t][group] : Piece<T>::of(0.f);
+        if constexpr (!WHOLE) {
+          o.s[t][g] = real ? scales[t][group] : Piece<T>::of(0.f);
+          if constexpr (ZEROS) o.z[t][g] = real ? zeros[t][group] : Piece<T>::of(0.f);
+        }
+      }
+    }
+    if constexpr (WHOLE) {                           // a piece's at once: one at a time 1024 x 8192, groups of 32, took 11.7 us
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        read_groups(scales[t] + c * GPC, o.s[t]);
+        if constexpr (ZEROS) read_groups(zeros[t] + c * GPC, o.z[t]);
       }
     }
   };
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  float acc[TILES][4];
+#pragma unroll
+  for (int i = 0; i < TILES; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
   auto multiply = [&](int c, const Step<T, GPC, ZEROS>& now) {
 #pragma unroll
     for (int g = 0; g < GPC; ++g) {
       const int group = c * GPC + g;
-      float part[4] = {0.f, 0.f, 0.f, 0.f}, ones[4] = {0.f, 0.f, 0.f, 0.f};
+      float part[TILES][4], ones[TILES][4];
+#pragma unroll
+      for (int i = 0; i < TILES; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) part[i][e] = ones[i][e] = 0.f;
 #pragma unroll
       for (int w = 0; w < WPG; ++w) {
-        uint32_t xs[4], a[4], b[4];
-        const uint4 v = WHOLE || group < p.groups ? __ldg(reinterpret_cast<const uint4*>(x + group * (WPG * 64)) + w) : make_uint4(0, 0, 0, 0);
-        x_pairs(v, xs);
+        uint32_t a[4], b[4];
         Codes<T>::pairs(now.w[0][g * WPG + w], a);
         Codes<T>::pairs(now.w[1][g * WPG + w], b);
-        mma<T>(part, a[0], b[0], a[1], b[1], xs[0], xs[1]);
-        mma<T>(part, a[2], b[2], a[3], b[3], xs[2], xs[3]);
-        if constexpr (ZEROS) {
-          constexpr uint32_t I = Codes<T>::ONES;
-          mma<T>(ones, I, I, I, I, xs[0], xs[1]);
-          mma<T>(ones, I, I, I, I, xs[2], xs[3]);
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) {
+          uint32_t xs[4];
+          const uint4 v = WHOLE || group < p.groups ? __ldg(reinterpret_cast<const uint4*>(x[i] + group * (WPG * 64)) + w) : make_uint4(0, 0, 0, 0);
+          x_pairs(v, xs);
+          mma<T>(part[i], a[0], b[0], a[1], b[1], xs[0], xs[1]);
+          mma<T>(part[i], a[2], b[2], a[3], b[3], xs[2], xs[3]);
+          if constexpr (ZEROS) {
+            constexpr uint32_t I = Codes<T>::ONES;
+            mma<T>(ones[i], I, I, I, I, xs[0], xs[1]);
+            mma<T>(ones[i], I, I, I, I, xs[2], xs[3]);
+          }
         }
       }
-      if constexpr (ZEROS) {
-        const float oa = 8.f - Piece<T>::one(now.z[0][g]), ob = 8.f - Piece<T>::one(now.z[1][g]);
-        part[0] = fmaf(oa, ones[0], part[0]);
-        part[1] = fmaf(oa, ones[1], part[1]);
-        part[2] = fmaf(ob, ones[2], part[2]);
-        part[3] = fmaf(ob, ones[3], part[3]);
-      }
       const float fa = Piece<T>::one(now.s[0][g]), fb = Piece<T>::one(now.s[1][g]);
-      acc[0] = fmaf(fa, part[0], acc[0]);
-      acc[1] = fmaf(fa, part[1], acc[1]);
-      acc[2] = fmaf(fb, part[2], acc[2]);
-      acc[3] = fmaf(fb, part[3], acc[3]);
+#pragma unroll
+      for (int i = 0; i < TILES; ++i) {
+        if constexpr (ZEROS) {
+          const float oa = 8.f - Piece<T>::one(now.z[0][g]), ob = 8.f - Piece<T>::one(now.z[1][g]);
+          part[i][0] = fmaf(oa, ones[i][0], part[i][0]);
+          part[i][1] = fmaf(oa, ones[i][1], part[i][1]);
+          part[i][2] = fmaf(ob, ones[i][2], part[i][2]);
+          part[i][3] = fmaf(ob, ones[i][3], part[i][3]);
+        }
+        acc[i][0] = fmaf(fa, part[i][0], acc[i][0]);
+        acc[i][1] = fmaf(fa, part[i][1], acc[i][1]);
+        acc[i][2] = fmaf(fb, part[i][2], acc[i][2]);
+        acc[i][3] = fmaf(fb, part[i][3], acc[i][3]);
+      }
     }
   };
   Step<T, GPC, ZEROS> next;
   if (warp < pieces) load(warp, next);
-  for (int c = warp; c < pieces; c += W4_WARPS) {
+  for (int c = warp; c < pieces; c += warps) {
     const Step<T, GPC, ZEROS> now = next;
-    load(c + W4_WARPS, next);
+    load(c + warps, next);
     multiply(c, now);
   }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) red[warp][2 * j + (e & 1)][r + 8 * (e >> 1)] = acc[e];
-  __syncthreads();
-  const int row = threadIdx.x % W4_ROWS, t = threadIdx.x / W4_ROWS;
-  if (t >= p.m || t >= W4_TOKENS || n0 + row >= p.n) return;
-  float s = 0.f;
+  for (int i = 0; i < TILES; ++i)
 #pragma unroll
-  for (int w = 0; w < W4_WARPS; ++w) s += red[w][t][row];
-  w4_store<T>(p, t, n0 + row, s);
+    for (int e = 0; e < 4; ++e) red[warp][8 * i + 2 * j + (e & 1)][r + 8 * (e >> 1)] = acc[i][e];
+  __syncthreads();
+  const int row = threadIdx.x % W4_ROWS;
+  if (n0 + row >= p.n) return;
+  for (int t = threadIdx.x / W4_ROWS; t < min(p.m, TILES * W4_TOKENS); t += blockDim.x / W4_ROWS) {
+    float s = 0.f;
+#pragma unroll 8
+    for (int w = 0; w < warps; ++w) s += red[w][t][row];
+    w4_store<T>(p, t, n0 + row, s);
+  }
 }
 
 // ------------------------------------------------------------------ host
 
+// Warps of a block: those of an SM shared by 4 to 1 blocks, whichever leaves the fewest turns (waves of blocks times pieces a
+// warp), then no more than the turns need.
+int warps_of(int blocks, int pieces, int most) {
+  int warps = 0, least = 0;
+  for (int b = 4; b >= 1; --b) {
+    const int w = std::min(most / b, pieces), turns = (blocks + W4_SMS * b - 1) / (W4_SMS * b) * ((pieces + w - 1) / w);
+    if (warps == 0 || turns < least) {
+      warps = w;
+      least = turns;
+    }
+  }
+  const int turns = (pieces + warps - 1) / warps;
+  return (pieces + turns - 1) / turns;
+}
+
+template <class T, int WPG, bool ZEROS, bool WHOLE, int TILES>
+cudaError_t launch_w4(const W4Params& p, cudaStream_t s) {
+  const int grid = static_cast<int>(ceil_div_ll(p.n, W4_ROWS));
+  const int warps = warps_of(grid, (p.k + W4_PIECE - 1) / W4_PIECE, W4_WARPS<WPG, ZEROS, TILES>);
+  mk_w4_kernel<T, WPG, ZEROS, WHOLE, TILES><<<grid, 32 * warps, 0, s>>>(p);
+  return cudaGetLastError();
+}
+template <class T, int WPG, bool ZEROS, bool WHOLE>
+cudaError_t launch_w4(const W4Params& p, cudaStream_t s) {
+  if (p.m <= 8) return launch_w4<T, WPG, ZEROS, WHOLE, 1>(p, s);
+  return p.m <= 16 ? launch_w4<T, WPG, ZEROS, WHOLE, 2>(p, s) : launch_w4<T, WPG, ZEROS, WHOLE, 4>(p, s);
+}
 template <class T, int WPG, bool ZEROS>
 cudaError_t launch_w4(const W4Params& p, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>(ceil_div_ll(p.n, W4_ROWS));
-  if (p.k % W4_PIECE == 0) mk_w4_kernel<T, WPG, ZEROS, true><<<grid, W4_THREADS, 0, s>>>(p);
-  else mk_w4_kernel<T, WPG, ZEROS, false><<<grid, W4_THREADS, 0, s>>>(p);
-  return cudaGetLastError();
+  const uintptr_t lie = reinterpret_cast<uintptr_t>(p.scales) | reinterpret_cast<uintptr_t>(p.zeros);
+  const bool whole = p.k % W4_PIECE == 0 && !(lie & (8 / WPG - 1));
+  return whole ? launch_w4<T, WPG, ZEROS, true>(p, s) : launch_w4<T, WPG, ZEROS, false>(p, s);
 }
 template <class T, int WPG>
 cudaError_t launch_w4(const W4Params& p, cudaStream_t s) {

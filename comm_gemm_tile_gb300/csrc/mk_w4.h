@@ -1,4 +1,4 @@
-// mk_w4.h -- 4-bit weights as the kernels of mk_w4.cu (few tokens) and mk_w4_tiles.cu (more of them) take them.
+// mk_w4.h -- 4-bit weights as the kernels of mk_w4.cu (few tokens) and mk_w4_tiles.cu (more of them, and large matrices) take them.
 #pragma once
 
 #include "mk_seq.cuh"
@@ -18,13 +18,17 @@ struct W4Params {
 
 constexpr int W4_PIECE = 128;          // k of a step
 
-// Whether mk_w4_tiles.cu serves a call: more than 8 tokens, and fewer where small groups make the other way's scales
-// dear and the matrix is large enough for three launches (graphs, us, mma.sync / tcgen05, one token: groups of 32,
-// 1024 x 2048 4.5 / 6.6, 3584 x 8192 16.8 / 12.8, 28672 x 8192 90 / 53; of 64 with zero points 8192 x 8192 18.2 / 17.3,
-// 28672 x 8192 52 / 46; of 128 without, 34 / 42).
+// Whether mk_w4_tiles.cu serves a call: its three launches and its steps' waits pay with many tokens or a large matrix
+// (graphs, weights out of L2, bf16, us, mma.sync / tcgen05.  32 tokens: 2048 x 4096, groups of 64 5.9 / 12.4, with zero points
+// 7.6 / 12.7; 4096 x 4096 10.0 / 12.0, 13.5 / 12.8, groups of 128 12.7 / 11.8.  16 tokens: 4096 x 4096 7.4 / 11.5, 9.3 / 11.9;
+// 3584 x 8192 11.9 / 14.2, 15.3 / 14.5; 8192 x 8192 21.7 / 19.3, 25.8 / 20.0.  One token: 8192 x 8192 15.0 / 18.8, 18.5 / 19.5;
+// 28672 x 8192 38 / 45, 50 / 49, groups of 32 49 / 45).
 inline bool w4_use_tiles(const W4Params& p, int group) {
   const long long weights = static_cast<long long>(p.n) * p.k;
-  return p.m > 8 || (group == 32 && weights >= (1LL << 24)) || (group == 64 && weights >= (1LL << 27));
+  if (p.m > 32) return true;
+  if (p.m > 16) return weights >= (1LL << 24);
+  if (p.m > 8) return weights > (p.zeros ? 1LL << 24 : 1LL << 25);
+  return weights >= (1LL << 27) && (p.zeros || group == 32);
 }
 size_t w4_tiles_scratch(const W4Params& p, int group);
 mk_status launch_w4_tiles(const W4Params& p, mk_dtype dtype, int group, void* scratch, uint32_t* hdr, const mk_config* cfg,

@@ -72,6 +72,27 @@ def test_long_rows(m, group, k):
     check(x, w, F32)
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("m,n,k", [(1, 16136, 8320), (8, 16136, 8320), (9, 4104, 8320), (16, 2056, 8320), (16, 4104, 8320),
+                                   (17, 2056, 8320), (32, 4104, 4224), (24, 1000, 8320)])
+def test_large_matrices(m, n, k, group):
+    """Both sides of the sizes from which few tokens are taken another way."""
+    for zeros, dtype in ((False, HF), (True, BF)):
+        x, w = problem(m, n, k, group, zeros, dtype, seed=m)
+        check(x, w, F32)
+
+
+def test_scales_off_whole_pieces():
+    x, w = problem(5, 40, 512, 32, True, BF, seed=14)
+    room = torch.zeros(2, 40 * 16 + 8, dtype=BF, device="cuda")
+    for off in (1, 2, 4):
+        s, z = (r[off:off + 640].view(40, 16) for r in room)
+        s.copy_(w.scales)
+        z.copy_(w.zeros)
+        for a, b in ((s, z), (s, w.zeros), (w.scales, z)):
+            check(x, mk.W4Weight(w.codes, a, b))
+
+
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("zeros", [True, False])
 @pytest.mark.parametrize("m,n,k,group", [(9, 4104, 8320, 32), (40, 4104, 8320, 32), (40, 4224, 8192, 64), (40, 4104, 8320, 128)])
@@ -162,7 +183,7 @@ def test_streams_and_graphs():
 
 def test_a_wait_that_runs_out_is_reported():
     """One CTA stops loading: its waits end, the call returns, and the next one serves."""
-    x, w = problem(16, 300, 4096, 128, True, BF, seed=12)
+    x, w = problem(48, 300, 4096, 128, True, BF, seed=12)
     want = mk.w4_gemm(x, w)
     ws = mk.Workspace()
     mk.w4_gemm(x, w, cfg=mk.Config(wait_limit_ns=20_000_000, inject=1), workspace=ws)
@@ -173,7 +194,7 @@ def test_a_wait_that_runs_out_is_reported():
 @pytest.mark.parametrize("ctas", [1, 3, 7, 64])
 def test_any_number_of_ctas(ctas):
     """Runs that hold many tiles, one, or a part: the joins differ, the sums' tolerance does not."""
-    for m, n, k, group in ((9, 260, 1152, 128), (40, 700, 640, 64), (33, 129, 96, 32)):
+    for m, n, k, group in ((50, 260, 1152, 128), (40, 700, 640, 64), (33, 129, 96, 32)):
         x, w = problem(m, n, k, group, True, HF, seed=13)
         check(x, w, F32, cfg=mk.Config(max_ctas=ctas))
 
