@@ -446,6 +446,14 @@ struct Turn {
 #pragma unroll
     for (int j = 0; j < N; ++j) x[j] = *reinterpret_cast<const uint2*>(from + j * ROWS * D);
   }
+  // A lane of the warp, known only when get's loads have come: one that says so before, while they wait behind others,
+  // would have their place filled again.
+  __device__ __forceinline__ int come() const {
+    uint32_t all = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) all ^= x[j].y;
+    return __any_sync(0xffffffffu, all & 1u) ? 1 : 0;
+  }
   __device__ __forceinline__ void put(uint8_t* out, int tw, int lane) const {
     uint8_t* to = out + v_piece(tw * (32 / PER) + lane / PER, lane % PER);
 #pragma unroll
@@ -520,8 +528,7 @@ __device__ void pr_turn(const PagedParams& p, Walk w, volatile int* dead, uint32
       // ---- K
       if (!pr_wait(dead, p, bars + B_RKFULL, u & 1u, WHERE_COPY)) return;
       turn.get(sm + P::RK, tw, lane);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + B_RKEMPTY);
+      if (lane == turn.come()) mbar_arrive(bars + B_RKEMPTY);
       if (!pr_wait(dead, p, bars + B_KEMPTY + 8u * st, ph ^ 1u, WHERE_COPY)) return;
       turn.put(sm + P::K + st * P::TILE, tw, lane);
       fence_proxy_async_smem();
@@ -530,8 +537,7 @@ __device__ void pr_turn(const PagedParams& p, Walk w, volatile int* dead, uint32
       // ---- V
       if (!pr_wait(dead, p, bars + B_RVFULL, u & 1u, WHERE_COPY)) return;
       turn.get(sm + P::RV, tw, lane);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + B_RVEMPTY);
+      if (lane == turn.come()) mbar_arrive(bars + B_RVEMPTY);
       if (!pr_wait(dead, p, bars + B_VEMPTY + 8u * st, ph ^ 1u, WHERE_COPY)) return;
       uint8_t* out = sm + P::V + st * P::TILE;
       turn.put(out, tw, lane);
