@@ -1042,8 +1042,8 @@ def w4_gemm(x, w: W4Weight, *, out_dtype=None, out=None, cfg: Config | None = No
     """y = x @ W^T for the rows of a decode step: x [m x k] of the weight's 16-bit type, y [m x n] in it or fp32
     (out_dtype).  Codes are multiplied as whole numbers, groups scaled and summed in fp32, y is rounded once.
     x's rows start on whole 16-byte pieces.  Any m is taken; for long prompts the 16-bit products are faster.  For serving: an
-    x that requires a gradient is refused.  Calls of more than 32 rows, and of large matrices, take scratch from the
-    stream's memory; a wait that runs out there sets the device status."""
+    x that requires a gradient is refused.  Calls of many rows or large matrices take scratch from the stream's
+    memory; a wait that runs out there sets the device status."""
     _need(isinstance(w, W4Weight), "w is not a W4Weight")
     _need(out_dtype in (None, torch.float32) or out_dtype == getattr(x, "dtype", None), "out_dtype is x's type or fp32")
     _need(not _wants_gradient(x), "x requires a gradient: w4_gemm has none (use torch.no_grad)")

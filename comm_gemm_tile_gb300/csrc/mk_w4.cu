@@ -7,7 +7,7 @@
 // by its scale in fp32: nothing is rounded before the output.  Zero points enter
 // as (8 - z) sum_k x[m][k] of the group, from one more product with ones.
 //
-// Here: few tokens, up to 8, 16 or 32 (more, and large matrices, go to mk_w4_tiles.cu).  The products are mma.sync
+// Here: few tokens, 8, 16 or 32 at a time (more of them, and large matrices, go to mk_w4_tiles.cu).  The products are mma.sync
 // m16n8k16 with weights as the 16 rows and 8 tokens as the columns, one for each 8 of them.  They sum over k in any
 // order, so a thread's own codes are its operands as they come, and x is read in the same order.  A block
 // has 16 rows of the matrix; its warps share out k in pieces of 128, a thread 16 bytes
@@ -86,9 +86,10 @@ __global__ void __launch_bounds__(32 * W4_WARPS<WPG, ZEROS, TILES>) mk_w4_kernel
     scales[t] = static_cast<const T*>(p.scales) + static_cast<long long>(row) * p.groups;
     zeros[t] = static_cast<const T*>(p.zeros) + static_cast<long long>(row) * p.groups;
   }
+  const int t0 = TILES == 4 ? blockIdx.y * (TILES * W4_TOKENS) : 0;
   const char* x[TILES];
 #pragma unroll
-  for (int i = 0; i < TILES; ++i) x[i] = p.x + min(8 * i + r, p.m - 1) * p.x_row + j * (WPG * 16);
+  for (int i = 0; i < TILES; ++i) x[i] = p.x + min(t0 + 8 * i + r, p.m - 1) * p.x_row + j * (WPG * 16);
   const int pieces = (p.k + W4_PIECE - 1) / W4_PIECE;
   auto load = [&](int c, Step<T, GPC, ZEROS>& o) {
     if (WHOLE && c >= pieces) return;
@@ -186,11 +187,11 @@ __global__ void __launch_bounds__(32 * W4_WARPS<WPG, ZEROS, TILES>) mk_w4_kernel
   __syncthreads();
   const int row = threadIdx.x % W4_ROWS;
   if (n0 + row >= p.n) return;
-  for (int t = threadIdx.x / W4_ROWS; t < min(p.m, TILES * W4_TOKENS); t += blockDim.x / W4_ROWS) {
+  for (int t = threadIdx.x / W4_ROWS; t < min(p.m - t0, TILES * W4_TOKENS); t += blockDim.x / W4_ROWS) {
     float s = 0.f;
 #pragma unroll 8
     for (int w = 0; w < warps; ++w) s += red[w][t][row];
-    w4_store<T>(p, t, n0 + row, s);
+    w4_store<T>(p, t0 + t, n0 + row, s);
   }
 }
 
@@ -213,9 +214,9 @@ int warps_of(int blocks, int pieces, int most) {
 
 template <class T, int WPG, bool ZEROS, bool WHOLE, int TILES>
 cudaError_t launch_w4(const W4Params& p, cudaStream_t s) {
-  const int grid = static_cast<int>(ceil_div_ll(p.n, W4_ROWS));
-  const int warps = warps_of(grid, (p.k + W4_PIECE - 1) / W4_PIECE, W4_WARPS<WPG, ZEROS, TILES>);
-  mk_w4_kernel<T, WPG, ZEROS, WHOLE, TILES><<<grid, 32 * warps, 0, s>>>(p);
+  const int grid = static_cast<int>(ceil_div_ll(p.n, W4_ROWS)), passes = (p.m + TILES * W4_TOKENS - 1) / (TILES * W4_TOKENS);
+  const int warps = warps_of(grid * passes, (p.k + W4_PIECE - 1) / W4_PIECE, W4_WARPS<WPG, ZEROS, TILES>);
+  mk_w4_kernel<T, WPG, ZEROS, WHOLE, TILES><<<dim3(grid, passes), 32 * warps, 0, s>>>(p);
   return cudaGetLastError();
 }
 template <class T, int WPG, bool ZEROS, bool WHOLE>

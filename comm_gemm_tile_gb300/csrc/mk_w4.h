@@ -22,11 +22,11 @@ constexpr int W4_PIECE = 128;          // k of a step
 // (graphs, weights out of L2, bf16, us, mma.sync / tcgen05.  32 tokens: 2048 x 4096, groups of 64 5.9 / 12.4, with zero points
 // 7.6 / 12.7; 4096 x 4096 10.0 / 12.0, 13.5 / 12.8, groups of 128 12.7 / 11.8.  16 tokens: 4096 x 4096 7.4 / 11.5, 9.3 / 11.9;
 // 3584 x 8192 11.9 / 14.2, 15.3 / 14.5; 8192 x 8192 21.7 / 19.3, 25.8 / 20.0.  One token: 8192 x 8192 15.0 / 18.8, 18.5 / 19.5;
-// 28672 x 8192 38 / 45, 50 / 49, groups of 32 49 / 45).
+// 28672 x 8192 38 / 45, 50 / 49, groups of 32 49 / 45.  More tokens, 32 at a time: 64 of 2048 x 2048, groups of 128, 7.3 / 9.5,
+// of 4096 x 1024 7.6 / 8.4, 128 of them 13.7 / 11.4).
 inline bool w4_use_tiles(const W4Params& p, int group) {
   const long long weights = static_cast<long long>(p.n) * p.k;
-  if (p.m > 32) return true;
-  if (p.m > 16) return weights >= (1LL << 24);
+  if (p.m > 16) return weights * ((p.m + 31) / 32) >= (1LL << 24) || p.m > (1 << 20);      // (more blocks of tokens than a grid has)
   if (p.m > 8) return weights > (p.zeros ? 1LL << 24 : 1LL << 25);
   return weights >= (1LL << 27) && (p.zeros || group == 32);
 }

@@ -609,7 +609,7 @@ size_t mk_w4_gemm_scratch_size(const mk_w4_weight *w, long long m);
  * numbers, groups are scaled and summed in fp32, y is rounded once.  A row of x that
  * holds an infinity gives infinities or NaN.  Built for the rows of a decode step; more
  * are taken 64 at a time (m below 2^24, and m n k below 2^49 or so).
- * Calls that take scratch (all of more than 32 rows, fewer of large matrices; 256-byte aligned, of the call alone, no
+ * Calls that take scratch (of many rows or large matrices; 256-byte aligned, of the call alone, no
  * clearing) also take a workspace of 256 bytes, zero-filled once, which holds the device status
  * and nothing else: MK_ERR_TIMEOUT if a bounded wait ran out, after which y is undefined.
  * Both may be NULL for the others.  cfg (may be NULL): max_ctas, wait_limit_ns and inject (1: one CTA does not

@@ -95,9 +95,9 @@ def weight(**kw):
 
 
 def test_w4_refusals(L):
-    size = L.mk_w4_gemm_scratch_size(ref(weight()), 33)
+    size = L.mk_w4_gemm_scratch_size(ref(weight()), 60000)
     assert size > 0 and L.mk_w4_gemm_scratch_size(ref(weight()), 32) == 0
-    assert L.mk_w4_gemm_scratch_size(ref(weight(k=0)), 33) == 0 == L.mk_w4_gemm_scratch_size(ref(weight()), -1)
+    assert L.mk_w4_gemm_scratch_size(ref(weight(k=0)), 60000) == 0 == L.mk_w4_gemm_scratch_size(ref(weight()), -1)
 
     def call(x=GOOD, x_row=256, w=weight(), y=GOOD, y_row=40, dtype=mk.MK_BF16, odt=mk.MK_BF16, m=4, scratch=None,
              scratch_bytes=0, ws=None, ws_bytes=0, cfg=None):
@@ -114,7 +114,7 @@ def test_w4_refusals(L):
                 dict(w=weight(n=(1 << 31) - 1, k=1 << 29)), dict(cfg=mk.Config(mode=1)), dict(cfg=mk.Config(operand=1)),
                 dict(cfg=mk.Config(max_ctas=-1))):
         assert call(**bad) == mk.MK_ERR_INVALID, bad
-    more = dict(m=33, scratch=GOOD, scratch_bytes=size, ws=GOOD, ws_bytes=256)
+    more = dict(m=60000, scratch=GOOD, scratch_bytes=size, ws=GOOD, ws_bytes=256)
     for bad in (dict(scratch=None), dict(scratch=GOOD + 64), dict(scratch_bytes=size - 1), dict(ws=None), dict(ws=GOOD + 8),
                 dict(ws_bytes=255)):
         assert call(**{**more, **bad}) == mk.MK_ERR_INVALID, bad

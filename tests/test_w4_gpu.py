@@ -74,7 +74,8 @@ def test_long_rows(m, group, k):
 
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("m,n,k", [(1, 16136, 8320), (8, 16136, 8320), (9, 4104, 8320), (16, 2056, 8320), (16, 4104, 8320),
-                                   (17, 2056, 8320), (32, 4104, 4224), (24, 1000, 8320)])
+                                   (17, 2056, 8320), (32, 4104, 4224), (24, 1000, 8320), (33, 2056, 8320), (64, 2100, 4224),
+                                   (65, 1030, 8320), (130, 1001, 4224), (8192, 300, 256), (3000, 77, 128)])
 def test_large_matrices(m, n, k, group):
     """Both sides of the sizes from which few tokens are taken another way."""
     for zeros, dtype in ((False, HF), (True, BF)):
@@ -159,8 +160,9 @@ def test_quantized_weights(symmetric, dtype):
     assert bool((w.dequantize(F32)[3, :64] == 0).all()) and w.dequantize().dtype == dtype
 
 
-def test_streams_and_graphs():
-    x, w = problem(4, 300, 1024, 128, False, BF, seed=11)
+@pytest.mark.parametrize("m,n,k", [(4, 300, 1024), (40, 4100, 4224)])
+def test_streams_and_graphs(m, n, k):
+    x, w = problem(m, n, k, 128, True, BF, seed=11)
     want = mk.w4_gemm(x, w)
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
@@ -183,7 +185,7 @@ def test_streams_and_graphs():
 
 def test_a_wait_that_runs_out_is_reported():
     """One CTA stops loading: its waits end, the call returns, and the next one serves."""
-    x, w = problem(48, 300, 4096, 128, True, BF, seed=12)
+    x, w = problem(48, 4100, 4096, 128, True, BF, seed=12)
     want = mk.w4_gemm(x, w)
     ws = mk.Workspace()
     mk.w4_gemm(x, w, cfg=mk.Config(wait_limit_ns=20_000_000, inject=1), workspace=ws)
@@ -194,7 +196,7 @@ def test_a_wait_that_runs_out_is_reported():
 @pytest.mark.parametrize("ctas", [1, 3, 7, 64])
 def test_any_number_of_ctas(ctas):
     """Runs that hold many tiles, one, or a part: the joins differ, the sums' tolerance does not."""
-    for m, n, k, group in ((50, 260, 1152, 128), (40, 700, 640, 64), (33, 129, 96, 32)):
+    for m, n, k, group in ((50, 2060, 8320, 128), (40, 4100, 4160, 64), (8192, 300, 96, 32), (600, 1000, 1152, 128)):
         x, w = problem(m, n, k, group, True, HF, seed=13)
         check(x, w, F32, cfg=mk.Config(max_ctas=ctas))
 
