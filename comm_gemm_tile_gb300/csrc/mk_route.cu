@@ -426,6 +426,7 @@ __global__ void __launch_bounds__(32 * RS_WARPS) mk_route_sums_kernel(const __gr
   __shared__ int s_c[RS_WARPS][32];
   __shared__ float share[8];                         // in the first block: every block's
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane, width = 2 * p.E + 2;
+  cluster_arrive();                                  // this block has started
   griddep_wait();
   float a = 0.f;
   int c = 0;
@@ -450,6 +451,7 @@ __global__ void __launch_bounds__(32 * RS_WARPS) mk_route_sums_kernel(const __gr
     n = __reduce_add_sync(0xffffffffu, n);
   }
   __syncthreads();
+  cluster_wait();                                    // so has the first, whose shared memory is stored to
   if (warp == 0) {
     a = 0.f;
     c = 0;
