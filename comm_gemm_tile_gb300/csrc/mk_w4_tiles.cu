@@ -273,11 +273,6 @@ __global__ void __launch_bounds__(WT_THREADS, 1) mk_w4_tiles_kernel(const __grid
     ahead(c);
     bool fresh = true;                                       // sc_next is this step's
     for (int i = 0; i < count; ++i) {
-      // (the sums of the step before have been used, by every lane)
-      if (ZEROS && i > 0 && lane == 0) {
-        mbar_arrive(bars + B_XEMPTY + 8 * (2 * (i - 1) % SX));
-        mbar_arrive(bars + B_XEMPTY + 8 * (2 * (i - 1) % SX) + 8);
-      }
       const bool ends = c + 1 == steps;
       const int row_now = row;
       if (fresh) {
@@ -352,14 +347,21 @@ __global__ void __launch_bounds__(WT_THREADS, 1) mk_w4_tiles_kernel(const __grid
         }
         if (h == 1) tc_fence_before();
       }
+      // The sums' place is free only once every lane has them, not merely asked for them: which lane says so is known from
+      // what they were added to (one word of each 16 bytes).
+      int who = 0;
+      if (ZEROS) {
+        uint64_t all = 0;
+#pragma unroll
+        for (int e = 0; e < TOK / 2; e += 2) all ^= acc[e];
+        who = __any_sync(0xffffffffu, static_cast<uint32_t>(all) & 1u) ? 1 : 0;
+      }
       __syncwarp();
-      if (lane == 0) {
+      if (lane == who) {
         mbar_arrive(bars + B_DEMPTY + 8 * place0);
         mbar_arrive(bars + B_DEMPTY + 8 * place0 + 8);
-        if (!ZEROS) {
-          mbar_arrive(bars + B_XEMPTY + 8 * x0);
-          mbar_arrive(bars + B_XEMPTY + 8 * x0 + 8);
-        }
+        mbar_arrive(bars + B_XEMPTY + 8 * x0);
+        mbar_arrive(bars + B_XEMPTY + 8 * x0 + 8);
       }
       if (ends || i + 1 == count) {
         // all of a tile, or the run's part of it: that at the run's beginning first, another second
