@@ -582,8 +582,15 @@ __device__ __forceinline__ void consume(const PagedParams& p, const Segment& g, 
         }
       }
       if (masked) fence_proxy_async_smem();   // the cleared rows before the next load of this stage
+      // The stage is free only once every lane has its values, not merely asked for them (behind loads from memory that
+      // miss, theirs from shared memory may take longer than the next tile does): which lane says so is known from the
+      // products' sums.  Those need the keys' values too, for the weights.
+      uint32_t all = 0;
+#pragma unroll
+      for (int j = 0; j < OT; ++j) all ^= __float_as_uint(o[0][j][0]);
+      const int who = __any_sync(0xffffffffu, all & 1u) ? 1 : 0;
       __syncwarp();
-      if (lane == 0) mbar_arrive(wk.empty + 8u * st);
+      if (lane == who) mbar_arrive(wk.empty + 8u * st);
     }
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
