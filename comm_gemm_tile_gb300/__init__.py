@@ -699,19 +699,30 @@ def rope_freqs(rot: int, *, base: float = 10000.0, scaling: str | None = None, f
     return f.to(device), magnitude
 
 
+def _used_here(other, *tensors):
+    """Of tensors that forward used on a stream it was given (`other`) and backward reads on the current one: their memory
+    goes back to that stream's pool only when the current one is done with it."""
+    if not other:
+        return
+    for t in tensors:
+        if t is not None:
+            t.record_stream(torch.cuda.current_stream(t.device))
+
+
 class _Rope(torch.autograd.Function):
     """rope under autograd: the gradient is the inverse rotation, through rope again, so that it has one too."""
 
     @staticmethod
     def forward(ctx, x, freqs, positions, how, stream):
         y = rope(x, freqs, positions, **how, stream=stream)
-        ctx.how = how
+        ctx.how, ctx.other = how, stream is not None
         ctx.save_for_backward(freqs, positions)
         return y
 
     @staticmethod
     def backward(ctx, dy):
         freqs, positions = ctx.saved_tensors
+        _used_here(ctx.other, freqs, positions)
         if dy.stride(-1) != 1:      # the gradient of a sum, for one, is expanded
             dy = dy.contiguous()
         # (autograd runs this on the stream that was current in forward, and orders it)
@@ -863,7 +874,7 @@ class _RmsNorm(torch.autograd.Function):
     def forward(ctx, x, weight, residual, eps, stream):
         ctx.set_materialize_grads(False)
         y = rms_norm(x, weight, residual=residual, eps=eps, stream=stream)
-        ctx.eps, ctx.residual = eps, residual is not None
+        ctx.eps, ctx.residual, ctx.other = eps, residual is not None, stream is not None
         ctx.save_for_backward(y[1] if ctx.residual else x, weight)
         return y
 
@@ -871,6 +882,7 @@ class _RmsNorm(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy, dh=None):
         h, weight = ctx.saved_tensors
+        _used_here(ctx.other, h, weight)
         dx = dh
         dw = None
         if dy is not None:       # (autograd runs this on the stream that was current in forward, and orders it)
@@ -935,7 +947,7 @@ class _MoeRoute(torch.autograd.Function):
     def forward(ctx, logits, topk, how, mask, workspace, stream):
         ctx.set_materialize_grads(False)
         r = moe_route(logits, topk, mask=mask, workspace=workspace, stream=stream, **how)
-        ctx.how = how
+        ctx.how, ctx.other = how, stream is not None
         ctx.save_for_backward(logits, r["topk_idx"], r["counts"], r["tokens"])
         ctx.mark_non_differentiable(r["topk_idx"], r["counts"], r["tokens"])
         return tuple(r[name] for name in _ROUTE)
@@ -946,6 +958,7 @@ class _MoeRoute(torch.autograd.Function):
         logits, idx, counts, tokens = ctx.saved_tensors
         if dgates is None and dbalance is None and dz is None:
             return (None,) * 6
+        _used_here(ctx.other, logits, idx, counts, tokens)
         route = {"topk_idx": idx, "counts": counts, "tokens": tokens}
         if dgates is not None:
             dgates = dgates.contiguous()
