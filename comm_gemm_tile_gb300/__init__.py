@@ -272,11 +272,13 @@ class Workspace:
     it.  A buffer stays allocated when a larger one takes its place, since calls in flight on any stream and
     graphs keep its address; buffers at least double, so that those kept are no more than the last.  A buffer made
     while capturing is filled by every captured call that uses it, until a call outside has filled it: graphs may be
-    replayed in any order."""
+    replayed in any order.  Calls whose scratch holds nothing from one call to the next (moe_route,
+    rms_norm_backward) have a buffer apart, so that they leave the others' flags and status alone."""
 
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
         self.buf = None
+        self.apart = None          # the Workspace of scratch
         self.kept = []             # outgrown buffers
         self.filled = True         # False: allocated while capturing, so that only a replay would fill it
 
@@ -300,6 +302,12 @@ class Workspace:
             if not capturing:
                 torch.cuda.current_stream(self.device).synchronize()
         return self.buf
+
+    def scratch(self, nbytes: int, stream=None) -> torch.Tensor:
+        """Memory that no other operator's call expects to find as it left it."""
+        if self.apart is None:
+            self.apart = Workspace(self.device)
+        return self.apart.get(nbytes, stream)
 
 
 _default_ws: dict = {}
@@ -818,7 +826,8 @@ def paged_attention(q, cache: KVCache, cu_q, kv_len, pages, *, causal: bool = Tr
     the first `sinks`.  max_q: an upper bound on a sequence's new tokens, if the caller knows
     one.  Returns out, or (out, lse) with return_lse; rows that see nothing are 0 (-inf).  For
     serving: no gradient comes through it.
-    Calls that may run at the same time (on several streams) need a workspace each."""
+    Calls that may run at the same time (on several streams) need a workspace each, and not one of the
+    collective calls (ag_gemm and so on)."""
     _need(isinstance(cache, KVCache), "cache is not a KVCache")
     lse = True if return_lse else None
     if stream is not None:
@@ -854,7 +863,7 @@ def _on_given(stream, x):
 
 
 def _getter(workspace, stream):
-    return None if workspace is None else functools.partial(workspace.get, stream=stream)
+    return None if workspace is None else functools.partial(getattr(workspace, "scratch", workspace.get), stream=stream)
 
 
 def _wants_gradient(*tensors):
@@ -976,7 +985,7 @@ def moe_route(logits, topk: int, *, normalize: bool = True, scale: float = 1.0, 
     mask [T] bool: False leaves a token out (ids -1, gates 0, counted nowhere), as tokens whose
     logits are all -inf are; an expert with a logit of -inf is not chosen.  `out` may pass
     preallocated buffers.  Where logits requires a gradient, autograd takes that of the gates and
-    both losses (not into buffers of the caller's: those are refused)."""
+    both losses (not into buffers of the caller's: those are refused).  Scratch as for rms_norm_backward."""
     o = out or {}
     if _wants_gradient(logits):
         _need(not o, "logits requires a gradient: moe_route cannot write to given outputs")

@@ -518,7 +518,8 @@ mk_status mk_paged_attention(const void *q, void *out, float *lse, mk_dtype dtyp
  * What stands around the products of a layer: the norm of its rows, the choice
  * of experts, and products with 4-bit weights.  These entry points keep
  * nothing between calls, and a CUDA graph may capture them.  Where no other use is given, a
- * workspace is scratch of the call alone and needs no clearing.  Strides count elements. */
+ * workspace is scratch of the call alone: it needs no clearing, and is written from its first byte on, so that
+ * it cannot be the workspace of an entry point above, whose flags and status stand there.  Strides count elements. */
 
 /* [tokens x heads x n] rows, the last dimension contiguous; any token and head
  * strides, 0 (an expanded dimension) for inputs only. */
