@@ -667,6 +667,13 @@ def _on(stream, device):
     return torch.cuda.stream(stream)
 
 
+def _written(*given):
+    """Tells autograd of the outputs that a call was given: a graph that has saved one may not use what it holds now."""
+    given = [t for t in given if isinstance(t, torch.Tensor)]
+    if given:
+        torch.autograd.graph.increment_version(given)
+
+
 def _new(shape, dtype, device, stream):
     with _on(stream, device):
         return torch.empty(shape, dtype=dtype, device=device)
@@ -750,6 +757,7 @@ def rope(x, freqs, positions=None, *, start: int = 0, interleaved: bool = False,
         _need(out is None, "x requires a gradient: rope cannot write it to a given out")
         return _Rope.apply(x, freqs, positions, dict(start=start, interleaved=interleaved, inverse=inverse,
                                                      magnitude=magnitude), stream)
+    given = out
     if out is None:
         _need(isinstance(x, torch.Tensor), "x is not a tensor")
         if stream is None:
@@ -760,6 +768,8 @@ def rope(x, freqs, positions=None, *, start: int = 0, interleaved: bool = False,
     st = _bind().rope(_address("mk_rope"), x, out, freqs, positions, start, interleaved, inverse, magnitude, _raw(stream))
     if st:
         _check(st, "mk_rope")
+    if given is not None:
+        _written(given)
     return out
 
 
@@ -801,6 +811,7 @@ def kv_append(cache: KVCache, k, v, cu_q, kv_len, pages, *, q=None, freqs=None, 
     Returns q_out (None without q).  Tokens without a slot set the device status.  For serving:
     no gradient comes through it (rope has one)."""
     _need(isinstance(cache, KVCache), "cache is not a KVCache")
+    given = q_out
     if q is not None and q_out is None and stream is not None:
         q_out = _new(q.shape, q.dtype, q.device, stream)
     st, q_out = _bind().append(_address("mk_kv_append"), cache._c, cache._device, k, v, cu_q, kv_len, pages, q, q_out,
@@ -808,6 +819,8 @@ def kv_append(cache: KVCache, k, v, cu_q, kv_len, pages, *, q=None, freqs=None, 
                                _raw(stream))
     if st:
         _check(st, "mk_kv_append")
+    if given is not None:
+        _written(given)
     return q_out
 
 
@@ -829,7 +842,7 @@ def paged_attention(q, cache: KVCache, cu_q, kv_len, pages, *, causal: bool = Tr
     Calls that may run at the same time (on several streams) need a workspace each, and not one of the
     collective calls (ag_gemm and so on)."""
     _need(isinstance(cache, KVCache), "cache is not a KVCache")
-    lse = True if return_lse else None
+    lse, given = True if return_lse else None, out
     if stream is not None:
         _need(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be a [tokens x heads x d] CUDA tensor")
         if out is None:
@@ -846,6 +859,8 @@ def paged_attention(q, cache: KVCache, cu_q, kv_len, pages, *, causal: bool = Tr
                                      ctypes.addressof(c) if c is not None else None, _raw(stream))
     if st:
         _check(st, "mk_paged_attention")
+    if given is not None:
+        _written(given)
     return (out, lse) if return_lse else out
 
 
@@ -924,6 +939,8 @@ def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, out_dtype=None
                                            _raw(stream))
     if st:
         _check(st, "mk_rms_norm")
+    if out is not None or scale_out is not None or h_out is not None:
+        _written(out, scale_out, h_out)
     if residual is not None:
         return (y, scale, h) if e4m3 else (y, h)
     return (y, scale) if e4m3 else y
@@ -944,6 +961,8 @@ def rms_norm_backward(dy, h, weight=None, *, dh=None, eps: float = 1e-6, weight_
                                                _getter(workspace, stream), dy, dh, h, weight, out, wants, eps, _raw(stream))
     if st:
         _check(st, "mk_rms_norm_backward")
+    if out is not None:
+        _written(out)
     return dx, dw
 
 
@@ -995,6 +1014,8 @@ def moe_route(logits, topk: int, *, normalize: bool = True, scale: float = 1.0, 
                                  logits, topk, normalize, scale, mask, tuple(map(o.get, _ROUTE)) if o else _NONE, _raw(stream))
     if st:
         _check(st, "mk_moe_route")
+    if o:
+        _written(*o.values())
     return dict(zip(_ROUTE, got))
 
 
@@ -1008,6 +1029,8 @@ def moe_route_backward(logits, route, dgates=None, dbalance=None, dz=None, *, no
                                         route["tokens"], dgates, dbalance, dz, normalize, scale, out, _raw(stream))
     if st:
         _check(st, "mk_moe_route_backward")
+    if out is not None:
+        _written(out)
     return dl
 
 
@@ -1078,6 +1101,8 @@ def w4_gemm(x, w: W4Weight, *, out_dtype=None, out=None, cfg: Config | None = No
                                 out_dtype == torch.float32, ctypes.addressof(c) if c is not None else None, _raw(stream))
     if st:
         _check(st, "mk_w4_gemm")
+    if out is not None:
+        _written(out)
     return y
 
 
