@@ -753,6 +753,7 @@ def rope(x, freqs, positions=None, *, start: int = 0, interleaved: bool = False,
     halves.  inverse=True is the gradient: rope(dy, ..., inverse=True) = dx; where x requires a
     gradient, autograd takes it (not through an `out` of the caller's: that is refused).
     Returns out (unless given: of x's shape and memory order, dense; out=x works in place)."""
+    _no_tangents(x)
     if torch.is_grad_enabled() and getattr(x, "requires_grad", False):
         _need(out is None, "x requires a gradient: rope cannot write it to a given out")
         return _Rope.apply(x, freqs, positions, dict(start=start, interleaved=interleaved, inverse=inverse,
@@ -888,6 +889,15 @@ def _wants_gradient(*tensors):
     return False
 
 
+def _no_tangents(*tensors):
+    """Refuses tensors of forward-mode differentiation, whose tangents would be lost."""
+    if torch.autograd.forward_ad._current_level < 0:
+        return
+    for t in tensors:
+        _need(not isinstance(t, torch.Tensor) or torch.autograd.forward_ad.unpack_dual(t).tangent is None,
+              "an input has a tangent of forward-mode differentiation: there is none of this call")
+
+
 def _rows_gradient(g):
     """A gradient as the calls read it: the one of a sum, for one, is expanded."""
     return g if g is None or g.stride(-1) == 1 else g.contiguous()
@@ -930,9 +940,10 @@ def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, out_dtype=None
     caller's: those are refused)."""
     e4m3 = out_dtype == FP8
     _need(out_dtype is None or e4m3 or out_dtype == getattr(x, "dtype", None), "out_dtype is x's type or float8_e4m3fn")
+    _no_tangents(x, weight, residual)
     if _wants_gradient(x, weight, residual):
         _need(not e4m3, "an input requires a gradient: an 8-bit output has none")
-        _need(out is None and h_out is None, "an input requires a gradient: rms_norm cannot write to a given out")
+        _need(out is None and scale_out is None and h_out is None, "an input requires a gradient: rms_norm cannot write to a given out")
         return _RmsNorm.apply(x, weight, residual, eps, stream)
     with _on_given(stream, x):
         st, y, scale, h = _bind().rms_norm(_address("mk_rms_norm"), x, residual, weight, out, scale_out, h_out, e4m3, eps,
@@ -954,6 +965,7 @@ def rms_norm_backward(dy, h, weight=None, *, dh=None, eps: float = 1e-6, weight_
     alike (out: where to write it, dy and dh too).  dweight is None without a weight or with
     weight_gradient=False.  Scratch comes from the stream's memory unless a workspace is given
     (calls that may run at the same time need one each)."""
+    _no_tangents(dy, h, weight, dh)
     wants = True if weight is not None and weight_gradient else None
     with _on_given(stream, dy):
         st, dx, dw = _bind().rms_norm_backward(_address("mk_rms_norm_backward"),
@@ -1006,6 +1018,7 @@ def moe_route(logits, topk: int, *, normalize: bool = True, scale: float = 1.0, 
     preallocated buffers.  Where logits requires a gradient, autograd takes that of the gates and
     both losses (not into buffers of the caller's: those are refused).  Scratch as for rms_norm_backward."""
     o = out or {}
+    _no_tangents(logits)
     if _wants_gradient(logits):
         _need(not o, "logits requires a gradient: moe_route cannot write to given outputs")
         return dict(zip(_ROUTE, _MoeRoute.apply(logits, topk, dict(normalize=normalize, scale=scale), mask, workspace, stream)))
@@ -1024,6 +1037,7 @@ def moe_route_backward(logits, route, dgates=None, dbalance=None, dz=None, *, no
     """The gradient of moe_route with respect to the logits, for the gradients of its gates [T x topk],
     balance_loss and z_loss (fp32 on the device; None: none).  route: what moe_route returned for these logits,
     normalize and scale as it had them.  The counts are constants."""
+    _no_tangents(logits, dgates, dbalance, dz)
     with _on_given(stream, logits):
         st, dl = _bind().route_backward(_address("mk_moe_route_backward"), logits, route["topk_idx"], route["counts"],
                                         route["tokens"], dgates, dbalance, dz, normalize, scale, out, _raw(stream))
@@ -1087,11 +1101,12 @@ def w4_gemm(x, w: W4Weight, *, out_dtype=None, out=None, cfg: Config | None = No
     """y = x @ W^T for the rows of a decode step: x [m x k] of the weight's 16-bit type, y [m x n] in it or fp32
     (out_dtype).  Codes are multiplied as whole numbers, groups scaled and summed in fp32, y is rounded once.
     x's rows start on whole 16-byte pieces.  Any m is taken; for long prompts the 16-bit products are faster.  For serving: an
-    x that requires a gradient is refused.  Calls of many rows or large matrices take scratch from the stream's
+    x, scales or zero points that require a gradient are refused.  Calls of many rows or large matrices take scratch from the stream's
     memory; a wait that runs out there sets the device status."""
     _need(isinstance(w, W4Weight), "w is not a W4Weight")
     _need(out_dtype in (None, torch.float32) or out_dtype == getattr(x, "dtype", None), "out_dtype is x's type or fp32")
-    _need(not _wants_gradient(x), "x requires a gradient: w4_gemm has none (use torch.no_grad)")
+    _no_tangents(x, *w._tensors[1:])
+    _need(not _wants_gradient(x, *w._tensors[1:]), "x, scales or zero points require a gradient: w4_gemm has none (use torch.no_grad)")
     c = cfg.c() if cfg is not None else None
     get = (workspace or _default_ws.get(w._device) or _ws(None, w.codes.device)).get
     if stream is not None:
