@@ -1052,7 +1052,8 @@ class W4Weight:
     """A matrix of 4-bit weights [n x k], W[i][j] = scales[i][j / group] * (code[i][j] - zeros[i][j / group]):
     codes [n x k / 2] uint8 (the code of an even j in the lower four bits), scales and zeros [n x k / group]
     bf16 or fp16, all contiguous; without zeros 8 takes their place.  Groups have 32, 64 or 128 weights.
-    W4Weight.quantize makes one."""
+    W4Weight.quantize makes one.  What the tensors hold may change, their memory may not: w4_gemm refuses a weight
+    one of whose tensors has been given other memory."""
 
     def __init__(self, codes, scales, zeros=None):
         self._w, self._device = _bind().w4(codes, scales, zeros)   # the bytes of an mk_w4_weight
@@ -1113,7 +1114,7 @@ def w4_gemm(x, w: W4Weight, *, out_dtype=None, out=None, cfg: Config | None = No
         get = functools.partial(get, stream=stream)
     with _on_given(stream, x):
         st, y = _bind().w4_gemm(_address("mk_w4_gemm"), _address("mk_w4_gemm_scratch_size"), get, x, w._w, w._device, out,
-                                out_dtype == torch.float32, ctypes.addressof(c) if c is not None else None, _raw(stream))
+                                out_dtype == torch.float32, ctypes.addressof(c) if c is not None else None, _raw(stream), w._tensors)
     if st:
         _check(st, "mk_w4_gemm")
     if out is not None:

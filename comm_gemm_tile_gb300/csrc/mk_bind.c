@@ -147,6 +147,25 @@ static int read_seqs(PyObject *cu_q, PyObject *kv_len, PyObject *pages, int devi
   return 0;
 }
 
+/* The memory of a descriptor's tensors: theirs still, or they have been given other memory (t.data = ..., set_, resize_) and
+ * what the descriptor names may be gone. */
+static int still_there(PyObject *tensors, const void *const *at, int n, const char *what) {
+  if (!PyTuple_Check(tensors) || PyTuple_GET_SIZE(tensors) != n) return refuse("not a descriptor's tensors");
+  for (int i = 0; i < n; ++i) {
+    PyObject *t = PyTuple_GET_ITEM(tensors, i);
+    if (t == Py_None) continue;
+    PyObject *p = PyObject_CallMethodNoArgs(t, s_data_ptr);
+    if (!p) return -1;
+    const void *now = PyLong_AsVoidPtr(p);
+    Py_DECREF(p);
+    if (now != at[i]) {
+      PyErr_Format(PyExc_ValueError, "a tensor of the %s has been given other memory: make another one of it", what);
+      return -1;
+    }
+  }
+  return 0;
+}
+
 /* A launch goes to the current device, whatever its pointers' and its stream's device. */
 static int check_device(int device) {
   PyObject *v = PyObject_CallNoArgs(current_device);
@@ -767,15 +786,18 @@ static PyObject *bind_w4(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 typedef size_t (*w4_size_fn)(const mk_w4_weight *, long long);
 typedef mk_status (*w4_fn)(const void *, long long, const mk_w4_weight *, void *, long long, mk_dtype, mk_dtype, long long,
                            void *, size_t, void *, size_t, const mk_config *, mk_stream_t);
-/* w4_gemm(fn, size_fn, get_workspace, x, weight, device, out, fp32, config address, stream) -> (status, out) */
+/* w4_gemm(fn, size_fn, get_workspace, x, weight, device, out, fp32, config address, stream, the weight's tensors)
+ * -> (status, out) */
 static PyObject *bind_w4_gemm(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   (void)self;
-  NEED(n == 10, "w4_gemm: 10 arguments");
+  NEED(n == 11, "w4_gemm: 11 arguments");
   tensor x, y, sc, ws;
   mk_stream_t st;
   if (read_matrix(a[3], &x, "x")) return NULL;
   NEED(PyBytes_Check(a[4]) && PyBytes_GET_SIZE(a[4]) == (Py_ssize_t)sizeof(mk_w4_weight), "not a 4-bit weight");
   const mk_w4_weight *w = (const mk_w4_weight *)PyBytes_AS_STRING(a[4]);
+  const void *const at[3] = {w->codes, w->scales, w->zeros};
+  if (still_there(a[10], at, 3, "4-bit weight")) return NULL;
   const int dev = (int)PyLong_AsLong(a[5]), f32 = PyObject_IsTrue(a[7]);
   void *cfg = a[8] == Py_None ? NULL : PyLong_AsVoidPtr(a[8]);
   if (PyErr_Occurred()) return NULL;
