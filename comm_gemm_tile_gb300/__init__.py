@@ -778,8 +778,8 @@ class KVCache:
     """A paged key / value cache: k, v [n_pages x heads x page_size x d] (any strides with d
     contiguous, the same for both; a cache laid out [n_pages x page_size x heads x d] is passed
     as k.transpose(1, 2)) in bf16, fp16 or float8_e4m3fn, the latter with k_scale, v_scale
-    [n_pages x heads] fp32, not negative.  KVCache.empty allocates one.  The tensors are the
-    cache's for good: a larger one is another KVCache."""
+    [n_pages x heads] fp32, not negative.  KVCache.empty allocates one.  The tensors and their memory are the
+    cache's for good: a larger one is another KVCache, and one of whose tensors has been given other memory is refused."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         self._c, self._device = _bind().cache(k, v, k_scale, v_scale)   # the bytes of an mk_kv_cache
@@ -817,7 +817,7 @@ def kv_append(cache: KVCache, k, v, cu_q, kv_len, pages, *, q=None, freqs=None, 
         q_out = _new(q.shape, q.dtype, q.device, stream)
     st, q_out = _bind().append(_address("mk_kv_append"), cache._c, cache._device, k, v, cu_q, kv_len, pages, q, q_out,
                                freqs, positions, interleaved, magnitude, (workspace or _default_ws.get(cache._device) or _ws(None, cache.k.device)).get(256, stream),
-                               _raw(stream))
+                               _raw(stream), cache._tensors)
     if st:
         _check(st, "mk_kv_append")
     if given is not None:
@@ -857,7 +857,7 @@ def paged_attention(q, cache: KVCache, cu_q, kv_len, pages, *, causal: bool = Tr
     st, out, lse = _bind().attention(_address("mk_paged_attention"), _address("mk_paged_attention_workspace_size"),
                                      get, q, cache._c, cache._device, cu_q, kv_len, pages, causal, window, sinks, scale,
                                      max_q, out, lse,
-                                     ctypes.addressof(c) if c is not None else None, _raw(stream))
+                                     ctypes.addressof(c) if c is not None else None, _raw(stream), cache._tensors)
     if st:
         _check(st, "mk_paged_attention")
     if given is not None:

@@ -274,28 +274,30 @@ static PyObject *bind_rope(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   return PyLong_FromLong(e);
 }
 
-static int read_cache(PyObject *bytes, PyObject *device, const mk_kv_cache **c, int *dev) {
+static int read_cache(PyObject *bytes, PyObject *device, PyObject *tensors, const mk_kv_cache **c, int *dev) {
   if (!PyBytes_Check(bytes) || PyBytes_GET_SIZE(bytes) != (Py_ssize_t)sizeof(mk_kv_cache)) return refuse("not a cache");
   *c = (const mk_kv_cache *)PyBytes_AS_STRING(bytes);
   *dev = (int)PyLong_AsLong(device);
-  return PyErr_Occurred() ? -1 : 0;
+  if (PyErr_Occurred()) return -1;
+  const void *const at[4] = {(*c)->k, (*c)->v, (*c)->k_scale, (*c)->v_scale};
+  return still_there(tensors, at, 4, "cache");
 }
 
 typedef mk_status (*append_fn)(const mk_kv_cache *, const void *, const void *, mk_dtype, long long, long long, long long,
                                long long, long long, const void *, void *, int, long long, long long, long long,
                                long long, const mk_seq_batch *, const mk_rotation *, void *, size_t, mk_stream_t);
 /* append(fn, cache, device, k, v, cu_q, kv_len, pages, q, q_out, freqs, positions, interleaved, magnitude, workspace,
- * stream) -> (status, q_out) */
+ * stream, the cache's tensors) -> (status, q_out) */
 static PyObject *bind_append(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   (void)self;
-  NEED(n == 16, "append: 16 arguments");
+  NEED(n == 17, "append: 17 arguments");
   const mk_kv_cache *c;
   int dev;
   tensor k, v, q, o, w;
   mk_seq_batch s;
   mk_rotation r;
   mk_stream_t st;
-  if (read_cache(a[1], a[2], &c, &dev) || read_rows(a[3], &k, "k", NULL, 0) || read_rows(a[4], &v, "v", &k, 1)) return NULL;
+  if (read_cache(a[1], a[2], a[16], &c, &dev) || read_rows(a[3], &k, "k", NULL, 0) || read_rows(a[4], &v, "v", &k, 1)) return NULL;
   NEED(k.shape[1] == c->heads && k.shape[2] == c->d, "k and v do not fit the cache's heads and d");
   NEED((k.dtype == MK_BF16 || k.dtype == MK_F16) && (c->dtype == k.dtype || c->dtype == MK_E4M3) && k.device == dev,
        "k and v do not have the cache's type or device");
@@ -340,16 +342,16 @@ typedef mk_status (*attention_fn)(const void *, void *, float *, mk_dtype, long 
                                   long long, const mk_kv_cache *, const mk_seq_batch *, float, int, int, int, int, void *,
                                   size_t, const mk_config *, mk_stream_t);
 /* attention(fn, size_fn, get_workspace, q, cache, device, cu_q, kv_len, pages, causal, window, sinks, scale, max_q, out,
- * lse (a tensor, True to make one, or None), config address, stream) -> (status, out, lse) */
+ * lse (a tensor, True to make one, or None), config address, stream, the cache's tensors) -> (status, out, lse) */
 static PyObject *bind_attention(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   (void)self;
-  NEED(n == 18, "attention: 18 arguments");
+  NEED(n == 19, "attention: 19 arguments");
   const mk_kv_cache *c;
   int dev;
   tensor q, o, l, w;
   mk_seq_batch s;
   mk_stream_t st;
-  if (read_rows(a[3], &q, "q", NULL, 0) || read_cache(a[4], a[5], &c, &dev)) return NULL;
+  if (read_rows(a[3], &q, "q", NULL, 0) || read_cache(a[4], a[5], a[18], &c, &dev)) return NULL;
   NEED((q.dtype == MK_BF16 || q.dtype == MK_F16) && (c->dtype == q.dtype || c->dtype == MK_E4M3) && q.device == dev,
        "q does not have the cache's type or device");
   NEED(c->dtype != MK_E4M3 || q.dtype == MK_BF16, "an 8-bit cache takes bf16 queries");
