@@ -667,11 +667,12 @@ def _on(stream, device):
     return torch.cuda.stream(stream)
 
 
+_increment_version = torch.autograd.graph.increment_version
+
+
 def _written(*given):
     """Tells autograd of the outputs that a call was given: a graph that has saved one may not use what it holds now."""
-    given = [t for t in given if isinstance(t, torch.Tensor)]
-    if given:
-        torch.autograd.graph.increment_version(given)
+    _increment_version([t for t in given if t is not None and isinstance(t, torch.Tensor)])
 
 
 def _new(shape, dtype, device, stream):
@@ -753,7 +754,8 @@ def rope(x, freqs, positions=None, *, start: int = 0, interleaved: bool = False,
     halves.  inverse=True is the gradient: rope(dy, ..., inverse=True) = dx; where x requires a
     gradient, autograd takes it (not through an `out` of the caller's: that is refused).
     Returns out (unless given: of x's shape and memory order, dense; out=x works in place)."""
-    _no_tangents(x)
+    if _forward_ad._current_level >= 0:
+        _no_tangents(x)
     if torch.is_grad_enabled() and getattr(x, "requires_grad", False):
         _need(out is None, "x requires a gradient: rope cannot write it to a given out")
         return _Rope.apply(x, freqs, positions, dict(start=start, interleaved=interleaved, inverse=inverse,
@@ -889,12 +891,13 @@ def _wants_gradient(*tensors):
     return False
 
 
+_forward_ad = torch.autograd.forward_ad      # (_current_level: -1 outside of forward-mode differentiation)
+
+
 def _no_tangents(*tensors):
     """Refuses tensors of forward-mode differentiation, whose tangents would be lost."""
-    if torch.autograd.forward_ad._current_level < 0:
-        return
     for t in tensors:
-        _need(not isinstance(t, torch.Tensor) or torch.autograd.forward_ad.unpack_dual(t).tangent is None,
+        _need(not isinstance(t, torch.Tensor) or _forward_ad.unpack_dual(t).tangent is None,
               "an input has a tangent of forward-mode differentiation: there is none of this call")
 
 
@@ -940,7 +943,8 @@ def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, out_dtype=None
     caller's: those are refused)."""
     e4m3 = out_dtype == FP8
     _need(out_dtype is None or e4m3 or out_dtype == getattr(x, "dtype", None), "out_dtype is x's type or float8_e4m3fn")
-    _no_tangents(x, weight, residual)
+    if _forward_ad._current_level >= 0:
+        _no_tangents(x, weight, residual)
     if _wants_gradient(x, weight, residual):
         _need(not e4m3, "an input requires a gradient: an 8-bit output has none")
         _need(out is None and scale_out is None and h_out is None, "an input requires a gradient: rms_norm cannot write to a given out")
@@ -965,7 +969,8 @@ def rms_norm_backward(dy, h, weight=None, *, dh=None, eps: float = 1e-6, weight_
     alike (out: where to write it, dy and dh too).  dweight is None without a weight or with
     weight_gradient=False.  Scratch comes from the stream's memory unless a workspace is given
     (calls that may run at the same time need one each)."""
-    _no_tangents(dy, h, weight, dh)
+    if _forward_ad._current_level >= 0:
+        _no_tangents(dy, h, weight, dh)
     wants = True if weight is not None and weight_gradient else None
     with _on_given(stream, dy):
         st, dx, dw = _bind().rms_norm_backward(_address("mk_rms_norm_backward"),
@@ -1018,7 +1023,8 @@ def moe_route(logits, topk: int, *, normalize: bool = True, scale: float = 1.0, 
     preallocated buffers.  Where logits requires a gradient, autograd takes that of the gates and
     both losses (not into buffers of the caller's: those are refused).  Scratch as for rms_norm_backward."""
     o = out or {}
-    _no_tangents(logits)
+    if _forward_ad._current_level >= 0:
+        _no_tangents(logits)
     if _wants_gradient(logits):
         _need(not o, "logits requires a gradient: moe_route cannot write to given outputs")
         return dict(zip(_ROUTE, _MoeRoute.apply(logits, topk, dict(normalize=normalize, scale=scale), mask, workspace, stream)))
@@ -1037,7 +1043,8 @@ def moe_route_backward(logits, route, dgates=None, dbalance=None, dz=None, *, no
     """The gradient of moe_route with respect to the logits, for the gradients of its gates [T x topk],
     balance_loss and z_loss (fp32 on the device; None: none).  route: what moe_route returned for these logits,
     normalize and scale as it had them.  The counts are constants."""
-    _no_tangents(logits, dgates, dbalance, dz)
+    if _forward_ad._current_level >= 0:
+        _no_tangents(logits, dgates, dbalance, dz)
     with _on_given(stream, logits):
         st, dl = _bind().route_backward(_address("mk_moe_route_backward"), logits, route["topk_idx"], route["counts"],
                                         route["tokens"], dgates, dbalance, dz, normalize, scale, out, _raw(stream))
@@ -1106,15 +1113,17 @@ def w4_gemm(x, w: W4Weight, *, out_dtype=None, out=None, cfg: Config | None = No
     memory; a wait that runs out there sets the device status."""
     _need(isinstance(w, W4Weight), "w is not a W4Weight")
     _need(out_dtype in (None, torch.float32) or out_dtype == getattr(x, "dtype", None), "out_dtype is x's type or fp32")
-    _no_tangents(x, *w._tensors[1:])
-    _need(not _wants_gradient(x, *w._tensors[1:]), "x, scales or zero points require a gradient: w4_gemm has none (use torch.no_grad)")
+    if _forward_ad._current_level >= 0:
+        _no_tangents(x, w.scales, w.zeros)
+    tensors = w._tensors
+    _need(not _wants_gradient(x, tensors[1], tensors[2]), "x, scales or zero points require a gradient: w4_gemm has none (use torch.no_grad)")
     c = cfg.c() if cfg is not None else None
     get = (workspace or _default_ws.get(w._device) or _ws(None, w.codes.device)).get
     if stream is not None:
         get = functools.partial(get, stream=stream)
     with _on_given(stream, x):
         st, y = _bind().w4_gemm(_address("mk_w4_gemm"), _address("mk_w4_gemm_scratch_size"), get, x, w._w, w._device, out,
-                                out_dtype == torch.float32, ctypes.addressof(c) if c is not None else None, _raw(stream), w._tensors)
+                                out_dtype == torch.float32, ctypes.addressof(c) if c is not None else None, _raw(stream), tensors)
     if st:
         _check(st, "mk_w4_gemm")
     if out is not None:
