@@ -232,6 +232,9 @@ __device__ __forceinline__ float2 over_row2(float2 v, int lanes, float2 (*buf)[3
 // Whether fp32 did not hold a row's sum of squares: high (or not a number), or low where eps does not cover it.
 __device__ __forceinline__ bool sum_high(float ss) { return !(ss <= 1e36f); }
 __device__ __forceinline__ bool sum_low(float ss, int n, float eps) { return eps < 1e-30f && ss < 1e-30f * n; }
+// Whether products of a row's elements with a gradient may be below fp32's range where those of u are not: small rows
+// that eps lets grow.
+__device__ __forceinline__ bool row_small(float ss, int n, float eps) { return eps < 1e-12f && ss < 1e-12f * n; }
 // r of a row whose sum of squares is ss; of (h by)^2 where that is not 1.  (A product of the two factors near fp32's
 // least numbers, for rows past 1e38, keeps 21 bits.)
 __device__ __forceinline__ float inverse_root(float ss, int n, float eps, float by) {
@@ -510,7 +513,7 @@ __global__ void __launch_bounds__(WIDE ? GradShape<T, WAY, U>::THREADS : NM_THRE
     };
     float2 s = sums(1.f, 1.f);
     float by = 1.f;
-    const bool high = sum_high(s.x), low = sum_low(s.x, p.n, p.eps), far = high || low || !(fabsf(s.y) <= 1e36f);
+    const bool high = sum_high(s.x), low = sum_low(s.x, p.n, p.eps), far = high || row_small(s.x, p.n, p.eps) || !(fabsf(s.y) <= 1e36f);
     const bool again = __any_sync(0xffffffffu, far);
     if (again) {
       by = high ? NM_DOWN : low ? NM_UP : 1.f;
