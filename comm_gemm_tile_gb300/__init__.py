@@ -1076,7 +1076,8 @@ class W4Weight:
         around 8, else scale (max - min) / 15 and the zero point of the least weight."""
         _need(w.dim() == 2 and group in (32, 64, 128) and w.shape[1] % group == 0, "w must be [n x k], k whole groups of 32, 64 or 128")
         _need(dtype in (torch.bfloat16, torch.float16), "scales are bf16 or fp16")
-        f = w.detach().float().view(w.shape[0], -1, group)
+        n, k = w.shape
+        f = w.detach().float().view(n, k // group, group)
         if symmetric:
             scale, zero = f.abs().amax(dim=-1) / 7, None
         else:
@@ -1087,7 +1088,7 @@ class W4Weight:
         if not symmetric:
             zero = (-lo / by[..., 0]).round().clamp(0, 15).to(dtype)
         code = (f / by).round() + (8 if symmetric else zero.float()[..., None])
-        code = code.clamp(0, 15).to(torch.uint8).view(w.shape[0], -1, 2)
+        code = code.clamp(0, 15).to(torch.uint8).view(n, k // 2, 2)
         return code[..., 0] | (code[..., 1] << 4), scale, zero
 
     @staticmethod
@@ -1099,7 +1100,7 @@ class W4Weight:
         """W [n x k] in the scales' type, or another (plain tensor operations): for checks, or for the 16-bit
         products of prompts."""
         c, s, z = self._tensors
-        code = torch.stack((c & 15, c >> 4), dim=-1).view(c.shape[0], s.shape[1], -1).float()
+        code = torch.stack((c & 15, c >> 4), dim=-1).view(*s.shape, 2 * c.shape[1] // s.shape[1]).float()
         w = (code - (8.0 if z is None else z.float()[..., None])) * s.float()[..., None]
         return w.flatten(1).to(dtype or s.dtype)
 
