@@ -708,11 +708,13 @@ cudaError_t launch_norm(const NormParams& p, const Split& s, Way way, cudaStream
 }
 
 // Shared memory: 24 KB a set of rows and block with two pieces a thread (three sets, three blocks of an SM), 48 to
-// 192 KB with four (two sets up to 512 threads, one beyond).
+// 192 KB with four (two sets up to 512 threads, which no 16-bit row passes, one beyond).
 template <class T, Way WAY>
 cudaError_t launch_pieces(const NormParams& p, const Split& s, cudaStream_t st) {
   if (s.u == 2) return launch_grad<T, WAY, 2, 3>(p, s, st);
-  return s.lanes <= 512 ? launch_grad<T, WAY, 4, 2>(p, s, st) : launch_grad<T, WAY, 4, 1>(p, s, st);
+  if constexpr (sizeof(T) == 4)
+    if (s.lanes > 512) return launch_grad<T, WAY, 4, 1>(p, s, st);
+  return launch_grad<T, WAY, 4, 2>(p, s, st);
 }
 template <class T>
 cudaError_t launch_grad(const NormParams& p, const Split& s, Way way, cudaStream_t st) {

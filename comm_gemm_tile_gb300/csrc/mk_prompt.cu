@@ -720,17 +720,8 @@ done:
 
 // ------------------------------------------------------------------ softmax (warps 4-7, 8-11)
 
-// (products and sums of two fp32 values at once: mk_ptx.cuh has two, split, fma2)
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
+// (products and sums of two fp32 values at once: mk_ptx.cuh has two, split, add2, mul2, fma2)
+
 // The weights 2^(c s + nref) of 32 scores as 16-bit pairs; returns their sum.  8-bit caches: scales
 // has those of the four groups of 8 keys, which c is multiplied by, and from 16 on those of their
 // values; the weight of a value is the weight times its scale and F, summed in sum_v.  ABOVE: the scores
