@@ -13,7 +13,7 @@
 // has 16 rows of the matrix; its warps share out k in pieces of 128, a thread 16 bytes
 // (32 codes) of two rows of each, loaded one piece ahead, and add their sums in shared memory, in order.
 //
-// What bounds it: instructions, some 170 of a warp for 16 x 128 weights (28672 x 8192, groups of 128, one token: 35 us,
+// What bounds it: instructions, some 170 of a warp for 16 x 128 weights (28672 x 8192, groups of 128, one token: 36 us,
 // 3.4 TB/s), and at small matrices how many pieces a warp has one after the other: the warps of an SM are shared by as many blocks as
 // leave the fewest (1024 x 8192, one token, weights out of L2: 9.0 us with 8 warps a block, 5.0 with 32; 2432 x 16384 16.5 and 7.9;
 // 8192 x 8192, groups of 64 with zero points 24 and 18).  More pieces ahead or two tiles of rows a

@@ -19,14 +19,17 @@ struct W4Params {
 constexpr int W4_PIECE = 128;          // k of a step
 
 // Whether mk_w4_tiles.cu serves a call: its three launches and its steps' waits pay with many tokens or a large matrix
-// (graphs, weights out of L2, bf16, us, mma.sync / tcgen05.  32 tokens: 2048 x 4096, groups of 64 5.9 / 12.4, with zero points
-// 7.6 / 12.7; 4096 x 4096 10.0 / 12.0, 13.5 / 12.8, groups of 128 12.7 / 11.8.  16 tokens: 4096 x 4096 7.4 / 11.5, 9.3 / 11.9;
-// 3584 x 8192 11.9 / 14.2, 15.3 / 14.5; 8192 x 8192 21.7 / 19.3, 25.8 / 20.0.  One token: 8192 x 8192 15.0 / 18.8, 18.5 / 19.5;
-// 28672 x 8192 38 / 45, 50 / 49, groups of 32 49 / 45.  More tokens, 32 at a time: 64 of 2048 x 2048, groups of 128, 7.3 / 9.5,
-// of 4096 x 1024 7.6 / 8.4, 128 of them 13.7 / 11.4).
+// (graphs, weights out of L2, bf16, us, mma.sync / tcgen05, by groups and (z) zero points).
+//   One token: 8192 x 8192 128 14.0 / 18.0, 64 15.0 / 18.3, 128 z 18.0 / 18.8, 32 17.2 / 18.8, 32 z 19.9 / 22.8;
+//   28672 x 8192 128 36.1 / 44.3, 64 37.8 / 44.8, 128 z 50.1 / 47.1, 64 z 52.2 / 49.1, 32 46.7 / 46.4, 32 z 59.2 / 59.0.
+//   16 tokens: 4096 x 4096 64 7.7 / 11.7, 128 z 10.0 / 11.8, 32 z 11.4 / 13.2; 3584 x 8192 128 13.7 / 13.8, 64 z 15.3 / 14.6;
+//   8192 x 4096 64 12.4 / 13.4, 128 z 16.4 / 13.7; 8192 x 8192 64 22.2 / 18.7, 32 z 31.8 / 23.2.
+//   More, 32 at a time: 17 and 32 tokens of 4096 x 4096 64 9.7 / 11.9 and 10.4 / 12.0, 128 10.8 / 11.9 and 12.8 / 12.0, 128 z 12.7 / 12.2 and
+//   14.2 / 12.3, 32 z 14.3 / 15.0 and 15.8 / 15.1; of 3584 x 8192 64 16.2 / 14.3 and 17.1 / 14.4; 64 of 2048 x 4096 64 9.8 / 13.8, 32 z 15.3 / 14.4;
+//   128 of 2048 x 2048 64 9.6 / 12.3, 128 12.5 / 12.2, 32 z 15.1 / 13.0, and of 2048 x 4096 17.3 / 13.1, 22.2 / 12.3, 27.6 / 18.2.
 inline bool w4_use_tiles(const W4Params& p, int group) {
   const long long weights = static_cast<long long>(p.n) * p.k;
-  if (p.m > 16) return weights * ((p.m + 31) / 32) >= (1LL << 24) || p.m > (1 << 20);      // (more blocks of tokens than a grid has)
+  if (p.m > 16) return weights * ((p.m + 31) / 32) > (1LL << 24) || p.m > (1 << 20);       // (more blocks of tokens than a grid has)
   if (p.m > 8) return weights > (p.zeros ? 1LL << 24 : 1LL << 25);
   return weights >= (1LL << 27) && (p.zeros || group == 32);
 }
