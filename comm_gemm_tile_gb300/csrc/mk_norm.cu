@@ -243,11 +243,12 @@ __device__ __forceinline__ float inverse_root(float ss, int n, float eps, float 
 constexpr float NM_DOWN = 8.271806125530277e-25f, NM_UP = 1.2089258196146292e24f;       // 2^-80, 2^80
 
 // v / s to nearest, for inv = 1 / s to nearest: the product with inv is a step off at most, and its remainder, which fma has
-// exactly, puts it right (Markstein 1990).  An infinite v has no remainder, and stays.  8192 x 8192 in bf16 with a residual, us:
+// exactly, puts it right (Markstein 1990).  Where there is none (v infinite, or a quotient that is exact, -0 among them) it
+// stays.  8192 x 8192 in bf16 with a residual, us:
 // the product alone 74, so 78, `/` 90.
 __device__ __forceinline__ float quotient(float v, float s, float inv) {
   const float q = v * inv, left = fmaf(-q, s, v);
-  return left == left ? fmaf(left, inv, q) : q;
+  return fabsf(left) > 0.f ? fmaf(left, inv, q) : q;
 }
 
 template <class T, Way WAY, int U, bool WIDE, bool OUT8>
