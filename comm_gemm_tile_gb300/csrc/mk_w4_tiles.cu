@@ -348,12 +348,12 @@ __global__ void __launch_bounds__(WT_THREADS, 1) mk_w4_tiles_kernel(const __grid
         if (h == 1) tc_fence_before();
       }
       // The sums' place is free only once every lane has them, not merely asked for them: which lane says so is known from
-      // what they were added to (one word of each 16 bytes).
+      // what they were added to (one word of each 8 bytes, however they were loaded).
       int who = 0;
       if (ZEROS) {
         uint64_t all = 0;
 #pragma unroll
-        for (int e = 0; e < TOK / 2; e += 2) all ^= acc[e];
+        for (int e = 0; e < TOK / 2; ++e) all ^= acc[e];
         who = __any_sync(0xffffffffu, static_cast<uint32_t>(all) & 1u) ? 1 : 0;
       }
       __syncwarp();
