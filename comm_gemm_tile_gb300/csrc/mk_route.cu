@@ -125,7 +125,10 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return m;
 }
 
-// exp(x), x <= 0: off by about |x| 2^-24 and 4 2^-24 of itself, 0 below 2^-126.  log(x) and 1 / x, x >= 1.
+// exp(x), x <= 0: off by about |x| 2^-24 and 4 2^-24 of itself (ex2.approx's documented 2^-22), 0 below 2^-126.  log(x) and
+// 1 / x, x >= 1: lg2.approx is off by 2^-22, past 2 by 2^-22 of itself, rcp.approx by a step.  With expf, logf and a division
+// to nearest instead 131072 x 256, 8 experts, takes 70 us forward and 51 back (58 and 47), and gates are off by 6.1e-8 (root mean
+// square, relative) for 6.6e-8, gradients by 8.3e-8 for 8.6e-8.
 __device__ __forceinline__ float exp2_of(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -355,7 +358,7 @@ __global__ void __launch_bounds__(RT_THREADS) mk_route_kernel(const __grid_const
         warp_sums(sum, own);
         const float inv = inverse(sum);
         add_times<PER>(psum, v, inv);
-        const float lse = top + log_of(sum);         // (sum is 1 .. 256: off by 3 2^-24)
+        const float lse = top + log_of(sum);         // (sum is 1 .. 256, its lg2 up to 8: off by 22 2^-24 at most)
         z = fmaf(lse, lse, z);
         ++n;
         w *= (p.normalize ? inverse(own) : inv) * p.scale;

@@ -39,7 +39,8 @@ mk_status launch_w4_tiles(const W4Params& p, mk_dtype dtype, int group, void* sc
 
 template <class T> struct Codes;
 template <> struct Codes<__half> {
-  // the 8 codes of a word as four pairs (codes i and i + 4), minus 8: exactly
+  // the 8 codes of a word as four pairs (codes i and i + 4), minus 8: exactly.  (A code in the low bits of 1024, or in
+  // those from 16 on, is a number at once: the way that is commonly published for small codes.)
   static __device__ __forceinline__ void pairs(uint32_t w, uint32_t (&o)[4]) {
     const uint32_t v = w >> 8;
     // 1024 + c, and 1024 + 16 c, in fp16

@@ -575,7 +575,8 @@ size_t mk_moe_route_workspace_size(long long T, int E);
  * An expert with a logit of -inf is never chosen: slots left over get id -1 and gate 0.  Tokens
  * that mask leaves out ([T] bytes, 0: left out; NULL: none is) and tokens without an
  * expert get ids -1 and gates 0 and count nowhere; with N = 0 both losses are 0.
- * E <= 256, 1 <= topk <= min(8, E).  fp32 sums in a fixed order. */
+ * E <= 256, 1 <= topk <= min(8, E).  fp32 sums in a fixed order; exponentials, logarithms and
+ * reciprocals of the special function unit, off by up to 2^-22 of themselves. */
 mk_status mk_moe_route(const void *logits, mk_dtype dtype, long long T, int E, long long row,
                        int topk, int normalize, float scale, const unsigned char *mask, int *topk_idx,
                        float *gates, int *counts, int *tokens, float *balance_loss, float *z_loss,
@@ -609,7 +610,7 @@ size_t mk_w4_gemm_scratch_size(const mk_w4_weight *w, long long m);
  * 16-byte pieces), y [m x n] of the same type or MK_F32.  Codes are multiplied as whole
  * numbers, groups are scaled and summed in fp32, y is rounded once.  A row of x that
  * holds an infinity gives infinities or NaN.  Built for the rows of a decode step; more
- * are taken 64 at a time (m below 2^24, and m n k below 2^49 or so).
+ * are taken 32 or 64 at a time (m below 2^24, and m n k below 2^49 or so).
  * Calls that take scratch (of many rows or large matrices; 256-byte aligned, of the call alone, no
  * clearing) also take a workspace of 256 bytes, zero-filled once, which holds the device status
  * and nothing else: MK_ERR_TIMEOUT if a bounded wait ran out, after which y is undefined.
